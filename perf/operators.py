@@ -227,7 +227,7 @@ def _prepare_clip(case, seed):
     s = {"op": "clip", "case": case, "grads": grads, "outs": outs, "flat": out, "max_norm": 1e-3 * math.sqrt(case["total"]) / 2}
     if own:
         from state_summary_scan_gb300 import api
-        s["plan"] = api.make_clip_plan(len(grads), case["total"], device=dev)
+        s["plan"] = api.make_clip_plan(len(grads), device=dev)
     return s
 
 
