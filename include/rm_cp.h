@@ -513,6 +513,117 @@ rm_status rm_gdr_backward_apply(const rm_cp_problem* p, const void* q, const voi
                                 const float* dS_out, void* dk, void* dv, float* dg, float* dbeta,
                                 void* ws, rm_stream_t stream);
 
+/*
+ * Norm of each head of queries and keys, and the position rotation, in one
+ * pass.  Per head row x in R^D with weight w [D] fp32 (NULL: 1):
+ *     r = (sum x^2 / D + eps)^(-1/2)   norm 1 (rms)
+ *         (sum x^2 + eps)^(-1/2)       norm 2 (l2)
+ *         1                            norm 0
+ *     y = x r w, then the first R elements of y are rotated in pairs (a, b):
+ *     a' = a c - b s,  b' = b c + a s,
+ * pair i being elements (i, i + R/2), or (2i, 2i + 1) with interleaved != 0,
+ * and (c, s) = table[position][0 | 1][i].  table is [max_pos][2][R/2] fp32
+ * (any scaling for long contexts is in its values).  The weights and the
+ * arithmetic are fp32; q', k' are rounded once.
+ *   q [B,T,Hq,D] and k [B,T,Hk,D] have strides in elements for (row, token,
+ *   head), elements of a head adjacent, every stride and base a multiple of
+ *   16 bytes (slices of a fused projection are read in place); q_out, k_out,
+ *   dq_out, dk_out, dq, dk are contiguous and alias no input.  D is a multiple
+ *   of 8, at most 256 (RM_ERR_UNSUPPORTED otherwise); R is even, 0 <= R <= D
+ *   (0: no rotation; table is then not read).
+ *   positions: int32 (pos64 = 0) or int64 (1), [B,T] (pos_rows = B), [T]
+ *   (pos_rows = 1), or NULL with pos_rows = 0: token t has position t.  A
+ *   position outside [0, max_pos) reads nothing and makes its token's rotated
+ *   elements NaN.
+ * rm_cp_qkr_backward: dq, dk from the gradients dq_out, dk_out of q', k', and
+ *   dwq, dwk [D] fp32 (each may be NULL).  Sums run in a fixed order.  ws:
+ *   rm_cp_qkr_workspace_size bytes (needed for dwq or dwk only).
+ */
+typedef struct {
+    int32_t B, T, Hq, Hk, D, R;
+    int32_t norm;
+    int32_t interleaved;
+    float eps;
+    rm_dtype dtype;
+    int32_t max_pos;
+    int32_t pos_rows;
+    int32_t pos64;
+    int64_t q_stride[3];
+    int64_t k_stride[3];
+} rm_cp_qkr_problem;
+size_t rm_cp_qkr_workspace_size(const rm_cp_qkr_problem* p);
+rm_status rm_cp_qkr_forward(const rm_cp_qkr_problem* p, const void* q, const void* k, const float* wq,
+                            const float* wk, const float* table, const void* positions, void* q_out,
+                            void* k_out, rm_stream_t stream);
+rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const void* k, const float* wq,
+                             const float* wk, const float* table, const void* positions,
+                             const void* dq_out, const void* dk_out, void* dq, void* dk, float* dwq,
+                             float* dwk, void* ws, rm_stream_t stream);
+
+/*
+ * Gated delta rule with a carried state, for serving: num_seqs sequences,
+ * each continuing (or beginning) a state of a pool state [num_slots,H,Dk,Dv],
+ * which the call updates in place.  Per sequence and head, from S = the
+ * sequence's slot (zero where fresh[seq] != 0), for each of its tokens:
+ *     S <- exp(g_t) (I - beta_t k_t k_t^T) S + beta_t k_t v_t^T,
+ *     o_t = scale S^T q_t.
+ * Packed tokens [num_tokens]: cu_seqlens [num_seqs + 1] int32 on the device
+ * gives each sequence's range (an empty one leaves its slot as it is, or zero
+ * when fresh; ranges are cut to [0, num_tokens]); NULL: every sequence has
+ * num_tokens / num_seqs tokens.  max_len bounds the longest sequence: tokens
+ * past it are not read, and their outputs not written.
+ *   q, k [num_tokens,qk_heads,Dk], v [num_tokens,H,Dv] in dtype, strides in
+ *   elements for (token, head), elements adjacent, bases and strides
+ *   multiples of 16 bytes; head h reads the q and k rows of head
+ *   h / (H / qk_heads).  g (log-gates), beta: fp32, a token stride, heads
+ *   adjacent.  o [num_tokens,H,Dv] contiguous, in dtype.  state: contiguous,
+ *   in state_dtype (bf16 states are rounded once a call).
+ *   slots [num_seqs] int32 on the device (NULL: sequence i uses slot i); a
+ *   slot outside [0, num_slots) marks a padding sequence: its outputs are 0
+ *   and no state is touched.  Slots in range must be distinct.  fresh
+ *   [num_seqs] bytes on the device, or NULL: every sequence continues.
+ *   Dk in {16, 32, 64, 128}, Dv a multiple of 8 up to 256.
+ *   ws: rm_gdr_state_workspace_size bytes, for problems of these sizes or
+ *   smaller num_seqs, num_tokens and max_len; not shared by calls that overlap.
+ * rm_gdr_state_path: 0 when the call runs as a token recurrence in fp32, 1
+ * when it runs in chunks on the tensor cores, -1 for a problem it rejects.
+ */
+typedef struct {
+    int32_t num_seqs, num_tokens, max_len;
+    int32_t H, qk_heads, Dk, Dv, num_slots;
+    float scale;
+    rm_dtype dtype, state_dtype;
+    int64_t q_stride[2];
+    int64_t k_stride[2];
+    int64_t v_stride[2];
+    int64_t g_stride, beta_stride;
+} rm_gdr_state_problem;
+int32_t rm_gdr_state_path(const rm_gdr_state_problem* p);
+size_t rm_gdr_state_workspace_size(const rm_gdr_state_problem* p);
+rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k,
+                               const void* v, const float* g, const float* beta,
+                               const int32_t* cu_seqlens, const int32_t* slots, const uint8_t* fresh,
+                               void* state, void* o, void* ws, rm_stream_t stream);
+
+/*
+ * Global norm of many gradient tensors, and clipping:
+ *     norm = sqrt(sum_i sum g_i^2),   out_i = g_i * min(1, max_norm / (norm + eps)).
+ * n tensors, numels[i] elements each (0 allowed), dtypes[i] RM_F32 or RM_BF16
+ * for grads[i] and out_dtypes[i] for outs[i]; grads, outs, numels, dtypes and
+ * out_dtypes are HOST arrays, the pointers in them device pointers aligned to
+ * their elements.  outs[i] may be grads[i] (in place).  outs NULL: the norm
+ * alone.  norm: one fp32 on the device.  The squares are summed in fp32 within
+ * a thread's few elements of a piece, in fp64 beyond, in an order that depends
+ * on the sizes alone; pieces whose squares would leave fp32's range are summed
+ * in fp64.  An infinite norm gives the factor 0 and a NaN norm a NaN factor,
+ * as the formula does; max_norm must be finite and not negative.
+ *   ws: rm_cp_clip_workspace_size(n) bytes.
+ */
+size_t rm_cp_clip_workspace_size(int32_t n);
+rm_status rm_cp_clip_grad_norm(int32_t n, const void* const* grads, const int64_t* numels,
+                               const int32_t* dtypes, void* const* outs, const int32_t* out_dtypes,
+                               float max_norm, float eps, float* norm, void* ws, rm_stream_t stream);
+
 /* Name of a status code (static string). */
 const char* rm_cp_status_string(rm_status s);
 

@@ -33,6 +33,9 @@ EXPORTS = (
     "rm_gdr_path", "rm_gdr_workspace_size", "rm_gdr_forward_prepare", "rm_gdr_compose_prefix",
     "rm_gdr_forward_apply",
     "rm_gdr_backward_prepare", "rm_gdr_compose_suffix", "rm_gdr_backward_apply",
+    "rm_cp_qkr_workspace_size", "rm_cp_qkr_forward", "rm_cp_qkr_backward",
+    "rm_gdr_state_path", "rm_gdr_state_workspace_size", "rm_gdr_state_forward",
+    "rm_cp_clip_workspace_size", "rm_cp_clip_grad_norm",
 )
 
 
@@ -69,6 +72,23 @@ class StepSet(ctypes.Structure):
 class StepState(ctypes.Structure):
     """Mirror of rm_cp_step_state."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("M", "dS", "S_in", "gamma", "dS_out", "ws")]
+
+
+class QkrProblem(ctypes.Structure):
+    """Mirror of rm_cp_qkr_problem."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hk", "D", "R", "norm", "interleaved")] + [
+        ("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("max_pos", ctypes.c_int32),
+        ("pos_rows", ctypes.c_int32), ("pos64", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3)]
+
+
+class GdrStateProblem(ctypes.Structure):
+    """Mirror of rm_gdr_state_problem."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_seqs", "num_tokens", "max_len", "H", "qk_heads", "Dk", "Dv",
+                                              "num_slots")] + [
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int), ("state_dtype", ctypes.c_int),
+        ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2),
+        ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64)]
 
 
 _P = ctypes.c_void_p
@@ -109,6 +129,14 @@ _SIGS = {
     "rm_gdr_backward_prepare": (_S, [_PP] + [_P] * 11),
     "rm_gdr_compose_suffix": (_S, [_PP] + [_P] * 4),
     "rm_gdr_backward_apply": (_S, [_PP] + [_P] * 13),
+    "rm_cp_qkr_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(QkrProblem)]),
+    "rm_cp_qkr_forward": (_S, [ctypes.POINTER(QkrProblem)] + [_P] * 9),
+    "rm_cp_qkr_backward": (_S, [ctypes.POINTER(QkrProblem)] + [_P] * 13),
+    "rm_gdr_state_path": (ctypes.c_int32, [ctypes.POINTER(GdrStateProblem)]),
+    "rm_gdr_state_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GdrStateProblem)]),
+    "rm_gdr_state_forward": (_S, [ctypes.POINTER(GdrStateProblem)] + [_P] * 12),
+    "rm_cp_clip_workspace_size": (ctypes.c_size_t, [ctypes.c_int32]),
+    "rm_cp_clip_grad_norm": (_S, [ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P]),
 }
 
 _lock = threading.Lock()
@@ -365,3 +393,50 @@ def rm_gdr_backward_apply(p, q, k, v, g, beta, dO, dS_out, dk, dv, dg, dbeta, ws
     _check(load().rm_gdr_backward_apply(p.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                         _ptr(dO), _ptr(dS_out), _ptr(dk), _ptr(dv), _ptr(dg),
                                         _ptr(dbeta), _ptr(ws), _stream(stream)))
+
+
+# ----------------------------------------------------------------- norm and rotation, carried state, clipping
+# These calls take strides in their problem, so tensors need only have adjacent head elements;
+# the callers in qk_rope.py, gdr_state.py and clip.py check shapes, types and strides.
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def rm_cp_qkr_workspace_size(p: QkrProblem) -> int:
+    return int(load().rm_cp_qkr_workspace_size(ctypes.byref(p)))
+
+
+def rm_cp_qkr_forward(p, q, k, wq, wk, table, positions, q_out, k_out, stream=None):
+    _check(load().rm_cp_qkr_forward(ctypes.byref(p), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(table),
+                                    _addr(positions), _addr(q_out), _addr(k_out), _stream(stream)))
+
+
+def rm_cp_qkr_backward(p, q, k, wq, wk, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws, stream=None):
+    _check(load().rm_cp_qkr_backward(ctypes.byref(p), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(table),
+                                     _addr(positions), _addr(dq_out), _addr(dk_out), _addr(dq), _addr(dk),
+                                     _addr(dwq), _addr(dwk), _addr(ws), _stream(stream)))
+
+
+def rm_gdr_state_path(p: GdrStateProblem) -> int:
+    return int(load().rm_gdr_state_path(ctypes.byref(p)))
+
+
+def rm_gdr_state_workspace_size(p: GdrStateProblem) -> int:
+    return int(load().rm_gdr_state_workspace_size(ctypes.byref(p)))
+
+
+def rm_gdr_state_forward(p, q, k, v, g, beta, cu_seqlens, slots, fresh, state, o, ws, stream=None):
+    _check(load().rm_gdr_state_forward(ctypes.byref(p), _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta),
+                                       _addr(cu_seqlens), _addr(slots), _addr(fresh), _addr(state), _addr(o),
+                                       _addr(ws), _stream(stream)))
+
+
+def rm_cp_clip_workspace_size(n: int) -> int:
+    return int(load().rm_cp_clip_workspace_size(int(n)))
+
+
+def rm_cp_clip_grad_norm(n, grads, numels, dtypes, outs, out_dtypes, max_norm, eps, norm, ws, stream=None):
+    """grads, numels, dtypes, outs, out_dtypes: addresses of host arrays (outs and out_dtypes may be None)."""
+    _check(load().rm_cp_clip_grad_norm(int(n), grads, numels, dtypes, outs, out_dtypes, float(max_norm), float(eps),
+                                       _addr(norm), _addr(ws), _stream(stream)))

@@ -442,3 +442,13 @@ class GdrStepGraph:
         """Runs the captured step on the current stream."""
         self.graph.replay()
         return (self.o,) + (self.grads if self.grads is not None else ())
+
+
+# ------------------------------------------------------------------ around the recurrences
+# per-head norm with rotation, the delta rule with a carried state, gradient clipping
+
+from .clip import ClipPlan, clip_grad_norm, make_clip_plan  # noqa: E402,F401
+from .gdr_state import (GdrStatePlan, gdr_decode, gdr_prefill, make_gdr_state,  # noqa: E402,F401
+                        make_gdr_state_plan)
+from .qk_rope import (QkNormRope, make_rope_table, qk_norm_rope, qk_norm_rope_backward,  # noqa: E402,F401
+                      qk_norm_rope_train)

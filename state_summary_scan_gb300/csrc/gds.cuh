@@ -1,0 +1,60 @@
+// gds.cuh -- launch arguments of the gated delta rule with a carried state, shared by its
+// token recurrence (gds_kernels.cu), its chunked form (gdstc_kernels.cu) and its host side.
+#pragma once
+
+#include "tc_tiles.cuh"
+
+namespace rmcp {
+namespace gds {
+
+struct Args {
+    int S, N, max_len;      // sequences, packed tokens, bound of a sequence's length
+    int H, hdiv, Dk, Dv;    // head h reads the q and k rows of head h / hdiv
+    int slots_n;
+    int each;               // tokens of every sequence without cu, else 0
+    float scale;
+    int64_t qs[2], ks[2], vs[2];  // token and head strides (elements)
+    int64_t gs, bs;         // token strides of g and beta
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    const float* beta;
+    const int32_t* cu;
+    const int32_t* slots;
+    const uint8_t* fresh;
+    void* state;            // [slots_n][H][Dk][Dv]
+    void* o;                // [N][H][Dv]
+    void* ws;
+};
+
+// Tokens [begin, begin + len) of a sequence; slot < 0: a padding sequence.
+struct Seq {
+    int begin, len, slot;
+    bool fresh;
+};
+
+__device__ __forceinline__ Seq sequence(const Args& a, int i) {
+    Seq s;
+    int e;
+    if (a.cu == nullptr) {
+        s.begin = i * a.each;
+        e = s.begin + a.each;
+    } else {  // ranges are cut to the tokens that there are
+        s.begin = min(max(__ldg(a.cu + i), 0), a.N);
+        e = min(max(__ldg(a.cu + i + 1), s.begin), a.N);
+    }
+    s.len = min(e - s.begin, a.max_len);
+    const int slot = a.slots ? __ldg(a.slots + i) : i;
+    s.slot = slot >= 0 && slot < a.slots_n ? slot : -1;
+    s.fresh = a.fresh != nullptr && __ldg(a.fresh + i) != 0;
+    return s;
+}
+
+// the chunked form on the tensor cores
+bool tc_supports(const Args& a, rm_dtype dt);
+size_t tc_workspace_bytes(const Args& a);
+rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s);
+
+}  // namespace gds
+}  // namespace rmcp

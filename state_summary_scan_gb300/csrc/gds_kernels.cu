@@ -1,0 +1,304 @@
+// gds_kernels.cu -- the gated delta rule with a carried state as a token recurrence in fp32
+// (rm_gdr_state_forward): decoding a few tokens for each of many sequences, and every shape
+// that the chunked form on the tensor cores does not take.
+//
+// Per token, S in R^{Dk x Dv}:
+//     d = beta (v - e^g S^T k),   o = scale (e^g S^T q + (q.k) d),   S <- e^g S + k d^T
+// Both products with S read the same old state, so a token needs one pass over it and one
+// reduction.  The columns of S are independent: a CTA owns 32 columns of one sequence's head
+// and keeps them in registers over its tokens (Dk / 16 rows x 4 columns a thread, 128
+// threads); the state is read from the pool once and written once, in 128-byte (fp32) pieces
+// of a row.
+//
+// Bound by HBM when decoding: the state's read and write are nearly all of the traffic.  One
+// CTA per 32 columns keeps the loads in flight per thread to 32 registers and gives even one
+// sequence of 16 heads 32 or more CTAs.
+#include <cstdio>
+
+#include "gds.cuh"
+
+namespace rmcp {
+namespace gds {
+
+namespace {
+
+constexpr int kCols = 32;      // columns of a CTA
+constexpr int kTpb = 128;
+constexpr unsigned kAllLanes = 0xffffffffu;
+
+__device__ __forceinline__ void load4(const float* p, float* x) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* x) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+    const float2 a = __bfloat1622float2(h[0]), b = __bfloat1622float2(h[1]);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
+    __nv_bfloat162 h[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
+}
+
+// One token's inputs of a CTA.
+template <int DK>
+struct Token {
+    float q[DK], k[DK], v[kCols];
+    float g, beta;
+};
+
+// A CTA: blockIdx.x = column block + blocks * head, blockIdx.y = sequence.
+template <typename T, typename TS, int DK>
+__global__ void __launch_bounds__(kTpb) gds_token_kernel(const __grid_constant__ Args a) {
+    constexpr int KR = DK / 16;  // rows of a thread: KR (tid / 8) ...
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int blocks = (a.Dv + kCols - 1) / kCols;
+    const int h = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * kCols;
+    const int col = c0 + (lane & 7) * 4, row = (tid >> 3) * KR;
+    const bool live = col < a.Dv;  // Dv is a multiple of 8, a thread's columns of 4
+    const Seq sq = sequence(a, blockIdx.y);
+    if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
+    T* o = static_cast<T*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + col;
+    const int64_t os = int64_t(a.H) * a.Dv;
+    if (sq.slot < 0) {  // padding
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        if (live && tid < 8)
+            for (int t = 0; t < sq.len; ++t) store4(o + t * os, zero);
+        return;
+    }
+    TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * a.Dk + row) * a.Dv + col;
+    float S[KR][4];
+#pragma unroll
+    for (int i = 0; i < KR; ++i) {
+        S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
+        if (live && !sq.fresh) load4(st + i * a.Dv, S[i]);
+    }
+
+    __shared__ Token<DK> tok[2];
+    __shared__ float4 sum[2][4][8][2];  // [parity][warp][column quad][k | q]
+    __shared__ float qk[2][4];
+    const int hk = h / a.hdiv;
+    const T* q = static_cast<const T*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
+    const T* k = static_cast<const T*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1];
+    const T* v = static_cast<const T*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + c0;
+    const float* g = a.g + sq.begin * a.gs + h;
+    const float* beta = a.beta + sq.begin * a.bs + h;
+    const bool has_v = tid < kCols && c0 + tid < a.Dv;
+    // the values that this thread stages for one token
+    float rq = 0.f, rk = 0.f, rv = 0.f, rg = 0.f;
+    auto fetch = [&](int t) {
+        if (tid < DK) {
+            rq = to_f32(q[t * a.qs[0] + tid]);
+            rk = to_f32(k[t * a.ks[0] + tid]);
+        }
+        if (has_v) rv = to_f32(v[t * a.vs[0] + tid]);
+        if (tid == 64) rg = g[t * a.gs];
+        if (tid == 96) rg = beta[t * a.bs];
+    };
+    auto stage = [&](int p) {
+        if (tid < DK) {
+            tok[p].q[tid] = rq;
+            tok[p].k[tid] = rk;
+        }
+        if (tid < kCols) tok[p].v[tid] = rv;
+        if (tid == 64) tok[p].g = expf(rg);
+        if (tid == 96) tok[p].beta = rg;
+    };
+    if (sq.len > 0) {
+        fetch(0);
+        stage(0);
+    }
+    __syncthreads();
+    for (int t = 0; t < sq.len; ++t) {
+        const int p = t & 1;
+        if (t + 1 < sq.len) fetch(t + 1);
+        float kr[KR], qr[KR];
+#pragma unroll
+        for (int i = 0; i < KR; ++i) {
+            kr[i] = tok[p].k[row + i];
+            qr[i] = tok[p].q[row + i];
+        }
+        float x[9];  // S^T k, S^T q of four columns, q.k
+#pragma unroll
+        for (int i = 0; i < 9; ++i) x[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < KR; ++i) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                x[c] = fmaf(kr[i], S[i][c], x[c]);
+                x[4 + c] = fmaf(qr[i], S[i][c], x[4 + c]);
+            }
+            x[8] = fmaf(qr[i], kr[i], x[8]);
+        }
+#pragma unroll
+        for (int i = 0; i < 9; ++i) {
+            x[i] += __shfl_xor_sync(kAllLanes, x[i], 8);
+            x[i] += __shfl_xor_sync(kAllLanes, x[i], 16);
+        }
+        if (lane < 8) {
+            sum[p][warp][lane][0] = make_float4(x[0], x[1], x[2], x[3]);
+            sum[p][warp][lane][1] = make_float4(x[4], x[5], x[6], x[7]);
+            if (lane == 0) qk[p][warp] = x[8];
+        }
+        if (t + 1 < sq.len) stage(p ^ 1);
+        __syncthreads();
+        float sk[4] = {0.f, 0.f, 0.f, 0.f}, so[4] = {0.f, 0.f, 0.f, 0.f}, dot = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float4 y = sum[p][w][lane & 7][0], z = sum[p][w][lane & 7][1];
+            sk[0] += y.x, sk[1] += y.y, sk[2] += y.z, sk[3] += y.w;
+            so[0] += z.x, so[1] += z.y, so[2] += z.z, so[3] += z.w;
+            dot += qk[p][w];
+        }
+        const float al = tok[p].g, be = tok[p].beta;
+        float d[4], out[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            d[c] = be * (tok[p].v[(lane & 7) * 4 + c] - al * sk[c]);
+            out[c] = a.scale * fmaf(dot, d[c], al * so[c]);
+        }
+#pragma unroll
+        for (int i = 0; i < KR; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) S[i][c] = fmaf(kr[i], d[c], al * S[i][c]);
+        if (live && tid < 8) store4(o + t * os, out);
+    }
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < KR; ++i) store4(st + i * a.Dv, S[i]);
+    }
+}
+
+template <typename T, typename TS>
+bool token_launch(const Args& a, cudaStream_t s) {
+    const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
+    if (a.Dk == 16) gds_token_kernel<T, TS, 16><<<grid, kTpb, 0, s>>>(a);
+    else if (a.Dk == 32) gds_token_kernel<T, TS, 32><<<grid, kTpb, 0, s>>>(a);
+    else if (a.Dk == 64) gds_token_kernel<T, TS, 64><<<grid, kTpb, 0, s>>>(a);
+    else gds_token_kernel<T, TS, 128><<<grid, kTpb, 0, s>>>(a);
+    note_launch(1);
+    return launch_ok();
+}
+
+rm_status check(const rm_gdr_state_problem* p, Args* a) {
+    if (p == nullptr) return api_fail(RM_ERR_INVALID_ARG, "problem is null");
+    if (p->num_seqs <= 0 || p->num_tokens < 0 || p->max_len < 0 || p->H <= 0 || p->qk_heads <= 0 || p->num_slots <= 0)
+        return api_fail(RM_ERR_INVALID_ARG, "num_seqs, H, qk_heads and num_slots must be positive, num_tokens and max_len not negative");
+    if (p->H % p->qk_heads) return api_fail(RM_ERR_INVALID_ARG, "qk_heads must divide H");
+    if ((p->dtype != RM_F32 && p->dtype != RM_BF16) || (p->state_dtype != RM_F32 && p->state_dtype != RM_BF16))
+        return api_fail(RM_ERR_INVALID_ARG, "dtype and state_dtype must be RM_F32 or RM_BF16");
+    if (!(p->scale > -3.0e38f && p->scale < 3.0e38f)) return api_fail(RM_ERR_INVALID_ARG, "scale must be finite");
+    if ((p->Dk != 16 && p->Dk != 32 && p->Dk != 64 && p->Dk != 128) || p->Dv <= 0 || p->Dv % 8 || p->Dv > 256)
+        return api_fail(RM_ERR_UNSUPPORTED, "Dk must be in {16, 32, 64, 128}, Dv a multiple of 8 up to 256");
+    if (p->num_seqs > 65535) return api_fail(RM_ERR_SHAPE, "num_seqs exceeds 65535");
+    if (int64_t(p->H) * 8 > (int64_t(1) << 30)) return api_fail(RM_ERR_SHAPE, "H is too large");
+    if (int64_t(p->num_tokens) > (int64_t(1) << 31) - 1 - 64 * 65536) return api_fail(RM_ERR_SHAPE, "num_tokens is too large");
+    const int es = p->dtype == RM_F32 ? 4 : 2;
+    for (int i = 0; i < 2; ++i) {
+        if (p->q_stride[i] < 0 || p->k_stride[i] < 0 || p->v_stride[i] < 0) return api_fail(RM_ERR_INVALID_ARG, "strides must not be negative");
+        if (p->q_stride[i] * es % 16 || p->k_stride[i] * es % 16 || p->v_stride[i] * es % 16)
+            return api_fail(RM_ERR_ALIGNMENT, "the strides of q, k and v must be multiples of 16 bytes");
+        a->qs[i] = p->q_stride[i], a->ks[i] = p->k_stride[i], a->vs[i] = p->v_stride[i];
+    }
+    if (p->g_stride < 0 || p->beta_stride < 0) return api_fail(RM_ERR_INVALID_ARG, "strides must not be negative");
+    a->gs = p->g_stride, a->bs = p->beta_stride;
+    a->S = p->num_seqs, a->N = p->num_tokens, a->max_len = p->max_len, a->H = p->H, a->hdiv = p->H / p->qk_heads;
+    a->Dk = p->Dk, a->Dv = p->Dv, a->slots_n = p->num_slots, a->scale = p->scale, a->each = 0;
+    return RM_OK;
+}
+
+rm_status element_aligned(const void* p, const char* name, int size) {
+    char msg[96];
+    if (p == nullptr || reinterpret_cast<uintptr_t>(p) % size) {
+        std::snprintf(msg, sizeof(msg), "%s is %s", name, p ? "not aligned to its elements" : "NULL");
+        return api_fail(p ? RM_ERR_ALIGNMENT : RM_ERR_INVALID_ARG, msg);
+    }
+    return RM_OK;
+}
+
+}  // namespace
+}  // namespace gds
+}  // namespace rmcp
+
+#define RM_GDS_NEED(ptr)                            \
+    do {                                            \
+        rm_status s_ = rmcp::api_need((ptr), #ptr); \
+        if (s_ != RM_OK) return s_;                 \
+    } while (0)
+#define RM_GDS_ELEM(ptr, size)                                           \
+    do {                                                                 \
+        rm_status s_ = rmcp::gds::element_aligned((ptr), #ptr, (size)); \
+        if (s_ != RM_OK) return s_;                                      \
+    } while (0)
+
+extern "C" {
+
+int32_t rm_gdr_state_path(const rm_gdr_state_problem* p) {
+    rmcp::gds::Args a{};
+    if (rmcp::gds::check(p, &a) != RM_OK) return -1;
+    return rmcp::gds::tc_supports(a, p->dtype) ? 1 : 0;
+}
+
+size_t rm_gdr_state_workspace_size(const rm_gdr_state_problem* p) {
+    rmcp::gds::Args a{};
+    if (rmcp::gds::check(p, &a) != RM_OK) return 0;
+    return rmcp::gds::tc_supports(a, p->dtype) ? rmcp::gds::tc_workspace_bytes(a) : 16;
+}
+
+rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k, const void* v,
+                               const float* g, const float* beta, const int32_t* cu_seqlens, const int32_t* slots,
+                               const uint8_t* fresh, void* state, void* o, void* ws, rm_stream_t stream) {
+    using namespace rmcp;
+    gds::Args a{};
+    rm_status st = gds::check(p, &a);
+    if (st != RM_OK) return st;
+    if (cu_seqlens == nullptr) {
+        if (a.N % a.S) return api_fail(RM_ERR_SHAPE, "without cu_seqlens num_seqs must divide num_tokens");
+        a.each = a.N / a.S;
+        if (a.each > a.max_len) return api_fail(RM_ERR_SHAPE, "max_len is below the sequences' length");
+    } else {
+        RM_GDS_ELEM(cu_seqlens, 4);
+    }
+    if (slots == nullptr && a.S > a.slots_n) return api_fail(RM_ERR_SHAPE, "without slots num_seqs must not exceed num_slots");
+    RM_GDS_NEED(state);
+    if (a.N > 0) {
+        RM_GDS_NEED(q);
+        RM_GDS_NEED(k);
+        RM_GDS_NEED(v);
+        RM_GDS_ELEM(g, 4);
+        RM_GDS_ELEM(beta, 4);
+        RM_GDS_NEED(o);
+    }
+    if (slots != nullptr) RM_GDS_ELEM(slots, 4);
+    a.q = q, a.k = k, a.v = v, a.g = g, a.beta = beta, a.cu = cu_seqlens, a.slots = slots, a.fresh = fresh;
+    a.state = state, a.o = o, a.ws = ws;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (gds::tc_supports(a, p->dtype)) {
+        RM_GDS_NEED(ws);
+        begin_launches();
+        return gds::tc_launch(a, p->state_dtype, s);
+    }
+    begin_launches();
+    const bool sf = p->state_dtype == RM_F32;
+    const bool ok = p->dtype == RM_F32 ? (sf ? gds::token_launch<float, float>(a, s) : gds::token_launch<float, __nv_bfloat16>(a, s))
+                                       : (sf ? gds::token_launch<__nv_bfloat16, float>(a, s)
+                                             : gds::token_launch<__nv_bfloat16, __nv_bfloat16>(a, s));
+    if (ok) return RM_OK;
+    char msg[256];
+    std::snprintf(msg, sizeof(msg), "gated delta rule with a carried state: launch failed: %s", cuda_error_text());
+    return api_fail(RM_ERR_CUDA, msg);
+}
+
+}  // extern "C"
+
+namespace rmcp {
+namespace gds {
+bool tc_supports(const Args&, rm_dtype) { return false; }
+size_t tc_workspace_bytes(const Args&) { return 16; }
+rm_status tc_launch(const Args&, rm_dtype, cudaStream_t) { return RM_ERR_UNSUPPORTED; }
+}  // namespace gds
+}  // namespace rmcp
