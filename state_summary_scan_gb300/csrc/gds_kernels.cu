@@ -199,7 +199,10 @@ rm_status check(const rm_gdr_state_problem* p, Args* a) {
     if (int64_t(p->num_tokens) > (int64_t(1) << 31) - 1 - 64 * 65536) return api_fail(RM_ERR_SHAPE, "num_tokens is too large");
     const int es = p->dtype == RM_F32 ? 4 : 2;
     for (int i = 0; i < 2; ++i) {
-        if (p->q_stride[i] < 0 || p->k_stride[i] < 0 || p->v_stride[i] < 0) return api_fail(RM_ERR_INVALID_ARG, "strides must not be negative");
+        // (a dimension of one element takes no step)
+        const bool steps_qk = i ? p->qk_heads > 1 : p->num_tokens > 1, steps_v = i ? p->H > 1 : p->num_tokens > 1;
+        if (p->q_stride[i] < int(steps_qk) || p->k_stride[i] < int(steps_qk) || p->v_stride[i] < int(steps_v))
+            return api_fail(RM_ERR_INVALID_ARG, "the strides of q, k and v must be positive");
         if (p->q_stride[i] * es % 16 || p->k_stride[i] * es % 16 || p->v_stride[i] * es % 16)
             return api_fail(RM_ERR_ALIGNMENT, "the strides of q, k and v must be multiples of 16 bytes");
         a->qs[i] = p->q_stride[i], a->ks[i] = p->k_stride[i], a->vs[i] = p->v_stride[i];
@@ -294,11 +297,3 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
 }
 
 }  // extern "C"
-
-namespace rmcp {
-namespace gds {
-bool tc_supports(const Args&, rm_dtype) { return false; }
-size_t tc_workspace_bytes(const Args&) { return 16; }
-rm_status tc_launch(const Args&, rm_dtype, cudaStream_t) { return RM_ERR_UNSUPPORTED; }
-}  // namespace gds
-}  // namespace rmcp

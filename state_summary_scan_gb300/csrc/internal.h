@@ -70,6 +70,9 @@ bool gdrtc_supports(const Dims& d, rm_dtype dt);
 rm_status launch_gdrtc(GdrOp op, const Dims& d, const GdrPtrs& p, cudaStream_t s);
 rm_status gdrtc_read_timeout_flag(int* host_flag, int clear, int* dev_scratch, cudaStream_t s);
 
+// the gated delta rule with a carried state on the tensor cores (gdstc_kernels.cu)
+rm_status gdstc_read_timeout_flag(int* host_flag, int clear, int* dev_scratch, cudaStream_t s);
+
 // vector (per key dimension) gates on the generic path (vg_kernels.cu)
 rm_status launch_vg(Op op, const Dims& d, rm_dtype dt, const Ptrs& p, cudaStream_t s);
 // vector gates on the tensor-core path (vgtc_kernels.cu)

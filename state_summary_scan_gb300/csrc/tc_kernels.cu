@@ -2661,20 +2661,25 @@ thread_local int g_map_result = 0;  // CUresult of the calling thread's last mak
 int last_map_result() { return g_map_result; }
 void clear_map_result() { g_map_result = 0; }
 
-// [B*T rows][H][D] bf16 viewed as a 3-D tensor; boxes of 64 tokens x 64 columns.
-bool make_map(CUtensorMap* m, const void* base, const Dims& d, int D, int heads) {
+bool make_map_strided(CUtensorMap* m, const void* base, int D, int heads, int64_t N, int64_t head_stride,
+                      int64_t row_stride) {
     auto fn = encode_fn();
     g_map_result = -1;  // no encoder
     if (!fn) return false;
-    if (heads <= 0) heads = d.H;
-    cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(d.B) * cuuint64_t(d.T)};
-    cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(heads) * D * 2};
+    cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(N)};
+    cuuint64_t strides[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(row_stride) * 2};
     cuuint32_t box[3] = {64, 1, uint32_t(kChunk)};
     cuuint32_t estr[3] = {1, 1, 1};
     g_map_result = int(fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE));
     return g_map_result == int(CUDA_SUCCESS);
+}
+
+// [B*T rows][H][D] bf16 viewed as a 3-D tensor; boxes of 64 tokens x 64 columns.
+bool make_map(CUtensorMap* m, const void* base, const Dims& d, int D, int heads) {
+    if (heads <= 0) heads = d.H;
+    return make_map_strided(m, base, D, heads, int64_t(d.B) * d.T, D, int64_t(heads) * D);
 }
 
 // multiprocessors of the current device (cached per device)

@@ -146,6 +146,9 @@ __device__ __forceinline__ void store_bf16x16(__nv_bfloat16* dst, const float* v
 // [B*T rows][heads][D] bf16 viewed as a 3-D tensor; boxes of 64 tokens x 64
 // columns, 128-byte swizzle (heads <= 0: d.H).
 bool make_map(CUtensorMap* m, const void* base, const Dims& d, int D, int heads = 0);
+// [N rows][heads][D] bf16 with head and row strides in elements, in the same boxes.
+bool make_map_strided(CUtensorMap* m, const void* base, int D, int heads, int64_t N, int64_t head_stride,
+                      int64_t row_stride);
 // the CUresult of the calling thread's last make_map (-1: no encoder found;
 // 0 after clear_map_result)
 int last_map_result();

@@ -295,7 +295,7 @@ PREFILL = [  # lens, H, Hqk, Dk, Dv, dtype, state dtype
     ([1], 1, 1, 16, 8, F32, F32),
     ([0, 5, 1, 63, 130, 0], 4, 2, 32, 40, F32, F32),
     ([64, 65, 200], 2, 2, 128, 128, F32, F32),
-    ([17, 0, 100], 3, 1, 64, 72, BF16, F32),
+    ([17, 0, 100], 3, 1, 32, 72, BF16, F32),
 ]
 
 
@@ -312,6 +312,99 @@ def test_gdr_prefill_token_recurrence_against_64_bits(case):
     o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda(), fresh=fr.cuda())
     tol = (max(lens) + Dk) * U
     gds_check(lens, q, k, v, g, beta, before, state, o, slots, fr, Dk ** -0.5, tol, tol)
+
+
+# In chunks on the tensor cores: S, W = T (K o gam) and P = mask(Q K^T) are rounded to bf16 once
+# (2^-8 at worst, 1.7e-3 in norm), o itself once more: four independent roundings in norm, at most
+# 3.4e-3 < 2^-8 for o; the state sees only those of S and W, through W S, which the unit keys keep
+# small beside T V: 2e-3 is the norm of one whole rounding of it.
+CHUNKED = [  # lens, H, Hqk, Dk, Dv, state dtype, fused
+    ([64], 1, 1, 128, 128, F32, False),
+    ([128, 64], 2, 2, 64, 64, F32, False),
+    ([100], 1, 1, 128, 64, BF16, True),
+    ([0, 5, 1, 63, 130, 64, 0, 65], 4, 2, 128, 128, F32, False),
+    ([333, 1, 200], 3, 1, 64, 200, BF16, True),
+    ([1000, 77], 2, 1, 128, 256, F32, True),
+    ([511, 513], 2, 2, 64, 128, BF16, False),
+]
+
+
+def rel2(got, want):
+    return float((got.double() - want.double()).norm() / (want.double().norm() + 1e-300))
+
+
+@pytest.mark.parametrize("case", CHUNKED, ids=str)
+def test_gdr_prefill_in_chunks_against_64_bits(case):
+    lens, H, Hqk, Dk, Dv, sdt, fused = case
+    S = len(lens)
+    q, k, v, g, beta, state, slots = gds_inputs(lens, H, Hqk, Dk, Dv, BF16, sdt, S + 1, fused=fused)
+    fr = (torch.arange(S) % 2 == 1).to(torch.uint8)
+    if S > 4:
+        slots[3] = S + 7  # a padding sequence
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    plan = api.make_gdr_state_plan(S, sum(lens), H, Dk, Dv, num_slots=S + 1, qk_heads=Hqk, state_dtype=sdt)
+    assert C.rm_gdr_state_path(plan.c) == 1
+    before = state.clone()
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda(), fresh=fr.cuda())
+    scratch = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert C.rm_cp_device_status(scratch) == 0
+    at, touched = 0, set()
+    for i, n in enumerate(lens):
+        s, j = slice(at, at + n), int(slots[i])
+        at += n
+        if not 0 <= j < S + 1:
+            assert not o[s].any()
+            continue
+        touched.add(j)
+        S0 = torch.zeros_like(before[j]) if int(fr[i]) else before[j]
+        want_o, want_S = gds_ref(q[s], k[s], v[s], g[s], beta[s], S0, Dk ** -0.5)
+        if n:
+            assert rel2(o[s], want_o) <= 2.0 ** -8, (i, rel2(o[s], want_o))
+            close(o[s], want_o, 2e-2, BF16, f"o of sequence {i}")
+            assert rel2(state[j], want_S) <= 2e-3 + (2.0 ** -8 if sdt == BF16 else 0), (i, rel2(state[j], want_S))
+        else:
+            assert torch.equal(state[j], S0)
+    for j in set(range(S + 1)) - touched:
+        assert torch.equal(state[j], before[j])
+
+
+def test_gdr_prefill_in_chunks_keeps_nan_and_resets_apart():
+    """A NaN key or value stays in its own sequence, on both sides of a shared tile; g = -inf
+    forgets the state; the same call twice gives the same bits."""
+    lens, H, D = [70, 50, 90], 2, 128
+    q, k, v, g, beta, state, slots = gds_inputs(lens, H, H, D, D, BF16, F32, 3, seed=5)
+    v[75, 0, 3] = float("nan")
+    k[100, 1, 0] = float("nan")
+    q[80] = float("inf")
+    g[30] = -float("inf")
+    g[120 + 64] = -1e30
+    g[120 + 10] = -500.0
+    plan = api.make_gdr_state_plan(3, 210, H, D, D)
+    cu = torch.tensor([0, 70, 120, 210], dtype=torch.int32, device="cuda")
+    before = state.clone()
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda())
+    for i, s in ((0, slice(0, 70)), (2, slice(120, 210))):
+        j = int(slots[i])
+        want_o, want_S = gds_ref(q[s], k[s], v[s], g[s], beta[s], before[j], D ** -0.5)
+        assert rel2(o[s], want_o) <= 2.0 ** -8 and rel2(state[j], want_S) <= 2e-3
+    again = before.clone()
+    o2 = api.gdr_prefill(plan, q, k, v, g, beta, again, cu, slots=slots.cuda())
+    for i, s in ((0, slice(0, 70)), (2, slice(120, 210))):
+        assert torch.equal(o2[s], o[s]) and torch.equal(again[int(slots[i])], state[int(slots[i])])
+
+
+def test_gdr_prefill_in_parts_continues_the_state():
+    """A prompt in two calls, the second from the state of the first, against the whole."""
+    T, H, D, cut = 300, 2, 128, 130
+    q, k, v, g, beta, state, _ = gds_inputs([T], H, H, D, D, BF16, F32, 1, seed=9)
+    plan = api.make_gdr_state_plan(1, T, H, D, D)
+    whole, parts = state.clone(), state.clone()
+    want = api.gdr_prefill(plan, q, k, v, g, beta, whole, torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    got = []
+    for a, b in ((0, cut), (cut, T)):
+        cu = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        got.append(api.gdr_prefill(plan, *(x[a:b] for x in (q, k, v, g, beta)), parts, cu))
+    assert rel2(torch.cat(got), want) <= 2.0 ** -8 and rel2(parts, whole) <= 2e-3
 
 
 def test_gdr_prefill_then_decode_equals_the_training_op():
