@@ -8,21 +8,21 @@
 //     O  = scale gam o (Q S) + P D, P = scale mask(Q K^T) o Gam
 //     S' = e^{b_63} S + K^T D~,     D~_t = e^{b_63 - b_t} D_t
 // Two launches:
-//   gds_factor_kernel  every (chunk, head) at once: T, P, -W and the decays, which do not depend
-//                      on the state, as images of the swizzled tiles that the walk copies in
-//   gds_walk_kernel    one CTA per (sequence, head, 128 columns of values): the chain over the
-//                      sequence's chunks
+//   gds_factor_kernel  every (chunk, head) at once: U = T V, P, -W and the decays, which do not
+//                      depend on the state, laid out as the walk copies them in
+//   gds_walk_kernel    one CTA per (sequence, head, 32 to 128 columns of values): the chain over
+//                      the sequence's chunks
 //
 // The walk is bound by the latency of its chain: S -> W S -> D -> K^T D~ -> S.  It keeps S
 // transposed, a value column a lane, so that every step of the chain is a row of tensor memory
 // per thread and the rounded S and D go back to tensor memory as A operands, with no transposition
 // and no shared memory; the state itself stays in fp32 registers.  Products that do not carry the
-// chain (T V of the next chunk, Q S, P D) are issued behind those that do, and the outputs are
-// read and stored by warps of their own.
+// chain (Q S, P D) are issued behind those that do, and the outputs are read and stored by warps
+// of their own.
 //
 // Rounding: K, Q and V enter as they are; T, D and D~ as the sum of two bf16 (16 significant
 // bits: two products with the exact operand), because T's and D's errors reach the state
-// undamped.  S, W and P are rounded once to bf16: S and W only enter through W S, which is small
+// undamped; U = T V stays in fp32.  S, W and P are rounded once to bf16: S and W only enter through W S, which is small
 // beside T V, and P only through O, which is rounded to bf16 anyway.  In fp64 with these roundings alone
 // (1024 tokens, 4 heads of 128): state 1.4e-4 off, o 2.4e-3 with its own rounding of 1.7e-3.
 #include <cstdio>
@@ -41,8 +41,16 @@ constexpr uint32_t T8 = kTileBytes;      // one [64][64] bf16 tile
 constexpr uint32_t kGateBytes = 1024;    // gam [64], dec [64], e^{b_63}, padding
 constexpr float kForget = -110.f;        // e^{-110} is 0 in fp32: lower gates are raised to it
 
-// Factors of a (chunk, head) in the workspace: T hi, T lo, P, -W (Dk / 64 tiles), gates.
-__host__ __device__ constexpr uint32_t factor_bytes(int Dk) { return (3 + Dk / 64) * T8 + kGateBytes; }
+// Factors of a (chunk, head) in the workspace: P, -W (Dk / 64 swizzled tiles), the gates, then
+// U in fp32 as [16 groups of 4 tokens][columns][4] for each block of up to 128 value columns, so
+// that a lane of the walk reads its column's four tokens at once.
+__host__ __device__ constexpr uint32_t u_cols(int Dv) { return Dv >= 128 ? 128u : uint32_t((Dv + 31) / 32 * 32); }
+__host__ __device__ constexpr uint32_t u_bytes(int Dv) { return kChunk * 4 * u_cols(Dv); }  // of a block
+__host__ __device__ constexpr uint32_t factor_gates(int Dk) { return (1 + Dk / 64) * T8; }
+__host__ __device__ constexpr uint32_t factor_u(int Dk) { return factor_gates(Dk) + kGateBytes; }
+__host__ __device__ constexpr uint32_t factor_bytes(int Dk, int Dv) {
+    return factor_u(Dk) + uint32_t((Dv + 127) / 128) * u_bytes(Dv);
+}
 
 // First chunk of sequence i: chunks of different sequences do not meet, since a sequence of n
 // tokens from token b has at most floor((b + n) / 64) - floor(b / 64) + 1 of them.
@@ -125,90 +133,112 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int tiles, int n, int t
         *reinterpret_cast<uint4*>(tile + (i / each) * T8 + n * 128 + (i % each) * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// Xs = (I + La)^{-1} for the strictly lower La ([64][64] fp32, pitches kP and kQ; see gdr_tri.cuh),
-// by halves: the four 16 x 16 diagonal blocks by forward substitution (a column's rows in 16
-// lanes), then twice the block below the diagonal of a pair, X21 = -X22 (A21 X11).  A21 X11 waits in
-// the pair's block above the diagonal, so that nothing but La and Xs is needed and three CTAs fit an
-// SM; entries above the diagonal are not zero afterwards.  All 256 threads call it.
-__device__ __forceinline__ void halves_inverse(const float* La, float* Xs) {
-    using gdrtc::kP;
-    using gdrtc::kQ;
-    const int tid = threadIdx.x;
+// [64][64] fp32 with the 16-byte units of a row permuted by the row, so that the same unit of
+// 16 rows, and the 64 columns of one row, lie in different banks.
+__device__ __forceinline__ int f_unit(int r, int u) { return r * 64 + ((u ^ (r & 15)) << 2); }
+__device__ __forceinline__ int f_at(int r, int c) { return f_unit(r, c >> 2) + (c & 3); }
+__device__ __forceinline__ float4 f_row4(const float* m, int r, int u) { return *reinterpret_cast<const float4*>(m + f_unit(r, u)); }
+
+// R rows of one column of a product, out[row + i][col] = f sum_{k < n} A[ar + i][ac + k] B[br + k][col']:
+// A's values are the same for a whole half warp, B's adjacent for its lanes.
+template <int R>
+__device__ __forceinline__ void tri_product(const float* A, int ar, int ac, const float* B, int br, int bc, int n, float* out, int row,
+                                            int col, float f) {
+    float x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[i] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < n; k += 4) {
+        float4 l[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) l[i] = f_row4(A, ar + i, (ac + k) >> 2);
+        const float b0 = B[f_at(br + k, bc)], b1 = B[f_at(br + k + 1, bc)], b2 = B[f_at(br + k + 2, bc)], b3 = B[f_at(br + k + 3, bc)];
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[i] = fmaf(l[i].w, b3, fmaf(l[i].z, b2, fmaf(l[i].y, b1, fmaf(l[i].x, b0, x[i]))));
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) out[f_at(row + i, col)] = f * x[i];
+}
+
+// X = (I + A)^{-1} for the strictly lower A, by halves: the four 16 x 16 diagonal blocks by forward
+// substitution (a column's rows in 16 lanes), then twice the block below the diagonal of a pair,
+// X21 = -X22 (A21 X11).  A21 X11 waits in the pair's block above the diagonal, so that nothing but A
+// and X is needed; entries above the diagonal are not zero afterwards.  All 256 threads call it.
+// Shared-memory reads bound it: a lane takes a column and four rows, which shares every read of X
+// between four rows and every read of A between 32 columns.
+__device__ __forceinline__ void halves_inverse(const float* A, float* X) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     {
-        const int w = tid >> 5, lane = tid & 31;
-        const int o = 16 * (w >> 1), r = lane & 15, grp = ((w & 1) << 1) | (lane >> 4);
-        float x[4];
+        const int o = 16 * (warp >> 1), r = lane & 15, grp = ((warp & 1) << 1) | (lane >> 4);
+        float l[16], x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float4 v = f_row4(A, o + r, o / 4 + u);
+            l[4 * u] = v.x, l[4 * u + 1] = v.y, l[4 * u + 2] = v.z, l[4 * u + 3] = v.w;
+        }
 #pragma unroll
         for (int m = 0; m < 4; ++m) x[m] = r == 4 * grp + m ? 1.f : 0.f;
-        const float* lrow = La + (o + r) * kP + o;
 #pragma unroll
-        for (int k = 0; k < 15; ++k) {
-            const float l = r > k ? lrow[k] : 0.f;
+        for (int k = 0; k < 15; ++k)  // (A is zero at and above its diagonal)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) x[m] = fmaf(-l, __shfl_sync(kFull, x[m], (lane & 16) | k), x[m]);
-        }
-        *reinterpret_cast<float4*>(Xs + (o + r) * kQ + o + 4 * grp) = make_float4(x[0], x[1], x[2], x[3]);
+            for (int m = 0; m < 4; ++m) x[m] = fmaf(-l[k], __shfl_sync(kFull, x[m], (lane & 16) | k), x[m]);
+        *reinterpret_cast<float4*>(X + f_unit(o + r, o / 4 + grp)) = make_float4(x[0], x[1], x[2], x[3]);
     }
     __syncthreads();
-    // one product of a level: out[r][4 q ..] = f sum_k a[r][k] b[k][4 q ..], n terms
-    auto product = [&](const float* arow, const float* b, float* out, int n, float f) {
-        float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float l = arow[k];
-            const float4 v = *reinterpret_cast<const float4*>(b + k * kQ);
-            a0 = fmaf(l, v.x, a0);
-            a1 = fmaf(l, v.y, a1);
-            a2 = fmaf(l, v.z, a2);
-            a3 = fmaf(l, v.w, a3);
-        }
-        *reinterpret_cast<float4*>(out) = make_float4(f * a0, f * a1, f * a2, f * a3);
-    };
-    {  // pairs of 16: 64 threads each
-        const int o = 32 * ((tid >> 6) & 1), r = (tid >> 2) & 15, q = 4 * (tid & 3);
-        if (tid < 128) product(La + (o + 16 + r) * kP + o, Xs + o * kQ + o + q, Xs + (o + r) * kQ + o + 16 + q, 16, 1.f);
+    {  // pairs of 16: four warps each, two rows a lane
+        const int o = 32 * (warp >> 2), r = 4 * (warp & 3) + 2 * (lane >> 4), c = lane & 15;
+        tri_product<2>(A, o + 16 + r, o, X, o, o + c, 16, X, o + r, o + 16 + c, 1.f);
         __syncthreads();
-        if (tid < 128) product(Xs + (o + 16 + r) * kQ + o + 16, Xs + o * kQ + o + 16 + q, Xs + (o + 16 + r) * kQ + o + q, 16, -1.f);
+        tri_product<2>(X, o + 16 + r, o + 16, X, o, o + 16 + c, 16, X, o + 16 + r, o + c, -1.f);
         __syncthreads();
     }
-    {  // the pair of 32.  X11's block above its diagonal holds sums, not zeros: its terms of row
-       // k < 16 and column 16 + c are left out (and X22's below)
-        const int r = tid >> 3, q = 4 * (tid & 7);
-        if (q < 16) product(La + (32 + r) * kP, Xs + q, Xs + r * kQ + 32 + q, 32, 1.f);
-        else product(La + (32 + r) * kP + 16, Xs + 16 * kQ + q, Xs + r * kQ + 32 + q, 16, 1.f);
+    {  // the pair of 32.  X11's and X22's blocks above their diagonals hold sums, not zeros: X11's are
+       // masked in B (columns 16 .. 31 start at row 16), X22's by the number of terms
+        const int r = 4 * warp;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = 0; k < 32; k += 4) {
+            float4 l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[i] = f_row4(A, 32 + r + i, k >> 2);
+            const bool on = k >= 16 || lane < 16;
+            const float b0 = on ? X[f_at(k, lane)] : 0.f, b1 = on ? X[f_at(k + 1, lane)] : 0.f;
+            const float b2 = on ? X[f_at(k + 2, lane)] : 0.f, b3 = on ? X[f_at(k + 3, lane)] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = fmaf(l[i].w, b3, fmaf(l[i].z, b2, fmaf(l[i].y, b1, fmaf(l[i].x, b0, x[i]))));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) X[f_at(r + i, 32 + lane)] = x[i];
         __syncthreads();
-        product(Xs + (32 + r) * kQ + 32, Xs + 32 + q, Xs + (32 + r) * kQ + q, r < 16 ? 16 : 32, -1.f);
+        tri_product<4>(X, 32 + r, 32, X, 0, 32 + lane, r < 16 ? 16 : 32, X, 32 + r, lane, -1.f);
         __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------------------
-// The factors of every (chunk, head).  Rows past the sequence's end have beta = 0, a zero key
-// and a zero row of P, so that they write nothing and read nothing.
+// The factors of every (chunk, head).  Rows past the sequence's end have beta = 0, zero keys and
+// values and a zero row of P, so that they write nothing and read nothing.
 // ---------------------------------------------------------------------------
-template <int DK>
-struct FactorSmem {
-    // staged results lie over what they no longer need: P over Q, T (hi, lo) over A, -W over K
-    static constexpr uint32_t K = 0, Q = (DK / 64) * T8, A = 2 * (DK / 64) * T8, T = A, X = A + 17 * 1024;
-    static constexpr size_t bytes = X + 17 * 1024 + 1024;
-    static_assert(gdrtc::kD * gdrtc::kQ * 4 <= 17 * 1024, "X");
-};
+// Shared memory: for each half h of the key dimensions K_h and Q_h side by side (one operand of
+// 128 rows), P, A, X.  V comes in over Q, T (hi, lo) lies over A, -W over K, each when the other is
+// done with.  72 KB and 128 columns of tensor memory: three CTAs an SM.
+constexpr uint32_t FA_K = 0, FA_Q = T8, FA_PANEL = 2 * T8, FA_P = 4 * T8, FA_A = 5 * T8, FA_T = FA_A, FA_X = 7 * T8;
+constexpr size_t kFactorSmem = 9 * T8 + 1024;
 
 template <int DK>
 __global__ void __launch_bounds__(256, 3)
     gds_factor_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq,
-                      const __grid_constant__ CUtensorMap mk) {
+                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     constexpr int NP = DK / 64;
-    using L = FactorSmem<DK>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    float* La = reinterpret_cast<float*>(smem + L::A);
-    float* Xs = reinterpret_cast<float*>(smem + L::X);
+    float* A = reinterpret_cast<float*>(smem + FA_A);
+    float* X = reinterpret_cast<float*>(smem + FA_X);
     __shared__ __align__(16) float b_s[kChunk], beta_s[kChunk], gam_s[kChunk];
-    __shared__ __align__(8) uint64_t full, mbar;
+    __shared__ __align__(8) uint64_t full, vfull, mbar;
     __shared__ uint32_t tmem_slot;
 
-    const Geo G = geo();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = blockIdx.x, h = blockIdx.y;
     // the sequence of this chunk slot: the last one whose first chunk is at or before it
     int lo = 0, hi = a.S - 1;
@@ -222,29 +252,31 @@ __global__ void __launch_bounds__(256, 3)
     if (t0 < 0 || t0 >= sq.len || sq.slot < 0) return;
     const int n = min(sq.len - t0, kChunk);  // tokens of the chunk
     const int64_t tok = sq.begin + t0;
+    uint8_t* fac = static_cast<uint8_t*>(a.ws) + (int64_t(c) * a.H + h) * factor_bytes(DK, a.Dv);
 
-    if (G.tid == 0) {
+    if (tid == 0) {
         mbar_init(smem_u32(&full), 1);
+        mbar_init(smem_u32(&vfull), 1);
         mbar_init(smem_u32(&mbar), 1);
         mbar_fence_init();
     }
-    if (G.warp == 0) tmem_alloc(smem_u32(&tmem_slot), 128);
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 128);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;  // [0,64) K K^T, [64,128) Q K^T; then [0,DK) W
-    if (G.tid == 0) {
+    const uint32_t tmem = tmem_slot;  // [0,64) K K^T and Q K^T, then W^T; [64,128) U^T
+    if (tid == 0) {
         mbar_expect_tx(smem_u32(&full), 2 * NP * T8);
         for (int p = 0; p < NP; ++p) {
-            tma_load_3d(smem_u32(smem + L::K + p * T8), &mk, 64 * p, h / a.hdiv, int(tok), smem_u32(&full));
-            tma_load_3d(smem_u32(smem + L::Q + p * T8), &mq, 64 * p, h / a.hdiv, int(tok), smem_u32(&full));
+            tma_load_3d(smem_u32(smem + FA_K + p * FA_PANEL), &mk, 64 * p, h / a.hdiv, int(tok), smem_u32(&full));
+            tma_load_3d(smem_u32(smem + FA_Q + p * FA_PANEL), &mq, 64 * p, h / a.hdiv, int(tok), smem_u32(&full));
         }
     }
-    if (G.warp == 0) {  // the running sum of the gates, two tokens a lane
+    if (warp == 0) {  // the running sum of the gates, two tokens a lane
         float g[2], be[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int t = 2 * G.lane + i;
+            const int t = 2 * lane + i;
             g[i] = t < n ? __ldg(a.g + (tok + t) * a.gs + h) : 0.f;
             be[i] = t < n ? __ldg(a.beta + (tok + t) * a.bs + h) : 0.f;
             g[i] = g[i] < kForget ? kForget : g[i];
@@ -253,109 +285,178 @@ __global__ void __launch_bounds__(256, 3)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const float x = __shfl_up_sync(kFull, ps, o);
-            if (G.lane >= o) ps += x;
+            if (lane >= o) ps += x;
         }
         const float end = __shfl_sync(kFull, ps, 31);
         const float b[2] = {ps - g[1], ps};
-        float* gates = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) +
-                                                (int64_t(c) * a.H + h) * factor_bytes(DK) + (3 + NP) * T8);
+        float* gates = reinterpret_cast<float*>(fac + factor_gates(DK));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int t = 2 * G.lane + i;
+            const int t = 2 * lane + i;
             b_s[t] = b[i];
             beta_s[t] = be[i];
             gam_s[t] = expf(b[i]);
             gates[t] = a.scale * expf(b[i]);
             gates[64 + t] = expf(end - b[i]);
         }
-        if (G.lane == 0) gates[128] = expf(end);
+        if (lane == 0) gates[128] = expf(end);
     }
     mbar_wait(smem_u32(&full), 0);
     if (n < kChunk) {
-        zero_rows(smem + L::K, NP, n, G.tid, 256);
+        for (int p = 0; p < NP; ++p) zero_rows(smem + FA_K + p * FA_PANEL, 1, n, tid, 256);
         fence_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint64_t DKK = sdesc(smem_u32(smem + L::K), 16, 1024), DQ = sdesc(smem_u32(smem + L::Q), 16, 1024);
     uint32_t mph = 0;
-    if (G.tid == 0) {
+    const int vblocks = (a.Dv + 127) / 128;
+    // V of a block over Q (whose product is done by then)
+    auto load_v = [&](int vb) {
+        const int tiles = min((a.Dv - 128 * vb + 63) / 64, 2);
+        mbar_expect_tx(smem_u32(&vfull), tiles * T8);
+        for (int p = 0; p < tiles; ++p)
+            tma_load_3d(smem_u32(smem + FA_Q + p * FA_PANEL), &mv, 128 * vb + 64 * p, h, int(tok), smem_u32(&vfull));
+    };
+    if (warp == 0) {
+        if (elect()) {  // [K; Q] K^T
+            const uint64_t d = sdesc(smem_u32(smem + FA_K), 16, 1024);
 #pragma unroll
-        for (int k = 0; k < DK / 16; ++k) {
-            const uint32_t at = (k >> 2) * T8 + (k & 3) * 32;
-            mma_bf16(tmem, desc_plus(DKK, at), desc_plus(DKK, at), idesc_bf16(64, 64, 0, 0), k > 0);
-            mma_bf16(tmem + 64, desc_plus(DQ, at), desc_plus(DKK, at), idesc_bf16(64, 64, 0, 0), k > 0);
+            for (int k = 0; k < DK / 16; ++k) {
+                const uint32_t at = (k >> 2) * FA_PANEL + (k & 3) * 32;
+                mma_bf16(tmem, desc_plus(d, at), desc_plus(d, at), idesc_bf16(128, 64, 0, 0), k > 0);
+            }
+            mma_commit(smem_u32(&mbar));
         }
-        mma_commit(smem_u32(&mbar));
+        __syncwarp();
     }
     mbar_wait(smem_u32(&mbar), mph);
     mph ^= 1;
     tc_fence_after();
-    uint8_t* fac = static_cast<uint8_t*>(a.ws) + (int64_t(c) * a.H + h) * factor_bytes(DK);
-    const int c0 = 32 * G.grp + 16 * G.hi;
+    if (tid == 0) load_v(0);
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t tl = tmem + (uint32_t(32 * quad) << 16) + 32 * half;
     {
-        float kk[16], qk[16], p[16];
-        tok16x2(tmem, G, 32 * G.grp, 64 + 32 * G.grp, kk, qk);
-        const float bt = b_s[G.tau], be = beta_s[G.tau];
+        // rows 0 .. 63 are K's, 64 .. 127 are Q's; this warp's columns r are 32 half ..
+        uint32_t x[32];
+        tmem_ld<32>(tl, x);
+        tmem_wait_ld();
+        const int t = 32 * (quad & 1) + lane;
+        const float bt = b_s[t];
+        if (quad < 2) {
+            const float be = beta_s[t];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int r = c0 + e;
-            const float m = __expf(bt - b_s[r]);
-            La[G.tau * gdrtc::kP + r] = r < G.tau ? be * kk[e] * m : 0.f;
-            p[e] = r <= G.tau && G.tau < n ? a.scale * qk[e] * m : 0.f;
+            for (int e = 0; e < 32; e += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(b_s + 32 * half + e);
+                const int r = 32 * half + e;
+                float4 y;
+                y.x = r < t ? be * __uint_as_float(x[e]) * __expf(bt - b.x) : 0.f;
+                y.y = r + 1 < t ? be * __uint_as_float(x[e + 1]) * __expf(bt - b.y) : 0.f;
+                y.z = r + 2 < t ? be * __uint_as_float(x[e + 2]) * __expf(bt - b.z) : 0.f;
+                y.w = r + 3 < t ? be * __uint_as_float(x[e + 3]) * __expf(bt - b.w) : 0.f;
+                *reinterpret_cast<float4*>(A + f_unit(t, r >> 2)) = y;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 32 * half + e + i;
+                    y[i] = r <= t && t < n ? a.scale * __uint_as_float(x[e + i]) * __expf(bt - b_s[r]) : 0.f;
+                }
+                *reinterpret_cast<uint4*>(smem + FA_P + sw_chunk(64, t, (32 * half + e) >> 3)) = pack8(y);
+            }
         }
-        store_row16(smem + L::Q, G.tau, c0, p);
     }
     // K o gam over K (its products are done)
 #pragma unroll
-    for (int p = 0; p < NP; ++p) gdrtc::rows_scaled(smem + L::K + p * T8, smem + L::K + p * T8, gam_s, 1.f, G.tid);
+    for (int p = 0; p < NP; ++p) gdrtc::rows_scaled(smem + FA_K + p * FA_PANEL, smem + FA_K + p * FA_PANEL, gam_s, 1.f, tid);
     __syncthreads();
-    halves_inverse(La, Xs);
-    {
-        float x[16], lo16[16];
-        gdrtc::xs_row16(Xs, G.tau, c0, x);
+    halves_inverse(A, X);
+    {  // T, hi and lo: 16 columns of a row
+        const int t = (tid & 7) | ((tid >> 5) << 3), c0 = 16 * ((tid >> 3) & 3);
+        float x[16], rest[16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float4 v = f_row4(X, t, c0 / 4 + u), be = *reinterpret_cast<const float4*>(beta_s + c0 + 4 * u);
+            x[4 * u] = v.x * be.x, x[4 * u + 1] = v.y * be.y, x[4 * u + 2] = v.z * be.z, x[4 * u + 3] = v.w * be.w;
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            x[e] = c0 + e <= G.tau ? x[e] * beta_s[c0 + e] : 0.f;
-            lo16[e] = x[e] - __bfloat162float(__float2bfloat16_rn(x[e]));
+            x[e] = c0 + e <= t ? x[e] : 0.f;
+            rest[e] = x[e] - __bfloat162float(__float2bfloat16_rn(x[e]));
         }
-        store_row16(smem + L::T, G.tau, c0, x);
-        store_row16(smem + L::T + T8, G.tau, c0, lo16);
+        store_row16(smem + FA_T, t, c0, x);
+        store_row16(smem + FA_T + T8, t, c0, rest);
     }
-    fence_async_smem();
-    tc_fence_before();
+    for (int vb = 0; vb < vblocks; ++vb) {
+        mbar_wait(smem_u32(&vfull), vb & 1);
+        if (n < kChunk)
+            for (int p = 0; p < 2; ++p) zero_rows(smem + FA_Q + p * FA_PANEL, 1, n, tid, 256);
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 0) {
+            if (elect()) {
+                const uint64_t dt = sdesc(smem_u32(smem + FA_T), 16, 1024), dv = sdesc(smem_u32(smem + FA_Q), FA_PANEL, 1024);
+                if (vb == 0) {  // W^T = (K o gam)^T T^T, with T's high part
+                    const uint64_t dk = sdesc(smem_u32(smem + FA_K), FA_PANEL, 1024);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem, desc_plus(dk, k * 2048), desc_plus(dt, k * 32), idesc_bf16(128, 64, 1, 0), k > 0);
+                    bulk_store(fac, smem_u32(smem + FA_P), T8);
+                    bulk_commit();
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)  // U^T = V^T T^T
+                    mma_bf16(tmem + 64, desc_plus(dv, (k & 3) * 2048), desc_plus(dt, (k >> 2) * T8 + (k & 3) * 32),
+                             idesc_bf16(128, 64, 1, 0), k > 0);
+                mma_commit(smem_u32(&mbar));
+            }
+            __syncwarp();
+        }
+        mbar_wait(smem_u32(&mbar), mph);
+        mph ^= 1;
+        tc_fence_after();
+        const int row = 32 * quad + lane;
+        uint32_t x[32];
+        if (vb == 0) {
+            tmem_ld<32>(tl, x);
+            tmem_wait_ld();
+            if (row < DK) {
+                uint8_t* w = smem + FA_K + (row >> 6) * FA_PANEL;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    *reinterpret_cast<__nv_bfloat16*>(w + sw_off(64, 32 * half + e, row & 63)) = __float2bfloat16_rn(-__uint_as_float(x[e]));
+            }
+            fence_async_smem();
+        }
+        if (tid == 0 && vb + 1 < vblocks) load_v(vb + 1);
+        tmem_ld<32>(tl + 64, x);
+        tmem_wait_ld();
+        if (row < int(u_cols(a.Dv))) {
+            float4* u = reinterpret_cast<float4*>(fac + factor_u(DK) + vb * u_bytes(a.Dv)) + row;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+                u[(8 * half + e / 4) * int(u_cols(a.Dv))] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                                                                    __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (vb == 0 && warp == 0) {
+            if (elect()) {
+                for (int p = 0; p < NP; ++p) bulk_store(fac + (1 + p) * T8, smem_u32(smem + FA_K + p * FA_PANEL), T8);
+                bulk_commit();
+                bulk_wait_read();  // shared memory is read before the CTA ends
+            }
+            __syncwarp();
+        }
+    }
     __syncthreads();
-    tc_fence_after();
-    if (G.tid == 0) {  // W = T (K o gam): K o gam is [tokens][Dk], MN-major
-        const uint64_t DT = sdesc(smem_u32(smem + L::T), 16, 1024), DM = sdesc(smem_u32(smem + L::K), T8, 1024);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem, desc_plus(DT, k * 32), desc_plus(DM, k * 2048), idesc_bf16(64, DK, 0, 1), k > 0);
-        mma_commit(smem_u32(&mbar));
-        bulk_store(fac, smem_u32(smem + L::T), 2 * T8);
-        bulk_store(fac + 2 * T8, smem_u32(smem + L::Q), T8);
-        bulk_commit();
-    }
-    mbar_wait(smem_u32(&mbar), mph);
-    tc_fence_after();
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        float w[16];
-        tok16(tmem, G, 64 * p + 32 * G.grp, w);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = -w[e];
-        store_row16(smem + L::K + p * T8, G.tau, c0, w);
-    }
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    if (G.tid == 0) {
-        bulk_store(fac + 3 * T8, smem_u32(smem + L::K), NP * T8);
-        bulk_commit();
-        bulk_wait_read();  // shared memory is read before the CTA ends
-    }
-    if (G.warp == 0) tmem_dealloc(tmem, 128);
+    if (warp == 0) tmem_dealloc(tmem, 128);
 }
 
 // ---------------------------------------------------------------------------
@@ -368,8 +469,8 @@ constexpr int kGateRing = 4;
 template <int DK>
 struct WalkSmem {
     static constexpr int NP = DK / 64;
-    // two of each piece, every one with barriers of its own: V with T, W, K, Q with P
-    static constexpr uint32_t VT = 0, vt = 4 * T8, W = VT + 2 * vt, w = NP * T8, K = W + 2 * w, k = NP * T8, QP = K + 2 * k,
+    // two of each piece, every one with barriers of its own: U, W, K, Q with P
+    static constexpr uint32_t U = 0, u = 4 * T8, W = U + 2 * u, w = NP * T8, K = W + 2 * w, k = NP * T8, QP = K + 2 * k,
                               qp = (NP + 1) * T8, GATES = QP + 2 * qp;
     static constexpr size_t bytes = GATES + kGateRing * kGateBytes + 1024;
 };
@@ -379,9 +480,21 @@ static_assert(WalkSmem<128>::bytes <= 227 * 1024, "shared memory of a CTA");
 constexpr uint32_t TM_S = 0, TM_DTH = 64, TM_DTL = 96, TM_DH = 128, TM_DL = 160, TM_D = 192, TM_X = 256, TM_O1 = 384,
                    TM_O2 = 448;
 
-// A bounded wait; after one that ran out the others of this thread give up soon.
+// A bounded wait; after one that ran out the others of this thread give up soon.  The clock is
+// read once in 64 polls: a read between two polls would delay the chain by its own latency.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& dead) {
-    if (!mbar_wait(smem_u32(bar), parity, dead ? 1000ull * 1000 : kWaitLimitNs)) dead = true;
+    const uint32_t b = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(b, parity); ++i) {
+        if ((i & 63u) != 0) continue;
+        const uint64_t t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > (dead ? 1000ull * 1000 : kWaitLimitNs)) {
+            atomicExch(&g_timeout_flag, 1);
+            dead = true;
+            return;
+        }
+    }
 }
 // One arrival of a warp after its tensor-memory or shared-memory work.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -390,15 +503,17 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 
 struct WalkBars {
-    uint64_t vt_full[2], vt_free[2], w_full[2], w_free[2], k_full[2], k_free[2], qp_full[2], qp_free[2];
+    uint64_t u_full[2], u_free[2], w_full[2], w_free[2], k_full[2], k_free[2], qp_full[2], qp_free[2];
     uint64_t gates[kGateRing];
-    uint64_t s_ready[kGroups], x_done[2], dt_ready, d_ready, d_done, o_done, o_free, fixed;
+    uint64_t s_ready[2], x_done[2], dt_ready, d_ready, d_done, o_done, o_free, fixed;
 };
 
-template <int DK, typename TS>
+// RQ: quadrants of tensor-memory lanes in use, of 32 value columns each (the warps of the others
+// leave at once).
+template <int DK, int RQ, typename TS>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     gds_walk_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq,
-                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+                    const __grid_constant__ CUtensorMap mk) {
     constexpr int NP = DK / 64;
     constexpr int GC = DK / kGroups;       // state rows (columns of tensor memory) of a group
     constexpr int GT = kChunk / kGroups;   // tokens of a group
@@ -409,8 +524,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     __shared__ uint32_t tmem_slot;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int blocks = (a.Dv + 127) / 128;
-    const int h = blockIdx.x / blocks, v0 = (blockIdx.x % blocks) * 128, nv = min(a.Dv - v0, 128);
+    constexpr int kCols = 32 * RQ;
+    const int blocks = (a.Dv + kCols - 1) / kCols;
+    const int h = blockIdx.x / blocks, v0 = (blockIdx.x % blocks) * kCols, nv = min(a.Dv - v0, kCols);
     const Seq sq = sequence(a, blockIdx.y);
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + v0;
     const int64_t os = int64_t(a.H) * a.Dv;
@@ -430,18 +546,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            for (uint64_t* b : {&bar.vt_full[i], &bar.vt_free[i], &bar.w_full[i], &bar.w_free[i], &bar.k_full[i], &bar.k_free[i],
+            for (uint64_t* b : {&bar.u_full[i], &bar.w_full[i], &bar.w_free[i], &bar.k_full[i], &bar.k_free[i],
                                 &bar.qp_full[i], &bar.qp_free[i], &bar.x_done[i]})
                 mbar_init(smem_u32(b), 1);
+            mbar_init(smem_u32(&bar.u_free[i]), RQ * kGroups);
         }
         for (int i = 0; i < kGateRing; ++i) mbar_init(smem_u32(&bar.gates[i]), 1);
-        for (int i = 0; i < kGroups; ++i) mbar_init(smem_u32(&bar.s_ready[i]), 4);
-        mbar_init(smem_u32(&bar.dt_ready), 4 * kGroups);
-        mbar_init(smem_u32(&bar.d_ready), 4 * kGroups);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bar.s_ready[i]), RQ * kGroups / 2);
+        mbar_init(smem_u32(&bar.dt_ready), RQ * kGroups);
+        mbar_init(smem_u32(&bar.d_ready), RQ * kGroups);
         mbar_init(smem_u32(&bar.d_done), 1);
         mbar_init(smem_u32(&bar.o_done), 1);
-        mbar_init(smem_u32(&bar.o_free), 4);
-        mbar_init(smem_u32(&bar.fixed), 4 * kGroups);
+        mbar_init(smem_u32(&bar.o_free), RQ);
+        mbar_init(smem_u32(&bar.fixed), RQ * kGroups);
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 512);
@@ -451,7 +568,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const uint32_t tmem = tmem_slot;
     bool dead = false;
 
-    if (warp < 4 * kGroups) {
+    if (warp < 4 * kGroups + 4 && (warp & 3) >= RQ) {
+        // no columns
+    } else if (warp < 4 * kGroups) {
         // ---- the chain: a lane is a value column, a group a quarter of the state's rows and of the tokens
         const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
@@ -463,11 +582,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         float end = 1.f;
         for (int c = 0; c <= chunks; ++c) {
             if (c == chunks - 1 && ragged) {
-                // rows past the sequence's end hold other tokens: they must not meet a zero of D or T as NaN
-                wait(&bar.vt_full[c & 1], (c >> 1) & 1, dead);
+                // keys past the sequence's end are other tokens': they must not meet a zero of D~ as NaN
                 wait(&bar.k_full[c & 1], (c >> 1) & 1, dead);
-                zero_rows(smem + L::VT + (c & 1) * L::vt, 2, last, tid, 128 * kGroups);
-                zero_rows(smem + L::K + (c & 1) * L::k, NP, last, tid, 128 * kGroups);
+                const int at = (grp * RQ + (warp & 3)) * 32 + lane;
+                zero_rows(smem + L::K + (c & 1) * L::k, NP, last, at, 32 * RQ * kGroups);
                 fence_async_smem();
                 warp_arrive(&bar.fixed, lane);
             }
@@ -488,39 +606,44 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tmem_st<GC / 2>(tl + TM_S + grp * (GC / 2), p);
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(&bar.s_ready[grp], lane);
+                warp_arrive(&bar.s_ready[grp >> 1], lane);
             }
-            // the decays of this group's tokens, while the product runs
             const float* gates = reinterpret_cast<const float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
+            const float4* u = reinterpret_cast<const float4*>(smem + L::U + (c & 1) * L::u) + GT / 4 * grp * kCols + row;
             wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, dead);
-            float dec[GT];
-#pragma unroll
-            for (int i = 0; i < GT; i += 4) {
-                const float4 e = *reinterpret_cast<const float4*>(gates + 64 + GT * grp + i);
-                dec[i] = e.x, dec[i + 1] = e.y, dec[i + 2] = e.z, dec[i + 3] = e.w;
-            }
             end = gates[128];
+            wait(&bar.u_full[c & 1], (c >> 1) & 1, dead);
             wait(&bar.d_done, c & 1, dead);
             tc_fence_after();
             uint32_t x[GT], hi[GT / 2], lo[GT / 2];
             tmem_ld<GT>(tl + TM_D + GT * grp, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < GT / 2; ++i) {  // D~, which the chain waits for, first
-                const float u = __uint_as_float(x[2 * i]) * dec[2 * i], w = __uint_as_float(x[2 * i + 1]) * dec[2 * i + 1];
-                hi[i] = pack2(u, w);
-                lo[i] = pack2_rest(u, w, hi[i]);
+            for (int i = 0; i < GT; i += 4) {  // D = U - W S; D~, which the chain waits for, first
+                const float4 y = u[i / 4 * kCols];
+                const float4 e = *reinterpret_cast<const float4*>(gates + 64 + GT * grp + i);
+                const float d0 = __uint_as_float(x[i]) + y.x, d1 = __uint_as_float(x[i + 1]) + y.y;
+                const float d2 = __uint_as_float(x[i + 2]) + y.z, d3 = __uint_as_float(x[i + 3]) + y.w;
+                x[i] = __float_as_uint(d0), x[i + 1] = __float_as_uint(d1), x[i + 2] = __float_as_uint(d2), x[i + 3] = __float_as_uint(d3);
+                hi[i / 2] = pack2(d0 * e.x, d1 * e.y);
+                lo[i / 2] = pack2_rest(d0 * e.x, d1 * e.y, hi[i / 2]);
+                hi[i / 2 + 1] = pack2(d2 * e.z, d3 * e.w);
+                lo[i / 2 + 1] = pack2_rest(d2 * e.z, d3 * e.w, hi[i / 2 + 1]);
             }
             tmem_st<GT / 2>(tl + TM_DTH + GT / 2 * grp, hi);
             tmem_st<GT / 2>(tl + TM_DTL + GT / 2 * grp, lo);
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&bar.dt_ready, lane);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bar.dt_ready));
+                mbar_arrive(smem_u32(&bar.u_free[c & 1]));
+            }
 #pragma unroll
             for (int i = 0; i < GT / 2; ++i) {
-                const float u = __uint_as_float(x[2 * i]), w = __uint_as_float(x[2 * i + 1]);
-                hi[i] = pack2(u, w);
-                lo[i] = pack2_rest(u, w, hi[i]);
+                const float v = __uint_as_float(x[2 * i]), w = __uint_as_float(x[2 * i + 1]);
+                hi[i] = pack2(v, w);
+                lo[i] = pack2_rest(v, w, hi[i]);
             }
             tmem_st<GT / 2>(tl + TM_DH + GT / 2 * grp, hi);
             tmem_st<GT / 2>(tl + TM_DL + GT / 2 * grp, lo);
@@ -543,25 +666,29 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, dead);
             wait(&bar.o_done, c & 1, dead);
             tc_fence_after();
-            const int n = c == chunks - 1 ? last : kChunk;
+            uint32_t y[kChunk / 2];
 #pragma unroll
             for (int j = 0; j < kChunk; j += 16) {
                 uint32_t p[16], q[16];
                 tmem_ld<16>(tl + TM_O1 + j, p);
                 tmem_ld<16>(tl + TM_O2 + j, q);
                 tmem_wait_ld();
-                float y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = fmaf(gam[j + i], __uint_as_float(p[i]), __uint_as_float(q[i]));
-                if (j == kChunk - 16) {  // the accumulators and the decays have been read
-                    tc_fence_before();
-                    warp_arrive(&bar.o_free, lane);
-                }
-                if (row < nv) {
+                for (int i = 0; i < 16; i += 2)
+                    y[(j + i) / 2] = pack2(fmaf(gam[j + i], __uint_as_float(p[i]), __uint_as_float(q[i])),
+                                           fmaf(gam[j + i + 1], __uint_as_float(p[i + 1]), __uint_as_float(q[i + 1])));
+            }
+            tc_fence_before();
+            warp_arrive(&bar.o_free, lane);  // the accumulators and the decays have been read
+            const int n = row < nv ? (c == chunks - 1 ? last : kChunk) : 0;
+            uint16_t* to = reinterpret_cast<uint16_t*>(mine);
+            if (n == kChunk) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (j + i < n) mine[(j + i) * os] = __float2bfloat16_rn(y[i]);
-                }
+                for (int i = 0; i < kChunk; ++i) to[i * os] = uint16_t(i & 1 ? y[i / 2] >> 16 : y[i / 2] & 0xffffu);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i)
+                    if (i < n) to[i * os] = uint16_t(i & 1 ? y[i / 2] >> 16 : y[i / 2] & 0xffffu);
             }
             mine += kChunk * os;
         }
@@ -570,54 +697,39 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         // descriptors stay in uniform registers: 30 cycles a product of N = 64 instead of 45 to 80
         // from inside a one-lane branch (measured with 8 to 64 in a row).
         const uint32_t base = smem_u32(smem);
-        constexpr uint32_t kTV = idesc_bf16(128, 64, 1, 0), kTS = idesc_bf16(128, 64, 0, 0), kTX = idesc_bf16(128, DK / 2, 0, 1);
-        // D^T = V^T T^T of chunk c (T as the sum of two)
-        auto tv = [&](int c) {
-            wait(&bar.vt_full[c & 1], (c >> 1) & 1, dead);
-            if (c == chunks - 1 && ragged) wait(&bar.fixed, 0, dead);
-            tc_fence_after();
-            const uint32_t s = base + L::VT + (c & 1) * L::vt;
-            const uint64_t dv = sdesc(s, T8, 1024), dt = sdesc(s + 2 * T8, 16, 1024);
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_bf16(tmem + TM_D, desc_plus(dv, (k & 3) * 2048), desc_plus(dt, (k >> 2) * T8 + (k & 3) * 32), kTV, k > 0);
-                mma_commit(smem_u32(&bar.vt_free[c & 1]));
-            }
-            __syncwarp();
-        };
-        tv(0);
+        constexpr uint32_t kTS = idesc_bf16(128, 64, 0, 0), kTX = idesc_bf16(128, DK / 2, 0, 1);
         for (int c = 0; c < chunks; ++c) {
             const int i = c & 1, ph = (c >> 1) & 1;
             const uint64_t dw = sdesc(base + L::W + i * L::w, 16, 1024), dk = sdesc(base + L::K + i * L::k, T8, 1024);
             const uint64_t dq = sdesc(base + L::QP + i * L::qp, 16, 1024), dp = desc_plus(dq, NP * T8);
+            // (a wait that passes costs some 100 cycles: the copies are waited for ahead of the chain)
             wait(&bar.w_full[i], ph, dead);
+            wait(&bar.qp_full[i], ph, dead);
+            wait(&bar.k_full[i], ph, dead);
+            if (c > 0) wait(&bar.o_free, (c - 1) & 1, dead);
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {  // D^T -= S^T W^T, each group's rows of the state as they come
+            for (int g = 0; g < 2; ++g) {  // D^T = U^T - S^T W^T without U, half of the state's rows as they come
                 wait(&bar.s_ready[g], c & 1, dead);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
-                    for (int k = g * (GC / 16); k < (g + 1) * (GC / 16); ++k)
-                        mma_ts(tmem + TM_D, tmem + TM_S + 8 * k, desc_plus(dw, (k >> 2) * T8 + (k & 3) * 32), kTS, 1);
-                    if (g == kGroups - 1) {
+                    for (int k = g * (DK / 32); k < (g + 1) * (DK / 32); ++k)
+                        mma_ts(tmem + TM_D, tmem + TM_S + 8 * k, desc_plus(dw, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
+                    if (g == 1) {
                         mma_commit(smem_u32(&bar.d_done));
                         mma_commit(smem_u32(&bar.w_free[i]));
                     }
                 }
                 __syncwarp();
             }
-            wait(&bar.qp_full[i], ph, dead);
-            if (c > 0) wait(&bar.o_free, (c - 1) & 1, dead);
-            tc_fence_after();
             if (elect()) {
 #pragma unroll
                 for (int k = 0; k < DK / 16; ++k)  // O1^T = S^T Q^T
                     mma_ts(tmem + TM_O1, tmem + TM_S + 8 * k, desc_plus(dq, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
             }
             __syncwarp();
-            wait(&bar.k_full[i], ph, dead);
             wait(&bar.dt_ready, c & 1, dead);
+            if (c == chunks - 1 && ragged) wait(&bar.fixed, 0, dead);
             tc_fence_after();
             if (elect()) {
 #pragma unroll
@@ -626,9 +738,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     for (int k = 0; k < 8; ++k)
                         mma_ts(tmem + TM_X + g * (DK / 2), tmem + (k < 4 ? TM_DTH : TM_DTL) + 8 * (k & 3),
                                desc_plus(dk, (DK == 128 ? g * T8 : g * 64) + (k & 3) * 2048), kTX, k > 0);
+                    if (g == 1) mma_commit(smem_u32(&bar.k_free[i]));
                     mma_commit(smem_u32(&bar.x_done[g]));
                 }
-                mma_commit(smem_u32(&bar.k_free[i]));
             }
             __syncwarp();
             wait(&bar.d_ready, c & 1, dead);
@@ -637,34 +749,40 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // O2^T = D^T P^T
                     mma_ts(tmem + TM_O2, tmem + (k < 4 ? TM_DH : TM_DL) + 8 * (k & 3), desc_plus(dp, (k & 3) * 32), kTS, k > 0);
-                mma_commit(smem_u32(&bar.o_done));
                 mma_commit(smem_u32(&bar.qp_free[i]));
+                mma_commit(smem_u32(&bar.o_done));
             }
             __syncwarp();
-            if (c + 1 < chunks) tv(c + 1);
         }
         wait(&bar.x_done[1], (chunks - 1) & 1, dead);
         wait(&bar.o_done, (chunks - 1) & 1, dead);
     } else {
         // ---- the copies: each piece of chunk c once the products that read chunk c - 2's are done
         if (lane == 0) {
-            const uint32_t vt = (nv + 63) / 64, base = smem_u32(smem);
-            const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y)) * a.H + h) * factor_bytes(DK);
-            for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * factor_bytes(DK)) {
+            const uint32_t base = smem_u32(smem), ucols = u_cols(a.Dv), fb = factor_bytes(DK, a.Dv);
+            const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y)) * a.H + h) * fb;
+            const uint32_t uat = factor_u(DK) + (v0 / 128) * u_bytes(a.Dv) + (v0 % 128) * 16;
+            for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * fb) {
                 const int i = c & 1, ph = ((c >> 1) & 1) ^ 1, tok = sq.begin + c * kChunk;
-                uint32_t b = smem_u32(&bar.vt_full[i]), s = base + L::VT + i * L::vt;
-                wait(&bar.vt_free[i], ph, dead);
-                // the gates of chunk c - 4 are read: V and T of chunk c - 2 are, which follows
-                const uint32_t gb = smem_u32(&bar.gates[c % kGateRing]);
-                mbar_expect_tx(gb, kGateBytes);
-                bulk_load(base + L::GATES + (c % kGateRing) * kGateBytes, fac + (3 + NP) * T8, kGateBytes, gb);
-                mbar_expect_tx(b, (vt + 2) * T8);
-                for (uint32_t p = 0; p < vt; ++p) tma_load_3d(s + p * T8, &mv, v0 + 64 * p, h, tok, b);
-                bulk_load(s + 2 * T8, fac, 2 * T8, b);
+                uint32_t b, s;
                 wait(&bar.w_free[i], ph, dead);
                 b = smem_u32(&bar.w_full[i]);
                 mbar_expect_tx(b, NP * T8);
-                bulk_load(base + L::W + i * L::w, fac + 3 * T8, NP * T8, b);
+                bulk_load(base + L::W + i * L::w, fac + T8, NP * T8, b);
+                // the gates of chunk c - 4 are read: W S of chunk c - 2 is done, which follows
+                b = smem_u32(&bar.gates[c % kGateRing]);
+                mbar_expect_tx(b, kGateBytes);
+                bulk_load(base + L::GATES + (c % kGateRing) * kGateBytes, fac + factor_gates(DK), kGateBytes, b);
+                wait(&bar.u_free[i], ph, dead);
+                b = smem_u32(&bar.u_full[i]), s = base + L::U + i * L::u;
+                // (columns past Dv are the factors' padding)
+                const uint32_t wide = min(uint32_t(kCols), ucols - v0 % 128);
+                mbar_expect_tx(b, kChunk * 4 * wide);
+                if (wide == ucols && wide == kCols) {
+                    bulk_load(s, fac + uat, kChunk * 4 * wide, b);
+                } else {
+                    for (int g = 0; g < kChunk / 4; ++g) bulk_load(s + g * kCols * 16, fac + uat + g * ucols * 16, wide * 16, b);
+                }
                 wait(&bar.k_free[i], ph, dead);
                 b = smem_u32(&bar.k_full[i]);
                 mbar_expect_tx(b, NP * T8);
@@ -673,12 +791,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 b = smem_u32(&bar.qp_full[i]), s = base + L::QP + i * L::qp;
                 mbar_expect_tx(b, (NP + 1) * T8);
                 for (int p = 0; p < NP; ++p) tma_load_3d(s + p * T8, &mq, 64 * p, h / a.hdiv, tok, b);
-                bulk_load(s + NP * T8, fac + 2 * T8, T8, b);
+                bulk_load(s + NP * T8, fac, T8, b);
             }
             // no copy outlives the CTA
             for (int c = max(chunks - 2, 0); c < chunks; ++c) {
                 const int i = c & 1, ph = (c >> 1) & 1;
-                wait(&bar.vt_full[i], ph, dead);
+                wait(&bar.u_full[i], ph, dead);
                 wait(&bar.w_full[i], ph, dead);
                 wait(&bar.k_full[i], ph, dead);
                 wait(&bar.qp_full[i], ph, dead);
@@ -718,13 +836,21 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     if (!map_of(&mk, a.k, DK, a.H / a.hdiv, a.N, a.ks)) return fail("k", true);
     if (!map_of(&mv, a.v, a.Dv, a.H, a.N, a.vs)) return fail("v", true);
     auto ff = gds_factor_kernel<DK>;
-    if (!set_smem(ff, FactorSmem<DK>::bytes)) return fail("shared-memory attribute of the factors", false);
-    ff<<<dim3(unsigned(chunk_slots(a)), unsigned(a.H)), 256, FactorSmem<DK>::bytes, s>>>(a, mq, mk);
+    if (!set_smem(ff, kFactorSmem)) return fail("shared-memory attribute of the factors", false);
+    ff<<<dim3(unsigned(chunk_slots(a)), unsigned(a.H)), 256, kFactorSmem, s>>>(a, mq, mk, mv);
     note_launch(1);
     if (!launch_ok()) return fail("launch of the factors", false);
-    auto fw = state_dt == RM_F32 ? gds_walk_kernel<DK, float> : gds_walk_kernel<DK, __nv_bfloat16>;
+    // Few sequences and heads leave multiprocessors idle: their CTAs take fewer columns then, which
+    // shortens the chain's arithmetic (the products take as long for 32 columns as for 128).
+    const int64_t wide = int64_t((a.Dv + 127) / 128) * a.H * a.S, sms = sm_count();
+    const int rq = a.Dv <= 32 || wide * 4 <= sms ? 1 : a.Dv <= 64 || wide * 2 <= sms ? 2 : 4;
+    const bool f = state_dt == RM_F32;
+    auto fw = rq == 1   ? (f ? gds_walk_kernel<DK, 1, float> : gds_walk_kernel<DK, 1, __nv_bfloat16>)
+              : rq == 2 ? (f ? gds_walk_kernel<DK, 2, float> : gds_walk_kernel<DK, 2, __nv_bfloat16>)
+                        : (f ? gds_walk_kernel<DK, 4, float> : gds_walk_kernel<DK, 4, __nv_bfloat16>);
     if (!set_smem(fw, WalkSmem<DK>::bytes)) return fail("shared-memory attribute of the walk", false);
-    fw<<<dim3(unsigned((a.Dv + 127) / 128 * a.H), unsigned(a.S)), kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, mq, mk, mv);
+    const int cols = 32 * rq;
+    fw<<<dim3(unsigned((a.Dv + cols - 1) / cols * a.H), unsigned(a.S)), kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, mq, mk);
     note_launch(1);
     if (!launch_ok()) return fail("launch of the walk", false);
     return RM_OK;
@@ -736,7 +862,7 @@ bool tc_supports(const Args& a, rm_dtype dt) {
     return dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
 }
 
-size_t tc_workspace_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk); }
+size_t tc_workspace_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk, a.Dv); }
 
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     return a.Dk == 64 ? launch<64>(a, state_dt, s) : launch<128>(a, state_dt, s);
