@@ -1,30 +1,35 @@
 // gdstc_kernels.cu -- the gated delta rule with a carried state in chunks of 64 tokens on the
 // tensor cores (tcgen05 + TMA): ragged prompts in bf16, Dk in {64, 128}, any Dv.
 //
-// With b_t the running sum of a chunk's gates, gam_t = e^{b_t}, Gam[t][r] = e^{b_t - b_r} (r <= t),
-// A[t][r] = beta_t (k_t.k_r) Gam[t][r] (r < t), T = (I + A)^{-1} diag(beta) and S the state before
-// the chunk, unrolling the recurrence gives (the WY form of the product of I - beta k k^T):
-//     D  = T V - W S,               W = T (K o gam)
-//     O  = scale gam o (Q S) + P D, P = scale mask(Q K^T) o Gam
-//     S' = e^{b_63} S + K^T D~,     D~_t = e^{b_63 - b_t} D_t
+// With b_t the running sum of a chunk's gates, Gam[t][r] = e^{b_t - b_r} (r <= t), A[t][r] =
+// beta_t (k_t.k_r) Gam[t][r] (r < t), T = (I + A)^{-1} diag(beta) and S the state before the chunk,
+// unrolling the recurrence gives (the WY form of the product of I - beta k k^T):
+//     D  = T V - T (K o e^b) S,    O = scale (e^b o (Q S) + (mask(Q K^T) o Gam) D)
+//     S' = e^{b_63} S + K^T D~,    D~_t = e^{b_63 - b_t} D_t
+// Where every |b_t - b_63| < 60 all decays are taken to the chunk's end, with dec_t = e^{b_63 - b_t}
+// and S~ = e^{b_63} S, so that nothing between the products but roundings is left to do:
+//     T~ = dec o T,   W = T~ (K o 1/dec),   P = mask(Q K^T)
+//     D~ = T~ V - W S~,   O = scale / dec o (Q S~ + P D~),   S' = S~ + K^T D~
+// Chunks of stronger decay, whose factors would leave fp32, take the first form (T~ = T, W = T (K o
+// e^b), P = mask(Q K^T) o Gam).
 // Two launches:
-//   gds_factor_kernel  every (chunk, head) at once: U = T V, P, -W and the decays, which do not
-//                      depend on the state, laid out as the walk copies them in
-//   gds_walk_kernel    one CTA per (sequence, head, 32 to 128 columns of values): the chain over
-//                      the sequence's chunks
+//   gds_factor_kernel  every (chunk, head) at once: T~, P, -W and the decays, which do not depend
+//                      on the state, as images of the swizzled tiles that the walk copies in
+//   gds_walk_kernel    one CTA per (sequence, head, 128 columns of values): the chain over the
+//                      sequence's chunks
 //
-// The walk is bound by the latency of its chain: S -> W S -> D -> K^T D~ -> S.  It keeps S
-// transposed, a value column a lane, so that every step of the chain is a row of tensor memory
-// per thread and the rounded S and D go back to tensor memory as A operands, with no transposition
-// and no shared memory; the state itself stays in fp32 registers.  Products that do not carry the
-// chain (Q S, P D) are issued behind those that do, and the outputs are read and stored by warps
-// of their own.
+// The walk is bound by the latency of its chain: S -> W S -> D~ -> K^T D~ -> S.  It keeps S
+// transposed, a value column a lane, so that every step of the chain is a row of tensor memory per
+// thread and the rounded S and D go back to tensor memory as A operands, with no transposition and
+// no shared memory.  The state itself accumulates in tensor memory in fp32.  Products that do not
+// carry the chain (T~ V of the next chunk, Q S, P D) are issued behind those that do, and the
+// outputs are read and stored by warps of their own.
 //
-// Rounding: K, Q and V enter as they are; T, D and D~ as the sum of two bf16 (16 significant
-// bits: two products with the exact operand), because T's and D's errors reach the state
-// undamped; U = T V stays in fp32.  S, W and P are rounded once to bf16: S and W only enter through W S, which is small
-// beside T V, and P only through O, which is rounded to bf16 anyway.  In fp64 with these roundings alone
-// (1024 tokens, 4 heads of 128): state 1.4e-4 off, o 2.4e-3 with its own rounding of 1.7e-3.
+// Rounding: K, Q and V enter as they are; T~ and D~ as the sum of two bf16 (16 significant bits:
+// two products with the exact operand), because their errors reach the state undamped.  S, W and P
+// are rounded once to bf16: S and W only enter through W S, which is small beside T V, and P only
+// through O, which is rounded to bf16 anyway.  In fp64 with these roundings alone (1024 tokens, 4
+// heads of 128): state 1.4e-4 off, o 2.4e-3 with its own rounding of 1.7e-3.
 #include <cstdio>
 
 #include "gds.cuh"
@@ -38,19 +43,14 @@ using namespace tc;
 namespace {
 
 constexpr uint32_t T8 = kTileBytes;      // one [64][64] bf16 tile
-constexpr uint32_t kGateBytes = 1024;    // gam [64], dec [64], e^{b_63}, padding
+constexpr uint32_t kGateBytes = 1024;    // the scale of O (weak) or of Q S [64], dec [64], e^{b_63}, weak (1 or 0)
+constexpr int kDec = 64, kEnd = 128, kWeak = 129;
 constexpr float kForget = -110.f;        // e^{-110} is 0 in fp32: lower gates are raised to it
+constexpr float kWeakLimit = 60.f;       // decays within a chunk that factor through its end
 
-// Factors of a (chunk, head) in the workspace: P, -W (Dk / 64 swizzled tiles), the gates, then
-// U in fp32 as [16 groups of 4 tokens][columns][4] for each block of up to 128 value columns, so
-// that a lane of the walk reads its column's four tokens at once.
-__host__ __device__ constexpr uint32_t u_cols(int Dv) { return Dv >= 128 ? 128u : uint32_t((Dv + 31) / 32 * 32); }
-__host__ __device__ constexpr uint32_t u_bytes(int Dv) { return kChunk * 4 * u_cols(Dv); }  // of a block
-__host__ __device__ constexpr uint32_t factor_gates(int Dk) { return (1 + Dk / 64) * T8; }
-__host__ __device__ constexpr uint32_t factor_u(int Dk) { return factor_gates(Dk) + kGateBytes; }
-__host__ __device__ constexpr uint32_t factor_bytes(int Dk, int Dv) {
-    return factor_u(Dk) + uint32_t((Dv + 127) / 128) * u_bytes(Dv);
-}
+// Factors of a (chunk, head) in the workspace: T~ hi, T~ lo, P, -W (Dk / 64 tiles), the gates.
+__host__ __device__ constexpr uint32_t factor_gates(int Dk) { return (3 + Dk / 64) * T8; }
+__host__ __device__ constexpr uint32_t factor_bytes(int Dk) { return factor_gates(Dk) + kGateBytes; }
 
 // First chunk of sequence i: chunks of different sequences do not meet, since a sequence of n
 // tokens from token b has at most floor((b + n) / 64) - floor(b / 64) + 1 of them.
@@ -70,6 +70,8 @@ __device__ __forceinline__ void tmem_st<16>(uint32_t at, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+template <>
+__device__ __forceinline__ void tmem_st<32>(uint32_t at, const uint32_t* r) { tmem_st32(at, r); }
 template <>
 __device__ __forceinline__ void tmem_st<8>(uint32_t at, const uint32_t* r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
@@ -117,13 +119,38 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
+// fp32 in pairs: one instruction an operation for two of them
+__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(float x, float y) { return pair(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ void unpair(uint64_t p, uint32_t& x, uint32_t& y) { asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(p)); }
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&p);
 }
-// the parts of x and y that pack2(x, y) leaves
-__device__ __forceinline__ uint32_t pack2_rest(float x, float y, uint32_t hi) {
-    return pack2(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+__device__ __forceinline__ uint32_t pack2(uint64_t p) {
+    uint32_t x, y;
+    unpair(p, x, y);
+    return pack2(__uint_as_float(x), __uint_as_float(y));
+}
+// p as the sum of two bf16 pairs
+__device__ __forceinline__ void split2(uint64_t p, uint32_t& hi, uint32_t& lo) {
+    hi = pack2(p);
+    lo = pack2(add2(p, pair((hi << 16) ^ 0x80000000u, (hi & 0xffff0000u) ^ 0x80000000u)));
 }
 
 // Zero rows [n, 64) of `tiles` adjacent [64][64] tiles.
@@ -220,23 +247,24 @@ __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
 // values and a zero row of P, so that they write nothing and read nothing.
 // ---------------------------------------------------------------------------
 // Shared memory: for each half h of the key dimensions K_h and Q_h side by side (one operand of
-// 128 rows), P, A, X.  V comes in over Q, T (hi, lo) lies over A, -W over K, each when the other is
-// done with.  72 KB and 128 columns of tensor memory: three CTAs an SM.
+// 128 rows), P, A, X.  T~ (hi, lo) lies over A and -W over K, each when the other is done with.
+// 72 KB: three CTAs an SM.
 constexpr uint32_t FA_K = 0, FA_Q = T8, FA_PANEL = 2 * T8, FA_P = 4 * T8, FA_A = 5 * T8, FA_T = FA_A, FA_X = 7 * T8;
 constexpr size_t kFactorSmem = 9 * T8 + 1024;
 
 template <int DK>
 __global__ void __launch_bounds__(256, 3)
     gds_factor_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq,
-                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+                      const __grid_constant__ CUtensorMap mk) {
     constexpr int NP = DK / 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
     float* A = reinterpret_cast<float*>(smem + FA_A);
     float* X = reinterpret_cast<float*>(smem + FA_X);
-    __shared__ __align__(16) float b_s[kChunk], beta_s[kChunk], gam_s[kChunk];
-    __shared__ __align__(8) uint64_t full, vfull, mbar;
+    __shared__ __align__(16) float b_s[kChunk], beta_s[kChunk], gam_s[kChunk], dec_s[kChunk];
+    __shared__ __align__(8) uint64_t full, mbar;
     __shared__ uint32_t tmem_slot;
+    __shared__ int weak_s;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = blockIdx.x, h = blockIdx.y;
@@ -252,19 +280,18 @@ __global__ void __launch_bounds__(256, 3)
     if (t0 < 0 || t0 >= sq.len || sq.slot < 0) return;
     const int n = min(sq.len - t0, kChunk);  // tokens of the chunk
     const int64_t tok = sq.begin + t0;
-    uint8_t* fac = static_cast<uint8_t*>(a.ws) + (int64_t(c) * a.H + h) * factor_bytes(DK, a.Dv);
+    uint8_t* fac = static_cast<uint8_t*>(a.ws) + (int64_t(c) * a.H + h) * factor_bytes(DK);
 
     if (tid == 0) {
         mbar_init(smem_u32(&full), 1);
-        mbar_init(smem_u32(&vfull), 1);
         mbar_init(smem_u32(&mbar), 1);
         mbar_fence_init();
     }
-    if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 128);
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 64);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;  // [0,64) K K^T and Q K^T, then W^T; [64,128) U^T
+    const uint32_t tmem = tmem_slot;  // K K^T and Q K^T, then W^T
     if (tid == 0) {
         mbar_expect_tx(smem_u32(&full), 2 * NP * T8);
         for (int p = 0; p < NP; ++p) {
@@ -289,17 +316,24 @@ __global__ void __launch_bounds__(256, 3)
         }
         const float end = __shfl_sync(kFull, ps, 31);
         const float b[2] = {ps - g[1], ps};
+        const bool weak = __all_sync(kFull, fabsf(b[0] - end) < kWeakLimit && fabsf(b[1] - end) < kWeakLimit);
         float* gates = reinterpret_cast<float*>(fac + factor_gates(DK));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
             b_s[t] = b[i];
             beta_s[t] = be[i];
-            gam_s[t] = expf(b[i]);
-            gates[t] = a.scale * expf(b[i]);
-            gates[64 + t] = expf(end - b[i]);
+            const float out = expf(weak ? b[i] - end : b[i]), dec = expf(end - b[i]);
+            gam_s[t] = out;
+            dec_s[t] = weak ? dec : 1.f;
+            gates[t] = a.scale * out;
+            gates[kDec + t] = dec;
         }
-        if (lane == 0) gates[128] = expf(end);
+        if (lane == 0) {
+            gates[kEnd] = expf(end);
+            gates[kWeak] = weak ? 1.f : 0.f;
+            weak_s = weak;
+        }
     }
     mbar_wait(smem_u32(&full), 0);
     if (n < kChunk) {
@@ -310,14 +344,6 @@ __global__ void __launch_bounds__(256, 3)
     __syncthreads();
     tc_fence_after();
     uint32_t mph = 0;
-    const int vblocks = (a.Dv + 127) / 128;
-    // V of a block over Q (whose product is done by then)
-    auto load_v = [&](int vb) {
-        const int tiles = min((a.Dv - 128 * vb + 63) / 64, 2);
-        mbar_expect_tx(smem_u32(&vfull), tiles * T8);
-        for (int p = 0; p < tiles; ++p)
-            tma_load_3d(smem_u32(smem + FA_Q + p * FA_PANEL), &mv, 128 * vb + 64 * p, h, int(tok), smem_u32(&vfull));
-    };
     if (warp == 0) {
         if (elect()) {  // [K; Q] K^T
             const uint64_t d = sdesc(smem_u32(smem + FA_K), 16, 1024);
@@ -333,7 +359,6 @@ __global__ void __launch_bounds__(256, 3)
     mbar_wait(smem_u32(&mbar), mph);
     mph ^= 1;
     tc_fence_after();
-    if (tid == 0) load_v(0);
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t tl = tmem + (uint32_t(32 * quad) << 16) + 32 * half;
     {
@@ -363,19 +388,20 @@ __global__ void __launch_bounds__(256, 3)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 32 * half + e + i;
-                    y[i] = r <= t && t < n ? a.scale * __uint_as_float(x[e + i]) * __expf(bt - b_s[r]) : 0.f;
+                    y[i] = r <= t && t < n ? (weak_s ? __uint_as_float(x[e + i]) : __uint_as_float(x[e + i]) * __expf(bt - b_s[r])) : 0.f;
                 }
                 *reinterpret_cast<uint4*>(smem + FA_P + sw_chunk(64, t, (32 * half + e) >> 3)) = pack8(y);
             }
         }
     }
-    // K o gam over K (its products are done)
+    // K o e^b, or K o 1/dec, over K (its products are done)
 #pragma unroll
     for (int p = 0; p < NP; ++p) gdrtc::rows_scaled(smem + FA_K + p * FA_PANEL, smem + FA_K + p * FA_PANEL, gam_s, 1.f, tid);
     __syncthreads();
     halves_inverse(A, X);
-    {  // T, hi and lo: 16 columns of a row
+    {  // T~, hi and lo: 16 columns of a row
         const int t = (tid & 7) | ((tid >> 5) << 3), c0 = 16 * ((tid >> 3) & 3);
+        const float dec = dec_s[t];
         float x[16], rest[16];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -384,79 +410,54 @@ __global__ void __launch_bounds__(256, 3)
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            x[e] = c0 + e <= t ? x[e] : 0.f;
+            x[e] = c0 + e <= t ? x[e] * dec : 0.f;
             rest[e] = x[e] - __bfloat162float(__float2bfloat16_rn(x[e]));
         }
         store_row16(smem + FA_T, t, c0, x);
         store_row16(smem + FA_T + T8, t, c0, rest);
     }
-    for (int vb = 0; vb < vblocks; ++vb) {
-        mbar_wait(smem_u32(&vfull), vb & 1);
-        if (n < kChunk)
-            for (int p = 0; p < 2; ++p) zero_rows(smem + FA_Q + p * FA_PANEL, 1, n, tid, 256);
-        fence_async_smem();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (warp == 0) {
-            if (elect()) {
-                const uint64_t dt = sdesc(smem_u32(smem + FA_T), 16, 1024), dv = sdesc(smem_u32(smem + FA_Q), FA_PANEL, 1024);
-                if (vb == 0) {  // W^T = (K o gam)^T T^T, with T's high part
-                    const uint64_t dk = sdesc(smem_u32(smem + FA_K), FA_PANEL, 1024);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem, desc_plus(dk, k * 2048), desc_plus(dt, k * 32), idesc_bf16(128, 64, 1, 0), k > 0);
-                    bulk_store(fac, smem_u32(smem + FA_P), T8);
-                    bulk_commit();
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k)  // U^T = V^T T^T
-                    mma_bf16(tmem + 64, desc_plus(dv, (k & 3) * 2048), desc_plus(dt, (k >> 2) * T8 + (k & 3) * 32),
-                             idesc_bf16(128, 64, 1, 0), k > 0);
-                mma_commit(smem_u32(&mbar));
-            }
-            __syncwarp();
-        }
-        mbar_wait(smem_u32(&mbar), mph);
-        mph ^= 1;
-        tc_fence_after();
-        const int row = 32 * quad + lane;
-        uint32_t x[32];
-        if (vb == 0) {
-            tmem_ld<32>(tl, x);
-            tmem_wait_ld();
-            if (row < DK) {
-                uint8_t* w = smem + FA_K + (row >> 6) * FA_PANEL;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    *reinterpret_cast<__nv_bfloat16*>(w + sw_off(64, 32 * half + e, row & 63)) = __float2bfloat16_rn(-__uint_as_float(x[e]));
-            }
-            fence_async_smem();
-        }
-        if (tid == 0 && vb + 1 < vblocks) load_v(vb + 1);
-        tmem_ld<32>(tl + 64, x);
-        tmem_wait_ld();
-        if (row < int(u_cols(a.Dv))) {
-            float4* u = reinterpret_cast<float4*>(fac + factor_u(DK) + vb * u_bytes(a.Dv)) + row;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-                u[(8 * half + e / 4) * int(u_cols(a.Dv))] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
-                                                                    __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-        }
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (vb == 0 && warp == 0) {
-            if (elect()) {
-                for (int p = 0; p < NP; ++p) bulk_store(fac + (1 + p) * T8, smem_u32(smem + FA_K + p * FA_PANEL), T8);
-                bulk_commit();
-                bulk_wait_read();  // shared memory is read before the CTA ends
-            }
-            __syncwarp();
-        }
-    }
+    fence_async_smem();
+    tc_fence_before();
     __syncthreads();
-    if (warp == 0) tmem_dealloc(tmem, 128);
+    tc_fence_after();
+    if (warp == 0) {
+        if (elect()) {  // W^T = (K o ...)^T T~^T, with T~'s high part
+            const uint64_t dt = sdesc(smem_u32(smem + FA_T), 16, 1024), dk = sdesc(smem_u32(smem + FA_K), FA_PANEL, 1024);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mma_bf16(tmem, desc_plus(dk, k * 2048), desc_plus(dt, k * 32), idesc_bf16(128, 64, 1, 0), k > 0);
+            mma_commit(smem_u32(&mbar));
+            bulk_store(fac, smem_u32(smem + FA_T), 2 * T8);
+            bulk_store(fac + 2 * T8, smem_u32(smem + FA_P), T8);
+            bulk_commit();
+        }
+        __syncwarp();
+    }
+    mbar_wait(smem_u32(&mbar), mph);
+    tc_fence_after();
+    const int row = 32 * quad + lane;
+    uint32_t x[32];
+    tmem_ld<32>(tl, x);
+    tmem_wait_ld();
+    if (row < DK) {
+        uint8_t* w = smem + FA_K + (row >> 6) * FA_PANEL;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            *reinterpret_cast<__nv_bfloat16*>(w + sw_off(64, 32 * half + e, row & 63)) = __float2bfloat16_rn(-__uint_as_float(x[e]));
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) {
+        if (elect()) {
+            for (int p = 0; p < NP; ++p) bulk_store(fac + (3 + p) * T8, smem_u32(smem + FA_K + p * FA_PANEL), T8);
+            bulk_commit();
+            bulk_wait_read();  // shared memory is read before the CTA ends
+        }
+        __syncwarp();
+        tmem_dealloc(tmem, 64);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -464,24 +465,25 @@ __global__ void __launch_bounds__(256, 3)
 // ---------------------------------------------------------------------------
 constexpr int kGroups = 4;                            // chain groups of four warps
 constexpr int kWalkThreads = (4 * kGroups + 6) * 32;  // and four output warps, the products', the copies'
-constexpr int kGateRing = 4;
+constexpr int kGateRing = 8;
 
 template <int DK>
 struct WalkSmem {
     static constexpr int NP = DK / 64;
-    // two of each piece, every one with barriers of its own: U, W, K, Q with P
-    static constexpr uint32_t U = 0, u = 4 * T8, W = U + 2 * u, w = NP * T8, K = W + 2 * w, k = NP * T8, QP = K + 2 * k,
-                              qp = (NP + 1) * T8, GATES = QP + 2 * qp;
+    // two of each piece: V with T~, W, K, Q, P; then the outputs' staging and the gates
+    static constexpr uint32_t VT = 0, vt = 4 * T8, W = VT + 2 * vt, w = NP * T8, K = W + 2 * w, k = NP * T8, Q = K + 2 * k,
+                              q = NP * T8, P = Q + 2 * q, OUT = P + 2 * T8, GATES = OUT + 2 * T8;
     static constexpr size_t bytes = GATES + kGateRing * kGateBytes + 1024;
 };
 static_assert(WalkSmem<128>::bytes <= 227 * 1024, "shared memory of a CTA");
 
-// Tensor-memory columns: A operands (bf16 pairs), then fp32 accumulators.
-constexpr uint32_t TM_S = 0, TM_DTH = 64, TM_DTL = 96, TM_DH = 128, TM_DL = 160, TM_D = 192, TM_X = 256, TM_O1 = 384,
-                   TM_O2 = 448;
+// Tensor-memory columns: A operands (bf16 pairs), then fp32 accumulators: D, the state, O twice.
+constexpr uint32_t TM_S = 0, TM_DTH = 64, TM_DTL = 96, TM_DH = 128, TM_DL = 160, TM_D = 192, TM_X = 256, TM_O = 384;
 
-// A bounded wait; after one that ran out the others of this thread give up soon.  The clock is
-// read once in 64 polls: a read between two polls would delay the chain by its own latency.
+// A converged warp's bounded wait; after one that ran out its others give up soon.  Every lane waits:
+// try_wait then suspends the warp until the phase ends (some 60 cycles from the arrival to the next
+// instruction), while a single lane's polls come back at once, take 200 to 350 cycles to notice and
+// slow the products down.  The clock is read once in 64 polls.
 __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& dead) {
     const uint32_t b = smem_u32(bar);
     uint64_t t0 = 0;
@@ -492,9 +494,10 @@ __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& dead)
         if (t - t0 > (dead ? 1000ull * 1000 : kWaitLimitNs)) {
             atomicExch(&g_timeout_flag, 1);
             dead = true;
-            return;
+            break;
         }
     }
+    __syncwarp();
 }
 // One arrival of a warp after its tensor-memory or shared-memory work.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -503,17 +506,15 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 
 struct WalkBars {
-    uint64_t u_full[2], u_free[2], w_full[2], w_free[2], k_full[2], k_free[2], qp_full[2], qp_free[2];
+    uint64_t vt_full[2], vt_free[2], wkq_full[2], w_free[2], k_free[2], q_free[2], p_full[2], p_free[2];
     uint64_t gates[kGateRing];
-    uint64_t s_ready[2], x_done[2], dt_ready, d_ready, d_done, o_done, o_free, fixed;
+    uint64_t s_ready[2], x_done[2], o_done[2], o_free[2], dt_ready, d_ready, d_done, fixed;
 };
 
-// RQ: quadrants of tensor-memory lanes in use, of 32 value columns each (the warps of the others
-// leave at once).
-template <int DK, int RQ, typename TS>
+template <int DK, typename TS>
 __global__ void __launch_bounds__(kWalkThreads, 1)
-    gds_walk_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq,
-                    const __grid_constant__ CUtensorMap mk) {
+    gds_walk_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
     constexpr int NP = DK / 64;
     constexpr int GC = DK / kGroups;       // state rows (columns of tensor memory) of a group
     constexpr int GT = kChunk / kGroups;   // tokens of a group
@@ -524,9 +525,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     __shared__ uint32_t tmem_slot;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kCols = 32 * RQ;
-    const int blocks = (a.Dv + kCols - 1) / kCols;
-    const int h = blockIdx.x / blocks, v0 = (blockIdx.x % blocks) * kCols, nv = min(a.Dv - v0, kCols);
+    const int blocks = (a.Dv + 127) / 128;
+    const int h = blockIdx.x / blocks, v0 = (blockIdx.x % blocks) * 128, nv = min(a.Dv - v0, 128);
     const Seq sq = sequence(a, blockIdx.y);
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + v0;
     const int64_t os = int64_t(a.H) * a.Dv;
@@ -543,22 +543,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     }
     const int chunks = (sq.len + kChunk - 1) / kChunk, last = sq.len - (chunks - 1) * kChunk;
     const bool ragged = last < kChunk;
+    const int quads = (nv + 31) / 32;  // quadrants of tensor-memory lanes with columns
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            for (uint64_t* b : {&bar.u_full[i], &bar.w_full[i], &bar.w_free[i], &bar.k_full[i], &bar.k_free[i],
-                                &bar.qp_full[i], &bar.qp_free[i], &bar.x_done[i]})
+            for (uint64_t* b : {&bar.vt_full[i], &bar.vt_free[i], &bar.w_free[i], &bar.k_free[i], &bar.q_free[i], &bar.p_full[i],
+                                &bar.p_free[i], &bar.x_done[i], &bar.o_done[i]})
                 mbar_init(smem_u32(b), 1);
-            mbar_init(smem_u32(&bar.u_free[i]), RQ * kGroups);
+            mbar_init(smem_u32(&bar.wkq_full[i]), 3);
+            mbar_init(smem_u32(&bar.s_ready[i]), quads * kGroups / 2);
+            mbar_init(smem_u32(&bar.o_free[i]), quads);
         }
         for (int i = 0; i < kGateRing; ++i) mbar_init(smem_u32(&bar.gates[i]), 1);
-        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bar.s_ready[i]), RQ * kGroups / 2);
-        mbar_init(smem_u32(&bar.dt_ready), RQ * kGroups);
-        mbar_init(smem_u32(&bar.d_ready), RQ * kGroups);
+        mbar_init(smem_u32(&bar.dt_ready), quads * kGroups);
+        mbar_init(smem_u32(&bar.d_ready), quads * kGroups);
         mbar_init(smem_u32(&bar.d_done), 1);
-        mbar_init(smem_u32(&bar.o_done), 1);
-        mbar_init(smem_u32(&bar.o_free), RQ);
-        mbar_init(smem_u32(&bar.fixed), RQ * kGroups);
+        mbar_init(smem_u32(&bar.fixed), quads * kGroups);
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 512);
@@ -567,154 +567,228 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     bool dead = false;
+    auto gates_of = [&](int c) {  // the chunk's gates, once they are there
+        wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, dead);
+        return reinterpret_cast<const float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
+    };
 
-    if (warp < 4 * kGroups + 4 && (warp & 3) >= RQ) {
+    if (warp < 4 * kGroups + 4 && (warp & 3) >= quads) {
         // no columns
     } else if (warp < 4 * kGroups) {
         // ---- the chain: a lane is a value column, a group a quarter of the state's rows and of the tokens
         const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
         const bool live = row < nv;
-        float S[GC];
         TS* mine = st + int64_t(grp * GC) * a.Dv + row;
 #pragma unroll
-        for (int i = 0; i < GC; ++i) S[i] = live && !sq.fresh ? to_f32(mine[int64_t(i) * a.Dv]) : 0.f;
-        float end = 1.f;
-        for (int c = 0; c <= chunks; ++c) {
+        for (int j = 0; j < GC; j += 16) {
+            uint32_t x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(live && !sq.fresh ? to_f32(mine[int64_t(j + i) * a.Dv]) : 0.f);
+            tmem_st<16>(tl + TM_X + grp * GC + j, x);
+        }
+        tmem_wait_st();
+        for (int c = 0; c < chunks; ++c) {
             if (c == chunks - 1 && ragged) {
-                // keys past the sequence's end are other tokens': they must not meet a zero of D~ as NaN
-                wait(&bar.k_full[c & 1], (c >> 1) & 1, dead);
-                const int at = (grp * RQ + (warp & 3)) * 32 + lane;
-                zero_rows(smem + L::K + (c & 1) * L::k, NP, last, at, 32 * RQ * kGroups);
+                // rows past the sequence's end are other tokens': they must not meet a zero of D~ or T~ as NaN
+                wait(&bar.vt_full[c & 1], (c >> 1) & 1, dead);
+                wait(&bar.wkq_full[c & 1], (c >> 1) & 1, dead);
+                const int at = (grp * quads + (warp & 3)) * 32 + lane;
+                zero_rows(smem + L::VT + (c & 1) * L::vt, 2, last, at, 32 * quads * kGroups);
+                zero_rows(smem + L::K + (c & 1) * L::k, NP, last, at, 32 * quads * kGroups);
                 fence_async_smem();
                 warp_arrive(&bar.fixed, lane);
             }
+            const float* gates = gates_of(c);
+            const bool weak = gates[kWeak] != 0.f;
+            const uint64_t end = pair(gates[kEnd], gates[kEnd]);
             if (c > 0) {
-                wait(&bar.x_done[grp >> 1], (c - 1) & 1, dead);
+                wait(&bar.x_done[2 * grp / kGroups], (c - 1) & 1, dead);
                 tc_fence_after();
+            }
+            {  // S~ = e^{b_63} S, to accumulate on; and S~ (or S) rounded, as an operand
                 uint32_t x[GC];
                 tmem_ld<GC>(tl + TM_X + grp * GC, x);
                 tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < GC; ++i) S[i] = fmaf(end, S[i], __uint_as_float(x[i]));
-                if (c == chunks) break;
-            }
-            {
                 uint32_t p[GC / 2];
 #pragma unroll
-                for (int i = 0; i < GC / 2; ++i) p[i] = pack2(S[2 * i], S[2 * i + 1]);
+                for (int i = 0; i < GC / 2; ++i) {
+                    const uint64_t s = pair(x[2 * i], x[2 * i + 1]), d = mul2(s, end);
+                    p[i] = pack2(weak ? d : s);
+                    unpair(d, x[2 * i], x[2 * i + 1]);
+                }
                 tmem_st<GC / 2>(tl + TM_S + grp * (GC / 2), p);
+                tmem_st<GC>(tl + TM_X + grp * GC, x);
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(&bar.s_ready[grp >> 1], lane);
+                warp_arrive(&bar.s_ready[2 * grp / kGroups], lane);
             }
-            const float* gates = reinterpret_cast<const float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
-            const float4* u = reinterpret_cast<const float4*>(smem + L::U + (c & 1) * L::u) + GT / 4 * grp * kCols + row;
-            wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, dead);
-            end = gates[128];
-            wait(&bar.u_full[c & 1], (c >> 1) & 1, dead);
             wait(&bar.d_done, c & 1, dead);
             tc_fence_after();
             uint32_t x[GT], hi[GT / 2], lo[GT / 2];
             tmem_ld<GT>(tl + TM_D + GT * grp, x);
             tmem_wait_ld();
+            if (!weak) {  // D~ from D
 #pragma unroll
-            for (int i = 0; i < GT; i += 4) {  // D = U - W S; D~, which the chain waits for, first
-                const float4 y = u[i / 4 * kCols];
-                const float4 e = *reinterpret_cast<const float4*>(gates + 64 + GT * grp + i);
-                const float d0 = __uint_as_float(x[i]) + y.x, d1 = __uint_as_float(x[i + 1]) + y.y;
-                const float d2 = __uint_as_float(x[i + 2]) + y.z, d3 = __uint_as_float(x[i + 3]) + y.w;
-                x[i] = __float_as_uint(d0), x[i + 1] = __float_as_uint(d1), x[i + 2] = __float_as_uint(d2), x[i + 3] = __float_as_uint(d3);
-                hi[i / 2] = pack2(d0 * e.x, d1 * e.y);
-                lo[i / 2] = pack2_rest(d0 * e.x, d1 * e.y, hi[i / 2]);
-                hi[i / 2 + 1] = pack2(d2 * e.z, d3 * e.w);
-                lo[i / 2 + 1] = pack2_rest(d2 * e.z, d3 * e.w, hi[i / 2 + 1]);
+                for (int i = 0; i < GT; i += 4) {
+                    const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(gates + kDec + GT * grp + i);
+                    split2(mul2(pair(x[i], x[i + 1]), e.x), hi[i / 2], lo[i / 2]);
+                    split2(mul2(pair(x[i + 2], x[i + 3]), e.y), hi[i / 2 + 1], lo[i / 2 + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < GT / 2; ++i) split2(pair(x[2 * i], x[2 * i + 1]), hi[i], lo[i]);
             }
-            tmem_st<GT / 2>(tl + TM_DTH + GT / 2 * grp, hi);
-            tmem_st<GT / 2>(tl + TM_DTL + GT / 2 * grp, lo);
+            // two buffers, since P D~ of a chunk is formed in the next chunk's pauses; a chunk of strong
+            // decay takes both
+            const uint32_t dt = tl + (weak && (c & 1) ? TM_DH : TM_DTH) + GT / 2 * grp;
+            tmem_st<GT / 2>(dt, hi);
+            tmem_st<GT / 2>(dt + TM_DTL - TM_DTH, lo);
             tmem_wait_st();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&bar.dt_ready));
-                mbar_arrive(smem_u32(&bar.u_free[c & 1]));
-            }
+            warp_arrive(&bar.dt_ready, lane);
+            if (!weak) {  // and D itself, for P D
 #pragma unroll
-            for (int i = 0; i < GT / 2; ++i) {
-                const float v = __uint_as_float(x[2 * i]), w = __uint_as_float(x[2 * i + 1]);
-                hi[i] = pack2(v, w);
-                lo[i] = pack2_rest(v, w, hi[i]);
+                for (int i = 0; i < GT / 2; ++i) split2(pair(x[2 * i], x[2 * i + 1]), hi[i], lo[i]);
+                tmem_st<GT / 2>(tl + TM_DH + GT / 2 * grp, hi);
+                tmem_st<GT / 2>(tl + TM_DL + GT / 2 * grp, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(&bar.d_ready, lane);
             }
-            tmem_st<GT / 2>(tl + TM_DH + GT / 2 * grp, hi);
-            tmem_st<GT / 2>(tl + TM_DL + GT / 2 * grp, lo);
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(&bar.d_ready, lane);
         }
+        wait(&bar.x_done[2 * grp / kGroups], (chunks - 1) & 1, dead);
+        tc_fence_after();
+        uint32_t x[GC];
+        tmem_ld<GC>(tl + TM_X + grp * GC, x);
+        tmem_wait_ld();
         if (live) {
 #pragma unroll
-            for (int i = 0; i < GC; ++i) mine[int64_t(i) * a.Dv] = from_f32<TS>(S[i]);
+            for (int i = 0; i < GC; ++i) mine[int64_t(i) * a.Dv] = from_f32<TS>(__uint_as_float(x[i]));
         }
         tc_fence_before();
     } else if (warp < 4 * kGroups + 4) {
-        // ---- the outputs: a lane is a value column, so a warp stores 64 bytes of a token at a time
+        // ---- the outputs: a lane is a value column; whole chunks leave as tiles, the last one by rows
         const int w = warp & 3, row = 32 * w + lane;
-        const uint32_t tl = tmem + (uint32_t(32 * w) << 16);
-        __nv_bfloat16* mine = o + row;
+        const uint32_t tl = tmem + (uint32_t(32 * w) << 16) + TM_O;
+        uint8_t* tile = smem + L::OUT;
         for (int c = 0; c < chunks; ++c) {
-            const float* gam = reinterpret_cast<const float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
-            wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, dead);
-            wait(&bar.o_done, c & 1, dead);
+            const float* gates = gates_of(c);
+            const bool weak = gates[kWeak] != 0.f;
+            const int b = c & 1;
+            wait(&bar.o_done[b], (c >> 1) & 1, dead);
             tc_fence_after();
             uint32_t y[kChunk / 2];
 #pragma unroll
-            for (int j = 0; j < kChunk; j += 16) {
-                uint32_t p[16], q[16];
-                tmem_ld<16>(tl + TM_O1 + j, p);
-                tmem_ld<16>(tl + TM_O2 + j, q);
+            for (int j = 0; j < kChunk; j += 32) {
+                uint32_t p[32];
+                tmem_ld<32>(tl + 64 * b + j, p);
                 tmem_wait_ld();
+                if (weak) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 2)
-                    y[(j + i) / 2] = pack2(fmaf(gam[j + i], __uint_as_float(p[i]), __uint_as_float(q[i])),
-                                           fmaf(gam[j + i + 1], __uint_as_float(p[i + 1]), __uint_as_float(q[i + 1])));
+                    for (int i = 0; i < 32; i += 4) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(gates + j + i);
+                        y[(j + i) / 2] = pack2(mul2(f.x, pair(p[i], p[i + 1])));
+                        y[(j + i) / 2 + 1] = pack2(mul2(f.y, pair(p[i + 2], p[i + 3])));
+                    }
+                } else {  // e^b o (Q S) in this chunk's accumulator, P D in the other one
+#pragma unroll
+                    for (int i0 = 0; i0 < 32; i0 += 16) {
+                        uint32_t q[16];
+                        tmem_ld<16>(tl + 64 * (b ^ 1) + j + i0, q);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float u = fmaf(gates[j + i0 + i], __uint_as_float(p[i0 + i]), a.scale * __uint_as_float(q[i]));
+                            const float v = fmaf(gates[j + i0 + i + 1], __uint_as_float(p[i0 + i + 1]), a.scale * __uint_as_float(q[i + 1]));
+                            y[(j + i0 + i) / 2] = pack2(u, v);
+                        }
+                    }
+                }
             }
             tc_fence_before();
-            warp_arrive(&bar.o_free, lane);  // the accumulators and the decays have been read
-            const int n = row < nv ? (c == chunks - 1 ? last : kChunk) : 0;
-            uint16_t* to = reinterpret_cast<uint16_t*>(mine);
-            if (n == kChunk) {
+            warp_arrive(&bar.o_free[b], lane);  // the accumulators and the decays have been read
+            // the store of the chunk before has read the staging
+            if (warp == 4 * kGroups && lane == 0) bulk_wait_read();
+            asm volatile("bar.sync 1, %0;" ::"r"(32 * quads) : "memory");
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i) to[i * os] = uint16_t(i & 1 ? y[i / 2] >> 16 : y[i / 2] & 0xffffu);
+            for (int i = 0; i < kChunk; ++i)
+                *reinterpret_cast<uint16_t*>(tile + (row >> 6) * T8 + sw_off(64, i, row & 63)) =
+                    uint16_t(i & 1 ? y[i / 2] >> 16 : y[i / 2] & 0xffffu);
+            const bool whole = c < chunks - 1 || !ragged;
+            if (whole) fence_async_smem();
+            asm volatile("bar.sync 1, %0;" ::"r"(32 * quads) : "memory");
+            if (whole) {
+                if (warp == 4 * kGroups && lane == 0) {
+                    for (int p = 0; p < (nv + 63) / 64; ++p)
+                        tma_store_3d(&mo, smem_u32(tile + p * T8), v0 + 64 * p, h, sq.begin + c * kChunk);
+                    bulk_commit();
+                }
             } else {
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i)
-                    if (i < n) to[i * os] = uint16_t(i & 1 ? y[i / 2] >> 16 : y[i / 2] & 0xffffu);
+                for (int i = (warp & 3) * 32 + lane; i < last * 16; i += 32 * quads) {
+                    const int t = i >> 4, e = (i & 15) * 8;
+                    if (e < nv)
+                        *reinterpret_cast<uint4*>(o + (int64_t(c) * kChunk + t) * os + e) =
+                            *reinterpret_cast<const uint4*>(tile + sw_chunk(64, t, e >> 3));
+                }
             }
-            mine += kChunk * os;
         }
+        if (warp == 4 * kGroups && lane == 0) bulk_wait_read();  // shared memory is read before the CTA ends
     } else if (warp == 4 * kGroups + 4) {
         // ---- the products.  The whole warp walks the loop and one elected lane issues, so that
         // descriptors stay in uniform registers: 30 cycles a product of N = 64 instead of 45 to 80
         // from inside a one-lane branch (measured with 8 to 64 in a row).
         const uint32_t base = smem_u32(smem);
-        constexpr uint32_t kTS = idesc_bf16(128, 64, 0, 0), kTX = idesc_bf16(128, DK / 2, 0, 1);
-        for (int c = 0; c < chunks; ++c) {
-            const int i = c & 1, ph = (c >> 1) & 1;
-            const uint64_t dw = sdesc(base + L::W + i * L::w, 16, 1024), dk = sdesc(base + L::K + i * L::k, T8, 1024);
-            const uint64_t dq = sdesc(base + L::QP + i * L::qp, 16, 1024), dp = desc_plus(dq, NP * T8);
-            // (a wait that passes costs some 100 cycles: the copies are waited for ahead of the chain)
-            wait(&bar.w_full[i], ph, dead);
-            wait(&bar.qp_full[i], ph, dead);
-            wait(&bar.k_full[i], ph, dead);
-            if (c > 0) wait(&bar.o_free, (c - 1) & 1, dead);
+        constexpr uint32_t kTV = idesc_bf16(128, 64, 1, 0), kTS = idesc_bf16(128, 64, 0, 0), kTX = idesc_bf16(128, DK / 2, 0, 1);
+        // D^T = V^T T~^T of chunk c (T~ as the sum of two)
+        auto tv = [&](int c) {
+            wait(&bar.vt_full[c & 1], (c >> 1) & 1, dead);
+            if (c == chunks - 1 && ragged) wait(&bar.fixed, 0, dead);
+            tc_fence_after();
+            const uint32_t s = base + L::VT + (c & 1) * L::vt;
+            const uint64_t dv = sdesc(s, T8, 1024), dt = sdesc(s + 2 * T8, 16, 1024);
+            if (elect()) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {  // D^T = U^T - S^T W^T without U, half of the state's rows as they come
+                for (int k = 0; k < 8; ++k)
+                    mma_bf16(tmem + TM_D, desc_plus(dv, (k & 3) * 2048), desc_plus(dt, (k >> 2) * T8 + (k & 3) * 32), kTV, k > 0);
+                mma_commit(smem_u32(&bar.vt_free[c & 1]));
+            }
+            __syncwarp();
+        };
+        // O^T += D~^T P^T of chunk c (or D^T P^T on its own)
+        auto pd = [&](int c, bool weak) {
+            const int i = c & 1;
+            wait(&bar.p_full[i], (c >> 1) & 1, dead);
+            tc_fence_after();
+            const uint64_t dp = sdesc(base + L::P + i * T8, 16, 1024);
+            const uint32_t d = tmem + (weak && !i ? TM_DTH : TM_DH), to = tmem + TM_O + 64 * (weak ? i : i ^ 1);
+            if (elect()) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(to, d + (k < 4 ? 0u : TM_DTL - TM_DTH) + 8 * (k & 3), desc_plus(dp, (k & 3) * 32), kTS, weak || k > 0);
+                mma_commit(smem_u32(&bar.p_free[i]));
+                mma_commit(smem_u32(&bar.o_done[i]));
+            }
+            __syncwarp();
+        };
+        tv(0);
+        uint32_t strong = 0;  // chunks of strong decay so far
+        bool weak = gates_of(0)[kWeak] != 0.f, was_weak = true, pending = false;
+        wait(&bar.wkq_full[0], 0, dead);
+        for (int c = 0; c < chunks; ++c) {
+            const int i = c & 1;
+            const uint64_t dw = sdesc(base + L::W + i * L::w, 16, 1024), dk = sdesc(base + L::K + i * L::k, T8, 1024);
+            const uint64_t dq = sdesc(base + L::Q + i * L::q, 16, 1024);
+            if (pending && !weak) pd(c - 1, true);  // its D~ is about to be overwritten
+            pending = pending && weak;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {  // D^T -= S^T W^T, half of the state's rows as they come
                 wait(&bar.s_ready[g], c & 1, dead);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
                     for (int k = g * (DK / 32); k < (g + 1) * (DK / 32); ++k)
-                        mma_ts(tmem + TM_D, tmem + TM_S + 8 * k, desc_plus(dw, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
+                        mma_ts(tmem + TM_D, tmem + TM_S + 8 * k, desc_plus(dw, (k >> 2) * T8 + (k & 3) * 32), kTS, 1);
                     if (g == 1) {
                         mma_commit(smem_u32(&bar.d_done));
                         mma_commit(smem_u32(&bar.w_free[i]));
@@ -722,88 +796,104 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 }
                 __syncwarp();
             }
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k)  // O1^T = S^T Q^T
-                    mma_ts(tmem + TM_O1, tmem + TM_S + 8 * k, desc_plus(dq, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
-            }
-            __syncwarp();
-            wait(&bar.dt_ready, c & 1, dead);
-            if (c == chunks - 1 && ragged) wait(&bar.fixed, 0, dead);
+            // while the chain reads D: P D~ of the chunk before, and O^T = S^T Q^T of this one.  O has two
+            // accumulators, taken in turn; a chunk of strong decay takes both
+            if (pending) pd(c - 1, true);
+            if (c > 1) wait(&bar.o_free[i], ((c - 2) >> 1) & 1, dead);
+            if (c > 0 && !(weak && was_weak)) wait(&bar.o_free[i ^ 1], ((c - 1) >> 1) & 1, dead);
             tc_fence_after();
             if (elect()) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {  // X^T = D~^T K, half of the columns at a time
+                for (int k = 0; k < DK / 16; ++k)
+                    mma_ts(tmem + TM_O + 64 * i, tmem + TM_S + 8 * k, desc_plus(dq, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
+                mma_commit(smem_u32(&bar.q_free[i]));
+            }
+            __syncwarp();
+            wait(&bar.dt_ready, c & 1, dead);
+            tc_fence_after();
+            if (elect()) {
+                const uint32_t d = tmem + (weak && i ? TM_DH : TM_DTH);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {  // S^T += D~^T K, half of the columns at a time
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + TM_X + g * (DK / 2), tmem + (k < 4 ? TM_DTH : TM_DTL) + 8 * (k & 3),
-                               desc_plus(dk, (DK == 128 ? g * T8 : g * 64) + (k & 3) * 2048), kTX, k > 0);
+                        mma_ts(tmem + TM_X + g * (DK / 2), d + (k < 4 ? 0u : TM_DTL - TM_DTH) + 8 * (k & 3),
+                               desc_plus(dk, (DK == 128 ? g * T8 : g * 64) + (k & 3) * 2048), kTX, 1);
                     if (g == 1) mma_commit(smem_u32(&bar.k_free[i]));
                     mma_commit(smem_u32(&bar.x_done[g]));
                 }
             }
             __syncwarp();
-            wait(&bar.d_ready, c & 1, dead);
-            tc_fence_after();
+            pending = weak;
+            if (!weak) {
+                wait(&bar.d_ready, strong & 1, dead);
+                ++strong;
+                pd(c, false);
+            }
+            // while the chain reads the state: the next chunk's T~ V, and the waits for its pieces
+            was_weak = weak;
+            if (c + 1 < chunks) {
+                tv(c + 1);
+                weak = gates_of(c + 1)[kWeak] != 0.f;
+                wait(&bar.wkq_full[i ^ 1], ((c + 1) >> 1) & 1, dead);
+            }
+        }
+        if (pending) pd(chunks - 1, true);
+        wait(&bar.x_done[1], (chunks - 1) & 1, dead);
+        wait(&bar.o_done[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, dead);
+    } else {
+        // ---- the copies: each piece of chunk c once the products that read chunk c - 2's are done
+        const uint32_t base = smem_u32(smem), vt = (nv + 63) / 64;
+        const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y)) * a.H + h) * factor_bytes(DK);
+        for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * factor_bytes(DK)) {
+            const int i = c & 1, ph = ((c >> 1) & 1) ^ 1, tok = sq.begin + c * kChunk;
+            wait(&bar.vt_free[i], ph, dead);
             if (elect()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)  // O2^T = D^T P^T
-                    mma_ts(tmem + TM_O2, tmem + (k < 4 ? TM_DH : TM_DL) + 8 * (k & 3), desc_plus(dp, (k & 3) * 32), kTS, k > 0);
-                mma_commit(smem_u32(&bar.qp_free[i]));
-                mma_commit(smem_u32(&bar.o_done));
+                const uint32_t b = smem_u32(&bar.vt_full[i]), s = base + L::VT + i * L::vt;
+                mbar_expect_tx(b, (vt + 2) * T8);
+                for (uint32_t p = 0; p < vt; ++p) tma_load_3d(s + p * T8, &mv, v0 + 64 * p, h, tok, b);
+                bulk_load(s + 2 * T8, fac, 2 * T8, b);
+                // the gates of chunk c - 8 are read: the products have waited for the outputs of chunk c - 5
+                const uint32_t g = smem_u32(&bar.gates[c % kGateRing]);
+                mbar_expect_tx(g, kGateBytes);
+                bulk_load(base + L::GATES + (c % kGateRing) * kGateBytes, fac + factor_gates(DK), kGateBytes, g);
+            }
+            __syncwarp();
+            const uint32_t b = smem_u32(&bar.wkq_full[i]);
+            wait(&bar.w_free[i], ph, dead);
+            if (elect()) {
+                mbar_expect_tx(b, NP * T8);
+                bulk_load(base + L::W + i * L::w, fac + 3 * T8, NP * T8, b);
+            }
+            __syncwarp();
+            wait(&bar.q_free[i], ph, dead);
+            if (elect()) {
+                mbar_expect_tx(b, NP * T8);
+                for (int p = 0; p < NP; ++p) tma_load_3d(base + L::Q + i * L::q + p * T8, &mq, 64 * p, h / a.hdiv, tok, b);
+            }
+            __syncwarp();
+            wait(&bar.k_free[i], ph, dead);
+            if (elect()) {
+                mbar_expect_tx(b, NP * T8);
+                for (int p = 0; p < NP; ++p) tma_load_3d(base + L::K + i * L::k + p * T8, &mk, 64 * p, h / a.hdiv, tok, b);
+            }
+            __syncwarp();
+            wait(&bar.p_free[i], ph, dead);
+            if (elect()) {
+                const uint32_t pb = smem_u32(&bar.p_full[i]);
+                mbar_expect_tx(pb, T8);
+                bulk_load(base + L::P + i * T8, fac + 2 * T8, T8, pb);
             }
             __syncwarp();
         }
-        wait(&bar.x_done[1], (chunks - 1) & 1, dead);
-        wait(&bar.o_done, (chunks - 1) & 1, dead);
-    } else {
-        // ---- the copies: each piece of chunk c once the products that read chunk c - 2's are done
-        if (lane == 0) {
-            const uint32_t base = smem_u32(smem), ucols = u_cols(a.Dv), fb = factor_bytes(DK, a.Dv);
-            const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y)) * a.H + h) * fb;
-            const uint32_t uat = factor_u(DK) + (v0 / 128) * u_bytes(a.Dv) + (v0 % 128) * 16;
-            for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * fb) {
-                const int i = c & 1, ph = ((c >> 1) & 1) ^ 1, tok = sq.begin + c * kChunk;
-                uint32_t b, s;
-                wait(&bar.w_free[i], ph, dead);
-                b = smem_u32(&bar.w_full[i]);
-                mbar_expect_tx(b, NP * T8);
-                bulk_load(base + L::W + i * L::w, fac + T8, NP * T8, b);
-                // the gates of chunk c - 4 are read: W S of chunk c - 2 is done, which follows
-                b = smem_u32(&bar.gates[c % kGateRing]);
-                mbar_expect_tx(b, kGateBytes);
-                bulk_load(base + L::GATES + (c % kGateRing) * kGateBytes, fac + factor_gates(DK), kGateBytes, b);
-                wait(&bar.u_free[i], ph, dead);
-                b = smem_u32(&bar.u_full[i]), s = base + L::U + i * L::u;
-                // (columns past Dv are the factors' padding)
-                const uint32_t wide = min(uint32_t(kCols), ucols - v0 % 128);
-                mbar_expect_tx(b, kChunk * 4 * wide);
-                if (wide == ucols && wide == kCols) {
-                    bulk_load(s, fac + uat, kChunk * 4 * wide, b);
-                } else {
-                    for (int g = 0; g < kChunk / 4; ++g) bulk_load(s + g * kCols * 16, fac + uat + g * ucols * 16, wide * 16, b);
-                }
-                wait(&bar.k_free[i], ph, dead);
-                b = smem_u32(&bar.k_full[i]);
-                mbar_expect_tx(b, NP * T8);
-                for (int p = 0; p < NP; ++p) tma_load_3d(base + L::K + i * L::k + p * T8, &mk, 64 * p, h / a.hdiv, tok, b);
-                wait(&bar.qp_free[i], ph, dead);
-                b = smem_u32(&bar.qp_full[i]), s = base + L::QP + i * L::qp;
-                mbar_expect_tx(b, (NP + 1) * T8);
-                for (int p = 0; p < NP; ++p) tma_load_3d(s + p * T8, &mq, 64 * p, h / a.hdiv, tok, b);
-                bulk_load(s + NP * T8, fac, T8, b);
-            }
-            // no copy outlives the CTA
-            for (int c = max(chunks - 2, 0); c < chunks; ++c) {
-                const int i = c & 1, ph = (c >> 1) & 1;
-                wait(&bar.u_full[i], ph, dead);
-                wait(&bar.w_full[i], ph, dead);
-                wait(&bar.k_full[i], ph, dead);
-                wait(&bar.qp_full[i], ph, dead);
-                wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, dead);
-            }
+        // no copy outlives the CTA
+        for (int c = max(chunks - 2, 0); c < chunks; ++c) {
+            const int i = c & 1, ph = (c >> 1) & 1;
+            wait(&bar.vt_full[i], ph, dead);
+            wait(&bar.wkq_full[i], ph, dead);
+            wait(&bar.p_full[i], ph, dead);
+            gates_of(c);
         }
-        __syncwarp();
     }
     __syncthreads();
     tc_fence_after();
@@ -831,26 +921,20 @@ rm_status fail(const char* what, bool map) {
 
 template <int DK>
 rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
+    const int64_t ostr[2] = {int64_t(a.H) * a.Dv, a.Dv};
     if (!map_of(&mq, a.q, DK, a.H / a.hdiv, a.N, a.qs)) return fail("q", true);
     if (!map_of(&mk, a.k, DK, a.H / a.hdiv, a.N, a.ks)) return fail("k", true);
     if (!map_of(&mv, a.v, a.Dv, a.H, a.N, a.vs)) return fail("v", true);
+    if (!map_of(&mo, a.o, a.Dv, a.H, a.N, ostr)) return fail("o", true);
     auto ff = gds_factor_kernel<DK>;
     if (!set_smem(ff, kFactorSmem)) return fail("shared-memory attribute of the factors", false);
-    ff<<<dim3(unsigned(chunk_slots(a)), unsigned(a.H)), 256, kFactorSmem, s>>>(a, mq, mk, mv);
+    ff<<<dim3(unsigned(chunk_slots(a)), unsigned(a.H)), 256, kFactorSmem, s>>>(a, mq, mk);
     note_launch(1);
     if (!launch_ok()) return fail("launch of the factors", false);
-    // Few sequences and heads leave multiprocessors idle: their CTAs take fewer columns then, which
-    // shortens the chain's arithmetic (the products take as long for 32 columns as for 128).
-    const int64_t wide = int64_t((a.Dv + 127) / 128) * a.H * a.S, sms = sm_count();
-    const int rq = a.Dv <= 32 || wide * 4 <= sms ? 1 : a.Dv <= 64 || wide * 2 <= sms ? 2 : 4;
-    const bool f = state_dt == RM_F32;
-    auto fw = rq == 1   ? (f ? gds_walk_kernel<DK, 1, float> : gds_walk_kernel<DK, 1, __nv_bfloat16>)
-              : rq == 2 ? (f ? gds_walk_kernel<DK, 2, float> : gds_walk_kernel<DK, 2, __nv_bfloat16>)
-                        : (f ? gds_walk_kernel<DK, 4, float> : gds_walk_kernel<DK, 4, __nv_bfloat16>);
+    auto fw = state_dt == RM_F32 ? gds_walk_kernel<DK, float> : gds_walk_kernel<DK, __nv_bfloat16>;
     if (!set_smem(fw, WalkSmem<DK>::bytes)) return fail("shared-memory attribute of the walk", false);
-    const int cols = 32 * rq;
-    fw<<<dim3(unsigned((a.Dv + cols - 1) / cols * a.H), unsigned(a.S)), kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, mq, mk);
+    fw<<<dim3(unsigned((a.Dv + 127) / 128 * a.H), unsigned(a.S)), kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, mq, mk, mv, mo);
     note_launch(1);
     if (!launch_ok()) return fail("launch of the walk", false);
     return RM_OK;
@@ -862,7 +946,7 @@ bool tc_supports(const Args& a, rm_dtype dt) {
     return dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
 }
 
-size_t tc_workspace_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk, a.Dv); }
+size_t tc_workspace_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk); }
 
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     return a.Dk == 64 ? launch<64>(a, state_dt, s) : launch<128>(a, state_dt, s);
