@@ -8,25 +8,25 @@
 //     S' = e^{b_63} S + K^T D~,    D~_t = e^{b_63 - b_t} D_t
 // Where every |b_t - b_63| < 60 all decays are taken to the chunk's end, with dec_t = e^{b_63 - b_t}
 // and S~ = e^{b_63} S, so that nothing between the products but roundings is left to do:
-//     T~ = dec o T,   W = T~ (K o 1/dec),   P = mask(Q K^T)
-//     D~ = T~ V - W S~,   O = scale / dec o (Q S~ + P D~),   S' = S~ + K^T D~
+//     T~ = dec o T,   U = T~ V,   W = T~ (K o 1/dec),   P = mask(Q K^T)
+//     D~ = U - W S~,   O = scale / dec o (Q S~ + P D~),   S' = S~ + K^T D~
 // Chunks of stronger decay, whose factors would leave fp32, take the first form (T~ = T, W = T (K o
 // e^b), P = mask(Q K^T) o Gam).
 // Two launches:
-//   gds_factor_kernel  every (chunk, head) at once: T~, P, -W and the decays, which do not depend
-//                      on the state, as images of the swizzled tiles that the walk copies in
+//   gds_factor_kernel  every (chunk, head) at once: U, P, -W and the decays, which do not depend on
+//                      the state, laid out as the walk copies them in
 //   gds_walk_kernel    one CTA per (sequence, head, 128 columns of values): the chain over the
 //                      sequence's chunks
 //
 // The walk is bound by the latency of its chain: S -> W S -> D~ -> K^T D~ -> S.  It keeps S
 // transposed, a value column a lane, so that every step of the chain is a row of tensor memory per
 // thread and the rounded S and D go back to tensor memory as A operands, with no transposition and
-// no shared memory.  The state itself accumulates in tensor memory in fp32.  Products that do not
-// carry the chain (T~ V of the next chunk, Q S, P D) are issued behind those that do, and the
-// outputs are read and stored by warps of their own.
+// no shared memory.  The state itself accumulates in tensor memory in fp32.  The products that do
+// not carry the chain (Q S, P D) run in its pauses, issued by a warp of their own, and the outputs
+// are read and stored by others.
 //
 // Rounding: K, Q and V enter as they are; T~ and D~ as the sum of two bf16 (16 significant bits:
-// two products with the exact operand), because their errors reach the state undamped.  S, W and P
+// two products with the exact operand), because their errors reach the state undamped; U is fp32.  S, W and P
 // are rounded once to bf16: S and W only enter through W S, which is small beside T V, and P only
 // through O, which is rounded to bf16 anyway.  In fp64 with these roundings alone (1024 tokens, 4
 // heads of 128): state 1.4e-4 off, o 2.4e-3 with its own rounding of 1.7e-3.
@@ -48,9 +48,16 @@ constexpr int kDec = 64, kEnd = 128, kWeak = 129;
 constexpr float kForget = -110.f;        // e^{-110} is 0 in fp32: lower gates are raised to it
 constexpr float kWeakLimit = 60.f;       // decays within a chunk that factor through its end
 
-// Factors of a (chunk, head) in the workspace: T~ hi, T~ lo, P, -W (Dk / 64 tiles), the gates.
-__host__ __device__ constexpr uint32_t factor_gates(int Dk) { return (3 + Dk / 64) * T8; }
-__host__ __device__ constexpr uint32_t factor_bytes(int Dk) { return factor_gates(Dk) + kGateBytes; }
+// Factors of a (chunk, head) in the workspace: P, -W (Dk / 64 swizzled tiles), the gates, then
+// U in fp32 as [16 groups of 4 tokens][columns][4] for each block of up to 128 value columns, so
+// that a lane of the walk reads its column's four tokens at once.
+__host__ __device__ constexpr uint32_t u_cols(int Dv) { return Dv >= 128 ? 128u : uint32_t((Dv + 31) / 32 * 32); }
+__host__ __device__ constexpr uint32_t u_bytes(int Dv) { return kChunk * 4 * u_cols(Dv); }  // of a block
+__host__ __device__ constexpr uint32_t factor_gates(int Dk) { return (1 + Dk / 64) * T8; }
+__host__ __device__ constexpr uint32_t factor_u(int Dk) { return factor_gates(Dk) + kGateBytes; }
+__host__ __device__ constexpr uint32_t factor_bytes(int Dk, int Dv) {
+    return factor_u(Dk) + uint32_t((Dv + 127) / 128) * u_bytes(Dv);
+}
 
 // First chunk of sequence i: chunks of different sequences do not meet, since a sequence of n
 // tokens from token b has at most floor((b + n) / 64) - floor(b / 64) + 1 of them.
@@ -127,6 +134,11 @@ __device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
 }
 __device__ __forceinline__ uint64_t pair(float x, float y) { return pair(__float_as_uint(x), __float_as_uint(y)); }
 __device__ __forceinline__ void unpair(uint64_t p, uint32_t& x, uint32_t& y) { asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(p)); }
+__device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -150,7 +162,7 @@ __device__ __forceinline__ uint32_t pack2(uint64_t p) {
 // p as the sum of two bf16 pairs
 __device__ __forceinline__ void split2(uint64_t p, uint32_t& hi, uint32_t& lo) {
     hi = pack2(p);
-    lo = pack2(add2(p, pair((hi << 16) ^ 0x80000000u, (hi & 0xffff0000u) ^ 0x80000000u)));
+    lo = pack2(sub2(p, pair(hi << 16, hi & 0xffff0000u)));
 }
 
 // Zero rows [n, 64) of `tiles` adjacent [64][64] tiles.
@@ -247,22 +259,22 @@ __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
 // values and a zero row of P, so that they write nothing and read nothing.
 // ---------------------------------------------------------------------------
 // Shared memory: for each half h of the key dimensions K_h and Q_h side by side (one operand of
-// 128 rows), P, A, X.  T~ (hi, lo) lies over A and -W over K, each when the other is done with.
-// 72 KB: three CTAs an SM.
+// 128 rows), P, A, X.  V comes in over Q, T~ (hi, lo) lies over A, -W over K, each when the other is
+// done with.  72 KB and 128 columns of tensor memory: three CTAs an SM.
 constexpr uint32_t FA_K = 0, FA_Q = T8, FA_PANEL = 2 * T8, FA_P = 4 * T8, FA_A = 5 * T8, FA_T = FA_A, FA_X = 7 * T8;
 constexpr size_t kFactorSmem = 9 * T8 + 1024;
 
 template <int DK>
 __global__ void __launch_bounds__(256, 3)
     gds_factor_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq,
-                      const __grid_constant__ CUtensorMap mk) {
+                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     constexpr int NP = DK / 64;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
     float* A = reinterpret_cast<float*>(smem + FA_A);
     float* X = reinterpret_cast<float*>(smem + FA_X);
     __shared__ __align__(16) float b_s[kChunk], beta_s[kChunk], gam_s[kChunk], dec_s[kChunk];
-    __shared__ __align__(8) uint64_t full, mbar;
+    __shared__ __align__(8) uint64_t full, vfull, mbar;
     __shared__ uint32_t tmem_slot;
     __shared__ int weak_s;
 
@@ -280,18 +292,19 @@ __global__ void __launch_bounds__(256, 3)
     if (t0 < 0 || t0 >= sq.len || sq.slot < 0) return;
     const int n = min(sq.len - t0, kChunk);  // tokens of the chunk
     const int64_t tok = sq.begin + t0;
-    uint8_t* fac = static_cast<uint8_t*>(a.ws) + (int64_t(c) * a.H + h) * factor_bytes(DK);
+    uint8_t* fac = static_cast<uint8_t*>(a.ws) + (int64_t(c) * a.H + h) * factor_bytes(DK, a.Dv);
 
     if (tid == 0) {
         mbar_init(smem_u32(&full), 1);
+        mbar_init(smem_u32(&vfull), 1);
         mbar_init(smem_u32(&mbar), 1);
         mbar_fence_init();
     }
-    if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 64);
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 128);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;  // K K^T and Q K^T, then W^T
+    const uint32_t tmem = tmem_slot;  // [0,64) K K^T and Q K^T, then W^T; [64,128) U^T
     if (tid == 0) {
         mbar_expect_tx(smem_u32(&full), 2 * NP * T8);
         for (int p = 0; p < NP; ++p) {
@@ -344,6 +357,14 @@ __global__ void __launch_bounds__(256, 3)
     __syncthreads();
     tc_fence_after();
     uint32_t mph = 0;
+    const int vblocks = (a.Dv + 127) / 128;
+    // V of a block over Q (whose product is done by then)
+    auto load_v = [&](int vb) {
+        const int tiles = min((a.Dv - 128 * vb + 63) / 64, 2);
+        mbar_expect_tx(smem_u32(&vfull), tiles * T8);
+        for (int p = 0; p < tiles; ++p)
+            tma_load_3d(smem_u32(smem + FA_Q + p * FA_PANEL), &mv, 128 * vb + 64 * p, h, int(tok), smem_u32(&vfull));
+    };
     if (warp == 0) {
         if (elect()) {  // [K; Q] K^T
             const uint64_t d = sdesc(smem_u32(smem + FA_K), 16, 1024);
@@ -359,6 +380,7 @@ __global__ void __launch_bounds__(256, 3)
     mbar_wait(smem_u32(&mbar), mph);
     mph ^= 1;
     tc_fence_after();
+    if (tid == 0) load_v(0);
     const int quad = warp & 3, half = warp >> 2;
     const uint32_t tl = tmem + (uint32_t(32 * quad) << 16) + 32 * half;
     {
@@ -416,62 +438,86 @@ __global__ void __launch_bounds__(256, 3)
         store_row16(smem + FA_T, t, c0, x);
         store_row16(smem + FA_T + T8, t, c0, rest);
     }
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) {
-        if (elect()) {  // W^T = (K o ...)^T T~^T, with T~'s high part
-            const uint64_t dt = sdesc(smem_u32(smem + FA_T), 16, 1024), dk = sdesc(smem_u32(smem + FA_K), FA_PANEL, 1024);
+    for (int vb = 0; vb < vblocks; ++vb) {
+        mbar_wait(smem_u32(&vfull), vb & 1);
+        if (n < kChunk)
+            for (int p = 0; p < 2; ++p) zero_rows(smem + FA_Q + p * FA_PANEL, 1, n, tid, 256);
+        fence_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 0) {
+            if (elect()) {
+                const uint64_t dt = sdesc(smem_u32(smem + FA_T), 16, 1024), dv = sdesc(smem_u32(smem + FA_Q), FA_PANEL, 1024);
+                if (vb == 0) {  // W^T = (K o ...)^T T~^T, with T~'s high part
+                    const uint64_t dk = sdesc(smem_u32(smem + FA_K), FA_PANEL, 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                mma_bf16(tmem, desc_plus(dk, k * 2048), desc_plus(dt, k * 32), idesc_bf16(128, 64, 1, 0), k > 0);
-            mma_commit(smem_u32(&mbar));
-            bulk_store(fac, smem_u32(smem + FA_T), 2 * T8);
-            bulk_store(fac + 2 * T8, smem_u32(smem + FA_P), T8);
-            bulk_commit();
-        }
-        __syncwarp();
-    }
-    mbar_wait(smem_u32(&mbar), mph);
-    tc_fence_after();
-    const int row = 32 * quad + lane;
-    uint32_t x[32];
-    tmem_ld<32>(tl, x);
-    tmem_wait_ld();
-    if (row < DK) {
-        uint8_t* w = smem + FA_K + (row >> 6) * FA_PANEL;
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(tmem, desc_plus(dk, k * 2048), desc_plus(dt, k * 32), idesc_bf16(128, 64, 1, 0), k > 0);
+                    bulk_store(fac, smem_u32(smem + FA_P), T8);
+                    bulk_commit();
+                }
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-            *reinterpret_cast<__nv_bfloat16*>(w + sw_off(64, 32 * half + e, row & 63)) = __float2bfloat16_rn(-__uint_as_float(x[e]));
-    }
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 0) {
-        if (elect()) {
-            for (int p = 0; p < NP; ++p) bulk_store(fac + (3 + p) * T8, smem_u32(smem + FA_K + p * FA_PANEL), T8);
-            bulk_commit();
-            bulk_wait_read();  // shared memory is read before the CTA ends
+                for (int k = 0; k < 8; ++k)  // U^T = V^T T~^T
+                    mma_bf16(tmem + 64, desc_plus(dv, (k & 3) * 2048), desc_plus(dt, (k >> 2) * T8 + (k & 3) * 32),
+                             idesc_bf16(128, 64, 1, 0), k > 0);
+                mma_commit(smem_u32(&mbar));
+            }
+            __syncwarp();
         }
-        __syncwarp();
-        tmem_dealloc(tmem, 64);
+        mbar_wait(smem_u32(&mbar), mph);
+        mph ^= 1;
+        tc_fence_after();
+        const int row = 32 * quad + lane;
+        uint32_t x[32];
+        if (vb == 0) {
+            tmem_ld<32>(tl, x);
+            tmem_wait_ld();
+            if (row < DK) {
+                uint8_t* w = smem + FA_K + (row >> 6) * FA_PANEL;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    *reinterpret_cast<__nv_bfloat16*>(w + sw_off(64, 32 * half + e, row & 63)) = __float2bfloat16_rn(-__uint_as_float(x[e]));
+            }
+            fence_async_smem();
+        }
+        if (tid == 0 && vb + 1 < vblocks) load_v(vb + 1);
+        tmem_ld<32>(tl + 64, x);
+        tmem_wait_ld();
+        if (row < int(u_cols(a.Dv))) {
+            float4* u = reinterpret_cast<float4*>(fac + factor_u(DK) + vb * u_bytes(a.Dv)) + row;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+                u[(8 * half + e / 4) * int(u_cols(a.Dv))] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                                                                    __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (vb == 0 && warp == 0) {
+            if (elect()) {
+                for (int p = 0; p < NP; ++p) bulk_store(fac + (1 + p) * T8, smem_u32(smem + FA_K + p * FA_PANEL), T8);
+                bulk_commit();
+                bulk_wait_read();  // shared memory is read before the CTA ends
+            }
+            __syncwarp();
+        }
     }
+    if (warp == 0) tmem_dealloc(tmem, 128);
 }
 
 // ---------------------------------------------------------------------------
 // The walk over a sequence's chunks.
 // ---------------------------------------------------------------------------
 constexpr int kGroups = 4;                            // chain groups of four warps
-constexpr int kWalkThreads = (4 * kGroups + 6) * 32;  // and four output warps, the products', the copies'
+constexpr int kWalkThreads = (4 * kGroups + 7) * 32;  // and four output warps, two of products, the copies'
 constexpr int kGateRing = 8;
 
 template <int DK>
 struct WalkSmem {
     static constexpr int NP = DK / 64;
-    // two of each piece: V with T~, W, K, Q, P; then the outputs' staging and the gates
-    static constexpr uint32_t VT = 0, vt = 4 * T8, W = VT + 2 * vt, w = NP * T8, K = W + 2 * w, k = NP * T8, Q = K + 2 * k,
+    // two of each piece: U, W, K, Q, P; then the outputs' staging and the gates
+    static constexpr uint32_t U = 0, u = 4 * T8, W = U + 2 * u, w = NP * T8, K = W + 2 * w, k = NP * T8, Q = K + 2 * k,
                               q = NP * T8, P = Q + 2 * q, OUT = P + 2 * T8, GATES = OUT + 2 * T8;
     static constexpr size_t bytes = GATES + kGateRing * kGateBytes + 1024;
 };
@@ -506,7 +552,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 
 struct WalkBars {
-    uint64_t vt_full[2], vt_free[2], wkq_full[2], w_free[2], k_free[2], q_free[2], p_full[2], p_free[2];
+    uint64_t u_full[2], u_free[2], wkq_full[2], w_free[2], k_free[2], q_free[2], p_full[2], p_free[2];
     uint64_t gates[kGateRing];
     uint64_t s_ready[2], x_done[2], o_done[2], o_free[2], dt_ready, d_ready, d_done, fixed;
 };
@@ -514,7 +560,7 @@ struct WalkBars {
 template <int DK, typename TS>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     gds_walk_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
+                    const __grid_constant__ CUtensorMap mo) {
     constexpr int NP = DK / 64;
     constexpr int GC = DK / kGroups;       // state rows (columns of tensor memory) of a group
     constexpr int GT = kChunk / kGroups;   // tokens of a group
@@ -547,17 +593,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            for (uint64_t* b : {&bar.vt_full[i], &bar.vt_free[i], &bar.w_free[i], &bar.k_free[i], &bar.q_free[i], &bar.p_full[i],
-                                &bar.p_free[i], &bar.x_done[i], &bar.o_done[i]})
+            for (uint64_t* b : {&bar.u_full[i], &bar.w_free[i], &bar.k_free[i], &bar.q_free[i], &bar.p_full[i],
+                                &bar.p_free[i], &bar.o_done[i]})
                 mbar_init(smem_u32(b), 1);
+            mbar_init(smem_u32(&bar.x_done[i]), 2);  // the state's update, and Q S, which reads the old one
             mbar_init(smem_u32(&bar.wkq_full[i]), 3);
+            mbar_init(smem_u32(&bar.u_free[i]), quads * kGroups);
             mbar_init(smem_u32(&bar.s_ready[i]), quads * kGroups / 2);
             mbar_init(smem_u32(&bar.o_free[i]), quads);
         }
         for (int i = 0; i < kGateRing; ++i) mbar_init(smem_u32(&bar.gates[i]), 1);
         mbar_init(smem_u32(&bar.dt_ready), quads * kGroups);
         mbar_init(smem_u32(&bar.d_ready), quads * kGroups);
-        mbar_init(smem_u32(&bar.d_done), 1);
+        mbar_init(smem_u32(&bar.d_done), 2);  // W S, and P D of the chunks before, whose D~ is overwritten
         mbar_init(smem_u32(&bar.fixed), quads * kGroups);
         mbar_fence_init();
     }
@@ -590,11 +638,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         tmem_wait_st();
         for (int c = 0; c < chunks; ++c) {
             if (c == chunks - 1 && ragged) {
-                // rows past the sequence's end are other tokens': they must not meet a zero of D~ or T~ as NaN
-                wait(&bar.vt_full[c & 1], (c >> 1) & 1, dead);
+                // keys past the sequence's end are other tokens': they must not meet a zero of D~ as NaN
                 wait(&bar.wkq_full[c & 1], (c >> 1) & 1, dead);
                 const int at = (grp * quads + (warp & 3)) * 32 + lane;
-                zero_rows(smem + L::VT + (c & 1) * L::vt, 2, last, at, 32 * quads * kGroups);
                 zero_rows(smem + L::K + (c & 1) * L::k, NP, last, at, 32 * quads * kGroups);
                 fence_async_smem();
                 warp_arrive(&bar.fixed, lane);
@@ -611,11 +657,15 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tmem_ld<GC>(tl + TM_X + grp * GC, x);
                 tmem_wait_ld();
                 uint32_t p[GC / 2];
+                if (!weak) {
 #pragma unroll
-                for (int i = 0; i < GC / 2; ++i) {
-                    const uint64_t s = pair(x[2 * i], x[2 * i + 1]), d = mul2(s, end);
-                    p[i] = pack2(weak ? d : s);
-                    unpair(d, x[2 * i], x[2 * i + 1]);
+                    for (int i = 0; i < GC / 2; ++i) p[i] = pack2(pair(x[2 * i], x[2 * i + 1]));
+                }
+#pragma unroll
+                for (int i = 0; i < GC / 2; ++i) unpair(mul2(pair(x[2 * i], x[2 * i + 1]), end), x[2 * i], x[2 * i + 1]);
+                if (weak) {
+#pragma unroll
+                    for (int i = 0; i < GC / 2; ++i) p[i] = pack2(pair(x[2 * i], x[2 * i + 1]));
                 }
                 tmem_st<GC / 2>(tl + TM_S + grp * (GC / 2), p);
                 tmem_st<GC>(tl + TM_X + grp * GC, x);
@@ -623,11 +673,21 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tc_fence_before();
                 warp_arrive(&bar.s_ready[2 * grp / kGroups], lane);
             }
+            wait(&bar.u_full[c & 1], (c >> 1) & 1, dead);
+            ulonglong2 u[GT / 4];
+#pragma unroll
+            for (int i = 0; i < GT / 4; ++i)
+                u[i] = (reinterpret_cast<const ulonglong2*>(smem + L::U + (c & 1) * L::u))[(GT / 4 * grp + i) * int(u_cols(a.Dv)) + row];
             wait(&bar.d_done, c & 1, dead);
             tc_fence_after();
             uint32_t x[GT], hi[GT / 2], lo[GT / 2];
             tmem_ld<GT>(tl + TM_D + GT * grp, x);
             tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < GT; i += 4) {
+                unpair(add2(pair(x[i], x[i + 1]), u[i / 4].x), x[i], x[i + 1]);
+                unpair(add2(pair(x[i + 2], x[i + 3]), u[i / 4].y), x[i + 2], x[i + 3]);
+            }
             if (!weak) {  // D~ from D
 #pragma unroll
                 for (int i = 0; i < GT; i += 4) {
@@ -646,7 +706,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             tmem_st<GT / 2>(dt + TM_DTL - TM_DTH, lo);
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&bar.dt_ready, lane);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bar.dt_ready));
+                mbar_arrive(smem_u32(&bar.u_free[c & 1]));
+            }
             if (!weak) {  // and D itself, for P D
 #pragma unroll
                 for (int i = 0; i < GT / 2; ++i) split2(pair(x[2 * i], x[2 * i + 1]), hi[i], lo[i]);
@@ -735,60 +799,24 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
         if (warp == 4 * kGroups && lane == 0) bulk_wait_read();  // shared memory is read before the CTA ends
     } else if (warp == 4 * kGroups + 4) {
-        // ---- the products.  The whole warp walks the loop and one elected lane issues, so that
-        // descriptors stay in uniform registers: 30 cycles a product of N = 64 instead of 45 to 80
+        // ---- the products of the chain.  The whole warp walks the loop and one elected lane issues, so
+        // that descriptors stay in uniform registers: 30 cycles a product of N = 64 instead of 45 to 80
         // from inside a one-lane branch (measured with 8 to 64 in a row).
         const uint32_t base = smem_u32(smem);
-        constexpr uint32_t kTV = idesc_bf16(128, 64, 1, 0), kTS = idesc_bf16(128, 64, 0, 0), kTX = idesc_bf16(128, DK / 2, 0, 1);
-        // D^T = V^T T~^T of chunk c (T~ as the sum of two)
-        auto tv = [&](int c) {
-            wait(&bar.vt_full[c & 1], (c >> 1) & 1, dead);
-            if (c == chunks - 1 && ragged) wait(&bar.fixed, 0, dead);
-            tc_fence_after();
-            const uint32_t s = base + L::VT + (c & 1) * L::vt;
-            const uint64_t dv = sdesc(s, T8, 1024), dt = sdesc(s + 2 * T8, 16, 1024);
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_bf16(tmem + TM_D, desc_plus(dv, (k & 3) * 2048), desc_plus(dt, (k >> 2) * T8 + (k & 3) * 32), kTV, k > 0);
-                mma_commit(smem_u32(&bar.vt_free[c & 1]));
-            }
-            __syncwarp();
-        };
-        // O^T += D~^T P^T of chunk c (or D^T P^T on its own)
-        auto pd = [&](int c, bool weak) {
-            const int i = c & 1;
-            wait(&bar.p_full[i], (c >> 1) & 1, dead);
-            tc_fence_after();
-            const uint64_t dp = sdesc(base + L::P + i * T8, 16, 1024);
-            const uint32_t d = tmem + (weak && !i ? TM_DTH : TM_DH), to = tmem + TM_O + 64 * (weak ? i : i ^ 1);
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(to, d + (k < 4 ? 0u : TM_DTL - TM_DTH) + 8 * (k & 3), desc_plus(dp, (k & 3) * 32), kTS, weak || k > 0);
-                mma_commit(smem_u32(&bar.p_free[i]));
-                mma_commit(smem_u32(&bar.o_done[i]));
-            }
-            __syncwarp();
-        };
-        tv(0);
-        uint32_t strong = 0;  // chunks of strong decay so far
-        bool weak = gates_of(0)[kWeak] != 0.f, was_weak = true, pending = false;
-        wait(&bar.wkq_full[0], 0, dead);
+        constexpr uint32_t kTS = idesc_bf16(128, 64, 0, 0), kTX = idesc_bf16(128, DK / 2, 0, 1);
         for (int c = 0; c < chunks; ++c) {
             const int i = c & 1;
             const uint64_t dw = sdesc(base + L::W + i * L::w, 16, 1024), dk = sdesc(base + L::K + i * L::k, T8, 1024);
-            const uint64_t dq = sdesc(base + L::Q + i * L::q, 16, 1024);
-            if (pending && !weak) pd(c - 1, true);  // its D~ is about to be overwritten
-            pending = pending && weak;
+            const bool weak = gates_of(c)[kWeak] != 0.f;
+            wait(&bar.wkq_full[i], (c >> 1) & 1, dead);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {  // D^T -= S^T W^T, half of the state's rows as they come
+            for (int g = 0; g < 2; ++g) {  // D^T = -S^T W^T, half of the state's rows as they come
                 wait(&bar.s_ready[g], c & 1, dead);
                 tc_fence_after();
                 if (elect()) {
 #pragma unroll
                     for (int k = g * (DK / 32); k < (g + 1) * (DK / 32); ++k)
-                        mma_ts(tmem + TM_D, tmem + TM_S + 8 * k, desc_plus(dw, (k >> 2) * T8 + (k & 3) * 32), kTS, 1);
+                        mma_ts(tmem + TM_D, tmem + TM_S + 8 * k, desc_plus(dw, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
                     if (g == 1) {
                         mma_commit(smem_u32(&bar.d_done));
                         mma_commit(smem_u32(&bar.w_free[i]));
@@ -796,20 +824,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 }
                 __syncwarp();
             }
-            // while the chain reads D: P D~ of the chunk before, and O^T = S^T Q^T of this one.  O has two
-            // accumulators, taken in turn; a chunk of strong decay takes both
-            if (pending) pd(c - 1, true);
-            if (c > 1) wait(&bar.o_free[i], ((c - 2) >> 1) & 1, dead);
-            if (c > 0 && !(weak && was_weak)) wait(&bar.o_free[i ^ 1], ((c - 1) >> 1) & 1, dead);
-            tc_fence_after();
-            if (elect()) {
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    mma_ts(tmem + TM_O + 64 * i, tmem + TM_S + 8 * k, desc_plus(dq, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
-                mma_commit(smem_u32(&bar.q_free[i]));
-            }
-            __syncwarp();
             wait(&bar.dt_ready, c & 1, dead);
+            if (c == chunks - 1 && ragged) wait(&bar.fixed, 0, dead);
             tc_fence_after();
             if (elect()) {
                 const uint32_t d = tmem + (weak && i ? TM_DH : TM_DTH);
@@ -824,35 +840,80 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 }
             }
             __syncwarp();
+        }
+        for (int g = 0; g < 2; ++g) wait(&bar.x_done[g], (chunks - 1) & 1, dead);
+    } else if (warp == 4 * kGroups + 5) {
+        // ---- the products beside the chain, while it reads D: P D~ of the chunk before, then Q S
+        const uint32_t base = smem_u32(smem);
+        constexpr uint32_t kTS = idesc_bf16(128, 64, 0, 0);
+        // O^T += D~^T P^T of chunk c (or D^T P^T on its own); an elected lane issues it
+        auto pd = [&](int c, bool weak) {
+            const int i = c & 1;
+            const uint64_t dp = sdesc(base + L::P + i * T8, 16, 1024);
+            const uint32_t d = tmem + (weak && !i ? TM_DTH : TM_DH), to = tmem + TM_O + 64 * (weak ? i : i ^ 1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                mma_ts(to, d + (k < 4 ? 0u : TM_DTL - TM_DTH) + 8 * (k & 3), desc_plus(dp, (k & 3) * 32), kTS, weak || k > 0);
+            mma_commit(smem_u32(&bar.p_free[i]));
+            mma_commit(smem_u32(&bar.o_done[i]));
+        };
+        uint32_t strong = 0;  // chunks of strong decay so far
+        bool weak = gates_of(0)[kWeak] != 0.f, was_weak = true, pending = false;
+        if (elect()) mma_commit(smem_u32(&bar.d_done));
+        __syncwarp();
+        for (int c = 0; c < chunks; ++c) {
+            const int i = c & 1;
+            const uint64_t dq = sdesc(base + L::Q + i * L::q, 16, 1024);
+            // every wait that does not hang on the chain is taken ahead of it.  O has two accumulators,
+            // taken in turn; a chunk of strong decay takes both
+            wait(&bar.wkq_full[i], (c >> 1) & 1, dead);
+            if (c > 1) wait(&bar.o_free[i], ((c - 2) >> 1) & 1, dead);
+            if (c > 0 && !(weak && was_weak)) wait(&bar.o_free[i ^ 1], ((c - 1) >> 1) & 1, dead);
+            wait(&bar.d_done, c & 1, dead);
+            tc_fence_after();
+            if (elect()) {
+                if (pending) pd(c - 1, true);
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)  // O^T = S^T Q^T
+                    mma_ts(tmem + TM_O + 64 * i, tmem + TM_S + 8 * k, desc_plus(dq, (k >> 2) * T8 + (k & 3) * 32), kTS, k > 0);
+                mma_commit(smem_u32(&bar.q_free[i]));
+                mma_commit(smem_u32(&bar.x_done[0]));
+                mma_commit(smem_u32(&bar.x_done[1]));
+            }
+            __syncwarp();
+            wait(&bar.p_full[i], (c >> 1) & 1, dead);
             pending = weak;
-            if (!weak) {
+            was_weak = weak;
+            const bool more = c + 1 < chunks;
+            if (more) weak = gates_of(c + 1)[kWeak] != 0.f;
+            // not left for the next chunk: a chunk of strong decay, the last one, and one before a chunk of
+            // strong decay, which overwrites both D~
+            if (!was_weak) {
                 wait(&bar.d_ready, strong & 1, dead);
                 ++strong;
-                pd(c, false);
+            } else if (!more || !weak) {
+                wait(&bar.dt_ready, c & 1, dead);
             }
-            // while the chain reads the state: the next chunk's T~ V, and the waits for its pieces
-            was_weak = weak;
-            if (c + 1 < chunks) {
-                tv(c + 1);
-                weak = gates_of(c + 1)[kWeak] != 0.f;
-                wait(&bar.wkq_full[i ^ 1], ((c + 1) >> 1) & 1, dead);
+            tc_fence_after();
+            if (elect()) {
+                if (!was_weak || !more || !weak) pd(c, was_weak);
+                if (more) mma_commit(smem_u32(&bar.d_done));
             }
+            __syncwarp();
+            if (!was_weak || !more || !weak) pending = false;
         }
-        if (pending) pd(chunks - 1, true);
-        wait(&bar.x_done[1], (chunks - 1) & 1, dead);
         wait(&bar.o_done[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1, dead);
     } else {
         // ---- the copies: each piece of chunk c once the products that read chunk c - 2's are done
-        const uint32_t base = smem_u32(smem), vt = (nv + 63) / 64;
-        const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y)) * a.H + h) * factor_bytes(DK);
-        for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * factor_bytes(DK)) {
+        const uint32_t base = smem_u32(smem), ub = u_bytes(a.Dv), uat = factor_u(DK) + (v0 / 128) * ub;
+        const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y)) * a.H + h) * factor_bytes(DK, a.Dv);
+        for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * factor_bytes(DK, a.Dv)) {
             const int i = c & 1, ph = ((c >> 1) & 1) ^ 1, tok = sq.begin + c * kChunk;
-            wait(&bar.vt_free[i], ph, dead);
+            wait(&bar.u_free[i], ph, dead);
             if (elect()) {
-                const uint32_t b = smem_u32(&bar.vt_full[i]), s = base + L::VT + i * L::vt;
-                mbar_expect_tx(b, (vt + 2) * T8);
-                for (uint32_t p = 0; p < vt; ++p) tma_load_3d(s + p * T8, &mv, v0 + 64 * p, h, tok, b);
-                bulk_load(s + 2 * T8, fac, 2 * T8, b);
+                const uint32_t b = smem_u32(&bar.u_full[i]);
+                mbar_expect_tx(b, ub);
+                bulk_load(base + L::U + i * L::u, fac + uat, ub, b);
                 // the gates of chunk c - 8 are read: the products have waited for the outputs of chunk c - 5
                 const uint32_t g = smem_u32(&bar.gates[c % kGateRing]);
                 mbar_expect_tx(g, kGateBytes);
@@ -863,7 +924,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             wait(&bar.w_free[i], ph, dead);
             if (elect()) {
                 mbar_expect_tx(b, NP * T8);
-                bulk_load(base + L::W + i * L::w, fac + 3 * T8, NP * T8, b);
+                bulk_load(base + L::W + i * L::w, fac + T8, NP * T8, b);
             }
             __syncwarp();
             wait(&bar.q_free[i], ph, dead);
@@ -882,14 +943,14 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (elect()) {
                 const uint32_t pb = smem_u32(&bar.p_full[i]);
                 mbar_expect_tx(pb, T8);
-                bulk_load(base + L::P + i * T8, fac + 2 * T8, T8, pb);
+                bulk_load(base + L::P + i * T8, fac, T8, pb);
             }
             __syncwarp();
         }
         // no copy outlives the CTA
         for (int c = max(chunks - 2, 0); c < chunks; ++c) {
             const int i = c & 1, ph = (c >> 1) & 1;
-            wait(&bar.vt_full[i], ph, dead);
+            wait(&bar.u_full[i], ph, dead);
             wait(&bar.wkq_full[i], ph, dead);
             wait(&bar.p_full[i], ph, dead);
             gates_of(c);
@@ -929,12 +990,12 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     if (!map_of(&mo, a.o, a.Dv, a.H, a.N, ostr)) return fail("o", true);
     auto ff = gds_factor_kernel<DK>;
     if (!set_smem(ff, kFactorSmem)) return fail("shared-memory attribute of the factors", false);
-    ff<<<dim3(unsigned(chunk_slots(a)), unsigned(a.H)), 256, kFactorSmem, s>>>(a, mq, mk);
+    ff<<<dim3(unsigned(chunk_slots(a)), unsigned(a.H)), 256, kFactorSmem, s>>>(a, mq, mk, mv);
     note_launch(1);
     if (!launch_ok()) return fail("launch of the factors", false);
     auto fw = state_dt == RM_F32 ? gds_walk_kernel<DK, float> : gds_walk_kernel<DK, __nv_bfloat16>;
     if (!set_smem(fw, WalkSmem<DK>::bytes)) return fail("shared-memory attribute of the walk", false);
-    fw<<<dim3(unsigned((a.Dv + 127) / 128 * a.H), unsigned(a.S)), kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, mq, mk, mv, mo);
+    fw<<<dim3(unsigned((a.Dv + 127) / 128 * a.H), unsigned(a.S)), kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, mq, mk, mo);
     note_launch(1);
     if (!launch_ok()) return fail("launch of the walk", false);
     return RM_OK;
@@ -946,7 +1007,7 @@ bool tc_supports(const Args& a, rm_dtype dt) {
     return dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
 }
 
-size_t tc_workspace_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk); }
+size_t tc_workspace_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk, a.Dv); }
 
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     return a.Dk == 64 ? launch<64>(a, state_dt, s) : launch<128>(a, state_dt, s);
