@@ -172,39 +172,39 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int tiles, int n, int t
         *reinterpret_cast<uint4*>(tile + (i / each) * T8 + n * 128 + (i % each) * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// [64][64] fp32 with the 16-byte units of a row permuted by the row, so that the same unit of
-// 16 rows, and the 64 columns of one row, lie in different banks.
-__device__ __forceinline__ int f_unit(int r, int u) { return r * 64 + ((u ^ (r & 15)) << 2); }
-__device__ __forceinline__ int f_at(int r, int c) { return f_unit(r, c >> 2) + (c & 3); }
-__device__ __forceinline__ float4 f_row4(const float* m, int r, int u) { return *reinterpret_cast<const float4*>(m + f_unit(r, u)); }
+// A is [64][64] fp32 with the 16-byte units of a row permuted by the row, so that the same unit of
+// 16 rows lies in different banks; X is plain, as its columns are read side by side.
+__device__ __forceinline__ int a_unit(int r, int u) { return r * 64 + ((u ^ (r & 15)) << 2); }
+__device__ __forceinline__ float4 a_row4(const float* A, int r, int u) { return *reinterpret_cast<const float4*>(A + a_unit(r, u)); }
+__device__ __forceinline__ float4 x_row4(const float* X, int r, int u) { return *reinterpret_cast<const float4*>(X + r * 64 + 4 * u); }
 
-// R rows of one column of a product, out[row + i][col] = f sum_{k < n} A[ar + i][ac + k] B[br + k][col']:
-// A's values are the same for a whole half warp, B's adjacent for its lanes.
-template <int R>
-__device__ __forceinline__ void tri_product(const float* A, int ar, int ac, const float* B, int br, int bc, int n, float* out, int row,
-                                            int col, float f) {
+// R rows of one column of a product: out[i * 64] = f sum_{k < n} l_i[k] b[k * 64], four terms of the
+// rows (kA: of A, from row r, unit u0; else of X) at a time.
+template <int R, bool kA>
+__device__ __forceinline__ void tri_product(const float* M, int r, int u0, const float* b, int n, float* out, float f) {
     float x[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) x[i] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < n; k += 4) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+        if (k >= n) break;
         float4 l[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) l[i] = f_row4(A, ar + i, (ac + k) >> 2);
-        const float b0 = B[f_at(br + k, bc)], b1 = B[f_at(br + k + 1, bc)], b2 = B[f_at(br + k + 2, bc)], b3 = B[f_at(br + k + 3, bc)];
+        for (int i = 0; i < R; ++i) l[i] = kA ? a_row4(M, r + i, u0 + k / 4) : x_row4(M, r + i, u0 + k / 4);
+        const float b0 = b[k * 64], b1 = b[(k + 1) * 64], b2 = b[(k + 2) * 64], b3 = b[(k + 3) * 64];
 #pragma unroll
         for (int i = 0; i < R; ++i) x[i] = fmaf(l[i].w, b3, fmaf(l[i].z, b2, fmaf(l[i].y, b1, fmaf(l[i].x, b0, x[i]))));
     }
 #pragma unroll
-    for (int i = 0; i < R; ++i) out[f_at(row + i, col)] = f * x[i];
+    for (int i = 0; i < R; ++i) out[i * 64] = f * x[i];
 }
 
 // X = (I + A)^{-1} for the strictly lower A, by halves: the four 16 x 16 diagonal blocks by forward
 // substitution (a column's rows in 16 lanes), then twice the block below the diagonal of a pair,
 // X21 = -X22 (A21 X11).  A21 X11 waits in the pair's block above the diagonal, so that nothing but A
-// and X is needed; entries above the diagonal are not zero afterwards.  All 256 threads call it.
-// Shared-memory reads bound it: a lane takes a column and four rows, which shares every read of X
-// between four rows and every read of A between 32 columns.
+// and X is needed; entries above the diagonal are not zero afterwards (those of A's diagonal blocks
+// must be).  All 256 threads call it.  A lane takes a column and two or four rows, which shares every
+// read of X between the rows and every read of A between the columns.
 __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     {
@@ -212,44 +212,43 @@ __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
         float l[16], x[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const float4 v = f_row4(A, o + r, o / 4 + u);
+            const float4 v = a_row4(A, o + r, o / 4 + u);
             l[4 * u] = v.x, l[4 * u + 1] = v.y, l[4 * u + 2] = v.z, l[4 * u + 3] = v.w;
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) x[m] = r == 4 * grp + m ? 1.f : 0.f;
 #pragma unroll
-        for (int k = 0; k < 15; ++k)  // (A is zero at and above its diagonal)
+        for (int k = 0; k < 15; ++k)
 #pragma unroll
             for (int m = 0; m < 4; ++m) x[m] = fmaf(-l[k], __shfl_sync(kFull, x[m], (lane & 16) | k), x[m]);
-        *reinterpret_cast<float4*>(X + f_unit(o + r, o / 4 + grp)) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(X + (o + r) * 64 + o + 4 * grp) = make_float4(x[0], x[1], x[2], x[3]);
     }
     __syncthreads();
     {  // pairs of 16: four warps each, two rows a lane
         const int o = 32 * (warp >> 2), r = 4 * (warp & 3) + 2 * (lane >> 4), c = lane & 15;
-        tri_product<2>(A, o + 16 + r, o, X, o, o + c, 16, X, o + r, o + 16 + c, 1.f);
+        tri_product<2, true>(A, o + 16 + r, o / 4, X + o * 64 + o + c, 16, X + (o + r) * 64 + o + 16 + c, 1.f);
         __syncthreads();
-        tri_product<2>(X, o + 16 + r, o + 16, X, o, o + 16 + c, 16, X, o + 16 + r, o + c, -1.f);
+        tri_product<2, false>(X, o + 16 + r, o / 4 + 4, X + o * 64 + o + 16 + c, 16, X + (o + 16 + r) * 64 + o + c, -1.f);
         __syncthreads();
     }
-    {  // the pair of 32.  X11's and X22's blocks above their diagonals hold sums, not zeros: X11's are
-       // masked in B (columns 16 .. 31 start at row 16), X22's by the number of terms
+    {  // the pair of 32, four rows a lane.  The blocks above the diagonals of X11 and X22 hold sums, not
+       // zeros: X11's columns 16 .. 31 start at its row 16, and X22's rows below 16 end at its column 16
         const int r = 4 * warp;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll
         for (int k = 0; k < 32; k += 4) {
             float4 l[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) l[i] = f_row4(A, 32 + r + i, k >> 2);
-            const bool on = k >= 16 || lane < 16;
-            const float b0 = on ? X[f_at(k, lane)] : 0.f, b1 = on ? X[f_at(k + 1, lane)] : 0.f;
-            const float b2 = on ? X[f_at(k + 2, lane)] : 0.f, b3 = on ? X[f_at(k + 3, lane)] : 0.f;
+            for (int i = 0; i < 4; ++i) l[i] = a_row4(A, 32 + r + i, k / 4);
+            float b0 = X[k * 64 + lane], b1 = X[(k + 1) * 64 + lane], b2 = X[(k + 2) * 64 + lane], b3 = X[(k + 3) * 64 + lane];
+            if (k < 16 && lane >= 16) b0 = b1 = b2 = b3 = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = fmaf(l[i].w, b3, fmaf(l[i].z, b2, fmaf(l[i].y, b1, fmaf(l[i].x, b0, x[i]))));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) X[f_at(r + i, 32 + lane)] = x[i];
+        for (int i = 0; i < 4; ++i) X[(r + i) * 64 + 32 + lane] = x[i];
         __syncthreads();
-        tri_product<4>(X, 32 + r, 32, X, 0, 32 + lane, r < 16 ? 16 : 32, X, 32 + r, lane, -1.f);
+        tri_product<4, false>(X, 32 + r, 8, X + 32 + lane, r < 16 ? 16 : 32, X + (32 + r) * 64 + lane, -1.f);
         __syncthreads();
     }
 }
@@ -259,8 +258,8 @@ __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
 // values and a zero row of P, so that they write nothing and read nothing.
 // ---------------------------------------------------------------------------
 // Shared memory: for each half h of the key dimensions K_h and Q_h side by side (one operand of
-// 128 rows), P, A, X.  V comes in over Q, T~ (hi, lo) lies over A, -W over K, each when the other is
-// done with.  72 KB and 128 columns of tensor memory: three CTAs an SM.
+// 128 rows), P, A, X.  V comes in over Q, T~ (hi, lo) lies over A, T~ o 1/dec over P, -W over K, each
+// when the other is done with.  72 KB and 128 columns of tensor memory: three CTAs an SM.
 constexpr uint32_t FA_K = 0, FA_Q = T8, FA_PANEL = 2 * T8, FA_P = 4 * T8, FA_A = 5 * T8, FA_T = FA_A, FA_X = 7 * T8;
 constexpr size_t kFactorSmem = 9 * T8 + 1024;
 
@@ -390,53 +389,73 @@ __global__ void __launch_bounds__(256, 3)
         tmem_wait_ld();
         const int t = 32 * (quad & 1) + lane;
         const float bt = b_s[t];
+        // (the decays of a weak chunk factor through its end, and P has none)
         if (quad < 2) {
-            const float be = beta_s[t];
+            const float f = beta_s[t] * (weak_s ? gam_s[t] : 1.f);
+            if (quad >= half) {  // the other block lies above the diagonal and is not read
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(b_s + 32 * half + e);
-                const int r = 32 * half + e;
-                float4 y;
-                y.x = r < t ? be * __uint_as_float(x[e]) * __expf(bt - b.x) : 0.f;
-                y.y = r + 1 < t ? be * __uint_as_float(x[e + 1]) * __expf(bt - b.y) : 0.f;
-                y.z = r + 2 < t ? be * __uint_as_float(x[e + 2]) * __expf(bt - b.z) : 0.f;
-                y.w = r + 3 < t ? be * __uint_as_float(x[e + 3]) * __expf(bt - b.w) : 0.f;
-                *reinterpret_cast<float4*>(A + f_unit(t, r >> 2)) = y;
+                for (int e = 0; e < 32; e += 4) {
+                    const int r = 32 * half + e;
+                    float4 m;
+                    if (weak_s) {
+                        m = *reinterpret_cast<const float4*>(dec_s + r);
+                    } else {
+                        const float4 b = *reinterpret_cast<const float4*>(b_s + r);
+                        m = make_float4(__expf(bt - b.x), __expf(bt - b.y), __expf(bt - b.z), __expf(bt - b.w));
+                    }
+                    float4 y;
+                    y.x = r < t ? f * __uint_as_float(x[e]) * m.x : 0.f;
+                    y.y = r + 1 < t ? f * __uint_as_float(x[e + 1]) * m.y : 0.f;
+                    y.z = r + 2 < t ? f * __uint_as_float(x[e + 2]) * m.z : 0.f;
+                    y.w = r + 3 < t ? f * __uint_as_float(x[e + 3]) * m.w : 0.f;
+                    *reinterpret_cast<float4*>(A + a_unit(t, r >> 2)) = y;
+                }
             }
         } else {
+            const int most = t < n ? t : -1;  // the last key that the row sees
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 32 * half + e + i;
-                    y[i] = r <= t && t < n ? (weak_s ? __uint_as_float(x[e + i]) : __uint_as_float(x[e + i]) * __expf(bt - b_s[r])) : 0.f;
+                    const float m = weak_s ? 1.f : __expf(bt - b_s[r]);
+                    y[i] = r <= most ? __uint_as_float(x[e + i]) * m : 0.f;
                 }
                 *reinterpret_cast<uint4*>(smem + FA_P + sw_chunk(64, t, (32 * half + e) >> 3)) = pack8(y);
             }
         }
     }
-    // K o e^b, or K o 1/dec, over K (its products are done)
-#pragma unroll
-    for (int p = 0; p < NP; ++p) gdrtc::rows_scaled(smem + FA_K + p * FA_PANEL, smem + FA_K + p * FA_PANEL, gam_s, 1.f, tid);
+    fence_async_smem();
     __syncthreads();
+    if (warp == 0) {
+        if (elect()) {
+            bulk_store(fac, smem_u32(smem + FA_P), T8);
+            bulk_commit();
+        }
+        __syncwarp();
+    }
     halves_inverse(A, X);
-    {  // T~, hi and lo: 16 columns of a row
-        const int t = (tid & 7) | ((tid >> 5) << 3), c0 = 16 * ((tid >> 3) & 3);
-        const float dec = dec_s[t];
-        float x[16], rest[16];
+    if (warp == 0) {
+        if (elect()) bulk_wait_read();  // P has left
+        __syncwarp();
+    }
+    __syncthreads();
+    {  // T~, hi and lo, and T~ o 1/dec (or T o e^b) for W: a row at a time, two columns a lane
+        const float2 be = *reinterpret_cast<const float2*>(beta_s + 2 * lane), ga = *reinterpret_cast<const float2*>(gam_s + 2 * lane);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float4 v = f_row4(X, t, c0 / 4 + u), be = *reinterpret_cast<const float4*>(beta_s + c0 + 4 * u);
-            x[4 * u] = v.x * be.x, x[4 * u + 1] = v.y * be.y, x[4 * u + 2] = v.z * be.z, x[4 * u + 3] = v.w * be.w;
+        for (int i = 0; i < 8; ++i) {
+            const int t = 8 * warp + i;
+            const float2 v = *reinterpret_cast<const float2*>(X + t * 64 + 2 * lane);
+            const float f = dec_s[t];
+            const float x0 = 2 * lane <= t ? v.x * be.x * f : 0.f, x1 = 2 * lane + 1 <= t ? v.y * be.y * f : 0.f;
+            const uint32_t at = t * 128 + (((lane >> 2) ^ i) << 4) + (lane & 3) * 4;
+            uint32_t high, low;
+            split2(pair(x0, x1), high, low);
+            *reinterpret_cast<uint32_t*>(smem + FA_T + at) = high;
+            *reinterpret_cast<uint32_t*>(smem + FA_T + T8 + at) = low;
+            *reinterpret_cast<uint32_t*>(smem + FA_P + at) = pack2(x0 * ga.x, x1 * ga.y);
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            x[e] = c0 + e <= t ? x[e] * dec : 0.f;
-            rest[e] = x[e] - __bfloat162float(__float2bfloat16_rn(x[e]));
-        }
-        store_row16(smem + FA_T, t, c0, x);
-        store_row16(smem + FA_T + T8, t, c0, rest);
     }
     for (int vb = 0; vb < vblocks; ++vb) {
         mbar_wait(smem_u32(&vfull), vb & 1);
@@ -449,13 +468,11 @@ __global__ void __launch_bounds__(256, 3)
         if (warp == 0) {
             if (elect()) {
                 const uint64_t dt = sdesc(smem_u32(smem + FA_T), 16, 1024), dv = sdesc(smem_u32(smem + FA_Q), FA_PANEL, 1024);
-                if (vb == 0) {  // W^T = (K o ...)^T T~^T, with T~'s high part
-                    const uint64_t dk = sdesc(smem_u32(smem + FA_K), FA_PANEL, 1024);
+                if (vb == 0) {  // W^T = K^T (T~ o 1/dec)^T
+                    const uint64_t dk = sdesc(smem_u32(smem + FA_K), FA_PANEL, 1024), dg = sdesc(smem_u32(smem + FA_P), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem, desc_plus(dk, k * 2048), desc_plus(dt, k * 32), idesc_bf16(128, 64, 1, 0), k > 0);
-                    bulk_store(fac, smem_u32(smem + FA_P), T8);
-                    bulk_commit();
+                        mma_bf16(tmem, desc_plus(dk, k * 2048), desc_plus(dg, k * 32), idesc_bf16(128, 64, 1, 0), k > 0);
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // U^T = V^T T~^T
