@@ -44,16 +44,71 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
 }
 
-// One token's inputs of a CTA.
+constexpr int kTile = 4;       // tokens staged at a time
+
+// The inputs of a tile of tokens, in fp32.
 template <int DK>
-struct Token {
-    float q[DK], k[DK], v[kCols];
-    float g, beta;
+struct alignas(16) Tile {
+    float q[kTile][DK], k[kTile][DK], v[kTile][kCols];
+    float decay[kTile], beta[kTile], qk[kTile];
 };
+
+// What a thread brings in of a tile: 16-byte units of q, k and v.  The loads of the next tile are
+// issued before this one's tokens are taken and stored after them, so that a token does not wait for
+// memory.
+template <typename T, int DK>
+struct Fetch {
+    static constexpr int E = 16 / sizeof(T);                        // elements of a unit
+    static constexpr int U = 2 * DK / E + kCols / E;                // units of a token
+    static constexpr int N = (kTile * U + kTpb - 1) / kTpb;         // units of a thread
+    uint4 x[N];
+    float gate;
+
+    __device__ __forceinline__ void load(const Args& a, const T* q, const T* k, const T* v, const float* g, const float* beta, int t0,
+                                         int n, int cols) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = threadIdx.x + i * kTpb, t = u / U, e = (u % U) * E;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (t >= n) continue;
+            if (e < DK) x[i] = __ldg(reinterpret_cast<const uint4*>(q + (t0 + t) * a.qs[0] + e));
+            else if (e < 2 * DK) x[i] = __ldg(reinterpret_cast<const uint4*>(k + (t0 + t) * a.ks[0] + e - DK));
+            else if (e - 2 * DK < cols) x[i] = __ldg(reinterpret_cast<const uint4*>(v + (t0 + t) * a.vs[0] + e - 2 * DK));
+        }
+        const int t = threadIdx.x & (kTile - 1);
+        gate = 0.f;
+        if (threadIdx.x < 2 * kTile && t < n) gate = threadIdx.x < kTile ? __ldg(g + (t0 + t) * a.gs) : __ldg(beta + (t0 + t) * a.bs);
+    }
+
+    __device__ __forceinline__ void store(Tile<DK>& s) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = threadIdx.x + i * kTpb, t = u / U, e = (u % U) * E;
+            if (t >= kTile) continue;
+            float* to = e < DK ? s.q[t] + e : e < 2 * DK ? s.k[t] + e - DK : s.v[t] + e - 2 * DK;
+            if (sizeof(T) == 4) {
+                *reinterpret_cast<uint4*>(to) = x[i];
+            } else {
+                float y[8];
+                tc::unpack8(x[i], y);
+                reinterpret_cast<float4*>(to)[0] = make_float4(y[0], y[1], y[2], y[3]);
+                reinterpret_cast<float4*>(to)[1] = make_float4(y[4], y[5], y[6], y[7]);
+            }
+        }
+        if (threadIdx.x < kTile) s.decay[threadIdx.x] = expf(gate);
+        else if (threadIdx.x < 2 * kTile) s.beta[threadIdx.x - kTile] = gate;
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void load_row(const float* p, float* x) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = p[i];
+}
 
 // A CTA: blockIdx.x = column block + blocks * head, blockIdx.y = sequence.
 template <typename T, typename TS, int DK>
-__global__ void __launch_bounds__(kTpb) gds_token_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kTpb, 6) gds_token_kernel(const __grid_constant__ Args a) {
     constexpr int KR = DK / 16;  // rows of a thread: KR (tid / 8) ...
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blocks = (a.Dv + kCols - 1) / kCols;
@@ -78,94 +133,79 @@ __global__ void __launch_bounds__(kTpb) gds_token_kernel(const __grid_constant__
         if (live && !sq.fresh) load4(st + i * a.Dv, S[i]);
     }
 
-    __shared__ Token<DK> tok[2];
+    __shared__ Tile<DK> tile;
     __shared__ float4 sum[2][4][8][2];  // [parity][warp][column quad][k | q]
-    __shared__ float qk[2][4];
     const int hk = h / a.hdiv;
     const T* q = static_cast<const T*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
     const T* k = static_cast<const T*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1];
     const T* v = static_cast<const T*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + c0;
     const float* g = a.g + sq.begin * a.gs + h;
     const float* beta = a.beta + sq.begin * a.bs + h;
-    const bool has_v = tid < kCols && c0 + tid < a.Dv;
-    // the values that this thread stages for one token
-    float rq = 0.f, rk = 0.f, rv = 0.f, rg = 0.f;
-    auto fetch = [&](int t) {
-        if (tid < DK) {
-            rq = to_f32(q[t * a.qs[0] + tid]);
-            rk = to_f32(k[t * a.ks[0] + tid]);
-        }
-        if (has_v) rv = to_f32(v[t * a.vs[0] + tid]);
-        if (tid == 64) rg = g[t * a.gs];
-        if (tid == 96) rg = beta[t * a.bs];
-    };
-    auto stage = [&](int p) {
-        if (tid < DK) {
-            tok[p].q[tid] = rq;
-            tok[p].k[tid] = rk;
-        }
-        if (tid < kCols) tok[p].v[tid] = rv;
-        if (tid == 64) tok[p].g = expf(rg);
-        if (tid == 96) tok[p].beta = rg;
-    };
-    if (sq.len > 0) {
-        fetch(0);
-        stage(0);
-    }
-    __syncthreads();
-    for (int t = 0; t < sq.len; ++t) {
-        const int p = t & 1;
-        if (t + 1 < sq.len) fetch(t + 1);
-        float kr[KR], qr[KR];
-#pragma unroll
-        for (int i = 0; i < KR; ++i) {
-            kr[i] = tok[p].k[row + i];
-            qr[i] = tok[p].q[row + i];
-        }
-        float x[9];  // S^T k, S^T q of four columns, q.k
-#pragma unroll
-        for (int i = 0; i < 9; ++i) x[i] = 0.f;
-#pragma unroll
-        for (int i = 0; i < KR; ++i) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                x[c] = fmaf(kr[i], S[i][c], x[c]);
-                x[4 + c] = fmaf(qr[i], S[i][c], x[4 + c]);
-            }
-            x[8] = fmaf(qr[i], kr[i], x[8]);
-        }
-#pragma unroll
-        for (int i = 0; i < 9; ++i) {
-            x[i] += __shfl_xor_sync(kAllLanes, x[i], 8);
-            x[i] += __shfl_xor_sync(kAllLanes, x[i], 16);
-        }
-        if (lane < 8) {
-            sum[p][warp][lane][0] = make_float4(x[0], x[1], x[2], x[3]);
-            sum[p][warp][lane][1] = make_float4(x[4], x[5], x[6], x[7]);
-            if (lane == 0) qk[p][warp] = x[8];
-        }
-        if (t + 1 < sq.len) stage(p ^ 1);
+    const int cols = a.Dv - c0;
+    Fetch<T, DK> next;
+    if (sq.len > 0) next.load(a, q, k, v, g, beta, 0, sq.len, cols);
+    for (int t0 = 0; t0 < sq.len; t0 += kTile) {
+        const int n = min(sq.len - t0, kTile);
+        next.store(tile);
         __syncthreads();
-        float sk[4] = {0.f, 0.f, 0.f, 0.f}, so[4] = {0.f, 0.f, 0.f, 0.f}, dot = 0.f;
+        if (t0 + kTile < sq.len) next.load(a, q, k, v, g, beta, t0 + kTile, sq.len - t0 - kTile, cols);
+        for (int t = warp; t < n; t += 4) {  // q.k of each token
+            float x = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float4 y = sum[p][w][lane & 7][0], z = sum[p][w][lane & 7][1];
-            sk[0] += y.x, sk[1] += y.y, sk[2] += y.z, sk[3] += y.w;
-            so[0] += z.x, so[1] += z.y, so[2] += z.z, so[3] += z.w;
-            dot += qk[p][w];
+            for (int e = 0; e < DK; e += 32)
+                if (DK >= 32 || lane < DK) x = fmaf(tile.q[t][e + lane], tile.k[t][e + lane], x);
+            x = warp_sum(x);
+            if (lane == 0) tile.qk[t] = x;
         }
-        const float al = tok[p].g, be = tok[p].beta;
-        float d[4], out[4];
+        for (int t = 0; t < n; ++t) {
+            const int p = t & 1;
+            float kr[KR], x[8];  // S^T k and S^T q of four columns
+            load_row<KR>(tile.k[t] + row, kr);
+            {
+                float qr[KR];
+                load_row<KR>(tile.q[t] + row, qr);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            d[c] = be * (tok[p].v[(lane & 7) * 4 + c] - al * sk[c]);
-            out[c] = a.scale * fmaf(dot, d[c], al * so[c]);
+                for (int i = 0; i < 8; ++i) x[i] = 0.f;
+#pragma unroll
+                for (int i = 0; i < KR; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        x[c] = fmaf(kr[i], S[i][c], x[c]);
+                        x[4 + c] = fmaf(qr[i], S[i][c], x[4 + c]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] += __shfl_xor_sync(kAllLanes, x[i], 8);
+                x[i] += __shfl_xor_sync(kAllLanes, x[i], 16);
+            }
+            if (lane < 8) {
+                sum[p][warp][lane][0] = make_float4(x[0], x[1], x[2], x[3]);
+                sum[p][warp][lane][1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
+            __syncthreads();
+            float sk[4] = {0.f, 0.f, 0.f, 0.f}, so[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 y = sum[p][w][lane & 7][0], z = sum[p][w][lane & 7][1];
+                sk[0] += y.x, sk[1] += y.y, sk[2] += y.z, sk[3] += y.w;
+                so[0] += z.x, so[1] += z.y, so[2] += z.z, so[3] += z.w;
+            }
+            const float al = tile.decay[t], be = tile.beta[t], dot = tile.qk[t];
+            const float4 vt = *reinterpret_cast<const float4*>(tile.v[t] + (lane & 7) * 4);
+            const float d[4] = {be * (vt.x - al * sk[0]), be * (vt.y - al * sk[1]), be * (vt.z - al * sk[2]), be * (vt.w - al * sk[3])};
+#pragma unroll
+            for (int i = 0; i < KR; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) S[i][c] = fmaf(kr[i], d[c], al * S[i][c]);
+            if (live && tid < 8) {
+                float out[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) out[c] = a.scale * fmaf(dot, d[c], al * so[c]);
+                store4(o + (t0 + t) * os, out);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < KR; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) S[i][c] = fmaf(kr[i], d[c], al * S[i][c]);
-        if (live && tid < 8) store4(o + t * os, out);
+        __syncthreads();  // the tile has been read
     }
     if (live) {
 #pragma unroll
