@@ -4,14 +4,14 @@
 //
 // Per token, S in R^{Dk x Dv}:
 //     d = beta (v - e^g S^T k),   o = scale (e^g S^T q + (q.k) d),   S <- e^g S + k d^T
-// Both products with S read the same old state, so a token needs one pass over it and one
-// reduction.  The columns of S are independent: a CTA owns 32 columns of one sequence's head
-// and keeps them in registers over its tokens (Dk / 16 rows x 4 columns a thread, 128
-// threads); the state is read from the pool once and written once, in 128-byte (fp32) pieces
-// of a row.
+// The columns of S are independent: a CTA owns 32 columns of one sequence's head and keeps them in
+// registers over its tokens (Dk / 16 rows x 4 columns a thread, 128 threads); the state is read
+// from the pool once and written once, in 128-byte (fp32) pieces of a row.  Several tokens are taken
+// four at a time, so that four share one pass over the state, one reduction across the threads and
+// one update.
 //
-// Bound by HBM when decoding: the state's read and write are nearly all of the traffic.  One
-// CTA per 32 columns keeps the loads in flight per thread to 32 registers and gives even one
+// Bound by HBM when decoding one token: the state's read and write are nearly all of the traffic.
+// One CTA per 32 columns keeps the loads in flight per thread to 32 registers and gives even one
 // sequence of 16 heads 32 or more CTAs.
 #include <cstdio>
 
@@ -44,23 +44,23 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(h);
 }
 
-constexpr int kTile = 4;       // tokens staged at a time
-
-// The inputs of a tile of tokens, in fp32.
-template <int DK>
+// The inputs of a tile of NT tokens, in fp32; keys and queries twice, as the factors of pairs.
+template <int DK, int NT>
 struct alignas(16) Tile {
-    float q[kTile][DK], k[kTile][DK], v[kTile][kCols];
-    float decay[kTile], beta[kTile], qk[kTile];
+    float2 q[NT][DK], k[NT][DK];
+    float v[NT][kCols];
+    float decay[NT], beta[NT];
+    float kk[NT][NT], qk[NT][NT];  // k_t.k_r and q_t.k_r
 };
 
 // What a thread brings in of a tile: 16-byte units of q, k and v.  The loads of the next tile are
-// issued before this one's tokens are taken and stored after them, so that a token does not wait for
+// issued before this one's tokens are taken and stored after them, so that a tile does not wait for
 // memory.
-template <typename T, int DK>
+template <typename T, int DK, int NT>
 struct Fetch {
-    static constexpr int E = 16 / sizeof(T);                        // elements of a unit
-    static constexpr int U = 2 * DK / E + kCols / E;                // units of a token
-    static constexpr int N = (kTile * U + kTpb - 1) / kTpb;         // units of a thread
+    static constexpr int E = 16 / sizeof(T);                // elements of a unit
+    static constexpr int U = 2 * DK / E + kCols / E;        // units of a token
+    static constexpr int N = (NT * U + kTpb - 1) / kTpb;    // units of a thread
     uint4 x[N];
     float gate;
 
@@ -70,71 +70,85 @@ struct Fetch {
         for (int i = 0; i < N; ++i) {
             const int u = threadIdx.x + i * kTpb, t = u / U, e = (u % U) * E;
             x[i] = make_uint4(0, 0, 0, 0);
-            if (t >= n) continue;
+            if (t >= n || t >= NT) continue;
             if (e < DK) x[i] = __ldg(reinterpret_cast<const uint4*>(q + (t0 + t) * a.qs[0] + e));
             else if (e < 2 * DK) x[i] = __ldg(reinterpret_cast<const uint4*>(k + (t0 + t) * a.ks[0] + e - DK));
             else if (e - 2 * DK < cols) x[i] = __ldg(reinterpret_cast<const uint4*>(v + (t0 + t) * a.vs[0] + e - 2 * DK));
         }
-        const int t = threadIdx.x & (kTile - 1);
+        const int t = threadIdx.x % NT;
         gate = 0.f;
-        if (threadIdx.x < 2 * kTile && t < n) gate = threadIdx.x < kTile ? __ldg(g + (t0 + t) * a.gs) : __ldg(beta + (t0 + t) * a.bs);
+        if (threadIdx.x < 2 * NT && t < n) gate = threadIdx.x < NT ? __ldg(g + (t0 + t) * a.gs) : __ldg(beta + (t0 + t) * a.bs);
     }
 
-    __device__ __forceinline__ void store(Tile<DK>& s) const {
+    __device__ __forceinline__ void store(Tile<DK, NT>& s) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int u = threadIdx.x + i * kTpb, t = u / U, e = (u % U) * E;
-            if (t >= kTile) continue;
-            float* to = e < DK ? s.q[t] + e : e < 2 * DK ? s.k[t] + e - DK : s.v[t] + e - 2 * DK;
-            if (sizeof(T) == 4) {
-                *reinterpret_cast<uint4*>(to) = x[i];
+            if (t >= NT) continue;
+            float y[E];
+            if (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = x[i];
+            else tc::unpack8(x[i], y);
+            if (e < 2 * DK) {
+                float2* to = e < DK ? s.q[t] + e : s.k[t] + e - DK;
+#pragma unroll
+                for (int j = 0; j < E; j += 2) *reinterpret_cast<float4*>(to + j) = make_float4(y[j], y[j], y[j + 1], y[j + 1]);
             } else {
-                float y[8];
-                tc::unpack8(x[i], y);
-                reinterpret_cast<float4*>(to)[0] = make_float4(y[0], y[1], y[2], y[3]);
-                reinterpret_cast<float4*>(to)[1] = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+                for (int j = 0; j < E; j += 4) *reinterpret_cast<float4*>(s.v[t] + e - 2 * DK + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
             }
         }
-        if (threadIdx.x < kTile) s.decay[threadIdx.x] = expf(gate);
-        else if (threadIdx.x < 2 * kTile) s.beta[threadIdx.x - kTile] = gate;
+        if (threadIdx.x < NT) s.decay[threadIdx.x] = expf(gate);
+        else if (threadIdx.x < 2 * NT) s.beta[threadIdx.x - NT] = gate;
     }
 };
 
+// N values of each lane, summed over the lanes that differ in bit `bit`, and shared between them: a
+// lane keeps the first or the second half of them, by that bit.
 template <int N>
-__device__ __forceinline__ void load_row(const float* p, float* x) {
+__device__ __forceinline__ void halve(float* x, int bit) {
+    const bool upper = threadIdx.x & bit;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = p[i];
+    for (int i = 0; i < N / 2; ++i) {
+        const float give = upper ? x[i] : x[N / 2 + i], keep = upper ? x[N / 2 + i] : x[i];
+        x[i] = keep + __shfl_xor_sync(kAllLanes, give, bit);
+    }
 }
 
-// A CTA: blockIdx.x = column block + blocks * head, blockIdx.y = sequence.
-template <typename T, typename TS, int DK>
-__global__ void __launch_bounds__(kTpb, 6) gds_token_kernel(const __grid_constant__ Args a) {
+// A CTA: blockIdx.x = column block + blocks * head, blockIdx.y = sequence.  NT tokens at a time: their
+// products with the state that the tile began with, one reduction, then the tile's own triangle
+//     d_t = beta_t (v_t - G_t S^T k_t - sum_{r < t} G_t / G_r (k_t.k_r) d_r),   G_t = e^{g_0 + .. + g_t}
+//     o_t = scale (G_t S^T q_t + sum_{r <= t} G_t / G_r (q_t.k_r) d_r)
+// a column a lane, and one update of the state.
+template <typename T, typename TS, int DK, int NT>
+__global__ void __launch_bounds__(kTpb, NT == 1 ? 8 : 5) gds_token_kernel(const __grid_constant__ Args a) {
     constexpr int KR = DK / 16;  // rows of a thread: KR (tid / 8) ...
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int P = 8 * NT + 4;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 7;
     const int blocks = (a.Dv + kCols - 1) / kCols;
     const int h = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * kCols;
-    const int col = c0 + (lane & 7) * 4, row = (tid >> 3) * KR;
+    const int col = c0 + quad * 4, row = (tid >> 3) * KR;
     const bool live = col < a.Dv;  // Dv is a multiple of 8, a thread's columns of 4
     const Seq sq = sequence(a, blockIdx.y);
     if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
-    T* o = static_cast<T*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + col;
+    T* o = static_cast<T*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + c0;
     const int64_t os = int64_t(a.H) * a.Dv;
     if (sq.slot < 0) {  // padding
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        if (live && tid < 8)
-            for (int t = 0; t < sq.len; ++t) store4(o + t * os, zero);
+        for (int t = warp; t < sq.len; t += 4)
+            if (c0 + lane < a.Dv) o[t * os + lane] = from_f32<T>(0.f);
         return;
     }
     TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * a.Dk + row) * a.Dv + col;
-    float S[KR][4];
+    uint64_t S[KR][2];  // pairs of columns
 #pragma unroll
     for (int i = 0; i < KR; ++i) {
-        S[i][0] = S[i][1] = S[i][2] = S[i][3] = 0.f;
-        if (live && !sq.fresh) load4(st + i * a.Dv, S[i]);
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (live && !sq.fresh) load4(st + i * a.Dv, x);
+        S[i][0] = pair(x[0], x[1]), S[i][1] = pair(x[2], x[3]);
     }
 
-    __shared__ Tile<DK> tile;
-    __shared__ float4 sum[2][4][8][2];  // [parity][warp][column quad][k | q]
+    __shared__ Tile<DK, NT> tile;
+    __shared__ __align__(16) float part[4][8][P];      // [warp][column quad][t][k | q][4]
+    __shared__ __align__(16) float coef[4][NT][kCols]; // [warp][t][column]: d_t decayed to the tile's end
     const int hk = h / a.hdiv;
     const T* q = static_cast<const T*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
     const T* k = static_cast<const T*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1];
@@ -142,84 +156,161 @@ __global__ void __launch_bounds__(kTpb, 6) gds_token_kernel(const __grid_constan
     const float* g = a.g + sq.begin * a.gs + h;
     const float* beta = a.beta + sq.begin * a.bs + h;
     const int cols = a.Dv - c0;
-    Fetch<T, DK> next;
+    Fetch<T, DK, NT> next;
     if (sq.len > 0) next.load(a, q, k, v, g, beta, 0, sq.len, cols);
-    for (int t0 = 0; t0 < sq.len; t0 += kTile) {
-        const int n = min(sq.len - t0, kTile);
+    for (int t0 = 0; t0 < sq.len; t0 += NT) {
+        const int n = min(sq.len - t0, NT);
         next.store(tile);
         __syncthreads();
-        if (t0 + kTile < sq.len) next.load(a, q, k, v, g, beta, t0 + kTile, sq.len - t0 - kTile, cols);
-        for (int t = warp; t < n; t += 4) {  // q.k of each token
-            float x = 0.f;
+        if (t0 + NT < sq.len) next.load(a, q, k, v, g, beta, t0 + NT, sq.len - t0 - NT, cols);
+        {  // the tile's products with the state
+            uint64_t acc[NT][4];
 #pragma unroll
-            for (int e = 0; e < DK; e += 32)
-                if (DK >= 32 || lane < DK) x = fmaf(tile.q[t][e + lane], tile.k[t][e + lane], x);
-            x = warp_sum(x);
-            if (lane == 0) tile.qk[t] = x;
-        }
-        for (int t = 0; t < n; ++t) {
-            const int p = t & 1;
-            float kr[KR], x[8];  // S^T k and S^T q of four columns
-            load_row<KR>(tile.k[t] + row, kr);
-            {
-                float qr[KR];
-                load_row<KR>(tile.q[t] + row, qr);
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                for (int c = 0; c < 4; ++c) acc[t][c] = 0;
 #pragma unroll
-                for (int i = 0; i < KR; ++i)
+            for (int t = 0; t < NT; ++t) {
+                if (t < n) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        x[c] = fmaf(kr[i], S[i][c], x[c]);
-                        x[4 + c] = fmaf(qr[i], S[i][c], x[4 + c]);
+                    for (int i = 0; i < KR; ++i) {
+                        const uint64_t kr = *reinterpret_cast<const uint64_t*>(&tile.k[t][row + i]), qr = *reinterpret_cast<const uint64_t*>(&tile.q[t][row + i]);
+                        acc[t][0] = fma2(kr, S[i][0], acc[t][0]);
+                        acc[t][1] = fma2(kr, S[i][1], acc[t][1]);
+                        acc[t][2] = fma2(qr, S[i][0], acc[t][2]);
+                        acc[t][3] = fma2(qr, S[i][1], acc[t][3]);
                     }
+                }
             }
+            float x[8 * NT];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] += __shfl_xor_sync(kAllLanes, x[i], 8);
-                x[i] += __shfl_xor_sync(kAllLanes, x[i], 16);
-            }
-            if (lane < 8) {
-                sum[p][warp][lane][0] = make_float4(x[0], x[1], x[2], x[3]);
-                sum[p][warp][lane][1] = make_float4(x[4], x[5], x[6], x[7]);
-            }
-            __syncthreads();
-            float sk[4] = {0.f, 0.f, 0.f, 0.f}, so[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float4 y = sum[p][w][lane & 7][0], z = sum[p][w][lane & 7][1];
-                sk[0] += y.x, sk[1] += y.y, sk[2] += y.z, sk[3] += y.w;
-                so[0] += z.x, so[1] += z.y, so[2] += z.z, so[3] += z.w;
-            }
-            const float al = tile.decay[t], be = tile.beta[t], dot = tile.qk[t];
-            const float4 vt = *reinterpret_cast<const float4*>(tile.v[t] + (lane & 7) * 4);
-            const float d[4] = {be * (vt.x - al * sk[0]), be * (vt.y - al * sk[1]), be * (vt.z - al * sk[2]), be * (vt.w - al * sk[3])};
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t lo, hi;
+                    unpair(acc[t][c], lo, hi);
+                    x[8 * t + 2 * c] = __uint_as_float(lo), x[8 * t + 2 * c + 1] = __uint_as_float(hi);
+                }
+            halve<8 * NT>(x, 16);
+            halve<4 * NT>(x, 8);
+            float* to = part[warp][quad] + (lane >> 4) * 4 * NT + ((lane >> 3) & 1) * 2 * NT;
+            if (NT == 1) {
+                *reinterpret_cast<float2*>(to) = make_float2(x[0], x[1]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < KR; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) S[i][c] = fmaf(kr[i], d[c], al * S[i][c]);
-            if (live && tid < 8) {
-                float out[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) out[c] = a.scale * fmaf(dot, d[c], al * so[c]);
-                store4(o + (t0 + t) * os, out);
+                for (int i = 0; i < 2 * NT; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             }
         }
-        __syncthreads();  // the tile has been read
+        // k_t.k_r and q_t.k_r of one token a warp
+        if (NT == 1) {
+            if (warp == 0) {
+                float x = 0.f;
+#pragma unroll
+                for (int e = 0; e < DK; e += 32)
+                    if (DK >= 32 || lane < DK) x = fmaf(tile.q[0][e + lane].x, tile.k[0][e + lane].x, x);
+                x = warp_sum(x);
+                if (lane == 0) tile.qk[0][0] = x;
+            }
+        } else {
+            float x[2 * NT];
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i) x[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < DK; e += 32) {
+                if (DK >= 32 || lane < DK) {
+                    const float kt = tile.k[warp][e + lane].x, qt = tile.q[warp][e + lane].x;
+#pragma unroll
+                    for (int r = 0; r < NT; ++r) {
+                        const float kr = tile.k[r][e + lane].x;
+                        x[r] = fmaf(kt, kr, x[r]);
+                        x[NT + r] = fmaf(qt, kr, x[NT + r]);
+                    }
+                }
+            }
+            halve<2 * NT>(x, 16);
+            halve<NT>(x, 8);
+            halve<NT / 2>(x, 4);
+            x[0] += __shfl_xor_sync(kAllLanes, x[0], 2);
+            x[0] += __shfl_xor_sync(kAllLanes, x[0], 1);
+            if ((lane & 3) == 0) {
+                const int at = lane >> 2;  // the three bits that chose the value
+                (at < NT ? tile.kk : tile.qk)[warp][at % NT] = x[0];
+            }
+        }
+        __syncthreads();
+        float total = 1.f;  // G of the tile's last token
+        {  // the tile's triangle: a column a lane, every warp the same; warp t stores token t
+            float d[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                d[t] = 0.f;
+                if (t < n) {
+                    const float al = tile.decay[t];
+                    total *= al;
+                    float sk = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) sk += part[w][lane >> 2][8 * t + (lane & 3)];
+                    float x = fmaf(-total, sk, tile.v[t][lane]);
+#pragma unroll
+                    for (int r = 0; r < t; ++r) {
+                        d[r] *= al;
+                        x = fmaf(-tile.kk[t][r], d[r], x);
+                    }
+                    d[t] = tile.beta[t] * x;
+                    if (warp == t) {
+                        float so = 0.f;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) so += part[w][lane >> 2][8 * t + 4 + (lane & 3)];
+                        so *= total;
+#pragma unroll
+                        for (int r = 0; r <= t; ++r) so = fmaf(tile.qk[t][r], d[r], so);
+                        if (lane < cols) o[(t0 + t) * os + lane] = from_f32<T>(a.scale * so);
+                    }
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) coef[warp][t][lane] = d[t];
+            __syncwarp();
+        }
+        const uint64_t al = pair(total, total);
+#pragma unroll
+        for (int i = 0; i < KR; ++i) S[i][0] = mul2(al, S[i][0]), S[i][1] = mul2(al, S[i][1]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t < n) {
+                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(&coef[warp][t][4 * quad]);
+#pragma unroll
+                for (int i = 0; i < KR; ++i) {
+                    const uint64_t kr = *reinterpret_cast<const uint64_t*>(&tile.k[t][row + i]);
+                    S[i][0] = fma2(kr, d.x, S[i][0]);
+                    S[i][1] = fma2(kr, d.y, S[i][1]);
+                }
+            }
+        }
+        if (t0 + NT < sq.len) __syncthreads();  // the tile has been read
     }
     if (live) {
 #pragma unroll
-        for (int i = 0; i < KR; ++i) store4(st + i * a.Dv, S[i]);
+        for (int i = 0; i < KR; ++i) {
+            uint32_t x[4];
+            unpair(S[i][0], x[0], x[1]);
+            unpair(S[i][1], x[2], x[3]);
+            const float y[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]), __uint_as_float(x[3])};
+            store4(st + i * a.Dv, y);
+        }
     }
 }
 
 template <typename T, typename TS>
 bool token_launch(const Args& a, cudaStream_t s) {
     const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
-    if (a.Dk == 16) gds_token_kernel<T, TS, 16><<<grid, kTpb, 0, s>>>(a);
-    else if (a.Dk == 32) gds_token_kernel<T, TS, 32><<<grid, kTpb, 0, s>>>(a);
-    else if (a.Dk == 64) gds_token_kernel<T, TS, 64><<<grid, kTpb, 0, s>>>(a);
-    else gds_token_kernel<T, TS, 128><<<grid, kTpb, 0, s>>>(a);
+    // a state's traffic bounds single tokens; several are taken four at a time
+    const bool one = a.max_len <= 1;
+    auto f = a.Dk == 16   ? (one ? gds_token_kernel<T, TS, 16, 1> : gds_token_kernel<T, TS, 16, 4>)
+             : a.Dk == 32 ? (one ? gds_token_kernel<T, TS, 32, 1> : gds_token_kernel<T, TS, 32, 4>)
+             : a.Dk == 64 ? (one ? gds_token_kernel<T, TS, 64, 1> : gds_token_kernel<T, TS, 64, 4>)
+                          : (one ? gds_token_kernel<T, TS, 128, 1> : gds_token_kernel<T, TS, 128, 4>);
+    f<<<grid, kTpb, 0, s>>>(a);
     note_launch(1);
     return launch_ok();
 }
