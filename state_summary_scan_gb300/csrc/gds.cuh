@@ -2,6 +2,7 @@
 // token recurrence (gds_kernels.cu), its chunked form (gdstc_kernels.cu) and its host side.
 #pragma once
 
+#include "pairs.cuh"
 #include "tc_tiles.cuh"
 
 namespace rmcp {
@@ -49,35 +50,6 @@ __device__ __forceinline__ Seq sequence(const Args& a, int i) {
     s.slot = slot >= 0 && slot < a.slots_n ? slot : -1;
     s.fresh = a.fresh != nullptr && __ldg(a.fresh + i) != 0;
     return s;
-}
-
-// fp32 in pairs: one instruction an operation for two of them
-__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair(float x, float y) { return pair(__float_as_uint(x), __float_as_uint(y)); }
-__device__ __forceinline__ void unpair(uint64_t p, uint32_t& x, uint32_t& y) { asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(p)); }
-__device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
 }
 
 // The chunked form on the tensor cores, for calls whose longest sequence has this many tokens.

@@ -14,6 +14,7 @@
 // keeps one token's cos and sin in registers over that token's heads.
 #include <cstdio>
 
+#include "pairs.cuh"
 #include "tc_tiles.cuh"
 
 namespace rmcp {
@@ -46,29 +47,82 @@ struct Args {
     float* part;            // backward: [blocks][2][D] partial weight gradients
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(p)), x);
+// Eight fp32 values as pairs.
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t* x) {
+    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* x) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
-    *reinterpret_cast<uint4*>(p) = pack8(x);
-}
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+__device__ __forceinline__ uint64_t swapped(uint64_t p) {
+    uint32_t x, y;
+    unpair(p, x, y);
+    return pair(y, x);
 }
 
-// Sum over the LANES lanes of a row.
+// Eight elements as they lie in memory.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+    uint32_t x[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    }
+    __device__ __forceinline__ void zero() { x[0] = x[1] = x[2] = x[3] = 0; }
+    __device__ __forceinline__ void pairs(uint64_t* v) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = pair(x[i] << 16, x[i] & 0xffff0000u);
+    }
+    __device__ __forceinline__ Raw from(int lane) const {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.x[i] = __shfl_sync(kAll, x[i], lane);
+        return r;
+    }
+};
+template <>
+struct Raw<float> {
+    uint64_t x[4];
+    __device__ __forceinline__ void load(const float* p) { load_pairs(p, x); }
+    __device__ __forceinline__ void zero() { x[0] = x[1] = x[2] = x[3] = 0; }
+    __device__ __forceinline__ void pairs(uint64_t* v) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = x[i];
+    }
+    __device__ __forceinline__ Raw from(int lane) const {
+        Raw r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t u, v;
+            unpair(x[i], u, v);
+            r.x[i] = pair(__shfl_sync(kAll, u, lane), __shfl_sync(kAll, v, lane));
+        }
+        return r;
+    }
+};
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const uint64_t* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u, v;
+        unpair(x[i], u, v);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u), __uint_as_float(v));
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const uint64_t* x) {
+    reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(x[0], x[1]);
+    reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(x[2], x[3]);
+}
+
+// Sum of a lane's eight products over the LANES lanes of a row.
 template <int LANES>
-__device__ __forceinline__ float row_sum(float x) {
+__device__ __forceinline__ float row_sum(uint64_t p) {
+    uint32_t u, v;
+    unpair(p, u, v);
+    float x = __uint_as_float(u) + __uint_as_float(v);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
     return x;
@@ -76,6 +130,7 @@ __device__ __forceinline__ float row_sum(float x) {
 
 // Position of token t of row b; -1 where it lies outside the table.
 __device__ __forceinline__ int position(const Args& a, int b, int t) {
+    if (a.R == 0) return 0;
     if (a.pos == nullptr) return t < a.max_pos ? t : -1;
     const int64_t i = (a.pos_rows > 1 ? int64_t(b) * a.T : 0) + t;
     const int64_t p = a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + i)
@@ -83,94 +138,101 @@ __device__ __forceinline__ int position(const Args& a, int b, int t) {
     return p >= 0 && p < a.max_pos ? int(p) : -1;
 }
 
-// The rotation of a lane's eight elements e0 .. e0 + 7, of which those below R turn.
-// kFast: R is a multiple of 16 (half layout) or 8 (interleaved), so a lane's elements turn
-// together and their partners sit in one lane; otherwise each element finds its own partner
-// through the warp's row buffer.
-template <int LANES, bool kInter, bool kFast>
+// The rotation of a lane's eight elements e0 .. e0 + 7, of which those below R turn: element e
+// becomes x_e c_e + x_p s_e, with p the other member of its pair and s_e negative for the first of a
+// pair; the transposed rotation has -s_e.  Elements that do not turn have c = 1, s = 0.
+// kFast: R is a multiple of 16 (half layout) or 8 (interleaved), so a lane's elements turn together
+// and their partners sit in one lane (from) or in the lane itself; otherwise each element finds its
+// own partner through the warp's row buffer.
+template <typename T, int LANES, bool kInter, bool kFast>
 struct Turn {
-    float c[kInter && kFast ? 4 : 8], s[kInter && kFast ? 4 : 8];
-    bool on;       // kFast: the lane's elements turn
-    int from;      // kFast, half: the partner's lane
+    uint64_t c[4], s[4];
+    bool on;
+    int from;
 
-    __device__ __forceinline__ void load(const Args& a, int b, int t, int e0, int lane) {
-        on = false;
+    __device__ __forceinline__ void load(const Args& a, int p, int e0, int lane) {
         from = lane;
+        on = e0 < a.R;
 #pragma unroll
-        for (int i = 0; i < int(sizeof(c) / 4); ++i) c[i] = 1.f, s[i] = 0.f;
-        if (a.R == 0) return;
-        const int p = position(a, b, t), h = a.R / 2;
+        for (int i = 0; i < 4; ++i) c[i] = both(1.f), s[i] = 0;
+        if (!on) return;
+        const int h = a.R / 2;
         const float* row = a.table + int64_t(p < 0 ? 0 : p) * a.R;
-        if (kFast) {
-            if (e0 >= a.R) return;
-            on = true;
-            const int n = kInter ? 4 : 8, at = kInter ? e0 / 2 : (e0 < h ? e0 : e0 - h);
+        const float nan = __int_as_float(0x7fffffff);
+        if (kFast && kInter) {
+            uint64_t x[2], y[2];
+            const ulonglong2 u = __ldg(reinterpret_cast<const ulonglong2*>(row + e0 / 2)), v = __ldg(reinterpret_cast<const ulonglong2*>(row + h + e0 / 2));
+            x[0] = u.x, x[1] = u.y, y[0] = v.x, y[1] = v.y;
 #pragma unroll
-            for (int i = 0; i < n; i += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(row + at + i));
-                const float4 y = __ldg(reinterpret_cast<const float4*>(row + h + at + i));
-                c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-                s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+            for (int i = 0; i < 4; ++i) {
+                uint32_t c0, c1, s0, s1;
+                unpair(x[i / 2], c0, c1);
+                unpair(y[i / 2], s0, s1);
+                const float cc = __uint_as_float(i & 1 ? c1 : c0), ss = __uint_as_float(i & 1 ? s1 : s0);
+                c[i] = both(p < 0 ? nan : cc);  // (a position outside the table: NaN)
+                s[i] = pair(-ss, ss);
             }
-            if (!kInter) {
-                from = e0 < h ? lane + h / 8 : lane - h / 8;
-                if (e0 < h) {
+        } else if (kFast) {
+            const bool first = e0 < h;
+            const int at = first ? e0 : e0 - h;
+            load_pairs(row + at, c);
+            load_pairs(row + h + at, s);
+            from = first ? lane + h / 8 : lane - h / 8;
+            const uint64_t sign = both(first ? -1.f : 1.f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[i] = -s[i];
-                }
+            for (int i = 0; i < 4; ++i) {
+                s[i] = mul2(s[i], sign);
+                if (p < 0) c[i] = both(nan);
             }
         } else {
-            // the second member of a pair adds s times the first, the first subtracts
+            float cc[8], ss[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int e = e0 + i;
+                cc[i] = 1.f, ss[i] = 0.f;
                 if (e >= a.R) continue;
                 const int at = kInter ? e / 2 : (e < h ? e : e - h);
                 const bool first = kInter ? !(e & 1) : e < h;
-                c[i] = __ldg(row + at);
-                s[i] = first ? -__ldg(row + h + at) : __ldg(row + h + at);
+                cc[i] = p < 0 ? nan : __ldg(row + at);
+                ss[i] = first ? -__ldg(row + h + at) : __ldg(row + h + at);
             }
-        }
-        if (p < 0) {  // a position outside the table: its rotated elements are NaN
 #pragma unroll
-            for (int i = 0; i < int(sizeof(c) / 4); ++i)
-                if (kFast || e0 + i < a.R) c[i] = __int_as_float(0x7fffffff);
+            for (int i = 0; i < 4; ++i) c[i] = pair(cc[2 * i], cc[2 * i + 1]), s[i] = pair(ss[2 * i], ss[2 * i + 1]);
         }
     }
 
-    // y <- rotation of y (kBack: of the transposed rotation).  Whole-warp call.
-    template <bool kBack>
-    __device__ __forceinline__ void apply(const Args& a, int e0, float* y, float* buf) const {
+    // The partners of a lane's elements x (v: as pairs), 0 for those that do not turn.  Whole-warp call.
+    __device__ __forceinline__ void partners(const Args& a, const Raw<T>& x, const uint64_t* v, int e0, float* buf, uint64_t* o) const {
         if (kFast && kInter) {
-            if (!on) return;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = y[2 * i], v = y[2 * i + 1], t = kBack ? -s[i] : s[i];
-                y[2 * i] = u * c[i] - v * t;
-                y[2 * i + 1] = v * c[i] + u * t;
-            }
+            for (int i = 0; i < 4; ++i) o[i] = swapped(v[i]);
         } else if (kFast) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl_sync(kAll, y[i], from);
-                const float z = kBack ? y[i] * c[i] - o * s[i] : y[i] * c[i] + o * s[i];
-                y[i] = on ? z : y[i];
-            }
+            x.from(from).pairs(o);
         } else {
             const int h = a.R / 2;
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) buf[i] = y[i];
+            for (int i = 0; i < 4; ++i) {
+                uint32_t u, w;
+                unpair(v[i], u, w);
+                buf[2 * i] = __uint_as_float(u), buf[2 * i + 1] = __uint_as_float(w);
+            }
             __syncwarp();
+            float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int e = e0 + i;
-                if (e >= a.R) continue;
-                const int o = kInter ? (e ^ 1) : (e < h ? e + h : e - h);
-                const float p = buf[o - e0];
-                y[i] = kBack ? y[i] * c[i] - p * s[i] : y[i] * c[i] + p * s[i];
+                const int e = e0 + i, p = kInter ? (e ^ 1) : (e < h ? e + h : e - h);
+                y[i] = e < a.R ? buf[p - e0] : 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = pair(y[2 * i], y[2 * i + 1]);
         }
+        if (kFast && a.R < a.D && !on) o[0] = o[1] = o[2] = o[3] = 0;
+    }
+    // The element that a lane's element i is paired with, for its weight; itself where it does not turn.
+    __device__ __forceinline__ int partner(const Args& a, int e) const {
+        const int h = a.R / 2;
+        return e >= a.R ? e : kInter ? (e ^ 1) : (e < h ? e + h : e - h);
     }
 };
 
@@ -185,148 +247,221 @@ __device__ __forceinline__ float* row_buffer(int e0) {
     return buf[threadIdx.x >> 5] + ((threadIdx.x & 31) / LANES) * (LANES * 8) + e0;
 }
 
-// One warp per (token, part): the heads of a token in groups of kU * 32 / LANES, the loads of
-// a group issued before its arithmetic.
-template <typename T, int LANES, bool kInter, bool kFast, int kU>
-__device__ __forceinline__ void forward_heads(const Args& a, const T* x, int64_t hs, T* out, int H,
-                                              const float* w, const Turn<LANES, kInter, kFast>& turn, int e0,
-                                              int sub, int part, float* buf) {
-    constexpr int kRows = 32 / LANES;  // rows a warp takes at once
-    const bool live = e0 < a.D;
-    float wt[8];
-    const bool has_w = w != nullptr;
+// The heads of a token in groups of kU * 32 / LANES rows, those of q and then those of k: a warp
+// takes every split-th group of its token.  The next group's loads are issued before this group's
+// arithmetic, and a token's first ones before its cos and sin, which wait for its position.
+template <int LANES, int kU>
+struct Groups {
+    static constexpr int kRows = 32 / LANES;  // rows that a warp takes at once
+    static constexpr int kHeads = kRows * kU;
+    int nq, n;                                // groups of q, and all
+    __device__ __forceinline__ explicit Groups(const Args& a) : nq((a.Hq + kHeads - 1) / kHeads), n(nq + (a.Hk + kHeads - 1) / kHeads) {}
+    __device__ __forceinline__ bool of_q(int g) const { return g < nq; }
+    __device__ __forceinline__ int head(int g) const { return (g < nq ? g : g - nq) * kHeads; }
+};
+
+// Row of head h of x: of the input, with its strides, or of a contiguous [B * T, H, D].
+template <typename T>
+__device__ __forceinline__ const T* row_in(const Args& a, bool q, int b, int t, int h) {
+    return q ? static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1] + h * a.qs[2]
+             : static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1] + h * a.ks[2];
+}
+__device__ __forceinline__ int64_t row_at(const Args& a, bool q, int64_t n, int h) { return (n * (q ? a.Hq : a.Hk) + h) * a.D; }
+
+// the weights of a lane's elements (1 without weights)
+__device__ __forceinline__ void weights(const float* w, bool live, int e0, uint64_t* x) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wt[i] = 1.f;
-    if (has_w && live) load8(w + e0, wt);
-    for (int h0 = part * kRows * kU; h0 < H; h0 += a.split * kRows * kU) {
-        float v[kU][8];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int h = h0 + u * kRows + sub;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-            if (h < H && live) load8(x + h * hs + e0, v[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int h = h0 + u * kRows + sub;
-            if (a.norm) {
-                float sq = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sq = fmaf(v[u][i], v[u][i], sq);
-                const float r = norm_scale(a, row_sum<LANES>(sq));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] *= r;
-            }
-            if (has_w) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] *= wt[i];
-            }
-            turn.template apply<false>(a, e0, v[u], buf);
-            if (h < H && live) store8(out + int64_t(h) * a.D + e0, v[u]);
-        }
-    }
+    for (int i = 0; i < 4; ++i) x[i] = both(1.f);
+    if (w != nullptr && live) load_pairs(w + e0, x);
 }
 
+// The weights go into the factors of the rotation, once a token and tensor, and the norm's scale
+// onto the result:  y_e = r (x_e (w_e c_e) + x_p (w_p s_e)).
 template <typename T, int LANES, bool kInter, bool kFast, int kU>
-__global__ void __launch_bounds__(kWarps * 32) qkr_forward_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) qkr_forward_kernel(const __grid_constant__ Args a) {
     const int lane = threadIdx.x & 31, e0 = (lane % LANES) * 8, sub = lane / LANES;
     const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     const int64_t n = item / a.split;
-    const int part = int(item % a.split);
     if (n >= int64_t(a.B) * a.T) return;
     const int b = int(n / a.T), t = int(n % a.T);
     float* buf = row_buffer<LANES, kFast>(e0);
-    Turn<LANES, kInter, kFast> turn;
-    turn.load(a, b, t, e0, lane);
-    const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1];
-    const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1];
-    forward_heads<T, LANES, kInter, kFast, kU>(a, q, a.qs[2], static_cast<T*>(a.qo) + n * a.Hq * a.D, a.Hq, a.wq, turn, e0,
-                                              sub, part, buf);
-    forward_heads<T, LANES, kInter, kFast, kU>(a, k, a.ks[2], static_cast<T*>(a.ko) + n * a.Hk * a.D, a.Hk, a.wk, turn, e0,
-                                              sub, part, buf);
-}
-
-// dw accumulates this thread's share of the weight gradient of its eight elements.
-template <typename T, int LANES, bool kInter, bool kFast, int kU>
-__device__ __forceinline__ void backward_heads(const Args& a, const T* x, int64_t hs, const T* g, T* out, int H,
-                                               const float* w, const Turn<LANES, kInter, kFast>& turn, int e0,
-                                               int sub, int part, float* buf, float* dw) {
-    constexpr int kRows = 32 / LANES;
+    const Groups<LANES, kU> groups(a);
+    constexpr int kRows = Groups<LANES, kU>::kRows;
     const bool live = e0 < a.D;
-    float wt[8];
-    const bool has_w = w != nullptr;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wt[i] = 1.f;
-    if (has_w && live) load8(w + e0, wt);
-    for (int h0 = part * kRows * kU; h0 < H; h0 += a.split * kRows * kU) {
-        float v[kU][8], d[kU][8];
+    const int p = position(a, b, t);
+    auto fetch = [&](int g, Raw<T>* x) {
+        const bool q = groups.of_q(g);
+        const int h0 = groups.head(g) + sub, left = (q ? a.Hq : a.Hk) - h0;
+        const int64_t hs = kRows * (q ? a.qs[2] : a.ks[2]);
+        const T* from = row_in<T>(a, q, b, t, h0) + e0;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int h = h0 + u * kRows + sub;
+            x[u].zero();
+            if (live && u * kRows < left) x[u].load(from + u * hs);
+        }
+    };
+    Raw<T> x[kU];
+    int g = int(item % a.split);
+    if (g < groups.n) fetch(g, x);
+    for (int side = 0; side < 2; ++side) {  // q's groups, then k's
+        const bool q = side == 0;
+        const int end = q ? groups.nq : groups.n;
+        if (g >= end) continue;
+        const float* wt = q ? a.wq : a.wk;
+        Turn<T, LANES, kInter, kFast> turn;
+        turn.load(a, p, e0, lane);
+        if (wt != nullptr && live) {
+            uint64_t w[4];
+            load_pairs(wt + e0, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = d[u][i] = 0.f;
-            if (h < H && live) {
-                load8(g + int64_t(h) * a.D + e0, d[u]);
-                if (a.norm || has_w) load8(x + h * hs + e0, v[u]);
+            for (int i = 0; i < 4; ++i) {
+                turn.c[i] = mul2(turn.c[i], w[i]);
+                turn.s[i] = mul2(turn.s[i], pair(__ldg(wt + turn.partner(a, e0 + 2 * i)), __ldg(wt + turn.partner(a, e0 + 2 * i + 1))));
             }
         }
+        T* out = static_cast<T*>(q ? a.qo : a.ko);
+        for (; g < end; g += a.split) {
+            Raw<T> ahead[kU];
+            if (g + a.split < groups.n) fetch(g + a.split, ahead);
+            const int h0 = groups.head(g) + sub, left = (q ? a.Hq : a.Hk) - h0;
+            T* to = out + row_at(a, q, n, h0) + e0;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int h = h0 + u * kRows + sub;
-            turn.template apply<true>(a, e0, d[u], buf);
-            if (a.norm) {
-                float sq = 0.f, ux = 0.f;
+            for (int u = 0; u < kU; ++u) {
+                uint64_t v[4], o[4];
+                x[u].pairs(v);
+                turn.partners(a, x[u], v, e0, buf, o);
+                uint64_t r = both(1.f);
+                if (a.norm) {
+                    uint64_t sq = mul2(v[0], v[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sq = fmaf(v[u][i], v[u][i], sq);
-                    ux = fmaf(d[u][i] * wt[i], v[u][i], ux);
+                    for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq);
+                    r = both(norm_scale(a, row_sum<LANES>(sq)));
                 }
-                sq = row_sum<LANES>(sq);
-                ux = row_sum<LANES>(ux);
-                const float r = norm_scale(a, sq);
-                const float m = r * r * (a.norm == 1 ? ux / float(a.D) : ux);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (has_w) dw[i] = fmaf(d[u][i], v[u][i] * r, dw[i]);
-                    d[u][i] = r * fmaf(-v[u][i], m, d[u][i] * wt[i]);
-                }
-            } else if (has_w) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dw[i] = fmaf(d[u][i], v[u][i], dw[i]);
-                    d[u][i] *= wt[i];
-                }
+                for (int i = 0; i < 4; ++i) v[i] = mul2(r, fma2(o[i], turn.s[i], mul2(v[i], turn.c[i])));
+                if (live && u * kRows < left) store8(to + u * kRows * a.D, v);
             }
-            if (h < H && live) store8(out + int64_t(h) * a.D + e0, d[u]);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) x[u] = ahead[u];
         }
     }
 }
 
-// A fixed grid of blocks walks the tokens, so that the weight gradients are summed in
-// registers over a block's rows, then over its warps, then (qkr_weight_kernel) over the
-// blocks, each in a fixed order.
+// A fixed grid of blocks walks the tokens, so that the weight gradients are summed in registers over
+// a block's rows, then over its warps, then (qkr_weight_kernel) over the blocks, each in a fixed order.
 template <typename T, int LANES, bool kInter, bool kFast>
-__global__ void __launch_bounds__(kWarps * 32) qkr_backward_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __grid_constant__ Args a) {
+    constexpr int kU = 2;
     const int lane = threadIdx.x & 31, e0 = (lane % LANES) * 8, sub = lane / LANES;
     float* buf = row_buffer<LANES, kFast>(e0);
+    const Groups<LANES, kU> groups(a);
+    constexpr int kRows = Groups<LANES, kU>::kRows;
+    const bool live = e0 < a.D;
+    uint64_t dw[2][4];  // of q's and k's weights
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = 0;
+    const float inv = a.norm == 1 ? 1.f / float(a.D) : 1.f;
+    const int64_t tokens = int64_t(a.B) * a.T;
+    // a warp keeps its part of every step-th token; warps that are left over have none
+    const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5), part = warp % a.split;
+    const int step = gridDim.x * kWarps / a.split;
+    int64_t n = warp < step * a.split ? warp / a.split : tokens;
+    int b = 0, t = 0;
+    auto fetch = [&](int g, Raw<T>* x, Raw<T>* d) {
+        const bool q = groups.of_q(g);
+        const int h0 = groups.head(g) + sub, left = (q ? a.Hq : a.Hk) - h0;
+        const int64_t hs = kRows * (q ? a.qs[2] : a.ks[2]);
+        const T* from = row_in<T>(a, q, b, t, h0) + e0;
+        const T* grad = static_cast<const T*>(q ? a.gq : a.gk) + row_at(a, q, n, h0) + e0;
+        const bool need = a.norm || (q ? a.wq : a.wk) != nullptr;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            x[u].zero();
+            d[u].zero();
+            if (live && u * kRows < left) {
+                d[u].load(grad + u * kRows * a.D);
+                if (need) x[u].load(from + u * hs);
+            }
+        }
+    };
+    if (n < tokens && part < groups.n) {
+        Raw<T> x[kU], dy[kU];
+        b = int(n / a.T), t = int(n % a.T);
+        int p = position(a, b, t), g = part;
+        fetch(g, x, dy);
+        uint64_t w[4];
+        while (true) {
+            Turn<T, LANES, kInter, kFast> turn;
+            turn.load(a, p, e0, lane);
+            const int64_t n0 = n;
+            bool more = true;
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {  // q's groups, then k's
+                const bool q = side == 0;
+                const int end = q ? groups.nq : groups.n;
+                if (g >= end) continue;
+                weights(q ? a.wq : a.wk, live, e0, w);
+                T* out = static_cast<T*>(q ? a.qo : a.ko);
+                while (g < end) {
+                    // the group after this one: of this token, or the first of the warp's next token
+                    const int g0 = g;
+                    Raw<T> ax[kU], ad[kU];
+                    g += a.split;
+                    if (g >= groups.n) {
+                        n += step;
+                        more = n < tokens;
+                        b = int(n / a.T), t = int(n % a.T);
+                        if (more) {
+                            p = position(a, b, t);
+                            fetch(part, ax, ad);
+                        }
+                    } else {
+                        fetch(g, ax, ad);
+                    }
+                    const int h0 = groups.head(g0) + sub, left = (q ? a.Hq : a.Hk) - h0;
+                    T* to = out + row_at(a, q, n0, h0) + e0;
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        uint64_t v[4], d[4], o[4];
+                        x[u].pairs(v);
+                        dy[u].pairs(d);
+                        turn.partners(a, dy[u], d, e0, buf, o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[i] = sub2(mul2(d[i], turn.c[i]), mul2(o[i], turn.s[i]));
+                        uint64_t dv[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) dv[i] = mul2(d[i], v[i]), d[i] = mul2(d[i], w[i]);
+                        uint64_t r2 = both(1.f);
+                        if (a.norm) {
+                            uint64_t sq = mul2(v[0], v[0]), ux = mul2(dv[0], w[0]);
+#pragma unroll
+                            for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq), ux = fma2(dv[i], w[i], ux);
+                            const float r = norm_scale(a, row_sum<LANES>(sq)), m = r * r * row_sum<LANES>(ux) * inv;
+                            r2 = both(r);
+                            const uint64_t m2 = both(-m);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) d[i] = mul2(r2, fma2(v[i], m2, d[i]));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) dw[side][i] = fma2(dv[i], r2, dw[side][i]);
+                        if (live && u * kRows < left) store8(to + u * kRows * a.D, d);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) x[u] = ax[u], dy[u] = ad[u];
+                }
+            }
+            if (!more) break;
+            g = part;
+        }
+    }
     float dwq[8], dwk[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
-    const int64_t items = int64_t(a.B) * a.T * a.split;
-    for (int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); item < items; item += int64_t(gridDim.x) * kWarps) {
-        const int64_t n = item / a.split;
-        const int part = int(item % a.split), b = int(n / a.T), t = int(n % a.T);
-        Turn<LANES, kInter, kFast> turn;
-        turn.load(a, b, t, e0, lane);
-        const T* q = static_cast<const T*>(a.q) + b * a.qs[0] + t * a.qs[1];
-        const T* k = static_cast<const T*>(a.k) + b * a.ks[0] + t * a.ks[1];
-        backward_heads<T, LANES, kInter, kFast, 2>(a, q, a.qs[2], static_cast<const T*>(a.gq) + n * a.Hq * a.D,
-                                                   static_cast<T*>(a.qo) + n * a.Hq * a.D, a.Hq, a.wq, turn, e0, sub,
-                                                   part, buf, dwq);
-        backward_heads<T, LANES, kInter, kFast, 2>(a, k, a.ks[2], static_cast<const T*>(a.gk) + n * a.Hk * a.D,
-                                                   static_cast<T*>(a.ko) + n * a.Hk * a.D, a.Hk, a.wk, turn, e0, sub,
-                                                   part, buf, dwk);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u, v;
+        unpair(dw[0][i], u, v);
+        dwq[2 * i] = __uint_as_float(u), dwq[2 * i + 1] = __uint_as_float(v);
+        unpair(dw[1][i], u, v);
+        dwk[2 * i] = __uint_as_float(u), dwk[2 * i + 1] = __uint_as_float(v);
     }
     if (a.part == nullptr) return;
     __shared__ float sum[kWarps][2][LANES * 8];
@@ -376,8 +511,8 @@ constexpr int kBackwardBlocks = 4;  // blocks a multiprocessor of the backward g
 // Warps of a token: one where the tokens alone fill the multiprocessors (the token's cos and
 // sin are then read once), else as many as there are groups of heads.
 int split_of(const Args& a, int lanes, int unroll) {
-    const int rows = 32 / lanes;
-    const int groups = (((a.Hq > a.Hk ? a.Hq : a.Hk) + rows * unroll - 1) / (rows * unroll));
+    const int heads = 32 / lanes * unroll;
+    const int groups = (a.Hq + heads - 1) / heads + (a.Hk + heads - 1) / heads;
     const int64_t want = int64_t(tc::sm_count()) * 32, tokens = int64_t(a.B) * a.T;
     if (tokens >= want) return 1;
     const int64_t s = (want + tokens - 1) / tokens;
@@ -395,7 +530,7 @@ void launch_forward(Args a, cudaStream_t s) {
 template <typename T, int LANES, bool kInter, bool kFast>
 void launch(Args a, bool back, int blocks, cudaStream_t s) {
     if (back) {
-        a.split = split_of(a, LANES, 2);
+        a.split = min(split_of(a, LANES, 2), blocks * kWarps);
         qkr_backward_kernel<T, LANES, kInter, kFast><<<blocks, kWarps * 32, 0, s>>>(a);
     } else if (kFast && int64_t(a.B) * a.T >= int64_t(tc::sm_count()) * 8) {
         launch_forward<T, LANES, kInter, kFast, kFast ? 4 : 1>(a, s);
