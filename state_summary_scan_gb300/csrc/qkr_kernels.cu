@@ -128,6 +128,12 @@ __device__ __forceinline__ float row_sum(uint64_t p) {
     return x;
 }
 
+// Row and token of token n of B * T (below 2^31).
+__device__ __forceinline__ void place(const Args& a, int64_t n, int& b, int& t) {
+    b = int(uint32_t(n) / uint32_t(a.T));
+    t = int(uint32_t(n) - uint32_t(b) * uint32_t(a.T));
+}
+
 // Position of token t of row b; -1 where it lies outside the table.
 __device__ __forceinline__ int position(const Args& a, int b, int t) {
     if (a.R == 0) return 0;
@@ -280,10 +286,12 @@ __device__ __forceinline__ void weights(const float* w, bool live, int e0, uint6
 template <typename T, int LANES, bool kInter, bool kFast, int kU>
 __global__ void __launch_bounds__(kWarps * 32, 3) qkr_forward_kernel(const __grid_constant__ Args a) {
     const int lane = threadIdx.x & 31, e0 = (lane % LANES) * 8, sub = lane / LANES;
-    const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t n = item / a.split;
+    // (tokens * split: a split is taken where the tokens are few, so the items fit 32 bits)
+    const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t n = item / uint32_t(a.split);
     if (n >= int64_t(a.B) * a.T) return;
-    const int b = int(n / a.T), t = int(n % a.T);
+    int b, t;
+    place(a, n, b, t);
     float* buf = row_buffer<LANES, kFast>(e0);
     const Groups<LANES, kU> groups(a);
     constexpr int kRows = Groups<LANES, kU>::kRows;
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qkr_forward_kernel(const __gri
         }
     };
     Raw<T> x[kU];
-    int g = int(item % a.split);
+    int g = int(item - uint32_t(n) * uint32_t(a.split));
     if (g < groups.n) fetch(g, x);
     for (int side = 0; side < 2; ++side) {  // q's groups, then k's
         const bool q = side == 0;
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
     };
     if (n < tokens && part < groups.n) {
         Raw<T> x[kU], dy[kU];
-        b = int(n / a.T), t = int(n % a.T);
+        place(a, n, b, t);
         int p = position(a, b, t), g = part;
         fetch(g, x, dy);
         uint64_t w[4];
@@ -410,8 +418,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
                     if (g >= groups.n) {
                         n += step;
                         more = n < tokens;
-                        b = int(n / a.T), t = int(n % a.T);
                         if (more) {
+                            place(a, n, b, t);
                             p = position(a, b, t);
                             fetch(part, ax, ad);
                         }
@@ -533,7 +541,7 @@ void launch(Args a, bool back, int blocks, cudaStream_t s) {
         a.split = min(split_of(a, LANES, 2), blocks * kWarps);
         qkr_backward_kernel<T, LANES, kInter, kFast><<<blocks, kWarps * 32, 0, s>>>(a);
     } else if (kFast && int64_t(a.B) * a.T >= int64_t(tc::sm_count()) * 8) {
-        launch_forward<T, LANES, kInter, kFast, kFast ? 4 : 1>(a, s);
+        launch_forward<T, LANES, kInter, kFast, !kFast ? 1 : sizeof(T) == 4 ? 2 : 4>(a, s);
     } else {  // few tokens: one group of heads a warp
         launch_forward<T, LANES, kInter, kFast, 1>(a, s);
     }
