@@ -141,6 +141,7 @@ _SIGS = {
 
 _lock = threading.Lock()
 _lib = None
+_by_address: dict = {}
 
 
 def library_path() -> str:
@@ -160,6 +161,10 @@ def load(build_if_needed: bool = True):
                 fn = getattr(so, name)
                 fn.restype = res
                 fn.argtypes = args
+            for name in ("rm_cp_qkr_forward", "rm_cp_qkr_backward", "rm_gdr_state_forward"):
+                fn = so[name]  # a function object of its own, taking the problem's address
+                fn.restype, fn.argtypes = _S, [_P] * len(_SIGS[name][1])
+                _by_address[name] = fn
             _lib = so
     return _lib
 
@@ -397,25 +402,48 @@ def rm_gdr_backward_apply(p, q, k, v, g, beta, dO, dS_out, dk, dv, dg, dbeta, ws
 
 # ----------------------------------------------------------------- norm and rotation, carried state, clipping
 # These calls take strides in their problem, so tensors need only have adjacent head elements;
-# the callers in qk_rope.py, gdr_state.py and clip.py check shapes, types and strides.
+# the callers in qk_rope.py, gdr_state.py and clip.py check shapes, types and strides.  Pointers are
+# passed as addresses and problems as the address of their struct: a decoding step is a few
+# microseconds long, and so must its call be.
 
 def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, device: int):
+    """Handle of the stream, or of the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def signature(t: Optional[torch.Tensor]):
+    """What a call's checks depend on; equal signatures pass the same checks."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
 
 def rm_cp_qkr_workspace_size(p: QkrProblem) -> int:
     return int(load().rm_cp_qkr_workspace_size(ctypes.byref(p)))
 
 
-def rm_cp_qkr_forward(p, q, k, wq, wk, table, positions, q_out, k_out, stream=None):
-    _check(load().rm_cp_qkr_forward(ctypes.byref(p), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(table),
-                                    _addr(positions), _addr(q_out), _addr(k_out), _stream(stream)))
+def rm_cp_qkr_forward(p: int, q, k, wq, wk, table, positions, q_out, k_out, stream):
+    """p: the address of a QkrProblem."""
+    if _lib is None:
+        load()
+    status = _by_address["rm_cp_qkr_forward"](p, q.data_ptr(), k.data_ptr(), _addr(wq), _addr(wk), _addr(table),
+                                                _addr(positions), q_out.data_ptr(), k_out.data_ptr(), stream)
+    if status:
+        _check(status)
 
 
-def rm_cp_qkr_backward(p, q, k, wq, wk, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws, stream=None):
-    _check(load().rm_cp_qkr_backward(ctypes.byref(p), _addr(q), _addr(k), _addr(wq), _addr(wk), _addr(table),
-                                     _addr(positions), _addr(dq_out), _addr(dk_out), _addr(dq), _addr(dk),
-                                     _addr(dwq), _addr(dwk), _addr(ws), _stream(stream)))
+def rm_cp_qkr_backward(p: int, q, k, wq, wk, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws, stream):
+    if _lib is None:
+        load()
+    status = _by_address["rm_cp_qkr_backward"](p, q.data_ptr(), k.data_ptr(), _addr(wq), _addr(wk), _addr(table),
+                                                 _addr(positions), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(),
+                                                 dk.data_ptr(), _addr(dwq), _addr(dwk), _addr(ws), stream)
+    if status:
+        _check(status)
 
 
 def rm_gdr_state_path(p: GdrStateProblem) -> int:
@@ -426,17 +454,24 @@ def rm_gdr_state_workspace_size(p: GdrStateProblem) -> int:
     return int(load().rm_gdr_state_workspace_size(ctypes.byref(p)))
 
 
-def rm_gdr_state_forward(p, q, k, v, g, beta, cu_seqlens, slots, fresh, state, o, ws, stream=None):
-    _check(load().rm_gdr_state_forward(ctypes.byref(p), _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta),
-                                       _addr(cu_seqlens), _addr(slots), _addr(fresh), _addr(state), _addr(o),
-                                       _addr(ws), _stream(stream)))
+def rm_gdr_state_forward(p: int, q, k, v, g, beta, cu_seqlens, slots, fresh, state, o, ws, stream):
+    """p: the address of a GdrStateProblem."""
+    if _lib is None:
+        load()
+    status = _by_address["rm_gdr_state_forward"](p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                                   _addr(cu_seqlens), _addr(slots), _addr(fresh), state.data_ptr(),
+                                                   o.data_ptr(), ws.data_ptr(), stream)
+    if status:
+        _check(status)
 
 
 def rm_cp_clip_workspace_size(n: int) -> int:
     return int(load().rm_cp_clip_workspace_size(int(n)))
 
 
-def rm_cp_clip_grad_norm(n, grads, numels, dtypes, outs, out_dtypes, max_norm, eps, norm, ws, stream=None):
+def rm_cp_clip_grad_norm(n, grads, numels, dtypes, outs, out_dtypes, max_norm, eps, norm, ws, stream):
     """grads, numels, dtypes, outs, out_dtypes: addresses of host arrays (outs and out_dtypes may be None)."""
-    _check(load().rm_cp_clip_grad_norm(int(n), grads, numels, dtypes, outs, out_dtypes, float(max_norm), float(eps),
-                                       _addr(norm), _addr(ws), _stream(stream)))
+    status = (_lib or load()).rm_cp_clip_grad_norm(n, grads, numels, dtypes, outs, out_dtypes, max_norm, eps,
+                                                   norm.data_ptr(), ws.data_ptr(), stream)
+    if status:
+        _check(status)

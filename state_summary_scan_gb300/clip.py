@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import array
 import dataclasses
+import operator
 from typing import Optional, Sequence
 
 import torch
@@ -28,18 +29,21 @@ def make_clip_plan(max_tensors: int, device="cuda") -> ClipPlan:
     return ClipPlan(max_tensors, ws.device, ws)
 
 
+_DTYPE = operator.attrgetter("dtype")
+_Tensor = torch.Tensor
+
+
 def _describe(tensors, device, name):
     """Addresses and type codes of contiguous fp32 or bf16 tensors on one device."""
     try:
-        types = array.array("i", [_DTYPES[t.dtype] for t in tensors])
+        types = array.array("i", map(_DTYPES.__getitem__, map(_DTYPE, tensors)))
     except KeyError as e:
         raise ValueError(f"{name} must be fp32 or bf16, not {e.args[0]}") from None
-    for t in tensors:
-        if t.device != device:
-            raise ValueError(f"{name} must be on the plan's device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return array.array("Q", [t.data_ptr() for t in tensors]), types
+    if set(map(_Tensor.get_device, tensors)) != {device.index}:
+        raise ValueError(f"{name} must be on the plan's device")
+    if not all(map(_Tensor.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    return array.array("Q", map(_Tensor.data_ptr, tensors)), types
 
 
 def clip_grad_norm(plan: ClipPlan, grads: Sequence[torch.Tensor], max_norm: Optional[float] = None, out=None,
@@ -48,18 +52,18 @@ def clip_grad_norm(plan: ClipPlan, grads: Sequence[torch.Tensor], max_norm: Opti
     max_norm each gradient is multiplied by min(1, max_norm / (norm + eps)), in place or, with
     out, into the tensors of out (same sizes, fp32 or bf16 each; gradients can be cast on the
     way).  grads: contiguous fp32 and bf16 tensors of any sizes and alignments, mixed."""
-    grads = [g.detach() if g.requires_grad else g for g in grads]
+    grads = grads if isinstance(grads, (list, tuple)) else list(grads)
     if not grads:
         raise ValueError("no gradients")
     if len(grads) > plan.max_tensors:
         raise ValueError(f"{len(grads)} tensors exceed the plan's {plan.max_tensors}")
     ptr, types = _describe(grads, plan.device, "gradients")
-    sizes = array.array("q", [g.numel() for g in grads])
+    sizes = array.array("q", map(_Tensor.numel, grads))
     out_ptr, out_types = ptr, types
     if out is not None:
         if max_norm is None:
             raise ValueError("out needs max_norm")
-        if [x.numel() for x in out] != list(sizes):
+        if array.array("q", map(_Tensor.numel, out)) != sizes:
             raise ValueError("out must have the sizes of the gradients")
         out_ptr, out_types = _describe(out, plan.device, "out")
     norm = torch.empty((), dtype=torch.float32, device=plan.device)
@@ -69,5 +73,5 @@ def clip_grad_norm(plan: ClipPlan, grads: Sequence[torch.Tensor], max_norm: Opti
 
     C.rm_cp_clip_grad_norm(len(grads), at(ptr), at(sizes), at(types), None if max_norm is None else at(out_ptr),
                            None if max_norm is None else at(out_types), 0.0 if max_norm is None else max_norm, eps, norm,
-                           plan.ws, stream)
+                           plan.ws, C._raw_stream(stream, plan.device.index))
     return norm

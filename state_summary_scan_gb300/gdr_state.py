@@ -6,6 +6,7 @@ prompt, or one token, at a time.
 """
 from __future__ import annotations
 
+import ctypes
 import dataclasses
 import math
 from typing import Optional
@@ -28,6 +29,7 @@ class GdrStatePlan:
     dtype: torch.dtype
     state_dtype: torch.dtype
     ws: torch.Tensor
+    checked: dict = dataclasses.field(default_factory=dict)  # problems of calls by signature
 
 
 def make_gdr_state_plan(max_seqs: int, max_tokens: int, H: int, Dk: int, Dv: int, num_slots: Optional[int] = None,
@@ -76,7 +78,7 @@ def _token_stride(x, lead, name):
     return x.stride(1) if n > 1 else x.stride(0)
 
 
-def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, o, stream):
+def _checked_problem(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh):
     c, dev = plan.c, plan.ws.device
     head = q.shape[:lead]
     if (q.shape != (*head, c.qk_heads, c.Dk) or k.shape != q.shape or v.shape != (*head, c.H, c.Dv)
@@ -88,7 +90,7 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, 
         raise ValueError("g and beta must be fp32")
     if state.dtype != plan.state_dtype or state.shape != (c.num_slots, c.H, c.Dk, c.Dv) or not state.is_contiguous():
         raise ValueError(f"state must be [{c.num_slots},{c.H},{c.Dk},{c.Dv}] {plan.state_dtype}, contiguous")
-    for x in (q, k, v, g, beta, state, cu, slots, fresh, o):
+    for x in (q, k, v, g, beta, state, cu, slots, fresh):
         if x is not None and x.device != dev:
             raise ValueError("every tensor must be on the plan's device")
     if S > plan.max_seqs or N > plan.max_tokens or max_len > plan.max_len:
@@ -100,17 +102,29 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, 
         raise ValueError("fresh must be [sequences] uint8 or bool, contiguous")
     if (g.stride(-1) != 1 or beta.stride(-1) != 1) and c.H > 1:
         raise ValueError("the heads of g and beta must be adjacent")
-    if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    elif o.shape != v.shape or o.dtype != v.dtype or not o.is_contiguous():
-        raise ValueError("o must be contiguous and have the shape and type of v")
-    if S == 0:
-        return o
     p = C.GdrStateProblem.from_buffer_copy(c)
     p.num_seqs, p.num_tokens, p.max_len = S, N, max_len
     p.q_stride, p.k_stride, p.v_stride = _strides(q, lead, "q"), _strides(k, lead, "k"), _strides(v, lead, "v")
     p.g_stride, p.beta_stride = _token_stride(g, lead, "g"), _token_stride(beta, lead, "beta")
-    C.rm_gdr_state_forward(p, q, k, v, g, beta, cu, slots, fresh, state, o, plan.ws, stream)
+    return p
+
+
+def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, o, stream):
+    sig = C.signature
+    key = (lead, max_len, sig(q), sig(k), sig(v), sig(g), sig(beta), sig(state), sig(cu), sig(slots), sig(fresh))
+    p = plan.checked.get(key)
+    if p is None:
+        p = _checked_problem(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh)
+        if len(plan.checked) >= 256:
+            plan.checked.clear()
+        plan.checked[key] = p
+    if o is None:
+        o = torch.empty_like(v, memory_format=torch.contiguous_format)
+    elif o.shape != v.shape or o.dtype != v.dtype or o.device != v.device or not o.is_contiguous():
+        raise ValueError("o must be contiguous and have the shape, type and device of v")
+    if S:
+        C.rm_gdr_state_forward(ctypes.addressof(p), q, k, v, g, beta, cu, slots, fresh, state, o, plan.ws,
+                               C._raw_stream(stream, q.get_device()))
     return o
 
 

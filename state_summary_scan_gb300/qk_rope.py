@@ -5,7 +5,10 @@ is the differentiable form.  `make_rope_table` computes the rotation's table onc
 """
 from __future__ import annotations
 
+import collections
+import ctypes
 import math
+import threading
 from typing import Optional
 
 import torch
@@ -54,7 +57,28 @@ def make_rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, 
     return (torch.stack([angle.cos(), angle.sin()], 1) * mult).to(torch.float32).to(device).contiguous()
 
 
-def _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved) -> C.QkrProblem:
+_CACHE: "collections.OrderedDict" = collections.OrderedDict()  # checked problems by signature
+_CACHE_MAX = 256
+_CACHE_LOCK = threading.Lock()
+
+
+def _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved):
+    """(problem, its address) of a call, checked once for each combination of shapes, strides,
+    types and options."""
+    sig = C.signature
+    key = (sig(q), sig(k), sig(table), sig(positions), sig(q_weight), sig(k_weight), norm, eps, interleaved)
+    hit = _CACHE.get(key)
+    if hit is None:
+        p = _checked_problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
+        hit = (p, ctypes.addressof(p))
+        with _CACHE_LOCK:
+            _CACHE[key] = hit
+            while len(_CACHE) > _CACHE_MAX:
+                _CACHE.popitem(last=False)
+    return hit
+
+
+def _checked_problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved) -> C.QkrProblem:
     if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
         raise ValueError("q and k must be [B,T,Hq,D] and [B,T,Hk,D]")
     if q.dtype != k.dtype or q.dtype not in _DTYPES:
@@ -102,14 +126,19 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     be slices of a fused projection (adjacent elements, 16-byte strides); the outputs are
     contiguous and alias no input.  A position outside the table makes its token's rotated
     elements NaN."""
-    p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
+    _, p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=k.device))
+        out = _new(q), _new(k)
     else:
         _like(out, (q, k), "out")
     if q.numel():
-        C.rm_cp_qkr_forward(p, q, k, q_weight, k_weight, table, positions, out[0], out[1], stream)
+        C.rm_cp_qkr_forward(p, q, k, q_weight, k_weight, table, positions, out[0], out[1],
+                            C._raw_stream(stream, q.get_device()))
     return out
+
+
+def _new(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _like(got, want, name):
@@ -122,19 +151,18 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, table=None, positions=None, q_we
                           norm: str = "rms", eps: float = 1e-6, interleaved: bool = False, stream=None):
     """(dq, dk, dq_weight, dk_weight) of sum(dq_out * q') + sum(dk_out * k'), with the arguments
     of the forward; a weight's gradient is [D] fp32, None without the weight."""
-    p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
+    problem, p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
     _like((dq_out, dk_out), (q, k), "dq_out and dk_out")
-    dev = q.device
-    dq, dk = torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=k.dtype, device=dev)
-    D = q.shape[3]
-    dwq = torch.empty(D, dtype=torch.float32, device=dev) if q_weight is not None else None
-    dwk = torch.empty(D, dtype=torch.float32, device=dev) if k_weight is not None else None
+    dq, dk = _new(q), _new(k)
+    dwq = torch.empty_like(q_weight) if q_weight is not None else None
+    dwk = torch.empty_like(k_weight) if k_weight is not None else None
     if not q.numel():
         return dq, dk, None if dwq is None else dwq.zero_(), None if dwk is None else dwk.zero_()
     ws = None
     if dwq is not None or dwk is not None:
-        ws = torch.empty(max(C.rm_cp_qkr_workspace_size(p), 16), dtype=torch.uint8, device=dev)
-    C.rm_cp_qkr_backward(p, q, k, q_weight, k_weight, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws, stream)
+        ws = torch.empty(C.rm_cp_qkr_workspace_size(problem), dtype=torch.uint8, device=q.device)
+    C.rm_cp_qkr_backward(p, q, k, q_weight, k_weight, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws,
+                         C._raw_stream(stream, q.get_device()))
     return dq, dk, dwq, dwk
 
 
