@@ -22,8 +22,8 @@ using tc::unpack8;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = 16384;   // elements: 64 a thread
-constexpr int kBlocks = 152 * 4;
+constexpr int kPiece = 32768;   // elements: 128 a thread
+constexpr int kBlocks = 152 * 6;
 constexpr int kFew = 96, kMany = 900;  // tensors of a launch
 
 template <int N>
@@ -123,7 +123,7 @@ __device__ __noinline__ double square_piece_wide(const T* p, int n) {
     return s;
 }
 
-// A thread's share of a piece is at most 66 elements.  Its squares stay inside fp32 when the
+// A thread's share of a piece is at most 130 elements.  Its squares stay inside fp32 when the
 // largest magnitude is in [1e-15, 1e18]: above, they could overflow; below, the squares
 // (< 1e-30) could lose bits to fp32's smallest numbers (1.2e-38), so they are summed in fp64.
 __device__ __forceinline__ bool in_range(float m) { return m == 0.f || (m >= 1e-15f && m <= 1e18f); }
@@ -142,7 +142,7 @@ __device__ __forceinline__ double block_sum(double x) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) clip_square_kernel(const __grid_constant__ Batch<N> b, double* part) {
+__global__ void __launch_bounds__(kThreads, 6) clip_square_kernel(const __grid_constant__ Batch<N> b, double* part) {
     double total = 0.;
     for (int64_t p = blockIdx.x; p < b.first[b.n]; p += gridDim.x) {
         const int t = find(b, p);
@@ -200,7 +200,7 @@ __device__ __forceinline__ void scale_piece(const TI* p, TO* o, int n, float c) 
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
     clip_scale_kernel(const __grid_constant__ Batch<N> b, const double* part, int parts, float max_norm, float eps, float* norm) {
     const double x = norm_of(part, parts);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = float(x);
