@@ -72,6 +72,8 @@ rm_status gdrtc_read_timeout_flag(int* host_flag, int clear, int* dev_scratch, c
 
 // the gated delta rule with a carried state on the tensor cores (gdstc_kernels.cu)
 rm_status gdstc_read_timeout_flag(int* host_flag, int clear, int* dev_scratch, cudaStream_t s);
+// per-head norm and rotation (qkr_kernels.cu)
+rm_status qkr_read_timeout_flag(int* host_flag, int clear, int* dev_scratch, cudaStream_t s);
 
 // vector (per key dimension) gates on the generic path (vg_kernels.cu)
 rm_status launch_vg(Op op, const Dims& d, rm_dtype dt, const Ptrs& p, cudaStream_t s);

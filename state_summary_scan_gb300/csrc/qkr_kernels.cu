@@ -69,6 +69,10 @@ struct Raw<__nv_bfloat16> {
         const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     }
+    __device__ __forceinline__ void shared(const __nv_bfloat16* p) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    }
     __device__ __forceinline__ void zero() { x[0] = x[1] = x[2] = x[3] = 0; }
     __device__ __forceinline__ void pairs(uint64_t* v) const {
 #pragma unroll
@@ -85,6 +89,10 @@ template <>
 struct Raw<float> {
     uint64_t x[4];
     __device__ __forceinline__ void load(const float* p) { load_pairs(p, x); }
+    __device__ __forceinline__ void shared(const float* p) {
+        const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0], b = reinterpret_cast<const ulonglong2*>(p)[1];
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    }
     __device__ __forceinline__ void zero() { x[0] = x[1] = x[2] = x[3] = 0; }
     __device__ __forceinline__ void pairs(uint64_t* v) const {
 #pragma unroll
@@ -157,17 +165,20 @@ struct Turn {
     int from;
 
     __device__ __forceinline__ void load(const Args& a, int p, int e0, int lane) {
+        load(a, a.table + int64_t(p < 0 ? 0 : p) * a.R, p < 0, e0, lane);
+    }
+    // row: the position's row of the table, in global or shared memory; bad: outside the table
+    __device__ __forceinline__ void load(const Args& a, const float* row, bool bad, int e0, int lane) {
         from = lane;
         on = e0 < a.R;
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = both(1.f), s[i] = 0;
         if (!on) return;
         const int h = a.R / 2;
-        const float* row = a.table + int64_t(p < 0 ? 0 : p) * a.R;
         const float nan = __int_as_float(0x7fffffff);
         if (kFast && kInter) {
             uint64_t x[2], y[2];
-            const ulonglong2 u = __ldg(reinterpret_cast<const ulonglong2*>(row + e0 / 2)), v = __ldg(reinterpret_cast<const ulonglong2*>(row + h + e0 / 2));
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(row + e0 / 2), v = *reinterpret_cast<const ulonglong2*>(row + h + e0 / 2);
             x[0] = u.x, x[1] = u.y, y[0] = v.x, y[1] = v.y;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -175,20 +186,22 @@ struct Turn {
                 unpair(x[i / 2], c0, c1);
                 unpair(y[i / 2], s0, s1);
                 const float cc = __uint_as_float(i & 1 ? c1 : c0), ss = __uint_as_float(i & 1 ? s1 : s0);
-                c[i] = both(p < 0 ? nan : cc);  // (a position outside the table: NaN)
+                c[i] = both(bad ? nan : cc);  // (a position outside the table: NaN)
                 s[i] = pair(-ss, ss);
             }
         } else if (kFast) {
             const bool first = e0 < h;
             const int at = first ? e0 : e0 - h;
-            load_pairs(row + at, c);
-            load_pairs(row + h + at, s);
+            const ulonglong2* x = reinterpret_cast<const ulonglong2*>(row + at);
+            const ulonglong2* y = reinterpret_cast<const ulonglong2*>(row + h + at);
+            c[0] = x[0].x, c[1] = x[0].y, c[2] = x[1].x, c[3] = x[1].y;
+            s[0] = y[0].x, s[1] = y[0].y, s[2] = y[1].x, s[3] = y[1].y;
             from = first ? lane + h / 8 : lane - h / 8;
             const uint64_t sign = both(first ? -1.f : 1.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s[i] = mul2(s[i], sign);
-                if (p < 0) c[i] = both(nan);
+                if (bad) c[i] = both(nan);
             }
         } else {
             float cc[8], ss[8];
@@ -199,12 +212,17 @@ struct Turn {
                 if (e >= a.R) continue;
                 const int at = kInter ? e / 2 : (e < h ? e : e - h);
                 const bool first = kInter ? !(e & 1) : e < h;
-                cc[i] = p < 0 ? nan : __ldg(row + at);
-                ss[i] = first ? -__ldg(row + h + at) : __ldg(row + h + at);
+                cc[i] = bad ? nan : row[at];
+                ss[i] = first ? -row[h + at] : row[h + at];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = pair(cc[2 * i], cc[2 * i + 1]), s[i] = pair(ss[2 * i], ss[2 * i + 1]);
         }
+    }
+
+    __device__ __forceinline__ void transpose() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = mul2(s[i], both(-1.f));
     }
 
     // The partners of a lane's elements x (v: as pairs), 0 for those that do not turn.  Whole-warp call.
@@ -242,9 +260,9 @@ struct Turn {
     }
 };
 
-__device__ __forceinline__ float norm_scale(const Args& a, float sq) {
-    return a.norm == 0 ? 1.f : rsqrtf((a.norm == 1 ? sq / float(a.D) : sq) + a.eps);
-}
+// r of a row, from its sum of squares (inv: 1 / D for rms, 1 for l2)
+__device__ __forceinline__ float norm_scale(const Args& a, float sq, float inv) { return rsqrtf(fmaf(sq, inv, a.eps)); }
+__device__ __forceinline__ float mean_factor(const Args& a) { return a.norm == 1 ? 1.f / float(a.D) : 1.f; }
 
 template <int LANES, bool kFast>
 __device__ __forceinline__ float* row_buffer(int e0) {
@@ -253,17 +271,18 @@ __device__ __forceinline__ float* row_buffer(int e0) {
     return buf[threadIdx.x >> 5] + ((threadIdx.x & 31) / LANES) * (LANES * 8) + e0;
 }
 
-// The heads of a token in groups of kU * 32 / LANES rows, those of q and then those of k: a warp
-// takes every split-th group of its token.  The next group's loads are issued before this group's
-// arithmetic, and a token's first ones before its cos and sin, which wait for its position.
+// A warp takes 32 / LANES tokens side by side, LANES lanes each, and their heads in groups of kU,
+// those of q and then those of k: every split-th group.  (Rows of one token side by side instead
+// leave lanes idle where the heads are few: one head of 64 over 123,000 tokens took 251 us that way.)
+// The next group's loads are issued before this group's arithmetic, and the first ones of a token
+// before its cos and sin, which wait for its position.
 template <int LANES, int kU>
 struct Groups {
-    static constexpr int kRows = 32 / LANES;  // rows that a warp takes at once
-    static constexpr int kHeads = kRows * kU;
-    int nq, n;                                // groups of q, and all
-    __device__ __forceinline__ explicit Groups(const Args& a) : nq((a.Hq + kHeads - 1) / kHeads), n(nq + (a.Hk + kHeads - 1) / kHeads) {}
+    static constexpr int kTokens = 32 / LANES;
+    int nq, n;  // groups of q, and all
+    __device__ __forceinline__ explicit Groups(const Args& a) : nq((a.Hq + kU - 1) / kU), n(nq + (a.Hk + kU - 1) / kU) {}
     __device__ __forceinline__ bool of_q(int g) const { return g < nq; }
-    __device__ __forceinline__ int head(int g) const { return (g < nq ? g : g - nq) * kHeads; }
+    __device__ __forceinline__ int head(int g) const { return (g < nq ? g : g - nq) * kU; }
 };
 
 // Row of head h of x: of the input, with its strides, or of a contiguous [B * T, H, D].
@@ -286,30 +305,31 @@ __device__ __forceinline__ void weights(const float* w, bool live, int e0, uint6
 template <typename T, int LANES, bool kInter, bool kFast, int kU>
 __global__ void __launch_bounds__(kWarps * 32, 3) qkr_forward_kernel(const __grid_constant__ Args a) {
     const int lane = threadIdx.x & 31, e0 = (lane % LANES) * 8, sub = lane / LANES;
-    // (tokens * split: a split is taken where the tokens are few, so the items fit 32 bits)
-    const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t n = item / uint32_t(a.split);
-    if (n >= int64_t(a.B) * a.T) return;
-    int b, t;
-    place(a, n, b, t);
-    float* buf = row_buffer<LANES, kFast>(e0);
     const Groups<LANES, kU> groups(a);
-    constexpr int kRows = Groups<LANES, kU>::kRows;
-    const bool live = e0 < a.D;
+    constexpr int kTokens = Groups<LANES, kU>::kTokens;
+    // (tokens * split: a split is taken where the tokens are few, so the items fit 32 bits)
+    const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5), set = item / uint32_t(a.split);
+    const int64_t first = int64_t(set) * kTokens, tokens = int64_t(a.B) * a.T, n = first + sub;
+    if (first >= tokens) return;
+    const bool live = e0 < a.D && n < tokens;
+    int b, t;
+    place(a, n < tokens ? n : first, b, t);
+    float* buf = row_buffer<LANES, kFast>(e0);
     const int p = position(a, b, t);
+    const float inv = mean_factor(a);
     auto fetch = [&](int g, Raw<T>* x) {
         const bool q = groups.of_q(g);
-        const int h0 = groups.head(g) + sub, left = (q ? a.Hq : a.Hk) - h0;
-        const int64_t hs = kRows * (q ? a.qs[2] : a.ks[2]);
+        const int h0 = groups.head(g), left = (q ? a.Hq : a.Hk) - h0;
+        const int64_t hs = q ? a.qs[2] : a.ks[2];
         const T* from = row_in<T>(a, q, b, t, h0) + e0;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             x[u].zero();
-            if (live && u * kRows < left) x[u].load(from + u * hs);
+            if (live && u < left) x[u].load(from + u * hs);
         }
     };
     Raw<T> x[kU];
-    int g = int(item - uint32_t(n) * uint32_t(a.split));
+    int g = int(item - set * uint32_t(a.split));
     if (g < groups.n) fetch(g, x);
     for (int side = 0; side < 2; ++side) {  // q's groups, then k's
         const bool q = side == 0;
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qkr_forward_kernel(const __gri
         for (; g < end; g += a.split) {
             Raw<T> ahead[kU];
             if (g + a.split < groups.n) fetch(g + a.split, ahead);
-            const int h0 = groups.head(g) + sub, left = (q ? a.Hq : a.Hk) - h0;
+            const int h0 = groups.head(g), left = (q ? a.Hq : a.Hk) - h0;
             T* to = out + row_at(a, q, n, h0) + e0;
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
@@ -343,11 +363,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) qkr_forward_kernel(const __gri
                     uint64_t sq = mul2(v[0], v[0]);
 #pragma unroll
                     for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq);
-                    r = both(norm_scale(a, row_sum<LANES>(sq)));
+                    r = both(norm_scale(a, row_sum<LANES>(sq), inv));
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i] = mul2(r, fma2(o[i], turn.s[i], mul2(v[i], turn.c[i])));
-                if (live && u * kRows < left) store8(to + u * kRows * a.D, v);
+                if (live && u < left) store8(to + u * a.D, v);
             }
 #pragma unroll
             for (int u = 0; u < kU; ++u) x[u] = ahead[u];
@@ -363,22 +383,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
     const int lane = threadIdx.x & 31, e0 = (lane % LANES) * 8, sub = lane / LANES;
     float* buf = row_buffer<LANES, kFast>(e0);
     const Groups<LANES, kU> groups(a);
-    constexpr int kRows = Groups<LANES, kU>::kRows;
-    const bool live = e0 < a.D;
+    constexpr int kTokens = Groups<LANES, kU>::kTokens;
     uint64_t dw[2][4];  // of q's and k's weights
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = 0;
-    const float inv = a.norm == 1 ? 1.f / float(a.D) : 1.f;
+    const float inv = mean_factor(a);
     const int64_t tokens = int64_t(a.B) * a.T;
-    // a warp keeps its part of every step-th token; warps that are left over have none
+    // a warp keeps its part of every step-th set of tokens; warps that are left over have none
     const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5), part = warp % a.split;
-    const int step = gridDim.x * kWarps / a.split;
-    int64_t n = warp < step * a.split ? warp / a.split : tokens;
+    const int64_t step = int64_t(gridDim.x * kWarps / a.split) * kTokens;
+    int64_t first = warp < int(gridDim.x) * kWarps / a.split * a.split ? int64_t(warp / a.split) * kTokens : tokens, n = 0;
     int b = 0, t = 0;
+    bool live = false;
+    auto begin = [&]() {  // this lane's token of the set
+        n = first + sub;
+        live = e0 < a.D && n < tokens;
+        place(a, n < tokens ? n : first, b, t);
+    };
     auto fetch = [&](int g, Raw<T>* x, Raw<T>* d) {
         const bool q = groups.of_q(g);
-        const int h0 = groups.head(g) + sub, left = (q ? a.Hq : a.Hk) - h0;
-        const int64_t hs = kRows * (q ? a.qs[2] : a.ks[2]);
+        const int h0 = groups.head(g), left = (q ? a.Hq : a.Hk) - h0;
+        const int64_t hs = q ? a.qs[2] : a.ks[2];
         const T* from = row_in<T>(a, q, b, t, h0) + e0;
         const T* grad = static_cast<const T*>(q ? a.gq : a.gk) + row_at(a, q, n, h0) + e0;
         const bool need = a.norm || (q ? a.wq : a.wk) != nullptr;
@@ -386,29 +411,31 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
         for (int u = 0; u < kU; ++u) {
             x[u].zero();
             d[u].zero();
-            if (live && u * kRows < left) {
-                d[u].load(grad + u * kRows * a.D);
+            if (live && u < left) {
+                d[u].load(grad + u * a.D);
                 if (need) x[u].load(from + u * hs);
             }
         }
     };
-    if (n < tokens && part < groups.n) {
+    if (first < tokens && part < groups.n) {
         Raw<T> x[kU], dy[kU];
-        place(a, n, b, t);
+        begin();
         int p = position(a, b, t), g = part;
         fetch(g, x, dy);
         uint64_t w[4];
         while (true) {
             Turn<T, LANES, kInter, kFast> turn;
             turn.load(a, p, e0, lane);
+            turn.transpose();
             const int64_t n0 = n;
+            const bool live0 = live;
             bool more = true;
 #pragma unroll
             for (int side = 0; side < 2; ++side) {  // q's groups, then k's
                 const bool q = side == 0;
                 const int end = q ? groups.nq : groups.n;
                 if (g >= end) continue;
-                weights(q ? a.wq : a.wk, live, e0, w);
+                weights(q ? a.wq : a.wk, e0 < a.D, e0, w);
                 T* out = static_cast<T*>(q ? a.qo : a.ko);
                 while (g < end) {
                     // the group after this one: of this token, or the first of the warp's next token
@@ -416,17 +443,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
                     Raw<T> ax[kU], ad[kU];
                     g += a.split;
                     if (g >= groups.n) {
-                        n += step;
-                        more = n < tokens;
+                        first += step;
+                        more = first < tokens;
                         if (more) {
-                            place(a, n, b, t);
+                            begin();
                             p = position(a, b, t);
                             fetch(part, ax, ad);
                         }
                     } else {
                         fetch(g, ax, ad);
                     }
-                    const int h0 = groups.head(g0) + sub, left = (q ? a.Hq : a.Hk) - h0;
+                    const int h0 = groups.head(g0), left = (q ? a.Hq : a.Hk) - h0;
                     T* to = out + row_at(a, q, n0, h0) + e0;
 #pragma unroll
                     for (int u = 0; u < kU; ++u) {
@@ -435,7 +462,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
                         dy[u].pairs(d);
                         turn.partners(a, dy[u], d, e0, buf, o);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) d[i] = sub2(mul2(d[i], turn.c[i]), mul2(o[i], turn.s[i]));
+                        for (int i = 0; i < 4; ++i) d[i] = fma2(o[i], turn.s[i], mul2(d[i], turn.c[i]));
                         uint64_t dv[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) dv[i] = mul2(d[i], v[i]), d[i] = mul2(d[i], w[i]);
@@ -444,7 +471,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
                             uint64_t sq = mul2(v[0], v[0]), ux = mul2(dv[0], w[0]);
 #pragma unroll
                             for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq), ux = fma2(dv[i], w[i], ux);
-                            const float r = norm_scale(a, row_sum<LANES>(sq)), m = r * r * row_sum<LANES>(ux) * inv;
+                            const float r = norm_scale(a, row_sum<LANES>(sq), inv), m = r * r * row_sum<LANES>(ux) * inv;
                             r2 = both(r);
                             const uint64_t m2 = both(-m);
 #pragma unroll
@@ -452,7 +479,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) dw[side][i] = fma2(dv[i], r2, dw[side][i]);
-                        if (live && u * kRows < left) store8(to + u * kRows * a.D, d);
+                        if (live0 && u < left) store8(to + u * a.D, d);
                     }
 #pragma unroll
                     for (int u = 0; u < kU; ++u) x[u] = ax[u], dy[u] = ad[u];
@@ -495,6 +522,191 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
     }
 }
 
+// ---------------------------------------------------------------------------
+// The same with the rows brought in by bulk copies: each warp owns two stages of shared memory and
+// fills one with the next item (all of q's or of k's heads of a token, their gradients, and the
+// token's row of the table) while it works on the other.  The loop above waits for memory between
+// its groups (115 + 161 us at 32768 tokens of 16 + 16 heads of 128 in bf16, 57% of the copy rate);
+// this one needs a token's heads side by side in memory, and enough of them to be worth a copy.
+// ---------------------------------------------------------------------------
+template <bool kBack>
+struct Stream {
+    static constexpr int kWarps = kBack ? 12 : 8;      // of a block
+    static constexpr int kBlocks = kBack ? 1 : 3;      // blocks a multiprocessor
+    static constexpr uint32_t kMost = 222 * 1024 / (kWarps * kBlocks * 2) / 128 * 128;  // bytes of a stage
+    static uint32_t stage(const Args& a, int es) {
+        return uint32_t((a.Hq > a.Hk ? a.Hq : a.Hk) * a.D * es * (kBack ? 2 : 1) + a.R * 4);
+    }
+};
+
+template <typename T, int LANES, bool kInter, bool kBack>
+__global__ void __launch_bounds__(Stream<kBack>::kWarps * 32, Stream<kBack>::kBlocks) qkr_stream_kernel(const __grid_constant__ Args a, const uint32_t stage_bytes) {
+    constexpr int kW = Stream<kBack>::kWarps;
+    constexpr int kRows = 32 / LANES;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[kW][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = (lane % LANES) * 8, sub = lane / LANES;
+    const bool live = e0 < a.D;
+    const uint32_t tokens = uint32_t(a.B) * uint32_t(a.T), step = gridDim.x * kW;
+    uint8_t* mine = smem + warp * 2 * stage_bytes;
+    if (lane == 0) {
+        tc::mbar_init(tc::smem_u32(&full[warp][0]), 1);
+        tc::mbar_init(tc::smem_u32(&full[warp][1]), 1);
+        tc::mbar_fence_init();
+    }
+    __syncwarp();
+    const uint32_t row_q = a.Hq * a.D * sizeof(T), row_k = a.Hk * a.D * sizeof(T), row_t = a.R * 4;
+    // stage s <- tensor `side` of token n, whose position is p
+    auto fetch = [&](uint32_t n, int side, int p, int s) {
+        if (tc::elect()) {
+            int b, t;
+            place(a, n, b, t);
+            const uint32_t bar = tc::smem_u32(&full[warp][s]), at = tc::smem_u32(mine + s * stage_bytes), row = side ? row_k : row_q;
+            tc::mbar_expect_tx(bar, row * (kBack ? 2 : 1) + row_t);
+            tc::bulk_load(at, row_in<T>(a, !side, b, t, 0), row, bar);
+            if (kBack) tc::bulk_load(at + row, static_cast<const T*>(side ? a.gk : a.gq) + row_at(a, !side, n, 0), row, bar);
+            if (row_t) tc::bulk_load(at + (kBack ? 2 : 1) * row, a.table + int64_t(p < 0 ? 0 : p) * a.R, row_t, bar);
+        }
+        __syncwarp();
+    };
+    auto position_of = [&](uint32_t n) {
+        int b, t;
+        place(a, n, b, t);
+        return position(a, b, t);
+    };
+    uint64_t dw[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[0][i] = dw[1][i] = 0;
+    const float inv = mean_factor(a);
+    uint32_t n = blockIdx.x * kW + warp;
+    int p = 0, ahead = 0;  // positions of this token and the next
+    if (n < tokens) {
+        p = position_of(n);
+        fetch(n, 0, p, 0);
+        fetch(n, 1, p, 1);
+        if (n + step < tokens) ahead = position_of(n + step);
+    }
+    uint32_t phase = 0;
+    for (; n < tokens; n += step, phase ^= 1) {
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {  // q in stage 0, k in stage 1
+            const int heads = side ? a.Hk : a.Hq;
+            const float* wt = side ? a.wk : a.wq;
+            const uint32_t row = side ? row_k : row_q;
+            const uint8_t* at = mine + side * stage_bytes;
+            tc::mbar_wait(tc::smem_u32(&full[warp][side]), phase);
+            __syncwarp();
+            Turn<T, LANES, kInter, true> turn;
+            turn.load(a, reinterpret_cast<const float*>(at + (kBack ? 2 : 1) * row), p < 0, e0, lane);
+            uint64_t w[4];
+            if (kBack) {
+                turn.transpose();
+                weights(wt, live, e0, w);
+            } else if (wt != nullptr && live) {
+                load_pairs(wt + e0, w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    turn.c[i] = mul2(turn.c[i], w[i]);
+                    turn.s[i] = mul2(turn.s[i], pair(__ldg(wt + turn.partner(a, e0 + 2 * i)), __ldg(wt + turn.partner(a, e0 + 2 * i + 1))));
+                }
+            }
+            T* to = static_cast<T*>(side ? a.ko : a.qo) + row_at(a, !side, n, sub) + e0;
+            const T* from = reinterpret_cast<const T*>(at) + sub * a.D + e0;
+            const int left = live ? heads - sub : 0, stride = kRows * a.D;
+            const bool whole = a.D == LANES * 8 && heads % kRows == 0;  // no lane is ever idle
+#pragma unroll 4
+            for (int h0 = 0; h0 < heads; h0 += kRows, to += stride, from += stride) {
+                const bool on = whole || h0 < left;
+                Raw<T> x;
+                if (!whole) x.zero();
+                if (on) x.shared(from);
+                uint64_t v[4], o[4];
+                x.pairs(v);
+                if (!kBack) {
+                    turn.partners(a, x, v, e0, nullptr, o);
+                    uint64_t r = both(1.f);
+                    if (a.norm) {
+                        uint64_t sq = mul2(v[0], v[0]);
+#pragma unroll
+                        for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq);
+                        r = both(norm_scale(a, row_sum<LANES>(sq), inv));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = mul2(r, fma2(o[i], turn.s[i], mul2(v[i], turn.c[i])));
+                    if (on) store8(to, v);
+                } else {
+                    Raw<T> dy;
+                    if (!whole) dy.zero();
+                    if (on) dy.shared(from + heads * a.D);
+                    uint64_t d[4];
+                    dy.pairs(d);
+                    turn.partners(a, dy, d, e0, nullptr, o);
+                    uint64_t dv[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        d[i] = fma2(o[i], turn.s[i], mul2(d[i], turn.c[i]));
+                        dv[i] = mul2(d[i], v[i]);
+                        d[i] = mul2(d[i], w[i]);
+                    }
+                    uint64_t r2 = both(1.f);
+                    if (a.norm) {
+                        uint64_t sq = mul2(v[0], v[0]), ux = mul2(dv[0], w[0]);
+#pragma unroll
+                        for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq), ux = fma2(dv[i], w[i], ux);
+                        const float r = norm_scale(a, row_sum<LANES>(sq), inv), m = r * r * row_sum<LANES>(ux) * inv;
+                        r2 = both(r);
+                        const uint64_t m2 = both(-m);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[i] = mul2(r2, fma2(v[i], m2, d[i]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dw[side][i] = fma2(dv[i], r2, dw[side][i]);
+                    if (on) store8(to, d);
+                }
+            }
+            __syncwarp();  // the stage has been read
+            if (n + step < tokens) fetch(n + step, side, ahead, side);
+        }
+        p = ahead;
+        if (uint64_t(n) + 2 * uint64_t(step) < tokens) ahead = position_of(n + 2 * step);
+    }
+    if constexpr (kBack) {
+        if (a.part == nullptr) return;
+        float x[2][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                uint32_t u, v;
+                unpair(dw[which][i], u, v);
+                x[which][2 * i] = __uint_as_float(u), x[which][2 * i + 1] = __uint_as_float(v);
+            }
+        __syncthreads();  // every warp is done with its stages
+        float* sum = reinterpret_cast<float*>(smem);  // [warp][2][LANES * 8]
+#pragma unroll
+        for (int which = 0; which < 2; ++which)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                for (int o = LANES; o < 32; o <<= 1) x[which][i] += __shfl_xor_sync(kAll, x[which][i], o);
+                if (sub == 0) sum[(warp * 2 + which) * LANES * 8 + e0 + i] = x[which][i];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * a.D; i += kW * 32) {
+            const int which = i / a.D, e = i % a.D;
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) y += sum[(w * 2 + which) * LANES * 8 + e];
+            a.part[(int64_t(blockIdx.x) * 2 + which) * a.D + e] = y;
+        }
+    }
+}
+
+__global__ void read_flag_kernel(int* out, int clear) {
+    *out = tc::g_timeout_flag;
+    if (clear) tc::g_timeout_flag = 0;
+}
+
 // dw[which][e] = sum over blocks of the partials: a block per 8 elements of one weight, 32
 // threads an element.
 __global__ void __launch_bounds__(256) qkr_weight_kernel(const float* part, int blocks, int D, float* dwq, float* dwk) {
@@ -516,39 +728,61 @@ __global__ void __launch_bounds__(256) qkr_weight_kernel(const float* part, int 
 
 constexpr int kBackwardBlocks = 4;  // blocks a multiprocessor of the backward grid
 
-// Warps of a token: one where the tokens alone fill the multiprocessors (the token's cos and
-// sin are then read once), else as many as there are groups of heads.
+// Warps of a set of 32 / lanes tokens: one where the sets alone fill the multiprocessors (a token's
+// cos and sin are then read once), else up to as many as there are groups of heads.
+int64_t sets_of(const Args& a, int lanes) { return (int64_t(a.B) * a.T * lanes + 31) / 32; }
 int split_of(const Args& a, int lanes, int unroll) {
-    const int heads = 32 / lanes * unroll;
-    const int groups = (a.Hq + heads - 1) / heads + (a.Hk + heads - 1) / heads;
-    const int64_t want = int64_t(tc::sm_count()) * 32, tokens = int64_t(a.B) * a.T;
-    if (tokens >= want) return 1;
-    const int64_t s = (want + tokens - 1) / tokens;
+    const int groups = (a.Hq + unroll - 1) / unroll + (a.Hk + unroll - 1) / unroll;
+    const int64_t want = int64_t(tc::sm_count()) * 32, sets = sets_of(a, lanes);
+    if (sets >= want) return 1;
+    const int64_t s = (want + sets - 1) / sets;
     return int(s < groups ? s : groups);
 }
 
 template <typename T, int LANES, bool kInter, bool kFast, int kU>
 void launch_forward(Args a, cudaStream_t s) {
     a.split = split_of(a, LANES, kU);
-    const int64_t items = int64_t(a.B) * a.T * a.split;
+    const int64_t items = sets_of(a, LANES) * a.split;
     qkr_forward_kernel<T, LANES, kInter, kFast, kU>
         <<<unsigned((items + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(a);
 }
 
+// The streaming kernel: heads side by side, rows of a token worth a copy that fit a stage, and more
+// tokens than the grid has warps.
+template <typename T, int LANES, bool kInter, bool kBack>
+bool stream(const Args& a, int* blocks, cudaStream_t s) {
+    using S = Stream<kBack>;
+    const uint32_t bytes = (S::stage(a, sizeof(T)) + 127) / 128 * 128;
+    const int rows = 32 / LANES, few = a.Hq < a.Hk ? a.Hq : a.Hk, grid = tc::sm_count() * S::kBlocks;
+    const int64_t tokens = int64_t(a.B) * a.T;
+    if ((a.Hq > 1 && a.qs[2] != a.D) || (a.Hk > 1 && a.ks[2] != a.D) || bytes > S::kMost || few < 2 * rows ||
+        few * a.D * int(sizeof(T)) < 1024 || tokens < 2 * int64_t(grid) * S::kWarps || (kBack && grid > *blocks))
+        return false;
+    auto f = qkr_stream_kernel<T, LANES, kInter, kBack>;
+    size_t smem = size_t(bytes) * 2 * S::kWarps;
+    if (kBack && smem < size_t(S::kWarps) * 2 * LANES * 8 * 4) smem = size_t(S::kWarps) * 2 * LANES * 8 * 4;
+    if (!tc::set_smem(f, smem)) return false;
+    f<<<grid, S::kWarps * 32, smem, s>>>(a, bytes);
+    *blocks = grid;
+    return true;
+}
+
 template <typename T, int LANES, bool kInter, bool kFast>
-void launch(Args a, bool back, int blocks, cudaStream_t s) {
+void launch(Args a, bool back, int* blocks_used, cudaStream_t s) {
+    const int blocks = *blocks_used;
+    if (kFast && (back ? stream<T, LANES, kInter, true>(a, blocks_used, s) : stream<T, LANES, kInter, false>(a, blocks_used, s))) return;
     if (back) {
         a.split = min(split_of(a, LANES, 2), blocks * kWarps);
         qkr_backward_kernel<T, LANES, kInter, kFast><<<blocks, kWarps * 32, 0, s>>>(a);
-    } else if (kFast && int64_t(a.B) * a.T >= int64_t(tc::sm_count()) * 8) {
+    } else if (kFast && a.Hq >= 4 && sets_of(a, LANES) >= int64_t(tc::sm_count()) * 8) {
         launch_forward<T, LANES, kInter, kFast, !kFast ? 1 : sizeof(T) == 4 ? 2 : 4>(a, s);
-    } else {  // few tokens: one group of heads a warp
+    } else {  // few tokens or heads: one head at a time
         launch_forward<T, LANES, kInter, kFast, 1>(a, s);
     }
 }
 
 template <typename T, int LANES>
-void pick_layout(const Args& a, bool back, int blocks, cudaStream_t s) {
+void pick_layout(const Args& a, bool back, int* blocks, cudaStream_t s) {
     const bool fast = a.R % (a.inter ? 8 : 16) == 0;
     if (a.inter) {
         if (fast) launch<T, LANES, true, true>(a, back, blocks, s);
@@ -560,7 +794,7 @@ void pick_layout(const Args& a, bool back, int blocks, cudaStream_t s) {
 }
 
 template <typename T>
-void pick_lanes(const Args& a, bool back, int blocks, cudaStream_t s) {
+void pick_lanes(const Args& a, bool back, int* blocks, cudaStream_t s) {
     if (a.D <= 32) pick_layout<T, 4>(a, back, blocks, s);
     else if (a.D <= 64) pick_layout<T, 8>(a, back, blocks, s);
     else if (a.D <= 128) pick_layout<T, 16>(a, back, blocks, s);
@@ -601,7 +835,7 @@ rm_status check(const rm_cp_qkr_problem* p, Args* a) {
     return RM_OK;
 }
 
-rm_status run(const rm_cp_qkr_problem* p, const Args& a, bool back, int blocks, cudaStream_t s) {
+rm_status run(const rm_cp_qkr_problem* p, const Args& a, bool back, int* blocks, cudaStream_t s) {
     if (p->dtype == RM_F32) pick_lanes<float>(a, back, blocks, s);
     else pick_lanes<__nv_bfloat16>(a, back, blocks, s);
     note_launch(1);
@@ -624,6 +858,16 @@ rm_status aligned_or_null(const void* p, const char* name) { return p == nullptr
 
 }  // namespace
 }  // namespace qkr
+}  // namespace rmcp
+
+namespace rmcp {
+rm_status qkr_read_timeout_flag(int* host_flag, int clear, int* dev_scratch, cudaStream_t s) {
+    qkr::read_flag_kernel<<<1, 1, 0, s>>>(dev_scratch, clear);
+    if (!launch_ok()) return RM_ERR_CUDA;
+    note_launch(1);
+    if (cudaMemcpyAsync(host_flag, dev_scratch, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess) return RM_ERR_CUDA;
+    return cudaStreamSynchronize(s) == cudaSuccess ? RM_OK : RM_ERR_CUDA;
+}
 }  // namespace rmcp
 
 #define RM_QKR_NEED(ptr)                            \
@@ -665,7 +909,8 @@ rm_status rm_cp_qkr_forward(const rm_cp_qkr_problem* p, const void* q, const voi
     a.q = q, a.k = k, a.wq = wq, a.wk = wk, a.table = table, a.qo = q_out, a.ko = k_out;
     a.pos = a.pos_rows > 0 ? positions : nullptr;
     rmcp::begin_launches();
-    return rmcp::qkr::run(p, a, false, 0, reinterpret_cast<cudaStream_t>(stream));
+    int none = 0;
+    return rmcp::qkr::run(p, a, false, &none, reinterpret_cast<cudaStream_t>(stream));
 }
 
 rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const void* k, const float* wq,
@@ -697,10 +942,10 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
     a.q = q, a.k = k, a.wq = wq, a.wk = wk, a.table = table, a.gq = dq_out, a.gk = dk_out, a.qo = dq, a.ko = dk;
     a.pos = a.pos_rows > 0 ? positions : nullptr;
     a.part = weights ? static_cast<float*>(ws) : nullptr;
-    const int blocks = rmcp::qkr::backward_blocks(int64_t(a.B) * a.T);
+    int blocks = rmcp::qkr::backward_blocks(int64_t(a.B) * a.T);  // those that left partial sums
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     rmcp::begin_launches();
-    st = rmcp::qkr::run(p, a, true, blocks, s);
+    st = rmcp::qkr::run(p, a, true, &blocks, s);
     if (st != RM_OK || !weights) return st;
     rmcp::qkr::qkr_weight_kernel<<<dim3(a.D / 8, 2), 256, 0, s>>>(a.part, blocks, a.D, dwq, dwk);
     rmcp::note_launch(1);
