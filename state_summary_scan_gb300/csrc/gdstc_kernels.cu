@@ -17,6 +17,10 @@
 //                      the state, laid out as the walk copies them in
 //   gds_walk_kernel    one CTA per (sequence, head, 128 columns of values): the chain over the
 //                      sequence's chunks
+// Where the sequences and heads are too few to fill the GPU, long sequences are cut into segments.  A
+// segment's map of the state is affine, S -> M S + dS: a first walk takes the first segment, and each
+// inner one from zero (dS) and from the identity without values (M); gds_compose_kernel then carries
+// the states from segment to segment, and a second walk takes the segments after the first from them.
 //
 // The walk is bound by the latency of its chain: S -> W S -> D~ -> K^T D~ -> S.  It keeps S
 // transposed, a value column a lane, so that every step of the chain is a row of tensor memory per
@@ -46,6 +50,8 @@ constexpr uint32_t T8 = kTileBytes;      // one [64][64] bf16 tile
 constexpr uint32_t kGateBytes = 1024;    // the scale of O (weak) or of Q S [64], dec [64], e^{b_63}, weak (1 or 0)
 constexpr int kDec = 64, kEnd = 128, kWeak = 129;
 constexpr float kForget = -110.f;        // e^{-110} is 0 in fp32: lower gates are raised to it
+constexpr int kMostSegments = 12;
+constexpr int kMostStates = 152 * 3;     // of segments: see segments()
 constexpr float kWeakLimit = 60.f;       // decays within a chunk that factor through its end
 
 // Factors of a (chunk, head) in the workspace: P, -W (Dk / 64 swizzled tiles), the gates, then
@@ -533,9 +539,28 @@ struct WalkBars {
     uint64_t s_ready[2], x_done[2], o_done[2], o_free[2], dt_ready, d_ready, d_done, fixed;
 };
 
-template <int DK, typename TS>
+// How a launch of the walk divides the sequences.
+//   whole   a CTA per sequence
+//   first   blockIdx.z = 0: the first segment; z = j > 0: inner segment j, its dS and (one more
+//           block of columns) its M
+//   rest    blockIdx.z = j: segment j + 1, from the state that segment j ends with
+enum class Part { whole, first, rest };
+struct Segments {
+    int chunks;      // of a segment
+    int most;        // segments of the longest sequence
+    float* ends;     // [S][H][most][Dk][Dv]: states at the segments' ends (dS before they are composed)
+    float* maps;     // [S][H][most][Dk][Dk]: M
+};
+__device__ __forceinline__ float* end_of(const Args& a, const Segments& g, int seq, int h, int j) {
+    return g.ends + ((int64_t(seq) * a.H + h) * g.most + j) * a.Dk * a.Dv;
+}
+__device__ __forceinline__ float* map_of(const Args& a, const Segments& g, int seq, int h, int j) {
+    return g.maps + ((int64_t(seq) * a.H + h) * g.most + j) * a.Dk * a.Dk;
+}
+
+template <int DK, typename TS, Part kPart>
 __global__ void __launch_bounds__(kWalkThreads, 1)
-    gds_walk_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+    gds_walk_kernel(const __grid_constant__ Args a, const Segments seg, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                     const __grid_constant__ CUtensorMap mo) {
     constexpr int NP = DK / 64;
     constexpr int GC = DK / kGroups;       // state rows (columns of tensor memory) of a group
@@ -547,10 +572,23 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     __shared__ uint32_t tmem_slot;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int blocks = (a.Dv + 127) / 128;
-    const int h = blockIdx.x / blocks, v0 = (blockIdx.x % blocks) * 128, nv = min(a.Dv - v0, 128);
+    const int vblocks = (a.Dv + 127) / 128, blocks = vblocks + (kPart == Part::first ? 1 : 0);
+    const int h = blockIdx.x / blocks, vb = blockIdx.x % blocks;
+    const bool map = vb == vblocks;  // the columns are those of M
+    const int v0 = map ? 0 : vb * 128, nv = map ? DK : min(a.Dv - v0, 128);
     const Seq sq = sequence(a, blockIdx.y);
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + v0;
+    const int all = (sq.len + kChunk - 1) / kChunk;  // the sequence's chunks
+    // this CTA's segment and its chunks
+    const int j = kPart == Part::whole ? 0 : int(blockIdx.z) + (kPart == Part::rest ? 1 : 0);
+    const int c_first = kPart == Part::whole ? 0 : j * seg.chunks;
+    const bool ends = kPart == Part::whole || c_first + seg.chunks >= all;  // it is the sequence's last
+    const int chunks = (ends ? all : c_first + seg.chunks) - c_first;
+    if (kPart != Part::whole) {
+        if (j > 0 && (sq.slot < 0 || chunks <= 0)) return;
+        if (kPart == Part::first && ((j > 0 && ends) || (j == 0 && map))) return;
+    }
+    const bool outs = kPart != Part::first || j == 0;  // it has outputs
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((int64_t(sq.begin) + int64_t(c_first) * kChunk) * a.H + h) * a.Dv + v0;
     const int64_t os = int64_t(a.H) * a.Dv;
     TS* st = static_cast<TS*>(a.state) + (int64_t(max(sq.slot, 0)) * a.H + h) * DK * a.Dv + v0;
     if (sq.slot < 0) {  // padding
@@ -563,7 +601,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             for (int i = tid; i < DK * nv; i += kWalkThreads) st[int64_t(i / nv) * a.Dv + i % nv] = from_f32<TS>(0.f);
         return;
     }
-    const int chunks = (sq.len + kChunk - 1) / kChunk, last = sq.len - (chunks - 1) * kChunk;
+    const int last = ends ? sq.len - (all - 1) * kChunk : kChunk;  // tokens of the last chunk
     const bool ragged = last < kChunk;
     const int quads = (nv + 31) / 32;  // quadrants of tensor-memory lanes with columns
 
@@ -572,8 +610,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             for (uint64_t* b : {&bar.u_full[i], &bar.w_free[i], &bar.k_free[i], &bar.q_free[i], &bar.p_full[i],
                                 &bar.p_free[i], &bar.o_done[i]})
                 mbar_init(smem_u32(b), 1);
-            mbar_init(smem_u32(&bar.x_done[i]), 2);  // the state's update, and Q S, which reads the old one
-            mbar_init(smem_u32(&bar.wkq_full[i]), 3);
+            mbar_init(smem_u32(&bar.x_done[i]), outs ? 2 : 1);  // the state's update, and Q S, which reads the old one
+            mbar_init(smem_u32(&bar.wkq_full[i]), outs ? 3 : 2);
             mbar_init(smem_u32(&bar.u_free[i]), quads * kGroups);
             mbar_init(smem_u32(&bar.s_ready[i]), quads * kGroups / 2);
             mbar_init(smem_u32(&bar.o_free[i]), quads);
@@ -581,7 +619,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         for (int i = 0; i < kGateRing; ++i) mbar_init(smem_u32(&bar.gates[i]), 1);
         mbar_init(smem_u32(&bar.dt_ready), quads * kGroups);
         mbar_init(smem_u32(&bar.d_ready), quads * kGroups);
-        mbar_init(smem_u32(&bar.d_done), 2);  // W S, and P D of the chunks before, whose D~ is overwritten
+        mbar_init(smem_u32(&bar.d_done), outs ? 2 : 1);  // W S, and P D of the chunks before, whose D~ is overwritten
         mbar_init(smem_u32(&bar.fixed), quads * kGroups);
         mbar_fence_init();
     }
@@ -596,20 +634,31 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         return reinterpret_cast<const float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
     };
 
-    if (warp < 4 * kGroups + 4 && (warp & 3) >= quads) {
-        // no columns
+    if (warp < 4 * kGroups + 4 && ((warp & 3) >= quads || (!outs && warp >= 4 * kGroups))) {
+        // no columns, or no outputs
     } else if (warp < 4 * kGroups) {
         // ---- the chain: a lane is a value column, a group a quarter of the state's rows and of the tokens
         const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
         const bool live = row < nv;
-        TS* mine = st + int64_t(grp * GC) * a.Dv + row;
+        const int r0 = grp * GC;  // the first of this thread's rows
 #pragma unroll
-        for (int j = 0; j < GC; j += 16) {
+        for (int i0 = 0; i0 < GC; i0 += 16) {
             uint32_t x[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(live && !sq.fresh ? to_f32(mine[int64_t(j + i) * a.Dv]) : 0.f);
-            tmem_st<16>(tl + TM_X + grp * GC + j, x);
+            for (int i = 0; i < 16; ++i) {
+                const int r = r0 + i0 + i;
+                float y = 0.f;
+                if (kPart == Part::whole || (kPart == Part::first && j == 0)) {
+                    if (live && !sq.fresh) y = to_f32(st[int64_t(r) * a.Dv + row]);
+                } else if (kPart == Part::first) {
+                    y = map && r == row ? 1.f : 0.f;
+                } else if (live) {
+                    y = end_of(a, seg, blockIdx.y, h, j - 1)[int64_t(r) * a.Dv + v0 + row];
+                }
+                x[i] = __float_as_uint(y);
+            }
+            tmem_st<16>(tl + TM_X + r0 + i0, x);
         }
         tmem_wait_st();
         for (int c = 0; c < chunks; ++c) {
@@ -649,11 +698,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 tc_fence_before();
                 warp_arrive(&bar.s_ready[2 * grp / kGroups], lane);
             }
-            wait(&bar.u_full[c & 1], (c >> 1) & 1, dead);
+            if (!map) wait(&bar.u_full[c & 1], (c >> 1) & 1, dead);
             ulonglong2 u[GT / 4];
 #pragma unroll
             for (int i = 0; i < GT / 4; ++i)
-                u[i] = (reinterpret_cast<const ulonglong2*>(smem + L::U + (c & 1) * L::u))[(GT / 4 * grp + i) * int(u_cols(a.Dv)) + row];
+                u[i] = map ? make_ulonglong2(0, 0)
+                           : (reinterpret_cast<const ulonglong2*>(smem + L::U + (c & 1) * L::u))[(GT / 4 * grp + i) * int(u_cols(a.Dv)) + row];
             wait(&bar.d_done, c & 1, dead);
             tc_fence_after();
             uint32_t x[GT], hi[GT / 2], lo[GT / 2];
@@ -687,7 +737,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 mbar_arrive(smem_u32(&bar.dt_ready));
                 mbar_arrive(smem_u32(&bar.u_free[c & 1]));
             }
-            if (!weak) {  // and D itself, for P D
+            if (!weak && outs) {  // and D itself, for P D
 #pragma unroll
                 for (int i = 0; i < GT / 2; ++i) split2(pair(x[2 * i], x[2 * i + 1]), hi[i], lo[i]);
                 tmem_st<GT / 2>(tl + TM_DH + GT / 2 * grp, hi);
@@ -702,9 +752,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         uint32_t x[GC];
         tmem_ld<GC>(tl + TM_X + grp * GC, x);
         tmem_wait_ld();
-        if (live) {
+        if (live && ends) {
 #pragma unroll
-            for (int i = 0; i < GC; ++i) mine[int64_t(i) * a.Dv] = from_f32<TS>(__uint_as_float(x[i]));
+            for (int i = 0; i < GC; ++i) st[int64_t(r0 + i) * a.Dv + row] = from_f32<TS>(__uint_as_float(x[i]));
+        } else if (live && kPart == Part::first) {
+            float* to = map ? map_of(a, seg, blockIdx.y, h, j) + row : end_of(a, seg, blockIdx.y, h, j) + v0 + row;
+#pragma unroll
+            for (int i = 0; i < GC; ++i) to[int64_t(r0 + i) * (map ? DK : a.Dv)] = __uint_as_float(x[i]);
         }
         tc_fence_before();
     } else if (warp < 4 * kGroups + 4) {
@@ -761,7 +815,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (whole) {
                 if (warp == 4 * kGroups && lane == 0) {
                     for (int p = 0; p < (nv + 63) / 64; ++p)
-                        tma_store_3d(&mo, smem_u32(tile + p * T8), v0 + 64 * p, h, sq.begin + c * kChunk);
+                        tma_store_3d(&mo, smem_u32(tile + p * T8), v0 + 64 * p, h, sq.begin + (c_first + c) * kChunk);
                     bulk_commit();
                 }
             } else {
@@ -818,6 +872,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             __syncwarp();
         }
         for (int g = 0; g < 2; ++g) wait(&bar.x_done[g], (chunks - 1) & 1, dead);
+    } else if (warp == 4 * kGroups + 5 && !outs) {
+        // nothing beside the chain
     } else if (warp == 4 * kGroups + 5) {
         // ---- the products beside the chain, while it reads D: P D~ of the chunk before, then Q S
         const uint32_t base = smem_u32(smem);
@@ -882,14 +938,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     } else {
         // ---- the copies: each piece of chunk c once the products that read chunk c - 2's are done
         const uint32_t base = smem_u32(smem), ub = u_bytes(a.Dv), uat = factor_u(DK) + (v0 / 128) * ub;
-        const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y)) * a.H + h) * factor_bytes(DK, a.Dv);
+        const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y) + c_first) * a.H + h) * factor_bytes(DK, a.Dv);
         for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * factor_bytes(DK, a.Dv)) {
-            const int i = c & 1, ph = ((c >> 1) & 1) ^ 1, tok = sq.begin + c * kChunk;
+            const int i = c & 1, ph = ((c >> 1) & 1) ^ 1, tok = sq.begin + (c_first + c) * kChunk;
             wait(&bar.u_free[i], ph, dead);
             if (elect()) {
                 const uint32_t b = smem_u32(&bar.u_full[i]);
-                mbar_expect_tx(b, ub);
-                bulk_load(base + L::U + i * L::u, fac + uat, ub, b);
+                if (!map) {
+                    mbar_expect_tx(b, ub);
+                    bulk_load(base + L::U + i * L::u, fac + uat, ub, b);
+                }
                 // the gates of chunk c - 8 are read: the products have waited for the outputs of chunk c - 5
                 const uint32_t g = smem_u32(&bar.gates[c % kGateRing]);
                 mbar_expect_tx(g, kGateBytes);
@@ -903,38 +961,123 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 bulk_load(base + L::W + i * L::w, fac + T8, NP * T8, b);
             }
             __syncwarp();
-            wait(&bar.q_free[i], ph, dead);
-            if (elect()) {
-                mbar_expect_tx(b, NP * T8);
-                for (int p = 0; p < NP; ++p) tma_load_3d(base + L::Q + i * L::q + p * T8, &mq, 64 * p, h / a.hdiv, tok, b);
+            if (outs) {
+                wait(&bar.q_free[i], ph, dead);
+                if (elect()) {
+                    mbar_expect_tx(b, NP * T8);
+                    for (int p = 0; p < NP; ++p) tma_load_3d(base + L::Q + i * L::q + p * T8, &mq, 64 * p, h / a.hdiv, tok, b);
+                }
+                __syncwarp();
             }
-            __syncwarp();
             wait(&bar.k_free[i], ph, dead);
             if (elect()) {
                 mbar_expect_tx(b, NP * T8);
                 for (int p = 0; p < NP; ++p) tma_load_3d(base + L::K + i * L::k + p * T8, &mk, 64 * p, h / a.hdiv, tok, b);
             }
             __syncwarp();
-            wait(&bar.p_free[i], ph, dead);
-            if (elect()) {
-                const uint32_t pb = smem_u32(&bar.p_full[i]);
-                mbar_expect_tx(pb, T8);
-                bulk_load(base + L::P + i * T8, fac, T8, pb);
+            if (outs) {
+                wait(&bar.p_free[i], ph, dead);
+                if (elect()) {
+                    const uint32_t pb = smem_u32(&bar.p_full[i]);
+                    mbar_expect_tx(pb, T8);
+                    bulk_load(base + L::P + i * T8, fac, T8, pb);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         // no copy outlives the CTA
         for (int c = max(chunks - 2, 0); c < chunks; ++c) {
             const int i = c & 1, ph = (c >> 1) & 1;
-            wait(&bar.u_full[i], ph, dead);
+            if (!map) wait(&bar.u_full[i], ph, dead);
             wait(&bar.wkq_full[i], ph, dead);
-            wait(&bar.p_full[i], ph, dead);
+            if (outs) wait(&bar.p_full[i], ph, dead);
             gates_of(c);
         }
     }
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// The states at the segments' ends, in order: E_j = M_j E_{j-1} + dS_j, E_0 from the first segment.
+// A CTA takes 16 columns of a (sequence, head), a thread two columns and every 32nd row; M_j is copied
+// in whole, the next one meanwhile.  fp32 throughout.
+constexpr int kComposeCols = 16;
+template <int DK>
+struct ComposeSmem {
+    static constexpr uint32_t pitch = DK * 4 + 16, map = DK * pitch;  // rows in different banks
+    static constexpr uint32_t E = 2 * map;
+    static constexpr size_t bytes = E + DK * kComposeCols * 4 + 128;
+};
+template <int DK>
+__global__ void __launch_bounds__(256) gds_compose_kernel(const __grid_constant__ Args a, const Segments seg) {
+    constexpr int R = DK / 32;  // rows of a thread
+    using L = ComposeSmem<DK>;
+    extern __shared__ __align__(128) uint8_t compose_smem[];
+    __shared__ __align__(8) uint64_t full[2];
+    float2* E = reinterpret_cast<float2*>(compose_smem + L::E);  // [Dk][8] pairs of columns
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blocks = (a.Dv + kComposeCols - 1) / kComposeCols;
+    const int h = blockIdx.x / blocks, v0 = (blockIdx.x % blocks) * kComposeCols;
+    const Seq sq = sequence(a, blockIdx.y);
+    const int segs = ((sq.len + kChunk - 1) / kChunk + seg.chunks - 1) / seg.chunks;
+    if (sq.slot < 0 || segs < 3) return;
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&full[0]), 1);
+        mbar_init(smem_u32(&full[1]), 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+    auto fetch = [&](int j) {  // M_j, by the first warp
+        const uint32_t bar = smem_u32(&full[j & 1]), to = smem_u32(compose_smem + (j & 1) * L::map);
+        const float* M = map_of(a, seg, blockIdx.y, h, j);
+        if (lane == 0) mbar_expect_tx(bar, DK * DK * 4);
+        __syncwarp();
+        for (int r = lane; r < DK; r += 32) bulk_load(to + r * L::pitch, M + r * DK, DK * 4, bar);
+    };
+    if (warp == 0) {
+        fetch(1);
+        if (3 < segs) fetch(2);
+    }
+    const int c = lane & 7, r0 = 4 * warp + (lane >> 3);
+    const bool live = v0 + 2 * c < a.Dv;  // (Dv is a multiple of 8)
+    auto load = [&](int j, float2* x) {
+        const float* end = end_of(a, seg, blockIdx.y, h, j) + v0 + 2 * c;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            x[i] = live ? *reinterpret_cast<const float2*>(end + int64_t(r0 + 32 * i) * a.Dv) : make_float2(0.f, 0.f);
+    };
+    float2 x[R], ahead[R];
+    load(0, x);
+    load(1, ahead);
+#pragma unroll
+    for (int i = 0; i < R; ++i) E[(r0 + 32 * i) * 8 + c] = x[i];
+    for (int j = 1; j + 1 < segs; ++j) {
+        float* end = end_of(a, seg, blockIdx.y, h, j) + v0 + 2 * c;
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[i] = ahead[i];
+        if (j + 2 < segs) load(j + 1, ahead);
+        mbar_wait(smem_u32(&full[j & 1]), ((j - 1) >> 1) & 1);
+        __syncthreads();  // and E of the segment before
+        const uint8_t* M = compose_smem + (j & 1) * L::map;
+#pragma unroll 8
+        for (int k = 0; k < DK; k += 4) {
+            const float2 e0 = E[k * 8 + c], e1 = E[(k + 1) * 8 + c], e2 = E[(k + 2) * 8 + c], e3 = E[(k + 3) * 8 + c];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float4 m = *reinterpret_cast<const float4*>(M + (r0 + 32 * i) * L::pitch + k * 4);
+                x[i].x = fmaf(m.w, e3.x, fmaf(m.z, e2.x, fmaf(m.y, e1.x, fmaf(m.x, e0.x, x[i].x))));
+                x[i].y = fmaf(m.w, e3.y, fmaf(m.z, e2.y, fmaf(m.y, e1.y, fmaf(m.x, e0.y, x[i].y))));
+            }
+        }
+        __syncthreads();
+        if (warp == 0 && j + 3 < segs) fetch(j + 2);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            E[(r0 + 32 * i) * 8 + c] = x[i];
+            if (live) *reinterpret_cast<float2*>(end + int64_t(r0 + 32 * i) * a.Dv) = x[i];
+        }
+    }
 }
 
 __global__ void read_flag_kernel(int* out, int clear) {
@@ -956,6 +1099,23 @@ rm_status fail(const char* what, bool map) {
     return api_fail(RM_ERR_CUDA, msg);
 }
 
+size_t factors_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk, a.Dv); }
+
+// Segments of the longest sequence (1: not cut), and their chunks.  With n segments the chain is
+// two walks of 1 / n of the chunks, so at least three are wanted, of four chunks or more, and as many
+// as keep the first walk's CTAs (one per block of columns for the first segment, one more for M in
+// each inner one) on the GPU at once.
+int segments(const Args& a, int* chunks) {
+    const int all = (a.max_len + kChunk - 1) / kChunk, blocks = (a.Dv + 127) / 128;
+    const int each = 152 / (a.H * a.S);  // CTAs of a sequence's head
+    int n = each > blocks ? 2 + (each - blocks) / (blocks + 1) : 1;
+    n = n < kMostSegments ? n : kMostSegments;
+    n = n < all / 4 ? n : all / 4;
+    if (n < 3) return 1;
+    *chunks = (all + n - 1) / n;
+    return (all + *chunks - 1) / *chunks;
+}
+
 template <int DK>
 rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     CUtensorMap mq, mk, mv, mo;
@@ -969,11 +1129,32 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     ff<<<dim3(unsigned(chunk_slots(a)), unsigned(a.H)), 256, kFactorSmem, s>>>(a, mq, mk, mv);
     note_launch(1);
     if (!launch_ok()) return fail("launch of the factors", false);
-    auto fw = state_dt == RM_F32 ? gds_walk_kernel<DK, float> : gds_walk_kernel<DK, __nv_bfloat16>;
-    if (!set_smem(fw, WalkSmem<DK>::bytes)) return fail("shared-memory attribute of the walk", false);
-    fw<<<dim3(unsigned((a.Dv + 127) / 128 * a.H), unsigned(a.S)), kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, mq, mk, mo);
+    Segments seg{0, 1, nullptr, nullptr};
+    const int segs = segments(a, &seg.chunks);
+    const unsigned blocks = unsigned((a.Dv + 127) / 128);
+    auto walk = [&](auto f, dim3 grid) {
+        if (!set_smem(f, WalkSmem<DK>::bytes)) return fail("shared-memory attribute of the walk", false);
+        f<<<grid, kWalkThreads, WalkSmem<DK>::bytes, s>>>(a, seg, mq, mk, mo);
+        note_launch(1);
+        return launch_ok() ? RM_OK : fail("launch of the walk", false);
+    };
+    const bool f = state_dt == RM_F32;
+    if (segs < 3)
+        return f ? walk(gds_walk_kernel<DK, float, Part::whole>, dim3(blocks * a.H, a.S))
+                 : walk(gds_walk_kernel<DK, __nv_bfloat16, Part::whole>, dim3(blocks * a.H, a.S));
+    seg.most = segs;
+    seg.ends = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + factors_bytes(a));
+    seg.maps = seg.ends + int64_t(a.S) * a.H * segs * a.Dk * a.Dv;
+    const dim3 g1((blocks + 1) * a.H, a.S, segs - 1), g2(blocks * a.H, a.S, segs - 1);
+    rm_status st = f ? walk(gds_walk_kernel<DK, float, Part::first>, g1) : walk(gds_walk_kernel<DK, __nv_bfloat16, Part::first>, g1);
+    if (st != RM_OK) return st;
+    auto fc = gds_compose_kernel<DK>;
+    if (!set_smem(fc, ComposeSmem<DK>::bytes)) return fail("shared-memory attribute of the composition", false);
+    fc<<<dim3(unsigned((a.Dv + kComposeCols - 1) / kComposeCols * a.H), unsigned(a.S)), 256, ComposeSmem<DK>::bytes, s>>>(a, seg);
     note_launch(1);
-    if (!launch_ok()) return fail("launch of the walk", false);
+    if (!launch_ok()) return fail("launch of the composition", false);
+    st = f ? walk(gds_walk_kernel<DK, float, Part::rest>, g2) : walk(gds_walk_kernel<DK, __nv_bfloat16, Part::rest>, g2);
+    if (st != RM_OK) return st;
     return RM_OK;
 }
 
@@ -983,7 +1164,11 @@ bool tc_supports(const Args& a, rm_dtype dt) {
     return dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
 }
 
-size_t tc_workspace_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk, a.Dv); }
+// A smaller problem may be cut into more segments than this one: the bound is that of all of them,
+// since the sequences' heads times their segments stay below the multiprocessors' number and a half.
+size_t tc_workspace_bytes(const Args& a) {
+    return factors_bytes(a) + size_t(kMostStates) * (size_t(a.Dk) * a.Dv + size_t(a.Dk) * a.Dk) * sizeof(float);
+}
 
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     return a.Dk == 64 ? launch<64>(a, state_dt, s) : launch<128>(a, state_dt, s);
