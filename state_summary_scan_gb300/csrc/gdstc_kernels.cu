@@ -1000,13 +1000,13 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 }
 
 // The states at the segments' ends, in order: E_j = M_j E_{j-1} + dS_j, E_0 from the first segment.
-// A CTA takes 16 columns of a (sequence, head), a thread two columns and every 32nd row; M_j is copied
-// in whole, the next one meanwhile.  fp32 throughout.
+// A CTA takes 16 columns of a (sequence, head), a thread two columns and every 32nd row; the next M_j
+// waits in registers while this one, in shared memory, is worked on.  fp32 throughout.
 constexpr int kComposeCols = 16;
 template <int DK>
 struct ComposeSmem {
     static constexpr uint32_t pitch = DK * 4 + 16, map = DK * pitch;  // rows in different banks
-    static constexpr uint32_t E = 2 * map;
+    static constexpr uint32_t E = map;
     static constexpr size_t bytes = E + DK * kComposeCols * 4 + 128;
 };
 template <int DK>
@@ -1014,7 +1014,6 @@ __global__ void __launch_bounds__(256) gds_compose_kernel(const __grid_constant_
     constexpr int R = DK / 32;  // rows of a thread
     using L = ComposeSmem<DK>;
     extern __shared__ __align__(128) uint8_t compose_smem[];
-    __shared__ __align__(8) uint64_t full[2];
     float2* E = reinterpret_cast<float2*>(compose_smem + L::E);  // [Dk][8] pairs of columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int blocks = (a.Dv + kComposeCols - 1) / kComposeCols;
@@ -1022,23 +1021,14 @@ __global__ void __launch_bounds__(256) gds_compose_kernel(const __grid_constant_
     const Seq sq = sequence(a, blockIdx.y);
     const int segs = ((sq.len + kChunk - 1) / kChunk + seg.chunks - 1) / seg.chunks;
     if (sq.slot < 0 || segs < 3) return;
-    if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&full[0]), 1);
-        mbar_init(smem_u32(&full[1]), 1);
-        mbar_fence_init();
-    }
-    __syncthreads();
-    auto fetch = [&](int j) {  // M_j, by the first warp
-        const uint32_t bar = smem_u32(&full[j & 1]), to = smem_u32(compose_smem + (j & 1) * L::map);
-        const float* M = map_of(a, seg, blockIdx.y, h, j);
-        if (lane == 0) mbar_expect_tx(bar, DK * DK * 4);
-        __syncwarp();
-        for (int r = lane; r < DK; r += 32) bulk_load(to + r * L::pitch, M + r * DK, DK * 4, bar);
+    constexpr int N = DK * DK / 4 / 256;  // 16-byte units of M a thread
+    float4 m4[N];
+    auto fetch = [&](int j) {
+        const float4* M = reinterpret_cast<const float4*>(map_of(a, seg, blockIdx.y, h, j)) + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m4[i] = M[i * 256];
     };
-    if (warp == 0) {
-        fetch(1);
-        if (3 < segs) fetch(2);
-    }
+    fetch(1);
     const int c = lane & 7, r0 = 4 * warp + (lane >> 3);
     const bool live = v0 + 2 * c < a.Dv;  // (Dv is a multiple of 8)
     auto load = [&](int j, float2* x) {
@@ -1056,10 +1046,17 @@ __global__ void __launch_bounds__(256) gds_compose_kernel(const __grid_constant_
         float* end = end_of(a, seg, blockIdx.y, h, j) + v0 + 2 * c;
 #pragma unroll
         for (int i = 0; i < R; ++i) x[i] = ahead[i];
-        if (j + 2 < segs) load(j + 1, ahead);
-        mbar_wait(smem_u32(&full[j & 1]), ((j - 1) >> 1) & 1);
-        __syncthreads();  // and E of the segment before
-        const uint8_t* M = compose_smem + (j & 1) * L::map;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = threadIdx.x + i * 256;
+            *reinterpret_cast<float4*>(compose_smem + at / (DK / 4) * L::pitch + at % (DK / 4) * 16) = m4[i];
+        }
+        if (j + 2 < segs) {
+            load(j + 1, ahead);
+            fetch(j + 1);
+        }
+        __syncthreads();  // M and E are in place
+        const uint8_t* M = compose_smem;
 #pragma unroll 8
         for (int k = 0; k < DK; k += 4) {
             const float2 e0 = E[k * 8 + c], e1 = E[(k + 1) * 8 + c], e2 = E[(k + 2) * 8 + c], e3 = E[(k + 3) * 8 + c];
@@ -1070,8 +1067,7 @@ __global__ void __launch_bounds__(256) gds_compose_kernel(const __grid_constant_
                 x[i].y = fmaf(m.w, e3.y, fmaf(m.z, e2.y, fmaf(m.y, e1.y, fmaf(m.x, e0.y, x[i].y))));
             }
         }
-        __syncthreads();
-        if (warp == 0 && j + 3 < segs) fetch(j + 2);
+        __syncthreads();  // and have been read
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             E[(r0 + 32 * i) * 8 + c] = x[i];
