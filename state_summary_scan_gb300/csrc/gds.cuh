@@ -53,7 +53,7 @@ __device__ __forceinline__ Seq sequence(const Args& a, int i) {
 }
 
 // The chunked form on the tensor cores, for calls whose longest sequence has this many tokens.
-constexpr int kChunkedLen = 48;
+constexpr int kChunkedLen = 40;
 bool tc_supports(const Args& a, rm_dtype dt);
 size_t tc_workspace_bytes(const Args& a);
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s);

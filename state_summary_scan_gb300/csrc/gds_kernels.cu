@@ -14,6 +14,7 @@
 // One CTA per 32 columns keeps the loads in flight per thread to 32 registers and gives even one
 // sequence of 16 heads 32 or more CTAs.
 #include <cstdio>
+#include <type_traits>
 
 #include "gds.cuh"
 
@@ -301,18 +302,359 @@ __global__ void __launch_bounds__(kTpb, NT == 1 ? 8 : 5) gds_token_kernel(const 
     }
 }
 
-template <typename T, typename TS>
-bool token_launch(const Args& a, cudaStream_t s) {
-    const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
-    // a state's traffic bounds single tokens; several are taken four at a time
-    const bool one = a.max_len <= 1;
-    auto f = a.Dk == 16   ? (one ? gds_token_kernel<T, TS, 16, 1> : gds_token_kernel<T, TS, 16, 4>)
-             : a.Dk == 32 ? (one ? gds_token_kernel<T, TS, 32, 1> : gds_token_kernel<T, TS, 32, 4>)
-             : a.Dk == 64 ? (one ? gds_token_kernel<T, TS, 64, 1> : gds_token_kernel<T, TS, 64, 4>)
-                          : (one ? gds_token_kernel<T, TS, 128, 1> : gds_token_kernel<T, TS, 128, 4>);
+// ---------------------------------------------------------------------------
+// bf16 inputs, several tokens: four at a time as products of the warp's matrix instructions.  The
+// four tokens' keys and queries are the eight columns of one m16n8k16 product with 16 value columns
+// of the state as its rows, and the update of 16 values by 8 keys is one product over 16 = 4 tokens x
+// 4 parts.  (A product of the larger matrix unit has 64 rows or more and would leave through tensor
+// memory; these tiles never leave the registers.)  A warp owns 16 value columns and all of Dk, so
+// that no two warps meet; the lanes' rows and columns are permuted such that the state's elements
+// are loaded and stored straight from the registers that enter the products, in pieces of a row of
+// 32 (bf16) or 64 bytes (fp32), four adjacent pieces to a block.
+//
+// Keys and queries are bf16 and enter as they are.  A bf16 state enters its first tile as it is; a
+// state in fp32, and d of a token, as the sum of three bf16, which hold its 24 bits.  Products
+// accumulate in fp32.
+// ---------------------------------------------------------------------------
+// D += A B, bf16: A [16][16] by rows, B [16][8] by columns, D [16][8] fp32
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Row r of a lane's Dk / 4 rows of the state, less its first: runs of kRun rows go to the four lanes
+// of a group in turn, so that they read a key side by side.
+template <int DK>
+struct Rows {
+    static constexpr int kRun = DK < 32 ? DK / 4 : 8;
+    static __device__ __forceinline__ constexpr int at(int r) { return r / kRun * 4 * kRun + r % kRun; }
+};
+
+// A lane's DK / 8 pairs of a key or query, or zeros
+template <int DK>
+__device__ __forceinline__ void load_pairs(const __nv_bfloat16* p, bool live, uint32_t* x) {
+#pragma unroll
+    for (int i = 0; i < DK / 8; ++i) x[i] = 0;
+    if (!live) return;
+    if (DK < 32) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        x[0] = u.x, x[1] = u.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < DK / 8; i += 4) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + Rows<DK>::at(2 * i)));
+            x[i] = u.x, x[i + 1] = u.y, x[i + 2] = u.z, x[i + 3] = u.w;
+        }
+    }
+}
+
+// N adjacent words
+template <int N>
+__device__ __forceinline__ void load_words(const void* p, uint32_t* x) {
+    if (N == 1) {
+        x[0] = *static_cast<const uint32_t*>(p);
+    } else if (N == 2) {
+        const uint2 u = *static_cast<const uint2*>(p);
+        x[0] = u.x, x[1] = u.y;
+    } else {
+        const uint4 u = *static_cast<const uint4*>(p);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* x) {
+    if (N == 1) *static_cast<uint32_t*>(p) = x[0];
+    else if (N == 2) *static_cast<uint2*>(p) = make_uint2(x[0], x[1]);
+    else *static_cast<uint4*>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// The state of a warp, W times 16 columns: lane (g, t) = (lane / 4, lane % 4) holds columns 2W g ..
+// 2W g + 2W - 1, two for each product, of its rows.  Element [w][b][c] is the pair of rows 2b, 2b + 1 of
+// column 2w + c.  kPacked keeps the pairs of bf16 that were read: a state of one tile.
+template <int DK, int W, bool kPacked>
+struct TileState {
+    using Pair = typename std::conditional<kPacked, uint32_t, uint64_t>::type;
+    Pair x[W][DK / 8][2];
+
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int b = 0; b < DK / 8; ++b) x[w][b][0] = x[w][b][1] = 0;
+    }
+    __device__ __forceinline__ void put(int w, int b, int c, uint32_t p) {
+        if constexpr (kPacked) x[w][b][c] = p;
+        else x[w][b][c] = widen2(p);
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int Dv) {
+#pragma unroll
+        for (int b = 0; b < DK / 8; ++b) {
+            uint32_t u[W], v[W];
+            load_words<W>(p + Rows<DK>::at(2 * b) * Dv, u);
+            load_words<W>(p + (Rows<DK>::at(2 * b) + 1) * Dv, v);
+#pragma unroll
+            for (int w = 0; w < W; ++w) put(w, b, 0, __byte_perm(u[w], v[w], 0x5410)), put(w, b, 1, __byte_perm(u[w], v[w], 0x7632));
+        }
+    }
+    __device__ __forceinline__ void load(const float* p, int Dv) {
+#pragma unroll
+        for (int b = 0; b < DK / 8; ++b) {
+            uint32_t u[2 * W], v[2 * W];
+            load_words<2 * W>(p + Rows<DK>::at(2 * b) * Dv, u);
+            load_words<2 * W>(p + (Rows<DK>::at(2 * b) + 1) * Dv, v);
+#pragma unroll
+            for (int w = 0; w < W; ++w) x[w][b][0] = pair(u[2 * w], v[2 * w]), x[w][b][1] = pair(u[2 * w + 1], v[2 * w + 1]);
+        }
+    }
+    __device__ __forceinline__ uint64_t at(int w, int b, int c) const {
+        if constexpr (kPacked) return widen2(x[w][b][c]);
+        else return x[w][b][c];
+    }
+    // y += S^T [k; q], from the lane's pairs of the keys and queries
+    __device__ __forceinline__ void product(const uint32_t* kq, float (*y)[4]) const {
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            float z[2][4] = {};
+#pragma unroll
+            for (int s = 0; s < DK / 16; ++s) {
+                if constexpr (kPacked) {
+                    const uint32_t a[4] = {x[w][2 * s][0], x[w][2 * s][1], x[w][2 * s + 1][0], x[w][2 * s + 1][1]};
+                    mma(s & 1 ? z[0] : y[w], a, kq[2 * s], kq[2 * s + 1]);
+                } else {
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) split2(x[w][2 * s + i / 2][i % 2], hi[i], mid[i], lo[i]);
+                    mma(z[1], lo, kq[2 * s], kq[2 * s + 1]);
+                    mma(z[0], mid, kq[2 * s], kq[2 * s + 1]);
+                    mma(y[w], hi, kq[2 * s], kq[2 * s + 1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[w][i] += z[0][i] + z[1][i];
+        }
+    }
+};
+
+// Rows 2b and 2b + 1 of a lane's columns, each product's as it leaves: (column 0, rows), (column 1, rows)
+template <int DK, int W>
+__device__ __forceinline__ void store_rows(__nv_bfloat16* p, int b, int Dv, const float (*c)[4]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint32_t x[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) x[w] = pack2(c[w][e], c[w][2 + e]);
+        store_words<W>(p + (Rows<DK>::at(2 * b) + e) * Dv, x);
+    }
+}
+template <int DK, int W>
+__device__ __forceinline__ void store_rows(float* p, int b, int Dv, const float (*c)[4]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint32_t x[2 * W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) x[2 * w] = __float_as_uint(c[w][e]), x[2 * w + 1] = __float_as_uint(c[w][2 + e]);
+        store_words<2 * W>(p + (Rows<DK>::at(2 * b) + e) * Dv, x);
+    }
+}
+
+template <typename TS, int DK, int W, bool kPacked>
+__global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant__ Args a) {
+    constexpr int NP = DK / 8, kRun = Rows<DK>::kRun;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int blocks = (a.Dv + 16 * W - 1) / (16 * W);
+    const int unit = blockIdx.x * (kTpb / 32) + (threadIdx.x >> 5), h = unit / blocks;
+    if (h >= a.H) return;
+    const int col = unit % blocks * 16 * W + 2 * W * g;
+    const bool live = col < a.Dv;  // Dv is a multiple of 8
+    const Seq sq = sequence(a, blockIdx.y);
+    if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + col;
+    const int64_t os = int64_t(a.H) * a.Dv;
+    if (sq.slot < 0) {  // padding
+        const uint32_t zeros[W] = {};
+        for (int i = t; i < sq.len; i += 4)
+            if (live) store_words<W>(o + i * os, zeros);
+        return;
+    }
+    TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * a.Dk + kRun * t) * a.Dv + col;
+    TileState<DK, W, kPacked> S;
+    if (live && !sq.fresh) S.load(st, a.Dv);
+    else S.zero();
+    const int hk = h / a.hdiv;
+    // this lane's key or query of a tile; the two keys of its terms of the update; its values
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1];
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + col;
+    const int64_t kqs = g < 4 ? a.ks[0] : a.qs[0];
+    const __nv_bfloat16* kq_row = (g < 4 ? k : q) + (g & 3) * kqs + kRun * t;
+    const int i0 = 2 * (t & 1);  // the lane's tokens i0 and i0 + 1
+    const __nv_bfloat16* up_row = k + i0 * a.ks[0] + kRun * (g >> 1);
+    const uint32_t half = g & 1 ? 0x7632 : 0x5410;
+    const float* gate = a.g + sq.begin * a.gs + h;
+    const float* beta = a.beta + sq.begin * a.bs + h;
+
+    uint32_t kq[NP], vx[4][W];
+    float al1, be1;  // the gate and beta of token t
+    auto fetch = [&](int t0) {
+        const int n = sq.len - t0;
+        load_pairs<DK>(kq_row + t0 * kqs, (g & 3) < n, kq);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int w = 0; w < W; ++w) vx[i][w] = 0;
+            if (live && i < n) load_words<W>(v + (t0 + i) * a.vs[0], vx[i]);
+        }
+        al1 = t < n ? __ldg(gate + (t0 + t) * a.gs) : 0.f;
+        be1 = t < n ? __ldg(beta + (t0 + t) * a.bs) : 0.f;
+    };
+    if (sq.len > 0) fetch(0);
+    for (int t0 = 0; t0 < sq.len; t0 += 4) {
+        const int n = min(sq.len - t0, 4);
+        // y: columns 0 .. 3 of the product are S^T k, 4 .. 7 S^T q; kk: row i of them times column r
+        float y[W][4] = {}, kk[4] = {};
+        S.product(kq, y);
+#pragma unroll
+        for (int s = 0; s < DK / 16; ++s) {
+            const uint32_t rows[4] = {kq[2 * s], 0u, kq[2 * s + 1], 0u};
+            mma(kk, rows, kq[2 * s], kq[2 * s + 1]);
+        }
+        const float al_t = expf(al1), be_t = be1;
+        uint64_t vf[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int w = 0; w < W; ++w) vf[i][w] = widen2(vx[i][w]);
+        if (!kPacked && t0 + 4 < sq.len) fetch(t0 + 4);
+        // the tile's triangle, every lane for its columns, two at a time
+        uint64_t d[4][W], out[2][W];
+        float total = 1.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float al = __shfl_sync(kAllLanes, al_t, i, 4), be = __shfl_sync(kAllLanes, be_t, i, 4);
+            total *= al;
+            const uint64_t al2 = pair(al, al), be2 = pair(be, be), to2 = pair(total, total), neg2 = pair(-total, -total);
+            uint64_t x[W], z[W];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float s0 = __shfl_sync(kAllLanes, y[w][i & 1], i >> 1, 4), s1 = __shfl_sync(kAllLanes, y[w][2 + (i & 1)], i >> 1, 4);
+                x[w] = fma2(neg2, pair(s0, s1), vf[i][w]);
+                z[w] = mul2(to2, pair(y[w][i & 1], y[w][2 + (i & 1)]));  // lanes t >= 2: S^T q of i0 and i0 + 1
+            }
+#pragma unroll
+            for (int r = 0; r < i; ++r) {
+                const float kr = -__shfl_sync(kAllLanes, kk[r & 1], 4 * i + (r >> 1));
+                const float qr = __shfl_sync(kAllLanes, kk[r & 1], 16 + 4 * i + (r >> 1));
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    d[r][w] = mul2(al2, d[r][w]);
+                    x[w] = fma2(pair(kr, kr), d[r][w], x[w]);
+                    z[w] = fma2(pair(qr, qr), d[r][w], z[w]);
+                }
+            }
+            const float qi = __shfl_sync(kAllLanes, kk[i & 1], 16 + 4 * i + (i >> 1));
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                d[i][w] = mul2(be2, x[w]);
+                z[w] = fma2(pair(qi, qi), d[i][w], z[w]);
+                if (i < 2 || t & 1) out[i & 1][w] = z[w];
+            }
+        }
+        if (t >= 2 && live) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t r[W];
+#pragma unroll
+                for (int w = 0; w < W; ++w) r[w] = pack2(mul2(pair(a.scale, a.scale), out[e][w]));
+                if (i0 + e < n) store_words<W>(o + (t0 + i0 + e) * os, r);
+            }
+        }
+        // the update, S <- G S + k d^T.  Terms 2t, 2t + 1 of a product are the first or second part of d of
+        // the lane's tokens, terms 8 + 2t, 9 + 2t the third or nothing
+        uint32_t da[W][4];
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            uint32_t d0[2], d1[2], hi, mid, lo;
+            unpair(t & 1 ? d[2][w] : d[0][w], d0[0], d0[1]);
+            unpair(t & 1 ? d[3][w] : d[1][w], d1[0], d1[1]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                split2(pair(d0[c], d1[c]), hi, mid, lo);
+                da[w][c] = t < 2 ? hi : mid;
+                da[w][2 + c] = t < 2 ? lo : 0u;
+            }
+        }
+        uint32_t ku[2][NP];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) load_pairs<DK>(up_row + (t0 + e) * a.ks[0], i0 + e < n, ku[e]);
+        const uint64_t al = pair(total, total);
+#pragma unroll
+        for (int b = 0; b < NP; ++b) {
+            const uint32_t kb = __byte_perm(ku[0][b], ku[1][b], half);
+            float c[W][4];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                uint32_t x[4];
+                unpair(mul2(al, S.at(w, b, 0)), x[0], x[1]);
+                unpair(mul2(al, S.at(w, b, 1)), x[2], x[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[w][i] = __uint_as_float(x[i]);
+                mma(c[w], da[w], kb, kb);
+                if constexpr (!kPacked) S.x[w][b][0] = pair(c[w][0], c[w][1]), S.x[w][b][1] = pair(c[w][2], c[w][3]);
+            }
+            if (kPacked && live) store_rows<DK, W>(st, b, a.Dv, c);
+        }
+    }
+    if (live && (!kPacked || sq.len <= 0)) {
+#pragma unroll
+        for (int b = 0; b < NP; ++b) {
+            float c[W][4];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                uint32_t x[4];
+                unpair(S.at(w, b, 0), x[0], x[1]);
+                unpair(S.at(w, b, 1), x[2], x[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) c[w][i] = __uint_as_float(x[i]);
+            }
+            store_rows<DK, W>(st, b, a.Dv, c);
+        }
+    }
+}
+
+template <typename TS, int W, bool kPacked>
+bool tile_launch(const Args& a, cudaStream_t s) {
+    const int64_t units = int64_t((a.Dv + 16 * W - 1) / (16 * W)) * a.H;
+    const dim3 grid(unsigned((units + kTpb / 32 - 1) / (kTpb / 32)), unsigned(a.S));
+    auto f = a.Dk == 16   ? gds_tile_kernel<TS, 16, W, kPacked>
+             : a.Dk == 32 ? gds_tile_kernel<TS, 32, W, kPacked>
+             : a.Dk == 64 ? gds_tile_kernel<TS, 64, W, kPacked>
+                          : gds_tile_kernel<TS, 128, W, kPacked>;
     f<<<grid, kTpb, 0, s>>>(a);
     note_launch(1);
     return launch_ok();
+}
+
+template <typename T, typename TS, int NT>
+bool token_launch(const Args& a, cudaStream_t s) {
+    const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
+    auto f = a.Dk == 16   ? gds_token_kernel<T, TS, 16, NT>
+             : a.Dk == 32 ? gds_token_kernel<T, TS, 32, NT>
+             : a.Dk == 64 ? gds_token_kernel<T, TS, 64, NT>
+                          : gds_token_kernel<T, TS, 128, NT>;
+    f<<<grid, kTpb, 0, s>>>(a);
+    note_launch(1);
+    return launch_ok();
+}
+
+template <typename TS>
+bool recurrence(const Args& a, bool f32, cudaStream_t s) {
+    const bool one = a.max_len <= 1;
+    if (f32) return one ? token_launch<float, TS, 1>(a, s) : token_launch<float, TS, 4>(a, s);
+    if (one) return token_launch<__nv_bfloat16, TS, 1>(a, s);
+    if constexpr (sizeof(TS) == 2)
+        if (a.max_len <= 4) return tile_launch<TS, 2, true>(a, s);
+    return tile_launch<TS, 1, false>(a, s);
 }
 
 rm_status check(const rm_gdr_state_problem* p, Args* a) {
@@ -418,9 +760,8 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
     }
     begin_launches();
     const bool sf = p->state_dtype == RM_F32;
-    const bool ok = p->dtype == RM_F32 ? (sf ? gds::token_launch<float, float>(a, s) : gds::token_launch<float, __nv_bfloat16>(a, s))
-                                       : (sf ? gds::token_launch<__nv_bfloat16, float>(a, s)
-                                             : gds::token_launch<__nv_bfloat16, __nv_bfloat16>(a, s));
+    const bool f32 = p->dtype == RM_F32;
+    const bool ok = sf ? gds::recurrence<float>(a, f32, s) : gds::recurrence<__nv_bfloat16>(a, f32, s);
     if (ok) return RM_OK;
     char msg[256];
     std::snprintf(msg, sizeof(msg), "gated delta rule with a carried state: launch failed: %s", cuda_error_text());

@@ -115,21 +115,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
-__device__ __forceinline__ uint32_t pack2(uint64_t p) {
-    uint32_t x, y;
-    unpair(p, x, y);
-    return pack2(__uint_as_float(x), __uint_as_float(y));
-}
-// p as the sum of two bf16 pairs
-__device__ __forceinline__ void split2(uint64_t p, uint32_t& hi, uint32_t& lo) {
-    hi = pack2(p);
-    lo = pack2(sub2(p, pair(hi << 16, hi & 0xffff0000u)));
-}
-
 // Zero rows [n, 64) of `tiles` adjacent [64][64] tiles.
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int tiles, int n, int tid, int threads) {
     const int each = (kChunk - n) * 8;  // 16-byte units of a tile
