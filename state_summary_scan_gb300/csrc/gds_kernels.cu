@@ -1,18 +1,21 @@
-// gds_kernels.cu -- the gated delta rule with a carried state as a token recurrence in fp32
+// gds_kernels.cu -- the gated delta rule with a carried state as a token recurrence
 // (rm_gdr_state_forward): decoding a few tokens for each of many sequences, and every shape
 // that the chunked form on the tensor cores does not take.
 //
 // Per token, S in R^{Dk x Dv}:
 //     d = beta (v - e^g S^T k),   o = scale (e^g S^T q + (q.k) d),   S <- e^g S + k d^T
-// The columns of S are independent: a CTA owns 32 columns of one sequence's head and keeps them in
-// registers over its tokens (Dk / 16 rows x 4 columns a thread, 128 threads); the state is read
-// from the pool once and written once, in 128-byte (fp32) pieces of a row.  Several tokens are taken
-// four at a time, so that four share one pass over the state, one reduction across the threads and
-// one update.
+// The columns of S are independent.  Bound by HBM when decoding: the state's read and write are
+// nearly all of the traffic, and each is done once.
 //
-// Bound by HBM when decoding one token: the state's read and write are nearly all of the traffic.
-// One CTA per 32 columns keeps the loads in flight per thread to 32 registers and gives even one
-// sequence of 16 heads 32 or more CTAs.
+//   gds_token_kernel  in fp32.  A CTA owns 32 columns of one sequence's head and keeps them in
+//                     registers over its tokens (Dk / 16 rows x 4 columns a thread, 128 threads); the
+//                     state moves in 128-byte (fp32) pieces of a row.  One CTA per 32 columns keeps the
+//                     loads in flight per thread to 32 registers and gives even one sequence of 16
+//                     heads 32 or more CTAs.  Several tokens are taken four at a time, so that four share
+//                     one pass over the state, one reduction across the threads and one update.
+//                     256 sequences, one token, 16 heads of 128 x 128, fp32 state: 82 us, 6.6 TB/s.
+//                     One fp32 prompt of 75 tokens: 88 us, the latency of its 19 tiles of four.
+//   gds_tile_kernel   bf16 inputs, four tokens as products of the warp's matrix instructions
 #include <cstdio>
 #include <type_traits>
 
@@ -303,14 +306,20 @@ __global__ void __launch_bounds__(kTpb, NT == 1 ? 8 : 5) gds_token_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
-// bf16 inputs, several tokens: four at a time as products of the warp's matrix instructions.  The
-// four tokens' keys and queries are the eight columns of one m16n8k16 product with 16 value columns
-// of the state as its rows, and the update of 16 values by 8 keys is one product over 16 = 4 tokens x
-// 4 parts.  (A product of the larger matrix unit has 64 rows or more and would leave through tensor
-// memory; these tiles never leave the registers.)  A warp owns 16 value columns and all of Dk, so
-// that no two warps meet; the lanes' rows and columns are permuted such that the state's elements
-// are loaded and stored straight from the registers that enter the products, in pieces of a row of
-// 32 (bf16) or 64 bytes (fp32), four adjacent pieces to a block.
+// bf16 inputs, four tokens at a time as products of the warp's matrix instructions.  The four
+// tokens' keys and queries are the eight columns of one m16n8k16 product with 16 value columns of
+// the state as its rows, and the update of 16 values by 8 keys is one product over 16 = 4 tokens x 4
+// parts.  (A product of the larger matrix unit has 64 rows or more and would leave through tensor
+// memory; these tiles never leave the registers.)  A warp owns 16 or 32 value columns and all of
+// Dk, so that no two warps meet; the lanes' rows and columns are permuted such that the state's
+// elements are loaded and stored straight from the registers that enter the products.
+//
+// 61 sequences, four tokens, 32 heads of 128 x 256, bf16 state: 55.7 us, 4.8 TB/s, against 120 us of
+// the fp32 recurrence, whose 1294 instructions for 4096 elements of state bound it.  What bounds it
+// now is the latency of the state's reads at 12 warps an SM: 32 columns a warp (8 bytes a lane and
+// row; 16 columns and 20 warps an SM: 78 us), everything else loaded before the state (after it:
+// 64 us).  Longer calls keep the state in fp32 and 16 columns a warp, for twice the warps (32
+// columns: 21 instead of 17 us for one prompt of 32 tokens and 16 heads).
 //
 // Keys and queries are bf16 and enter as they are.  A bf16 state enters its first tile as it is; a
 // state in fp32, and d of a token, as the sum of three bf16, which hold its 24 bits.  Products
@@ -478,9 +487,6 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
         return;
     }
     TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * a.Dk + kRun * t) * a.Dv + col;
-    TileState<DK, W, kPacked> S;
-    if (live && !sq.fresh) S.load(st, a.Dv);
-    else S.zero();
     const int hk = h / a.hdiv;
     // this lane's key or query of a tile; the two keys of its terms of the update; its values
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
@@ -509,6 +515,9 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
         be1 = t < n ? __ldg(beta + (t0 + t) * a.bs) : 0.f;
     };
     if (sq.len > 0) fetch(0);
+    TileState<DK, W, kPacked> S;
+    if (live && !sq.fresh) S.load(st, a.Dv);
+    else S.zero();
     for (int t0 = 0; t0 < sq.len; t0 += 4) {
         const int n = min(sq.len - t0, 4);
         // y: columns 0 .. 3 of the product are S^T k, 4 .. 7 S^T q; kk: row i of them times column r
@@ -649,11 +658,16 @@ bool token_launch(const Args& a, cudaStream_t s) {
 
 template <typename TS>
 bool recurrence(const Args& a, bool f32, cudaStream_t s) {
+    // Single tokens with a fp32 state: the token kernel, whose loads of 16 bytes a lane fill whole lines
+    // (256 sequences, 16 heads of 128 x 128: 82 us; tiles: 97).  With a bf16 state: tiles (54 us; the
+    // token kernel 66).
     const bool one = a.max_len <= 1;
     if (f32) return one ? token_launch<float, TS, 1>(a, s) : token_launch<float, TS, 4>(a, s);
-    if (one) return token_launch<__nv_bfloat16, TS, 1>(a, s);
-    if constexpr (sizeof(TS) == 2)
+    if constexpr (sizeof(TS) == 2) {
         if (a.max_len <= 4) return tile_launch<TS, 2, true>(a, s);
+    } else {
+        if (one) return token_launch<__nv_bfloat16, TS, 1>(a, s);
+    }
     return tile_launch<TS, 1, false>(a, s);
 }
 

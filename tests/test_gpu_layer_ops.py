@@ -271,6 +271,11 @@ DECODE = [  # S, n, H, Hqk, Dk, Dv, dtype, state dtype, fused
     (4, 2, 3, 1, 128, 24, F32, BF16, True),
     (9, 1, 16, 16, 128, 128, BF16, F32, True),
     (2, 33, 2, 1, 64, 128, BF16, F32, False),
+    (5, 1, 4, 2, 128, 136, BF16, BF16, True),
+    (3, 3, 3, 3, 16, 40, BF16, BF16, False),
+    (4, 5, 4, 4, 128, 8, BF16, BF16, True),
+    (1, 39, 2, 1, 32, 256, BF16, BF16, False),
+    (3, 4, 2, 2, 64, 72, BF16, F32, True),
 ]
 
 
@@ -296,6 +301,10 @@ PREFILL = [  # lens, H, Hqk, Dk, Dv, dtype, state dtype
     ([0, 5, 1, 63, 130, 0], 4, 2, 32, 40, F32, F32),
     ([64, 65, 200], 2, 2, 128, 128, F32, F32),
     ([17, 0, 100], 3, 1, 32, 72, BF16, F32),
+    ([1, 4, 5, 0, 39, 2, 8], 4, 2, 128, 72, BF16, F32),
+    ([0, 7, 0, 38], 2, 1, 64, 256, BF16, BF16),
+    ([2, 3, 4, 1, 0], 3, 3, 128, 136, BF16, BF16),
+    ([13, 29], 2, 2, 16, 40, BF16, F32),
 ]
 
 
@@ -306,7 +315,8 @@ def test_gdr_prefill_token_recurrence_against_64_bits(case):
     q, k, v, g, beta, state, slots = gds_inputs(lens, H, Hqk, Dk, Dv, dtype, sdt, S + 1)
     fr = (torch.arange(S) % 3 == 0).to(torch.uint8)
     cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
-    plan = api.make_gdr_state_plan(S, sum(lens), H, Dk, Dv, num_slots=S + 1, qk_heads=Hqk, dtype=dtype, state_dtype=sdt)
+    plan = api.make_gdr_state_plan(S, sum(lens), H, Dk, Dv, num_slots=S + 1, qk_heads=Hqk, max_len=max(lens), dtype=dtype,
+                                   state_dtype=sdt)
     assert C.rm_gdr_state_path(plan.c) == 0
     before = state.clone()
     o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda(), fresh=fr.cuda())
@@ -472,6 +482,31 @@ def test_gdr_state_gates_at_their_ends_and_nan():
     bad = torch.isnan(state[int(slots[2])])
     assert bad[0, :, 3].all() and int(bad.sum()) == D  # the columns of the values are independent
     assert torch.isnan(o[12:, 0, 3]).all() and int(torch.isnan(o).sum()) == 6
+
+
+@pytest.mark.parametrize("lens,sdt", [([4, 3, 2], BF16), ([6, 9, 5], BF16), ([4, 3, 2], F32)])
+def test_gdr_few_tokens_keep_nan_and_resets_apart(lens, sdt):
+    """In tiles of four tokens: what comes later, another sequence and another column do not reach a token."""
+    H, D = 2, 128
+    q, k, v, g, beta, state, slots = gds_inputs(lens, H, H, D, D, BF16, sdt, 3, seed=8)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    ends = [sum(lens[: i + 1]) - 1 for i in range(3)]
+    g[1] = -float("inf")
+    k[ends[0], 0, 5] = float("nan")     # the last key: its own output and the state
+    v[ends[1], 1, 7] = float("inf")     # one column
+    plan = api.make_gdr_state_plan(3, sum(lens), H, D, D, state_dtype=sdt)
+    before = state.clone()
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda())
+    assert torch.isnan(o[ends[0], 0]).all() and torch.isnan(state[int(slots[0]), 0]).all()
+    assert int((~torch.isfinite(o)).sum()) == D + 1
+    q2, k2, v2 = (x.clone() for x in (q, k, v))
+    k2[ends[0], 0, 5] = 0
+    v2[ends[1], 1, 7] = 0
+    again = before.clone()
+    o2 = api.gdr_prefill(plan, q2, k2, v2, g, beta, again, cu, slots=slots.cuda())
+    same = torch.isfinite(o)
+    assert torch.equal(o[same], o2[same])
+    gds_check(lens, q2, k2, v2, g, beta, before, again, o2, slots, None, D ** -0.5, (max(lens) + D) * U, (max(lens) + D) * U)
 
 
 def test_gdr_state_refuses():
