@@ -1082,17 +1082,23 @@ rm_status fail(const char* what, bool map) {
 
 size_t factors_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * factor_bytes(a.Dk, a.Dv); }
 
-// Segments of the longest sequence (1: not cut), and their chunks.  With n segments the chain is
-// two walks of 1 / n of the chunks, so at least three are wanted, of four chunks or more, and as many
-// as keep the first walk's CTAs (one per block of columns for the first segment, one more for M in
-// each inner one) on the GPU at once.
+// Segments of the longest sequence (1: not cut), and their chunks.  As many as keep the first walk's
+// CTAs (one per block of columns for the first segment, one more for M in each inner one) on the
+// GPU's 152 multiprocessors at once, of eight chunks or more.  With n segments the chain is two walks
+// of 1 / n of the chunks, some 1.2 us a chunk; two more launches and the composition cost some 30 us.  So
+// a cut has to save 28 chunks.  us, whole / cut, 128 x 128:
+//     chunks                          16          32          128
+//     16 heads (6 segments)           48 / 60     76 / 85     240 / 177
+//     32 heads (3)                    56 / 74     91 / 103    292 / 283
+//     48 heads (3)                    64 / 89     107 / 130   347 / 365
+// and with three segments the second walk shares the memory with too many others to gain.
 int segments(const Args& a, int* chunks) {
     const int all = (a.max_len + kChunk - 1) / kChunk, blocks = (a.Dv + 127) / 128;
     const int each = 152 / (a.H * a.S);  // CTAs of a sequence's head
     int n = each > blocks ? 2 + (each - blocks) / (blocks + 1) : 1;
     n = n < kMostSegments ? n : kMostSegments;
-    n = n < all / 4 ? n : all / 4;
-    if (n < 3) return 1;
+    n = n < all / 8 ? n : all / 8;
+    if (n < 4 || all * (n - 2) < 28 * n) return 1;
     *chunks = (all + n - 1) / n;
     return (all + *chunks - 1) / *chunks;
 }
@@ -1120,7 +1126,7 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
         return launch_ok() ? RM_OK : fail("launch of the walk", false);
     };
     const bool f = state_dt == RM_F32;
-    if (segs < 3)
+    if (segs == 1)
         return f ? walk(gds_walk_kernel<DK, float, Part::whole>, dim3(blocks * a.H, a.S))
                  : walk(gds_walk_kernel<DK, __nv_bfloat16, Part::whole>, dim3(blocks * a.H, a.S));
     seg.most = segs;

@@ -774,9 +774,9 @@ void launch(Args a, bool back, int* blocks_used, cudaStream_t s) {
     if (back) {
         a.split = min(split_of(a, LANES, 2), blocks * kWarps);
         qkr_backward_kernel<T, LANES, kInter, kFast><<<blocks, kWarps * 32, 0, s>>>(a);
-    } else if (kFast && a.Hq >= 4 && sets_of(a, LANES) >= int64_t(tc::sm_count()) * 8) {
+    } else if (kFast && a.Hq >= 4 && sets_of(a, LANES) >= tc::sm_count()) {
         launch_forward<T, LANES, kInter, kFast, !kFast ? 1 : sizeof(T) == 4 ? 2 : 4>(a, s);
-    } else {  // few tokens or heads: one head at a time
+    } else {  // one head at a time, for more warps a token
         launch_forward<T, LANES, kInter, kFast, 1>(a, s);
     }
 }

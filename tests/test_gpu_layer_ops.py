@@ -381,18 +381,19 @@ def test_gdr_prefill_in_chunks_against_64_bits(case):
 @pytest.mark.parametrize("Dk,Dv,sdt,strong", [(128, 128, F32, False), (128, 136, BF16, False), (64, 64, F32, True), (64, 256, F32, False)])
 def test_gdr_prefill_in_segments_against_64_bits(Dk, Dv, sdt, strong):
     """Few heads and long prompts: the walk is cut into segments whose maps are composed."""
-    lens, H, Hqk = [1500, 0, 130, 800, 1088], 2, 1
+    lens, H, Hqk = [4100, 0, 130, 2500, 3000], 2, 1
     S = len(lens)
     q, k, v, g, beta, state, slots = gds_inputs(lens, H, Hqk, Dk, Dv, BF16, sdt, S + 1, seed=4)
     if strong:  # chunks of strong decay among weak ones, and forgotten states
         g[300:420, 0] = -3.0
         g[900] = -float("inf")
         g[2000:2300, 1] *= 40
+        g[5000:5070, 0] = -4.0
     fr = torch.tensor([0, 1, 0, 1, 0], dtype=torch.uint8)
     cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
     plan = api.make_gdr_state_plan(S, sum(lens), H, Dk, Dv, num_slots=S + 1, qk_heads=Hqk, state_dtype=sdt)
     before, n0 = state.clone(), C.rm_cp_launch_count()
-    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda(), fresh=fr.cuda(), max_len=1500)
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda(), fresh=fr.cuda(), max_len=4100)
     assert C.rm_cp_launch_count() - n0 == 4  # factors, first walk, composition, second walk
     assert C.rm_cp_device_status(torch.zeros(4, dtype=torch.int32, device="cuda")) == 0
     at = 0
