@@ -577,7 +577,8 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  *   multiples of 16 bytes; head h reads the q and k rows of head
  *   h / (H / qk_heads).  g (log-gates), beta: fp32, a token stride, heads
  *   adjacent.  o [num_tokens,H,Dv] contiguous, in dtype.  state: contiguous,
- *   in state_dtype (bf16 states are rounded once a call).
+ *   in state_dtype (bf16 states are rounded once a call).  Strides of q, k
+ *   and v are positive where there is more than one token or head.
  *   slots [num_seqs] int32 on the device (NULL: sequence i uses slot i); a
  *   slot outside [0, num_slots) marks a padding sequence: its outputs are 0
  *   and no state is touched.  Slots in range must be distinct.  fresh
@@ -585,8 +586,12 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  *   Dk in {16, 32, 64, 128}, Dv a multiple of 8 up to 256.
  *   ws: rm_gdr_state_workspace_size bytes, for problems of these sizes or
  *   smaller num_seqs, num_tokens and max_len; not shared by calls that overlap.
- * rm_gdr_state_path: 0 when the call runs as a token recurrence in fp32, 1
- * when it runs in chunks on the tensor cores, -1 for a problem it rejects.
+ * rm_gdr_state_path: 0 when the call runs as a token recurrence with fp32's
+ * precision, 1 when it runs in chunks on the tensor cores (dtype bf16, Dk 64
+ * or 128, max_len >= 48), -1 for a problem it rejects.  In chunks, the state
+ * and two factors that meet it are rounded to bf16 where they enter a product
+ * (the state itself is kept in fp32): outputs are off by up to one and a half
+ * times their own rounding in norm, the final state by some 1e-4.
  */
 typedef struct {
     int32_t num_seqs, num_tokens, max_len;

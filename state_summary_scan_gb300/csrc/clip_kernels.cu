@@ -9,6 +9,11 @@
 // that what the norm read last is still in L2.  Each block adds up its pieces, every block of
 // the scaling adds up the blocks' sums in one order, and no atomics are used: the result
 // depends on the sizes alone.
+//
+// 311 tensors of 805 million elements, half of them bf16: 1.08 ms, of which the norm 347 us at 6.1 TB/s;
+// the second read makes the floor 938 us.  Pieces of 16384 elements on four blocks a multiprocessor took
+// 1.23 ms.  75 small tensors: 33 us on the device, and the
+// host's 43 us of collecting addresses from the tensors, which a call waits for.
 #include <cstdio>
 
 #include "tc_tiles.cuh"
@@ -24,7 +29,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPiece = 32768;   // elements: 128 a thread
 constexpr int kBlocks = 152 * 6;
-constexpr int kFew = 96, kMany = 900;  // tensors of a launch
+// Tensors of a launch: few are passed in a small block of parameters (75 tensors: 33 us on the device and
+// 43 on the host; in the large one 36 and 51), many in as large a block as there is.
+constexpr int kFew = 96, kMany = 900;
 
 template <int N>
 struct Batch {

@@ -51,7 +51,7 @@ constexpr uint32_t kGateBytes = 1024;    // the scale of O (weak) or of Q S [64]
 constexpr int kDec = 64, kEnd = 128, kWeak = 129;
 constexpr float kForget = -110.f;        // e^{-110} is 0 in fp32: lower gates are raised to it
 constexpr int kMostSegments = 12;
-constexpr int kMostStates = 152 * 3;     // of segments: see segments()
+constexpr int kMostStates = 152;         // of segments: see tc_workspace_bytes()
 constexpr float kWeakLimit = 60.f;       // decays within a chunk that factor through its end
 
 // Factors of a (chunk, head) in the workspace: P, -W (Dk / 64 swizzled tiles), the gates, then
@@ -210,6 +210,11 @@ __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
 // Shared memory: for each half h of the key dimensions K_h and Q_h side by side (one operand of
 // 128 rows), P, A, X.  V comes in over Q, T~ (hi, lo) lies over A, T~ o 1/dec over P, -W over K, each
 // when the other is done with.  72 KB and 128 columns of tensor memory: three CTAs an SM.
+//
+// 32 heads of 128 x 128, 13 ragged prompts of up to 4096 tokens: 291 us.  Its floor is the traffic of
+// what it leaves the walk (57 KB a chunk and head, 33 KB of it U) beside its inputs, some 170 us; the
+// rest is the time of a CTA's own steps (two product rounds, the inverse, the epilogues), of which
+// three CTAs an SM overlap only part.
 constexpr uint32_t FA_K = 0, FA_Q = T8, FA_PANEL = 2 * T8, FA_P = 4 * T8, FA_A = 5 * T8, FA_T = FA_A, FA_X = 7 * T8;
 constexpr size_t kFactorSmem = 9 * T8 + 1024;
 
@@ -475,6 +480,12 @@ __global__ void __launch_bounds__(256, 3)
 
 // ---------------------------------------------------------------------------
 // The walk over a sequence's chunks.
+//
+// A chunk takes 2640 cycles, 1.35 us: 128 chunks of 16 heads of 128 x 128 173 us, and the ragged
+// prompts above 200 us, where its copies (4.1 TB/s) and the chain are about even.  The chain is four
+// hops between the products and the four groups of warps, which take a quarter of the state's rows
+// and of the tokens each; the products that do not carry it (Q S, P D) are issued by a warp of their
+// own in its pauses, and U = T V is formed ahead by the factors (236 to 173 us for both).
 // ---------------------------------------------------------------------------
 constexpr int kGroups = 4;                            // chain groups of four warps
 constexpr int kWalkThreads = (4 * kGroups + 7) * 32;  // and four output warps, two of products, the copies'
@@ -986,7 +997,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 
 // The states at the segments' ends, in order: E_j = M_j E_{j-1} + dS_j, E_0 from the first segment.
 // A CTA takes 16 columns of a (sequence, head), a thread two columns and every 32nd row; the next M_j
-// waits in registers while this one, in shared memory, is worked on.  fp32 throughout.
+// waits in registers while this one, in shared memory, is worked on (both copied into shared memory
+// by bulk copies: 28 us instead of 20 for six segments of 16 heads of 128 x 128).  fp32 throughout.
 constexpr int kComposeCols = 16;
 template <int DK>
 struct ComposeSmem {
@@ -1151,8 +1163,9 @@ bool tc_supports(const Args& a, rm_dtype dt) {
     return dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
 }
 
-// A smaller problem may be cut into more segments than this one: the bound is that of all of them,
-// since the sequences' heads times their segments stay below the multiprocessors' number and a half.
+// A smaller problem may be cut into more segments than this one, so the bound is that of all of them:
+// n <= 2 + (152 / (heads sequences) - 1) / 2, and four or more only for heads x sequences <= 30, so
+// heads x sequences x n <= 2 x 30 + 152 / 2 = 136.
 size_t tc_workspace_bytes(const Args& a) {
     return factors_bytes(a) + size_t(kMostStates) * (size_t(a.Dk) * a.Dv + size_t(a.Dk) * a.Dk) * sizeof(float);
 }

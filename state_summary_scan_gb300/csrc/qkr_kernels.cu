@@ -11,7 +11,9 @@
 // and the row and writes one.  A row is spread over D/8 lanes (16 bytes of bf16 a lane), so the
 // sums of a row are a few shuffles and nothing is staged in shared memory; in the half layout
 // the partner of a lane's eight elements is the eight elements of the lane R/16 away.  A warp
-// keeps one token's cos and sin in registers over that token's heads.
+// keeps one token's cos and sin in registers over that token's heads.  Long inputs go through
+// qkr_stream_kernel.  32768 tokens, 16 + 16 heads of 128 in bf16: forward 87 us (6.1 TB/s), backward with
+// both weight gradients 139 us (5.8 TB/s); one token of 32 + 8 heads: 5 us, a launch.
 #include <cstdio>
 
 #include "pairs.cuh"
@@ -526,8 +528,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
 // The same with the rows brought in by bulk copies: each warp owns two stages of shared memory and
 // fills one with the next item (all of q's or of k's heads of a token, their gradients, and the
 // token's row of the table) while it works on the other.  The loop above waits for memory between
-// its groups (115 + 161 us at 32768 tokens of 16 + 16 heads of 128 in bf16, 57% of the copy rate);
-// this one needs a token's heads side by side in memory, and enough of them to be worth a copy.
+// its groups; this one needs a token's heads side by side in memory, and enough of them to be worth
+// a copy.  us, the loop / this kernel, forward and backward:
+//     16 + 16 heads of 128, bf16, 8192 tokens     40 / 33      52 / 48
+//     the same, 32768 tokens                      107 / 101    150 / 130
+//     8 + 4 heads of 128, bf16, 32768 tokens      54 / 52      70 / 72
+//     16 + 16 heads of 64, fp32, 32768 tokens     101 / 99     129 / 102
+// Three blocks of eight warps forward, one of twelve backward: the stages fill the shared memory.
 // ---------------------------------------------------------------------------
 template <bool kBack>
 struct Stream {
@@ -771,6 +778,11 @@ template <typename T, int LANES, bool kInter, bool kFast>
 void launch(Args a, bool back, int* blocks_used, cudaStream_t s) {
     const int blocks = *blocks_used;
     if (kFast && (back ? stream<T, LANES, kInter, true>(a, blocks_used, s) : stream<T, LANES, kInter, false>(a, blocks_used, s))) return;
+    // Forward: groups of heads once the tokens give every multiprocessor a warp; below, one head at a time, for
+    // more warps a token.  us, groups / single heads, 32 + 8 and 8 + 4 heads of 128 in bf16:
+    //     64 tokens      8.8 / 6.8      8.8 / 6.8
+    //     1024 tokens    15 / 17        9.8 / 11
+    //     2048 tokens    21 / 23        11 / 15
     if (back) {
         a.split = min(split_of(a, LANES, 2), blocks * kWarps);
         qkr_backward_kernel<T, LANES, kInter, kFast><<<blocks, kWarps * 32, 0, s>>>(a);
