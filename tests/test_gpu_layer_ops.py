@@ -625,3 +625,34 @@ def test_clip_of_zeros_and_refusals():
         api.clip_grad_norm(plan, [z], out=[z])
     with pytest.raises(C.RmCpError):
         api.clip_grad_norm(plan, [z], -1.0)
+
+
+def test_a_decoding_step_as_a_cuda_graph():
+    """Norm with rotation, decoding and a norm of gradients captured once and replayed: the direct calls' values."""
+    S, H, D = 3, 4, 128
+    q, k, v, g, beta, state, slots = gds_inputs([1] * S, H, H, D, D, BF16, F32, S, seed=6)
+    q, k, v, g, beta = (x.unflatten(0, (S, 1)) for x in (q, k, v, g, beta))
+    table, pos, slots = api.make_rope_table(64, D), torch.tensor([[3], [9], [40]], dtype=torch.int32, device="cuda"), slots.cuda()
+    plan, clip = api.make_gdr_state_plan(S, S, H, D, D), api.make_clip_plan(2)
+    grads = [rnd(1000, seed=1), rnd(77, seed=2, dtype=BF16)]
+
+    def step(st):
+        a, b = api.qk_norm_rope(q, k, table, pos, norm="l2")
+        return api.gdr_decode(plan, a, b, v, g, beta, st, slots=slots), api.clip_grad_norm(clip, grads)
+
+    want_state = state.clone()
+    want = [step(want_state) for _ in range(2)]
+    held = state.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(held)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, norm = step(held)
+    held.copy_(state)
+    for w, wn in want:
+        graph.replay()
+        assert torch.equal(o, w) and torch.equal(norm, wn)
+    assert torch.equal(held, want_state)
