@@ -150,28 +150,30 @@ __device__ __forceinline__ void tri_product(const float* M, int r, int u0, const
 }
 
 // X = (I + A)^{-1} for the strictly lower A, by halves: the four 16 x 16 diagonal blocks by forward
-// substitution (a column's rows in 16 lanes), then twice the block below the diagonal of a pair,
+// substitution (a column a lane), then twice the block below the diagonal of a pair,
 // X21 = -X22 (A21 X11).  A21 X11 waits in the pair's block above the diagonal, so that nothing but A
 // and X is needed; entries above the diagonal are not zero afterwards (those of A's diagonal blocks
 // must be).  All 256 threads call it.  A lane takes a column and two or four rows, which shares every
 // read of X between the rows and every read of A between the columns.
 __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    {
-        const int o = 16 * (warp >> 1), r = lane & 15, grp = ((warp & 1) << 1) | (lane >> 4);
-        float l[16], x[4];
+    if (warp < 2) {
+        const int o = 16 * (2 * warp + (lane >> 4)), c = lane & 15;
+        float x[16];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float4 v = a_row4(A, o + r, o / 4 + u);
-            l[4 * u] = v.x, l[4 * u + 1] = v.y, l[4 * u + 2] = v.z, l[4 * u + 3] = v.w;
+        for (int r = 0; r < 16; ++r) {
+            float y = r == c ? 1.f : 0.f;
+#pragma unroll
+            for (int k = 0; k < r; k += 4) {
+                const float4 l = a_row4(A, o + r, (o + k) / 4);
+                y = fmaf(-l.x, x[k], y);  // in order: only the last term waits for the row before
+                if (k + 1 < r) y = fmaf(-l.y, x[k + 1], y);
+                if (k + 2 < r) y = fmaf(-l.z, x[k + 2], y);
+                if (k + 3 < r) y = fmaf(-l.w, x[k + 3], y);
+            }
+            x[r] = y;
+            X[(o + r) * 64 + o + c] = y;
         }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = r == 4 * grp + m ? 1.f : 0.f;
-#pragma unroll
-        for (int k = 0; k < 15; ++k)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) x[m] = fmaf(-l[k], __shfl_sync(kFull, x[m], (lane & 16) | k), x[m]);
-        *reinterpret_cast<float4*>(X + (o + r) * 64 + o + 4 * grp) = make_float4(x[0], x[1], x[2], x[3]);
     }
     __syncthreads();
     {  // pairs of 16: four warps each, two rows a lane
@@ -235,11 +237,13 @@ __global__ void __launch_bounds__(256, 3)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = blockIdx.x, h = blockIdx.y;
     // the sequence of this chunk slot: the last one whose first chunk is at or before it
-    int lo = 0, hi = a.S - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_chunk(a, mid) <= c) lo = mid;
-        else hi = mid - 1;
+    int lo = 0;
+    for (int left = a.S; left > 1;) {  // 32 of them looked at at once
+        const int step = (left + 31) / 32, i = lane * step;
+        const int before = __popc(__ballot_sync(kFull, i < left && first_chunk(a, lo + min(i, left - 1)) <= c));
+        const int skip = max(before - 1, 0) * step;
+        lo += skip;
+        left = min(step, left - skip);
     }
     const Seq sq = sequence(a, lo);
     const int t0 = (c - first_chunk(a, lo)) * kChunk;
@@ -248,33 +252,29 @@ __global__ void __launch_bounds__(256, 3)
     const int64_t tok = sq.begin + t0;
     uint8_t* fac = static_cast<uint8_t*>(a.ws) + (int64_t(c) * a.H + h) * factor_bytes(DK, a.Dv);
 
-    if (tid == 0) {
+    float g[2], be[2];  // warp 0: two tokens a lane
+    if (warp == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            g[i] = t < n ? __ldg(a.g + (tok + t) * a.gs + h) : 0.f;
+            be[i] = t < n ? __ldg(a.beta + (tok + t) * a.bs + h) : 0.f;
+        }
+        tmem_alloc(smem_u32(&tmem_slot), 128);
+    } else if (tid == 32) {
         mbar_init(smem_u32(&full), 1);
         mbar_init(smem_u32(&vfull), 1);
         mbar_init(smem_u32(&mbar), 1);
         mbar_fence_init();
-    }
-    if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 128);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_slot;  // [0,64) K K^T and Q K^T, then W^T; [64,128) U^T
-    if (tid == 0) {
         mbar_expect_tx(smem_u32(&full), 2 * NP * T8);
         for (int p = 0; p < NP; ++p) {
             tma_load_3d(smem_u32(smem + FA_K + p * FA_PANEL), &mk, 64 * p, h / a.hdiv, int(tok), smem_u32(&full));
             tma_load_3d(smem_u32(smem + FA_Q + p * FA_PANEL), &mq, 64 * p, h / a.hdiv, int(tok), smem_u32(&full));
         }
     }
-    if (warp == 0) {  // the running sum of the gates, two tokens a lane
-        float g[2], be[2];
+    if (warp == 0) {  // the running sum of the gates
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 2 * lane + i;
-            g[i] = t < n ? __ldg(a.g + (tok + t) * a.gs + h) : 0.f;
-            be[i] = t < n ? __ldg(a.beta + (tok + t) * a.bs + h) : 0.f;
-            g[i] = g[i] < kForget ? kForget : g[i];
-        }
+        for (int i = 0; i < 2; ++i) g[i] = g[i] < kForget ? kForget : g[i];
         float ps = g[0] + g[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -302,14 +302,16 @@ __global__ void __launch_bounds__(256, 3)
             weak_s = weak;
         }
     }
+    tc_fence_before();
+    __syncthreads();  // barriers, tensor memory and the decays are in place
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;  // [0,64) K K^T and Q K^T, then W^T; [64,128) U^T
     mbar_wait(smem_u32(&full), 0);
     if (n < kChunk) {
         for (int p = 0; p < NP; ++p) zero_rows(smem + FA_K + p * FA_PANEL, 1, n, tid, 256);
         fence_async_smem();
+        __syncthreads();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     uint32_t mph = 0;
     const int vblocks = (a.Dv + 127) / 128;
     // V of a block over Q (whose product is done by then)
