@@ -71,6 +71,19 @@ __device__ __forceinline__ int first_chunk(const Args& a, int i) {
     const int b = a.cu ? min(max(__ldg(a.cu + i), 0), a.N) : i * a.each;
     return b / kChunk + i;
 }
+// The y-th longest of up to 32 sequences, so that the longest walks begin first.  Whole-warp call.
+__device__ __forceinline__ int by_length(const Args& a, int y) {
+    if (a.cu == nullptr || a.S > 32) return y;
+    const int lane = threadIdx.x & 31, i = min(lane, a.S - 1);
+    const int b = min(max(__ldg(a.cu + i), 0), a.N), len = lane < a.S ? min(max(__ldg(a.cu + i + 1), b), a.N) - b : -1;
+    int rank = 0;
+    for (int j = 0; j < a.S; ++j) {
+        const int other = __shfl_sync(kFull, len, j);
+        rank += other > len || (other == len && j < lane);
+    }
+    const unsigned m = __ballot_sync(kFull, lane < a.S && rank == y);
+    return m ? __ffs(m) - 1 : y;
+}
 int chunk_slots(const Args& a) { return a.N / kChunk + a.S + 1; }
 
 template <int N>
@@ -574,7 +587,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const int h = blockIdx.x / blocks, vb = blockIdx.x % blocks;
     const bool map = vb == vblocks;  // the columns are those of M
     const int v0 = map ? 0 : vb * 128, nv = map ? DK : min(a.Dv - v0, 128);
-    const Seq sq = sequence(a, blockIdx.y);
+    const int si = kPart == Part::whole ? by_length(a, blockIdx.y) : int(blockIdx.y);
+    const Seq sq = sequence(a, si);
     const int all = (sq.len + kChunk - 1) / kChunk;  // the sequence's chunks
     // this CTA's segment and its chunks
     const int j = kPart == Part::whole ? 0 : int(blockIdx.z) + (kPart == Part::rest ? 1 : 0);
@@ -652,7 +666,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 } else if (kPart == Part::first) {
                     y = map && r == row ? 1.f : 0.f;
                 } else if (live) {
-                    y = end_of(a, seg, blockIdx.y, h, j - 1)[int64_t(r) * a.Dv + v0 + row];
+                    y = end_of(a, seg, si, h, j - 1)[int64_t(r) * a.Dv + v0 + row];
                 }
                 x[i] = __float_as_uint(y);
             }
@@ -754,7 +768,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
 #pragma unroll
             for (int i = 0; i < GC; ++i) st[int64_t(r0 + i) * a.Dv + row] = from_f32<TS>(__uint_as_float(x[i]));
         } else if (live && kPart == Part::first) {
-            float* to = map ? map_of(a, seg, blockIdx.y, h, j) + row : end_of(a, seg, blockIdx.y, h, j) + v0 + row;
+            float* to = map ? map_of(a, seg, si, h, j) + row : end_of(a, seg, si, h, j) + v0 + row;
 #pragma unroll
             for (int i = 0; i < GC; ++i) to[int64_t(r0 + i) * (map ? DK : a.Dv)] = __uint_as_float(x[i]);
         }
@@ -936,7 +950,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     } else {
         // ---- the copies: each piece of chunk c once the products that read chunk c - 2's are done
         const uint32_t base = smem_u32(smem), ub = u_bytes(a.Dv), uat = factor_u(DK) + (v0 / 128) * ub;
-        const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, blockIdx.y) + c_first) * a.H + h) * factor_bytes(DK, a.Dv);
+        const uint8_t* fac = static_cast<const uint8_t*>(a.ws) + (int64_t(first_chunk(a, si) + c_first) * a.H + h) * factor_bytes(DK, a.Dv);
         for (int c = 0; c < chunks; ++c, fac += int64_t(a.H) * factor_bytes(DK, a.Dv)) {
             const int i = c & 1, ph = ((c >> 1) & 1) ^ 1, tok = sq.begin + (c_first + c) * kChunk;
             wait(&bar.u_free[i], ph, dead);
