@@ -71,7 +71,8 @@ __device__ __forceinline__ int first_chunk(const Args& a, int i) {
     const int b = a.cu ? min(max(__ldg(a.cu + i), 0), a.N) : i * a.each;
     return b / kChunk + i;
 }
-// The y-th longest of up to 32 sequences, so that the longest walks begin first.  Whole-warp call.
+// The y-th longest of up to 32 sequences, so that the longest walks begin first (13 ragged prompts of up to
+// 4096 tokens: 208 to 181 us; with more sequences they even out by themselves).  Whole-warp call.
 __device__ __forceinline__ int by_length(const Args& a, int y) {
     if (a.cu == nullptr || a.S > 32) return y;
     const int lane = threadIdx.x & 31, i = min(lane, a.S - 1);
@@ -226,7 +227,7 @@ __device__ __forceinline__ void halves_inverse(const float* A, float* X) {
 // 128 rows), P, A, X.  V comes in over Q, T~ (hi, lo) lies over A, T~ o 1/dec over P, -W over K, each
 // when the other is done with.  72 KB and 128 columns of tensor memory: three CTAs an SM.
 //
-// 32 heads of 128 x 128, 13 ragged prompts of up to 4096 tokens: 291 us.  Its floor is the traffic of
+// 32 heads of 128 x 128, 13 ragged prompts of up to 4096 tokens: 270 us.  Its floor is the traffic of
 // what it leaves the walk (57 KB a chunk and head, 33 KB of it U) beside its inputs, some 170 us; the
 // rest is the time of a CTA's own steps (two product rounds, the inverse, the epilogues), of which
 // three CTAs an SM overlap only part.
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(256, 3)
 // The walk over a sequence's chunks.
 //
 // A chunk takes 2640 cycles, 1.35 us: 128 chunks of 16 heads of 128 x 128 173 us, and the ragged
-// prompts above 200 us, where its copies (4.1 TB/s) and the chain are about even.  The chain is four
+// prompts above 181 us (1.0 GB, 5.6 TB/s), where its copies and the chain are about even.  The chain is four
 // hops between the products and the four groups of warps, which take a quarter of the state's rows
 // and of the tokens each; the products that do not carry it (Q S, P D) are issued by a warp of their
 // own in its pauses, and U = T V is formed ahead by the factors (236 to 173 us for both).
