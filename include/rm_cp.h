@@ -587,7 +587,11 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  *   ws: rm_gdr_state_workspace_size bytes, for problems of these sizes or
  *   smaller num_seqs, num_tokens and max_len; not shared by calls that overlap.
  * rm_gdr_state_path: 0 when the call runs as a token recurrence with fp32's
- * precision, 1 when it runs in chunks on the tensor cores (dtype bf16, Dk 64
+ * precision from the states it finds (a bf16 pool ends that at the hand-over:
+ * an element of the state on a rounding boundary goes up or down by what is
+ * left in fp32's last bits, so that the fp32 outputs of a later call of two
+ * correct programs differ by up to some 3e-3 of their rms in a few elements),
+ * 1 when it runs in chunks on the tensor cores (dtype bf16, Dk 64
  * or 128, max_len >= 48), -1 for a problem it rejects.  In chunks, the state
  * and two factors that meet it are rounded to bf16 where they enter a product
  * (the state itself is kept in fp32): outputs are off by up to one and a half
