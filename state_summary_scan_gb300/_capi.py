@@ -417,6 +417,19 @@ def _raw_stream(stream, device: int):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def allocated(make, stream, device: int):
+    """make(): a call's outputs and workspaces.  They come from the pool of the stream that the call
+    runs on; memory of the current stream's pool may still be in use there, and goes to that
+    stream's next tensor while another stream's call runs."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def signature(t: Optional[torch.Tensor]):
     """What a call's checks depend on; equal signatures pass the same checks."""
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())

@@ -119,7 +119,7 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, 
             plan.checked.clear()
         plan.checked[key] = p
     if o is None:
-        o = torch.empty_like(v, memory_format=torch.contiguous_format)
+        o = C.allocated(lambda: torch.empty_like(v, memory_format=torch.contiguous_format), stream, v.get_device())
     elif o.shape != v.shape or o.dtype != v.dtype or o.device != v.device or not o.is_contiguous():
         raise ValueError("o must be contiguous and have the shape, type and device of v")
     if S:

@@ -128,7 +128,7 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     elements NaN."""
     _, p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
     if out is None:
-        out = _new(q), _new(k)
+        out = C.allocated(lambda: (_new(q), _new(k)), stream, q.get_device())
     else:
         _like(out, (q, k), "out")
     if q.numel():
@@ -153,14 +153,16 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, table=None, positions=None, q_we
     of the forward; a weight's gradient is [D] fp32, None without the weight."""
     problem, p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
     _like((dq_out, dk_out), (q, k), "dq_out and dk_out")
-    dq, dk = _new(q), _new(k)
-    dwq = torch.empty_like(q_weight) if q_weight is not None else None
-    dwk = torch.empty_like(k_weight) if k_weight is not None else None
+    size = C.rm_cp_qkr_workspace_size(problem) if q.numel() and (q_weight is not None or k_weight is not None) else 0
+
+    def buffers():
+        weight = torch.empty_like if q.numel() else torch.zeros_like  # no rows: their sum is 0
+        return (_new(q), _new(k), None if q_weight is None else weight(q_weight), None if k_weight is None else weight(k_weight),
+                torch.empty(size, dtype=torch.uint8, device=q.device) if size else None)
+
+    dq, dk, dwq, dwk, ws = C.allocated(buffers, stream, q.get_device())
     if not q.numel():
-        return dq, dk, None if dwq is None else dwq.zero_(), None if dwk is None else dwk.zero_()
-    ws = None
-    if dwq is not None or dwk is not None:
-        ws = torch.empty(C.rm_cp_qkr_workspace_size(problem), dtype=torch.uint8, device=q.device)
+        return dq, dk, dwq, dwk
     C.rm_cp_qkr_backward(p, q, k, q_weight, k_weight, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws,
                          C._raw_stream(stream, q.get_device()))
     return dq, dk, dwq, dwk

@@ -10,6 +10,59 @@ from test_gpu_layer_ops import BF16, F32, U, close, gds_check, gds_inputs, gds_r
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------------------------ norm and rotation
+
+def qkr_case(B, T, Hq, Hk, D, R, dtype, fused=False, pos=None, weights=True, seed=0):
+    if fused:
+        x = (2 * rnd(B, T, (Hq + 2 * Hk) * D, seed=seed)).to(dtype)
+        q, k = x[..., : Hq * D].unflatten(-1, (Hq, D)), x[..., Hq * D: (Hq + Hk) * D].unflatten(-1, (Hk, D))
+    else:
+        q, k = rnd(B, T, Hq, D, seed=seed, dtype=dtype), rnd(B, T, Hk, D, seed=seed + 1, dtype=dtype)
+    table = api.make_rope_table(max(2000, T), R) if R else None
+    p = None
+    if pos:
+        p = torch.randint(0, 2000, (B, T), generator=torch.Generator("cuda").manual_seed(seed + 2), device="cuda", dtype=pos)
+    w = (1 + 0.3 * rnd(D, seed=seed + 3), 1 + 0.3 * rnd(D, seed=seed + 4)) if weights else (None, None)
+    full = (torch.arange(T, device="cuda") if p is None else p.long()).expand(B, T)
+    return q, k, dict(table=table, positions=p, q_weight=w[0], k_weight=w[1]), full
+
+
+def pollute(n=64, floats=1 << 20):
+    """Takes what the current stream's pool has free and writes NaN to it."""
+    return [torch.full((floats >> (i % 12),), float("nan"), device="cuda") for i in range(n)]
+
+
+@pytest.mark.parametrize("given", ["stream", "handle"])
+def test_calls_on_another_stream_keep_their_buffers_to_themselves(given):
+    """A call on a stream that is still busy: what the current stream allocates and writes after the call's
+    return meets neither its workspace nor its outputs."""
+    q, k, how, _ = qkr_case(1, 300, 4, 2, 128, 64, F32)
+    dy = rnd(*q.shape, seed=7), rnd(*k.shape, seed=8)
+    sq, sk, sv, g, beta, state, slots = gds_inputs([40], 2, 2, 64, 64, BF16, F32, 1)
+    plan, clip = api.make_gdr_state_plan(1, 40, 2, 64, 64), api.make_clip_plan(1)
+    cu = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+
+    def calls(st, stream=None):
+        a = api.qk_norm_rope(q, k, **how, stream=stream)
+        b = api.qk_norm_rope_backward(q, k, *dy, **how, stream=stream)
+        return *a, *b, api.gdr_prefill(plan, sq, sk, sv, g, beta, st, cu, stream=stream), api.clip_grad_norm(clip, [q], stream=stream)
+
+    want = [x.clone() for x in calls(state.clone())]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        st, junk = state.clone(), pollute()
+        del junk  # free blocks of every size in the current stream's pool
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # some 10 ms
+        got = calls(st, side if given == "stream" else side.cuda_stream)
+        junk = pollute()
+        side.synchronize()
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(got, want)):
+            assert torch.equal(x, y), i
+
+
 # ------------------------------------------------------------------ the delta rule with a state
 
 @pytest.mark.parametrize("lens,H,Hqk,Dk,Dv", [([1] * 5, 4, 2, 128, 128), ([1] * 3, 3, 3, 16, 40), ([4] * 3, 2, 1, 64, 72),
