@@ -473,7 +473,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
                             uint64_t sq = mul2(v[0], v[0]), ux = mul2(dv[0], w[0]);
 #pragma unroll
                             for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq), ux = fma2(dv[i], w[i], ux);
-                            const float r = norm_scale(a, row_sum<LANES>(sq), inv), m = r * r * row_sum<LANES>(ux) * inv;
+                            // (a row that is not there adds 0 to the weights' gradients: its own r is infinite without eps)
+                            const float ss = row_sum<LANES>(sq), r = live0 && u < left ? norm_scale(a, ss, inv) : 0.f, m = r * r * row_sum<LANES>(ux) * inv;
                             r2 = both(r);
                             const uint64_t m2 = both(-m);
 #pragma unroll
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(Stream<kBack>::kWarps * 32, Stream<kBack>::kBl
                         uint64_t sq = mul2(v[0], v[0]), ux = mul2(dv[0], w[0]);
 #pragma unroll
                         for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq), ux = fma2(dv[i], w[i], ux);
-                        const float r = norm_scale(a, row_sum<LANES>(sq), inv), m = r * r * row_sum<LANES>(ux) * inv;
+                        const float ss = row_sum<LANES>(sq), r = on ? norm_scale(a, ss, inv) : 0.f, m = r * r * row_sum<LANES>(ux) * inv;
                         r2 = both(r);
                         const uint64_t m2 = both(-m);
 #pragma unroll

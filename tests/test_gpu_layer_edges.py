@@ -63,6 +63,34 @@ def test_calls_on_another_stream_keep_their_buffers_to_themselves(given):
             assert torch.equal(x, y), i
 
 
+def qkr_check(q, k, how, pos, tol=32 * U, seed=9):
+    """Forward and backward against 64 bits, with the tolerances of test_qkr_against_64_bits."""
+    dtype, t64 = q.dtype, None if how["table"] is None else how["table"].double()
+    got = api.qk_norm_rope(q, k, **how)
+    dy = [rnd(*x.shape, seed=seed + i, dtype=dtype) for i, x in enumerate((q, k))]
+    back = api.qk_norm_rope_backward(q, k, *dy, **how)
+    for i, (x, w) in enumerate(((q, how["q_weight"]), (k, how["k_weight"]))):
+        x64 = x.double().requires_grad_(True)
+        w64 = None if w is None else w.double().requires_grad_(True)
+        y = qkr_ref(x64, w64, t64, pos, how["norm"], how["eps"], how.get("interleaved", False))
+        close(got[i], y.detach(), tol, dtype, f"output {i}")
+        want = torch.autograd.grad(y, [x64] + ([] if w is None else [w64]), dy[i].double())
+        close(back[i], want[0], 2 * tol, dtype, f"gradient {i}")
+        if w is not None:
+            n = x.numel() // x.shape[-1]
+            scale = float((dy[i].double().abs() * 4).sum((0, 1, 2)).max())
+            assert float((back[2 + i].double() - want[1]).abs().max()) <= (32 + n / 64) * U * scale, f"weight {i}"
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,dtype", [(1, 5, 3, 1, 128, F32), (1, 5, 2, 2, 64, BF16), (2, 3, 1, 1, 80, F32), (1, 4001, 5, 5, 128, BF16),
+                                               (1, 3700, 8, 9, 64, F32)], ids=str)
+def test_qkr_without_eps(norm, B, T, Hq, Hk, D, dtype):
+    """eps = 0: the rows that a group or a step of rows lacks have no say in the weights' gradients."""
+    q, k, how, pos = qkr_case(B, T, Hq, Hk, D, D // 2, dtype)
+    qkr_check(q, k, {**how, "norm": norm, "eps": 0.0}, pos)
+
+
 # ------------------------------------------------------------------ the delta rule with a state
 
 @pytest.mark.parametrize("lens,H,Hqk,Dk,Dv", [([1] * 5, 4, 2, 128, 128), ([1] * 3, 3, 3, 16, 40), ([4] * 3, 2, 1, 64, 72),
