@@ -262,7 +262,8 @@ struct Turn {
     }
 };
 
-// r of a row, from its sum of squares (inv: 1 / D for rms, 1 for l2)
+// r of a row, from its sum of squares (inv: 1 / D for rms, 1 for l2).  Without eps r reaches 1e22, and r^2 leaves
+// fp32: the backward takes r (r sum u x).
 __device__ __forceinline__ float norm_scale(const Args& a, float sq, float inv) { return rsqrtf(fmaf(sq, inv, a.eps)); }
 __device__ __forceinline__ float mean_factor(const Args& a) { return a.norm == 1 ? 1.f / float(a.D) : 1.f; }
 
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
 #pragma unroll
                             for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq), ux = fma2(dv[i], w[i], ux);
                             // (a row that is not there adds 0 to the weights' gradients: its own r is infinite without eps)
-                            const float ss = row_sum<LANES>(sq), r = live0 && u < left ? norm_scale(a, ss, inv) : 0.f, m = r * r * row_sum<LANES>(ux) * inv;
+                            const float ss = row_sum<LANES>(sq), r = live0 && u < left ? norm_scale(a, ss, inv) : 0.f, m = r * (r * row_sum<LANES>(ux)) * inv;
                             r2 = both(r);
                             const uint64_t m2 = both(-m);
 #pragma unroll
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(Stream<kBack>::kWarps * 32, Stream<kBack>::kBl
                         uint64_t sq = mul2(v[0], v[0]), ux = mul2(dv[0], w[0]);
 #pragma unroll
                         for (int i = 1; i < 4; ++i) sq = fma2(v[i], v[i], sq), ux = fma2(dv[i], w[i], ux);
-                        const float ss = row_sum<LANES>(sq), r = on ? norm_scale(a, ss, inv) : 0.f, m = r * r * row_sum<LANES>(ux) * inv;
+                        const float ss = row_sum<LANES>(sq), r = on ? norm_scale(a, ss, inv) : 0.f, m = r * (r * row_sum<LANES>(ux)) * inv;
                         r2 = both(r);
                         const uint64_t m2 = both(-m);
 #pragma unroll
