@@ -570,8 +570,10 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  * Packed tokens [num_tokens]: cu_seqlens [num_seqs + 1] int32 on the device
  * gives each sequence's range (an empty one leaves its slot as it is, or zero
  * when fresh; ranges are cut to [0, num_tokens]); NULL: every sequence has
- * num_tokens / num_seqs tokens.  max_len bounds the longest sequence: tokens
- * past it are not read, and their outputs not written.
+ * num_tokens / num_seqs tokens.  max_len is the length that the kernels are
+ * chosen for, a bound of the longest sequence; a longer one is taken whole all
+ * the same, only slower, and with max_len <= 4 a bf16 state is rounded after
+ * every four of its tokens.  Without cu_seqlens max_len has to hold.
  *   q, k [num_tokens,qk_heads,Dk], v [num_tokens,H,Dv] in dtype, strides in
  *   elements for (token, head), elements adjacent, bases and strides
  *   multiples of 16 bytes; head h reads the q and k rows of head

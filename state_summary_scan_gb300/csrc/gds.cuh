@@ -9,7 +9,7 @@ namespace rmcp {
 namespace gds {
 
 struct Args {
-    int S, N, max_len;      // sequences, packed tokens, bound of a sequence's length
+    int S, N, max_len;      // sequences, packed tokens, tokens of a sequence that the launch is chosen for
     int H, hdiv, Dk, Dv;    // head h reads the q and k rows of head h / hdiv
     int slots_n;
     int each;               // tokens of every sequence without cu, else 0
@@ -45,7 +45,7 @@ __device__ __forceinline__ Seq sequence(const Args& a, int i) {
         s.begin = min(max(__ldg(a.cu + i), 0), a.N);
         e = min(max(__ldg(a.cu + i + 1), s.begin), a.N);
     }
-    s.len = min(e - s.begin, a.max_len);
+    s.len = e - s.begin;  // whatever max_len says
     const int slot = a.slots ? __ldg(a.slots + i) : i;
     s.slot = slot >= 0 && slot < a.slots_n ? slot : -1;
     s.fresh = a.fresh != nullptr && __ldg(a.fresh + i) != 0;

@@ -613,6 +613,10 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
             }
             if (kPacked && live) store_rows<DK, W>(st, b, a.Dv, c);
         }
+        if (kPacked && t0 + 4 < sq.len) {  // a sequence longer than its bound: on from the state just stored
+            fetch(t0 + 4);
+            if (live) S.load(st, a.Dv);
+        }
     }
     if (live && (!kPacked || sq.len <= 0)) {
 #pragma unroll

@@ -594,7 +594,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     // this CTA's segment and its chunks
     const int j = kPart == Part::whole ? 0 : int(blockIdx.z) + (kPart == Part::rest ? 1 : 0);
     const int c_first = kPart == Part::whole ? 0 : j * seg.chunks;
-    const bool ends = kPart == Part::whole || c_first + seg.chunks >= all;  // it is the sequence's last
+    // it is the sequence's last (the last one that there is takes what a sequence has beyond max_len)
+    const bool ends = kPart == Part::whole || j == seg.most - 1 || c_first + seg.chunks >= all;
     const int chunks = (ends ? all : c_first + seg.chunks) - c_first;
     if (kPart != Part::whole) {
         if (j > 0 && (sq.slot < 0 || chunks <= 0)) return;
@@ -1033,7 +1034,7 @@ __global__ void __launch_bounds__(256) gds_compose_kernel(const __grid_constant_
     const int blocks = (a.Dv + kComposeCols - 1) / kComposeCols;
     const int h = blockIdx.x / blocks, v0 = (blockIdx.x % blocks) * kComposeCols;
     const Seq sq = sequence(a, blockIdx.y);
-    const int segs = ((sq.len + kChunk - 1) / kChunk + seg.chunks - 1) / seg.chunks;
+    const int segs = min(((sq.len + kChunk - 1) / kChunk + seg.chunks - 1) / seg.chunks, seg.most);
     if (sq.slot < 0 || segs < 3) return;
     constexpr int N = DK * DK / 4 / 256;  // 16-byte units of M a thread
     float4 m4[N];

@@ -142,9 +142,10 @@ def gdr_decode(plan: GdrStatePlan, q, k, v, g, beta, state, slots=None, fresh=No
 def gdr_prefill(plan: GdrStatePlan, q, k, v, g, beta, state, cu_seqlens, slots=None, fresh=None, max_len=None, o=None,
                 stream=None) -> torch.Tensor:
     """o [N,H,Dv] of S ragged prompts packed along N tokens; cu_seqlens [S + 1] int32 on the
-    device.  max_len bounds the longest prompt (default the plan's); the rest as gdr_decode,
-    with q, k [N,qk_heads,Dk], v [N,H,Dv], g, beta [N,H].  An empty prompt leaves its slot as it
-    is, or zero when fresh."""
+    device.  max_len, a bound of the longest prompt (default the plan's), chooses the kernels: a
+    longer prompt is taken whole too, in a form made for shorter ones.  The rest as gdr_decode, with
+    q, k [N,qk_heads,Dk], v [N,H,Dv], g, beta [N,H].  An empty prompt leaves its slot as it is, or
+    zero when fresh."""
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, Dk]")
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:

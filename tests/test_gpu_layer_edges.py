@@ -121,3 +121,55 @@ def test_fp32_tokens_on_a_bf16_pool_call_by_call(lens, H, Hqk, Dk, Dv):
             again = before.clone()
             o2 = api.gdr_decode(plan, *(x.unflatten(0, (S, lens[0])) for x in (q, k, v, g, beta)), again, slots=slots.cuda())
             assert torch.equal(o2.flatten(0, 1), o) and torch.equal(again, state)
+
+
+KINDS = {  # Dk, Dv, dtype, state dtype: which kernels a call with the bound below goes through
+    "fp32": (32, 40, F32, F32),
+    "few": (128, 136, BF16, BF16),       # tiles of a bf16 state, up to four tokens
+    "some": (64, 72, BF16, F32),
+    "chunks": (128, 136, BF16, F32),
+    "segments": (64, 64, BF16, F32),
+}
+
+
+def prefill_check(kind, lens, bound, begin=0, rest=0, padding=None):
+    """Prompts that begin at token `begin` and leave `rest` tokens over, against 64 bits; two heads of one key head."""
+    Dk, Dv, dtype, sdt = KINDS[kind]
+    S, N = len(lens), begin + sum(lens) + rest
+    q, k, v, g, beta, state, slots = gds_inputs([begin] + lens + [rest], 2, 1, Dk, Dv, dtype, sdt, S + 3)
+    slots = slots[:S]
+    if padding is not None:
+        slots[padding] = -1
+    plan = api.make_gdr_state_plan(S, N, 2, Dk, Dv, num_slots=S + 3, qk_heads=1, max_len=bound, dtype=dtype, state_dtype=sdt)
+    cu = torch.tensor([begin] + lens).cumsum(0).to(torch.int32).cuda()
+    before, o = state.clone(), torch.full_like(v, float("nan"))
+    n0 = C.rm_cp_launch_count()
+    api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda(), max_len=bound, o=o)
+    assert C.rm_cp_launch_count() - n0 == {"chunks": 2, "segments": 4}.get(kind, 1)
+    assert C.rm_cp_device_status(torch.zeros(4, dtype=torch.int32, device="cuda")) == 0
+    assert not o[:begin].any() and not o[N - rest:].any()
+    if kind in ("fp32", "some"):
+        tol, at = (max(lens) + Dk) * U, slice(begin, N - rest)
+        gds_check(lens, q[at], k[at], v[at], g[at], beta[at], before, state, o[at], slots, None, Dk ** -0.5, tol, tol)
+        return
+    at, idle = begin, set(range(S + 3))
+    for i, n in enumerate(lens):
+        s, j = slice(at, at + n), int(slots[i])
+        at += n
+        if j < 0:
+            assert not o[s].any()
+            continue
+        idle.discard(j)
+        want_o, want_S = gds_ref(q[s], k[s], v[s], g[s], beta[s], before[j], Dk ** -0.5)
+        if n:  # as in chunks; and a bf16 state rounded at most twice on the way to o: sqrt(3) of a rounding (1.7e-3)
+            assert rel2(o[s], want_o) <= 2.0 ** -8, (i, rel2(o[s], want_o))
+        assert rel2(state[j], want_S) <= 2e-3 + (2.0 ** -8 if sdt == BF16 else 0), (i, rel2(state[j], want_S))
+    for j in idle:
+        assert torch.equal(state[j], before[j])
+
+
+@pytest.mark.parametrize("kind,lens,bound", [("fp32", [30, 5], 10), ("fp32", [7, 0, 3], 1), ("few", [9, 2, 4], 4), ("few", [6, 1], 1), ("some", [5, 3], 1),
+                                             ("some", [30, 41], 7), ("chunks", [200, 30, 129], 64), ("chunks", [300], 48),
+                                             ("segments", [4400, 5, 100], 3000)], ids=str)
+def test_gdr_prefill_takes_prompts_over_the_bound(kind, lens, bound):
+    prefill_check(kind, lens, bound)
