@@ -569,7 +569,8 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  *     o_t = scale S^T q_t.
  * Packed tokens [num_tokens]: cu_seqlens [num_seqs + 1] int32 on the device
  * gives each sequence's range (an empty one leaves its slot as it is, or zero
- * when fresh; ranges are cut to [0, num_tokens]); NULL: every sequence has
+ * when fresh; ranges are cut to [0, num_tokens], and tokens before the first
+ * and after the last range have outputs 0); NULL: every sequence has
  * num_tokens / num_seqs tokens.  max_len is the length that the kernels are
  * chosen for, a bound of the longest sequence; a longer one is taken whole all
  * the same, only slower, and with max_len <= 4 a bf16 state is rounded after

@@ -430,9 +430,9 @@ def _launch(device: int, fn, *args):
         _check(status)
 
 
-def allocated(make, stream, device: int):
-    """make(): a call's outputs and workspaces.  They come from the pool of the stream that the call
-    runs on; memory of the current stream's pool may still be in use there, and goes to that
+def on_stream(make, stream, device: int):
+    """make() on the stream of a call.  Its outputs and workspaces are made so: they come from that
+    stream's pool.  Memory of the current stream's pool may still be in use there, and goes to that
     stream's next tensor while another stream's call runs."""
     if stream is None:
         return make()

@@ -29,6 +29,19 @@ struct Args {
     void* ws;
 };
 
+// Zeros in `cols` adjacent outputs (a multiple of 8, at most 8 a thread) of `rows` tokens, os elements apart.
+template <typename T>
+__device__ __forceinline__ void zero_outputs(T* o, int64_t os, int rows, int cols, int tid, int threads) {
+    const int each = cols / 8, step = threads / each;
+    if (tid >= step * each) return;
+    o += tid % each * 8;
+    for (int r = tid / each; r < rows; r += step) {
+        uint4* to = reinterpret_cast<uint4*>(o + r * os);
+#pragma unroll
+        for (int u = 0; u < int(sizeof(T)) / 2; ++u) to[u] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 // Tokens [begin, begin + len) of a sequence; slot < 0: a padding sequence.
 struct Seq {
     int begin, len, slot;
@@ -50,6 +63,17 @@ __device__ __forceinline__ Seq sequence(const Args& a, int i) {
     s.slot = slot >= 0 && slot < a.slots_n ? slot : -1;
     s.fresh = a.fresh != nullptr && __ldg(a.fresh + i) != 0;
     return s;
+}
+
+// The outputs of the tokens that no sequence has, those before the first one and after the last one: 0.  o: the
+// first of the `cols` columns of token 0.  Called for every sequence.
+template <typename T>
+__device__ __forceinline__ void zero_others(const Args& a, int i, const Seq& s, T* o, int cols, int tid, int threads) {
+    if (a.cu == nullptr) return;
+    const int64_t os = int64_t(a.H) * a.Dv;
+    if (i == 0 && s.begin > 0) zero_outputs(o, os, s.begin, cols, tid, threads);
+    const int end = s.begin + s.len;
+    if (i == a.S - 1 && end < a.N) zero_outputs(o + end * os, os, a.N - end, cols, tid, threads);
 }
 
 // The chunked form on the tensor cores, for calls whose longest sequence has this many tokens.  Its two

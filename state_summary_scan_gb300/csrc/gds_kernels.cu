@@ -133,12 +133,13 @@ __global__ void __launch_bounds__(kTpb, NT == 1 ? 8 : 5) gds_token_kernel(const 
     const int col = c0 + quad * 4, row = (tid >> 3) * KR;
     const bool live = col < a.Dv;  // Dv is a multiple of 8, a thread's columns of 4
     const Seq sq = sequence(a, blockIdx.y);
+    const int cols = min(a.Dv - c0, kCols);
+    zero_others(a, blockIdx.y, sq, static_cast<T*>(a.o) + int64_t(h) * a.Dv + c0, cols, tid, kTpb);
     if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
     T* o = static_cast<T*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + c0;
     const int64_t os = int64_t(a.H) * a.Dv;
     if (sq.slot < 0) {  // padding
-        for (int t = warp; t < sq.len; t += 4)
-            if (c0 + lane < a.Dv) o[t * os + lane] = from_f32<T>(0.f);
+        zero_outputs(o, os, sq.len, cols, tid, kTpb);
         return;
     }
     TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * a.Dk + row) * a.Dv + col;
@@ -159,7 +160,6 @@ __global__ void __launch_bounds__(kTpb, NT == 1 ? 8 : 5) gds_token_kernel(const 
     const T* v = static_cast<const T*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + c0;
     const float* g = a.g + sq.begin * a.gs + h;
     const float* beta = a.beta + sq.begin * a.bs + h;
-    const int cols = a.Dv - c0;
     Fetch<T, DK, NT> next;
     if (sq.len > 0) next.load(a, q, k, v, g, beta, 0, sq.len, cols);
     for (int t0 = 0; t0 < sq.len; t0 += NT) {
@@ -477,13 +477,13 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
     const int col = unit % blocks * 16 * W + 2 * W * g;
     const bool live = col < a.Dv;  // Dv is a multiple of 8
     const Seq sq = sequence(a, blockIdx.y);
+    const int64_t os = int64_t(a.H) * a.Dv;
+    const int c0 = unit % blocks * 16 * W, cols = min(a.Dv - c0, 16 * W);
+    zero_others(a, blockIdx.y, sq, static_cast<__nv_bfloat16*>(a.o) + int64_t(h) * a.Dv + c0, cols, lane, 32);
     if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + col;
-    const int64_t os = int64_t(a.H) * a.Dv;
     if (sq.slot < 0) {  // padding
-        const uint32_t zeros[W] = {};
-        for (int i = t; i < sq.len; i += 4)
-            if (live) store_words<W>(o + i * os, zeros);
+        zero_outputs(o - 2 * W * g, os, sq.len, cols, lane, 32);
         return;
     }
     TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * a.Dk + kRun * t) * a.Dv + col;

@@ -605,9 +605,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((int64_t(sq.begin) + int64_t(c_first) * kChunk) * a.H + h) * a.Dv + v0;
     const int64_t os = int64_t(a.H) * a.Dv;
     TS* st = static_cast<TS*>(a.state) + (int64_t(max(sq.slot, 0)) * a.H + h) * DK * a.Dv + v0;
+    if (kPart != Part::rest && j == 0)
+        zero_others(a, si, sq, static_cast<__nv_bfloat16*>(a.o) + int64_t(h) * a.Dv + v0, nv, tid, kWalkThreads);
     if (sq.slot < 0) {  // padding
-        for (int i = tid; i < sq.len * (nv / 8); i += kWalkThreads)
-            *reinterpret_cast<uint4*>(o + (i / (nv / 8)) * os + (i % (nv / 8)) * 8) = make_uint4(0, 0, 0, 0);
+        zero_outputs(o, os, sq.len, nv, tid, kWalkThreads);
         return;
     }
     if (sq.len == 0) {

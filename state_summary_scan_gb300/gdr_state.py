@@ -119,12 +119,14 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, 
             plan.checked.clear()
         plan.checked[key] = p
     if o is None:
-        o = C.allocated(lambda: torch.empty_like(v, memory_format=torch.contiguous_format), stream, v.get_device())
+        o = C.on_stream(lambda: torch.empty_like(v, memory_format=torch.contiguous_format), stream, v.get_device())
     elif o.shape != v.shape or o.dtype != v.dtype or o.device != v.device or not o.is_contiguous():
         raise ValueError("o must be contiguous and have the shape, type and device of v")
     if S:
         C.rm_gdr_state_forward(ctypes.addressof(p), q, k, v, g, beta, cu, slots, fresh, state, o, plan.ws,
                                C._raw_stream(stream, q.get_device()))
+    else:
+        C.on_stream(o.zero_, stream, o.get_device())
     return o
 
 
@@ -145,7 +147,7 @@ def gdr_prefill(plan: GdrStatePlan, q, k, v, g, beta, state, cu_seqlens, slots=N
     device.  max_len, a bound of the longest prompt (default the plan's), chooses the kernels: a
     longer prompt is taken whole too, in a form made for shorter ones.  The rest as gdr_decode, with
     q, k [N,qk_heads,Dk], v [N,H,Dv], g, beta [N,H].  An empty prompt leaves its slot as it is, or
-    zero when fresh."""
+    zero when fresh.  Tokens before the first prompt and after the last one have outputs 0."""
     if q.dim() != 3:
         raise ValueError("q must be [tokens, heads, Dk]")
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:

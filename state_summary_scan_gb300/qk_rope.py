@@ -128,7 +128,7 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     elements NaN."""
     _, p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
     if out is None:
-        out = C.allocated(lambda: (_new(q), _new(k)), stream, q.get_device())
+        out = C.on_stream(lambda: (_new(q), _new(k)), stream, q.get_device())
     else:
         _like(out, (q, k), "out")
     if q.numel():
@@ -160,7 +160,7 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, table=None, positions=None, q_we
         return (_new(q), _new(k), None if q_weight is None else weight(q_weight), None if k_weight is None else weight(k_weight),
                 torch.empty(size, dtype=torch.uint8, device=q.device) if size else None)
 
-    dq, dk, dwq, dwk, ws = C.allocated(buffers, stream, q.get_device())
+    dq, dk, dwq, dwk, ws = C.on_stream(buffers, stream, q.get_device())
     if not q.numel():
         return dq, dk, dwq, dwk
     C.rm_cp_qkr_backward(p, q, k, q_weight, k_weight, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws,

@@ -173,3 +173,20 @@ def prefill_check(kind, lens, bound, begin=0, rest=0, padding=None):
                                              ("segments", [4400, 5, 100], 3000)], ids=str)
 def test_gdr_prefill_takes_prompts_over_the_bound(kind, lens, bound):
     prefill_check(kind, lens, bound)
+
+
+@pytest.mark.parametrize("kind,lens,bound", [("fp32", [9, 0, 3], 9), ("few", [4, 0, 2], 4), ("some", [11, 12, 0], 12), ("chunks", [70, 0, 129], 129),
+                                             ("segments", [0, 3100, 5], 3100)], ids=str)
+@pytest.mark.parametrize("begin,rest", [(0, 5), (3, 200), (70, 0)])
+def test_gdr_prefill_writes_zeros_for_tokens_of_no_prompt(kind, lens, bound, begin, rest):
+    prefill_check(kind, lens, bound, begin, rest)
+    prefill_check(kind, lens, bound, begin, rest, padding=0)
+    prefill_check(kind, lens, bound, begin, rest, padding=len(lens) - 1)
+
+
+def test_gdr_prefill_of_no_prompts():
+    plan = api.make_gdr_state_plan(2, 100, 2, 64, 64)
+    q, k, v, g, beta, state, _ = gds_inputs([10], 2, 2, 64, 64, BF16, F32, 2)
+    before, o = state.clone(), torch.full_like(v, 7.0)
+    api.gdr_prefill(plan, q, k, v, g, beta, state, torch.zeros(1, dtype=torch.int32, device="cuda"), o=o)
+    assert not o.any() and torch.equal(state, before)
