@@ -419,15 +419,15 @@ def _raw_stream(stream, device: int):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _launch(device: int, fn, *args):
-    """fn(*args) with the tensors' device as the current one: the library launches on that."""
+def _on_device(fn, device: int):
+    """fn as it is called with `device` as the current one: the library launches on that."""
     if torch._C._cuda_getDevice() == device:
-        status = fn(*args)
-    else:
+        return fn
+
+    def call(*args):
         with torch.cuda.device(device):
-            status = fn(*args)
-    if status:
-        _check(status)
+            return fn(*args)
+    return call
 
 
 def on_stream(make, stream, device: int):
@@ -456,16 +456,21 @@ def rm_cp_qkr_forward(p: int, q, k, wq, wk, table, positions, q_out, k_out, stre
     """p: the address of a QkrProblem."""
     if _lib is None:
         load()
-    _launch(q.get_device(), _by_address["rm_cp_qkr_forward"], p, q.data_ptr(), k.data_ptr(), _addr(wq), _addr(wk), _addr(table),
-            _addr(positions), q_out.data_ptr(), k_out.data_ptr(), stream)
+    fn = _on_device(_by_address["rm_cp_qkr_forward"], q.get_device())
+    status = fn(p, q.data_ptr(), k.data_ptr(), _addr(wq), _addr(wk), _addr(table), _addr(positions), q_out.data_ptr(),
+                k_out.data_ptr(), stream)
+    if status:
+        _check(status)
 
 
 def rm_cp_qkr_backward(p: int, q, k, wq, wk, table, positions, dq_out, dk_out, dq, dk, dwq, dwk, ws, stream):
     if _lib is None:
         load()
-    _launch(q.get_device(), _by_address["rm_cp_qkr_backward"], p, q.data_ptr(), k.data_ptr(), _addr(wq), _addr(wk), _addr(table),
-            _addr(positions), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _addr(dwq), _addr(dwk),
-            _addr(ws), stream)
+    fn = _on_device(_by_address["rm_cp_qkr_backward"], q.get_device())
+    status = fn(p, q.data_ptr(), k.data_ptr(), _addr(wq), _addr(wk), _addr(table), _addr(positions), dq_out.data_ptr(),
+                dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _addr(dwq), _addr(dwk), _addr(ws), stream)
+    if status:
+        _check(status)
 
 
 def rm_gdr_state_path(p: GdrStateProblem) -> int:
@@ -480,9 +485,11 @@ def rm_gdr_state_forward(p: int, q, k, v, g, beta, cu_seqlens, slots, fresh, sta
     """p: the address of a GdrStateProblem."""
     if _lib is None:
         load()
-    _launch(q.get_device(), _by_address["rm_gdr_state_forward"], p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
-            beta.data_ptr(), _addr(cu_seqlens), _addr(slots), _addr(fresh), state.data_ptr(), o.data_ptr(), ws.data_ptr(),
-            stream)
+    fn = _on_device(_by_address["rm_gdr_state_forward"], q.get_device())
+    status = fn(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(cu_seqlens), _addr(slots),
+                _addr(fresh), state.data_ptr(), o.data_ptr(), ws.data_ptr(), stream)
+    if status:
+        _check(status)
 
 
 def rm_cp_clip_workspace_size(n: int) -> int:
@@ -491,5 +498,7 @@ def rm_cp_clip_workspace_size(n: int) -> int:
 
 def rm_cp_clip_grad_norm(n, grads, numels, dtypes, outs, out_dtypes, max_norm, eps, norm, ws, stream):
     """grads, numels, dtypes, outs, out_dtypes: addresses of host arrays (outs and out_dtypes may be None)."""
-    _launch(ws.get_device(), (_lib or load()).rm_cp_clip_grad_norm, n, grads, numels, dtypes, outs, out_dtypes, max_norm, eps,
-            norm.data_ptr(), ws.data_ptr(), stream)
+    fn = _on_device((_lib or load()).rm_cp_clip_grad_norm, ws.get_device())
+    status = fn(n, grads, numels, dtypes, outs, out_dtypes, max_norm, eps, norm.data_ptr(), ws.data_ptr(), stream)
+    if status:
+        _check(status)

@@ -66,7 +66,10 @@ def clip_grad_norm(plan: ClipPlan, grads: Sequence[torch.Tensor], max_norm: Opti
         if array.array("q", map(_Tensor.numel, out)) != sizes:
             raise ValueError("out must have the sizes of the gradients")
         out_ptr, out_types = _describe(out, plan.device, "out")
-    norm = C.on_stream(lambda: torch.empty((), dtype=torch.float32, device=plan.device), stream, plan.device.index)
+    if stream is None:
+        norm = torch.empty((), dtype=torch.float32, device=plan.device)
+    else:
+        norm = C.on_stream(lambda: torch.empty((), dtype=torch.float32, device=plan.device), stream, plan.device.index)
 
     def at(a):
         return a.buffer_info()[0]

@@ -109,6 +109,10 @@ def _checked_problem(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slo
     return p
 
 
+def _new(v):
+    return torch.empty_like(v, memory_format=torch.contiguous_format)
+
+
 def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, o, stream):
     sig = C.signature
     key = (lead, max_len, sig(q), sig(k), sig(v), sig(g), sig(beta), sig(state), sig(cu), sig(slots), sig(fresh))
@@ -119,7 +123,7 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, 
             plan.checked.clear()
         plan.checked[key] = p
     if o is None:
-        o = C.on_stream(lambda: torch.empty_like(v, memory_format=torch.contiguous_format), stream, v.get_device())
+        o = _new(v) if stream is None else C.on_stream(lambda: _new(v), stream, v.get_device())
     elif o.shape != v.shape or o.dtype != v.dtype or o.device != v.device or not o.is_contiguous():
         raise ValueError("o must be contiguous and have the shape, type and device of v")
     if S:

@@ -128,7 +128,7 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
     elements NaN."""
     _, p = _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
     if out is None:
-        out = C.on_stream(lambda: (_new(q), _new(k)), stream, q.get_device())
+        out = (_new(q), _new(k)) if stream is None else C.on_stream(lambda: (_new(q), _new(k)), stream, q.get_device())
     else:
         _like(out, (q, k), "out")
     if q.numel():
