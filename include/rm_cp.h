@@ -595,7 +595,7 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  * left in fp32's last bits, so that the fp32 outputs of a later call of two
  * correct programs differ by up to some 3e-3 of their rms in a few elements),
  * 1 when it runs in chunks on the tensor cores (dtype bf16, Dk 64
- * or 128, max_len >= 48), -1 for a problem it rejects.  In chunks, the state
+ * or 128, max_len and num_tokens >= 48), -1 for a problem it rejects.  In chunks, the state
  * and two factors that meet it are rounded to bf16 where they enter a product
  * (the state itself is kept in fp32): outputs are off by up to one and a half
  * times their own rounding in norm, the final state by some 1e-4.

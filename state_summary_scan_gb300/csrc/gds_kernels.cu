@@ -700,7 +700,9 @@ rm_status check(const rm_gdr_state_problem* p, Args* a) {
     }
     if (p->g_stride < 0 || p->beta_stride < 0) return api_fail(RM_ERR_INVALID_ARG, "strides must not be negative");
     a->gs = p->g_stride, a->bs = p->beta_stride;
-    a->S = p->num_seqs, a->N = p->num_tokens, a->max_len = p->max_len, a->H = p->H, a->hdiv = p->H / p->qk_heads;
+    // (no sequence is longer than all of them; no tokens at all: the recurrence, which needs none)
+    a->max_len = p->max_len < p->num_tokens ? p->max_len : p->num_tokens;
+    a->S = p->num_seqs, a->N = p->num_tokens, a->H = p->H, a->hdiv = p->H / p->qk_heads;
     a->Dk = p->Dk, a->Dv = p->Dv, a->slots_n = p->num_slots, a->scale = p->scale, a->each = 0;
     return RM_OK;
 }

@@ -190,3 +190,18 @@ def test_gdr_prefill_of_no_prompts():
     before, o = state.clone(), torch.full_like(v, 7.0)
     api.gdr_prefill(plan, q, k, v, g, beta, state, torch.zeros(1, dtype=torch.int32, device="cuda"), o=o)
     assert not o.any() and torch.equal(state, before)
+
+
+@pytest.mark.parametrize("bound", [None, 1, 64])
+@pytest.mark.parametrize("sdt", [F32, BF16])
+def test_gdr_prefill_of_empty_prompts_alone(bound, sdt):
+    plan = api.make_gdr_state_plan(3, 100, 2, 64, 64, state_dtype=sdt)
+    state = rnd(3, 2, 64, 64, dtype=sdt)
+    before = state.clone()
+    qkv = [torch.empty(0, 2, 64, device="cuda", dtype=BF16)] * 3
+    gates = [torch.empty(0, 2, device="cuda")] * 2
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    fresh = torch.tensor([0, 1], dtype=torch.uint8, device="cuda")
+    o = api.gdr_prefill(plan, *qkv, *gates, state, cu, fresh=fresh, max_len=bound)
+    assert o.shape == (0, 2, 64)
+    assert torch.equal(state[0], before[0]) and not state[1].any() and torch.equal(state[2], before[2])
