@@ -81,6 +81,8 @@ def _problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved)
 def _checked_problem(q, k, table, positions, q_weight, k_weight, norm, eps, interleaved) -> C.QkrProblem:
     if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
         raise ValueError("q and k must be [B,T,Hq,D] and [B,T,Hk,D]")
+    if 0 in q.shape[2:] or 0 in k.shape[2:]:
+        raise ValueError("q and k must have heads and elements")
     if q.dtype != k.dtype or q.dtype not in _DTYPES:
         raise ValueError("q and k must both be fp32 or both bf16")
     if not q.is_cuda or q.device != k.device:

@@ -100,6 +100,16 @@ def test_qkr_gradient_of_tiny_rows(norm, T):
     qkr_check(q * 3e-21, k * 3e-21, {**how, "norm": norm, "eps": 0.0}, pos, tol=3e-4)
 
 
+@pytest.mark.parametrize("Hq,Hk,D", [(0, 2, 64), (2, 0, 64), (0, 0, 64), (2, 2, 0)])
+def test_qkr_refuses_no_heads(Hq, Hk, D):
+    """No heads of q and some of k: k' was never written."""
+    q, k = rnd(1, 3, Hq, D), rnd(1, 3, Hk, D)
+    with pytest.raises(ValueError):
+        api.qk_norm_rope(q, k)
+    with pytest.raises(ValueError):
+        api.qk_norm_rope_backward(q, k, q, k)
+
+
 # ------------------------------------------------------------------ the delta rule with a state
 
 @pytest.mark.parametrize("lens,H,Hqk,Dk,Dv", [([1] * 5, 4, 2, 128, 128), ([1] * 3, 3, 3, 16, 40), ([4] * 3, 2, 1, 64, 72),
