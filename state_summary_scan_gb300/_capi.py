@@ -443,6 +443,11 @@ def on_stream(make, stream, device: int):
         return make()
 
 
+# What a call writes into tensors that the caller gave it raises their version counters, as an in-place
+# operation of PyTorch does.
+written = torch.autograd.graph.increment_version
+
+
 def signature(t: Optional[torch.Tensor]):
     """What a call's checks depend on; equal signatures pass the same checks."""
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())

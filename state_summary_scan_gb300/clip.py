@@ -77,4 +77,6 @@ def clip_grad_norm(plan: ClipPlan, grads: Sequence[torch.Tensor], max_norm: Opti
     C.rm_cp_clip_grad_norm(len(grads), at(ptr), at(sizes), at(types), None if max_norm is None else at(out_ptr),
                            None if max_norm is None else at(out_types), 0.0 if max_norm is None else max_norm, eps, norm,
                            plan.ws, C._raw_stream(stream, plan.device.index))
+    if max_norm is not None:
+        C.written(grads if out is None else out)
     return norm

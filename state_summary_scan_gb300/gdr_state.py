@@ -122,10 +122,14 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh, 
         if len(plan.checked) >= 256:
             plan.checked.clear()
         plan.checked[key] = p
+    given = [state]
     if o is None:
         o = _new(v) if stream is None else C.on_stream(lambda: _new(v), stream, v.get_device())
     elif o.shape != v.shape or o.dtype != v.dtype or o.device != v.device or not o.is_contiguous():
         raise ValueError("o must be contiguous and have the shape, type and device of v")
+    else:
+        given.append(o)
+    C.written(given)
     if S:
         C.rm_gdr_state_forward(ctypes.addressof(p), q, k, v, g, beta, cu, slots, fresh, state, o, plan.ws,
                                C._raw_stream(stream, q.get_device()))

@@ -133,6 +133,7 @@ def qk_norm_rope(q, k, table=None, positions=None, q_weight=None, k_weight=None,
         out = (_new(q), _new(k)) if stream is None else C.on_stream(lambda: (_new(q), _new(k)), stream, q.get_device())
     else:
         _like(out, (q, k), "out")
+        C.written(out)
     if q.numel():
         C.rm_cp_qkr_forward(p, q, k, q_weight, k_weight, table, positions, out[0], out[1],
                             C._raw_stream(stream, q.get_device()))

@@ -215,3 +215,33 @@ def test_gdr_prefill_of_empty_prompts_alone(bound, sdt):
     o = api.gdr_prefill(plan, *qkv, *gates, state, cu, fresh=fresh, max_len=bound)
     assert o.shape == (0, 2, 64)
     assert torch.equal(state[0], before[0]) and not state[1].any() and torch.equal(state[2], before[2])
+
+
+# ------------------------------------------------------------------ what a call writes in place
+
+def test_calls_raise_the_versions_of_what_they_write():
+    """As in-place operations do, so that autograd sees that a saved tensor has changed."""
+    plan, clip = api.make_gdr_state_plan(1, 10, 2, 64, 64), api.make_clip_plan(2)
+    q, k, v, g, beta, state, _ = gds_inputs([10], 2, 2, 64, 64, BF16, F32, 1)
+    a = [x[None] for x in (q, k, v, g, beta)]
+    o, out, grads, clipped = torch.empty_like(a[2]), (torch.empty_like(a[0]), torch.empty_like(a[1])), [rnd(10), rnd(7)], [rnd(10), rnd(7)]
+    with torch.inference_mode():
+        kept = state.clone()  # has no version
+
+    def changed(call, *tensors):
+        before = [t._version for t in tensors]
+        call()
+        return [t._version > n for t, n in zip(tensors, before)]
+
+    assert changed(lambda: api.gdr_decode(plan, *a, state, o=o), state, o, *a) == [True] * 2 + [False] * 5
+    assert changed(lambda: api.gdr_decode(plan, *a, state), state, o) == [True, False]
+    api.gdr_decode(plan, *a, kept)
+    assert changed(lambda: api.qk_norm_rope(a[0], a[1], out=out), *out, *a) == [True] * 2 + [False] * 5
+    assert changed(lambda: api.clip_grad_norm(clip, grads), *grads) == [False] * 2
+    assert changed(lambda: api.clip_grad_norm(clip, grads, 1.0), *grads) == [True] * 2
+    assert changed(lambda: api.clip_grad_norm(clip, grads, 1.0, out=clipped), *grads, *clipped) == [False] * 2 + [True] * 2
+    w = rnd(10).requires_grad_(True)
+    y = w * grads[0]
+    api.clip_grad_norm(clip, grads, 1.0)
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
