@@ -63,19 +63,20 @@ def make_gdr_state(plan: GdrStatePlan) -> torch.Tensor:
 
 
 def _strides(x, lead, name):
-    """(token, head) strides of x [*lead, heads, D]; the tokens must be evenly spaced."""
+    """(token, head) strides of x [*lead, heads, D]; the tokens must be evenly spaced.  A dimension of one
+    element takes no step, whatever its stride."""
     if x.stride(-1) != 1 and x.shape[-1] != 1:
         raise ValueError(f"the elements of a head of {name} must be adjacent")
-    return _token_stride(x, lead, name), x.stride(-2)
+    return _token_stride(x, lead, name), x.stride(-2) if x.shape[-2] > 1 else 0
 
 
 def _token_stride(x, lead, name):
     if lead == 1:
-        return x.stride(0)
+        return x.stride(0) if x.shape[0] > 1 else 0
     S, n = x.shape[0], x.shape[1]
     if S > 1 and n > 1 and x.stride(0) != n * x.stride(1):
         raise ValueError(f"the tokens of {name} must be evenly spaced")
-    return x.stride(1) if n > 1 else x.stride(0)
+    return x.stride(1) if n > 1 else x.stride(0) if S > 1 else 0
 
 
 def _checked_problem(plan, lead, S, N, max_len, q, k, v, g, beta, state, cu, slots, fresh):

@@ -217,6 +217,33 @@ def test_gdr_prefill_of_empty_prompts_alone(bound, sdt):
     assert torch.equal(state[0], before[0]) and not state[1].any() and torch.equal(state[2], before[2])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 3])
+def test_gdr_strides_of_one_token_or_one_head_do_not_matter(dtype, n):
+    """One token of rows, or one head of tokens, whose strides are not multiples of 16 bytes: no step is taken."""
+    H = 2 if n == 1 else 1  # one of the two dimensions has one element
+    row = 3 * 64 + 8
+
+    def parts(seed):
+        if n == 1:
+            x = rnd(1, 3 * row, seed=seed, dtype=dtype).as_strided((1, H, row), (3 * row + 1, row, 1))
+        else:
+            x = rnd(n, row, seed=seed, dtype=dtype).as_strided((n, 1, row), (row, row + 1, 1))
+        q, k, v = x[..., :64], x[..., 64: 128], x[..., 128: 192]
+        assert any(s * q.element_size() % 16 for s in q.stride()[:2])
+        return q, (k * 0.125).as_strided(k.shape, (H * 64, 64, 1)), v
+
+    q, k, v = parts(1)
+    g, beta, state = -rnd(n, H, seed=2).abs(), torch.sigmoid(rnd(n, H, seed=3)), rnd(1, H, 64, 64, seed=4)
+    plan = api.make_gdr_state_plan(1, n, H, 64, 64, dtype=dtype)
+    before, tol = state.clone(), (n + 64) * U
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    gds_check([n], q, k, v, g, beta, before, state, o, [0], None, 0.125, tol, tol)
+    again = before.clone()
+    o2 = api.gdr_decode(plan, *(x[None] for x in (q, k, v, g, beta)), again)
+    assert torch.equal(o2[0], o) and torch.equal(again, state)
+
+
 # ------------------------------------------------------------------ what a call writes in place
 
 def test_calls_raise_the_versions_of_what_they_write():
