@@ -595,7 +595,8 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  * left in fp32's last bits, so that the fp32 outputs of a later call of two
  * correct programs differ by up to some 3e-3 of their rms in a few elements),
  * 1 when it runs in chunks on the tensor cores (dtype bf16, Dk 64
- * or 128, max_len and num_tokens >= 48), -1 for a problem it rejects.  In chunks, the state
+ * or 128, max_len and num_tokens >= 48, recurrent 0), -1 for a problem it
+ * rejects.  recurrent != 0 keeps every call a token recurrence.  In chunks, the state
  * and two factors that meet it are rounded to bf16 where they enter a product
  * (the state itself is kept in fp32): outputs are off by up to one and a half
  * times their own rounding in norm, the final state by some 1e-4.
@@ -609,6 +610,7 @@ typedef struct {
     int64_t k_stride[2];
     int64_t v_stride[2];
     int64_t g_stride, beta_stride;
+    int32_t recurrent;
 } rm_gdr_state_problem;
 int32_t rm_gdr_state_path(const rm_gdr_state_problem* p);
 size_t rm_gdr_state_workspace_size(const rm_gdr_state_problem* p);

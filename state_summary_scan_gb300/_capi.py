@@ -88,7 +88,7 @@ class GdrStateProblem(ctypes.Structure):
                                               "num_slots")] + [
         ("scale", ctypes.c_float), ("dtype", ctypes.c_int), ("state_dtype", ctypes.c_int),
         ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2), ("v_stride", ctypes.c_int64 * 2),
-        ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64)]
+        ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64), ("recurrent", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p

@@ -12,6 +12,7 @@ struct Args {
     int S, N, max_len;      // sequences, packed tokens, tokens of a sequence that the launch is chosen for
     int H, hdiv, Dk, Dv;    // head h reads the q and k rows of head h / hdiv
     int slots_n;
+    int recurrent;          // never in chunks
     int each;               // tokens of every sequence without cu, else 0
     float scale;
     int64_t qs[2], ks[2], vs[2];  // token and head strides (elements)

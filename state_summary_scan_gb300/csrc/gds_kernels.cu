@@ -704,6 +704,7 @@ rm_status check(const rm_gdr_state_problem* p, Args* a) {
     a->max_len = p->max_len < p->num_tokens ? p->max_len : p->num_tokens;
     a->S = p->num_seqs, a->N = p->num_tokens, a->H = p->H, a->hdiv = p->H / p->qk_heads;
     a->Dk = p->Dk, a->Dv = p->Dv, a->slots_n = p->num_slots, a->scale = p->scale, a->each = 0;
+    a->recurrent = p->recurrent != 0;
     return RM_OK;
 }
 

@@ -1179,7 +1179,7 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
 }  // namespace
 
 bool tc_supports(const Args& a, rm_dtype dt) {
-    return dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
+    return !a.recurrent && dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
 }
 
 // A smaller problem may be cut into more segments than this one, so the bound is that of all of them:

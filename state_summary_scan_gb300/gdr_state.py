@@ -34,10 +34,13 @@ class GdrStatePlan:
 
 def make_gdr_state_plan(max_seqs: int, max_tokens: int, H: int, Dk: int, Dv: int, num_slots: Optional[int] = None,
                         qk_heads: int = 0, max_len: Optional[int] = None, scale=None, dtype=torch.bfloat16,
-                        state_dtype=torch.float32, device="cuda") -> GdrStatePlan:
+                        state_dtype=torch.float32, device="cuda", recurrent: bool = False) -> GdrStatePlan:
     """Plan of calls with up to max_seqs sequences, max_tokens tokens in all and max_len tokens a
     sequence (default max_tokens).  qk_heads > 0: q and k have that many heads, each shared by
-    H / qk_heads consecutive heads."""
+    H / qk_heads consecutive heads.  bf16 calls of 48 tokens a sequence or more (Dk 64 or 128) run in
+    chunks on the tensor cores, which rounds some factors to bf16: outputs are off by up to one and a
+    half times their own rounding, the state by some 1e-4.  recurrent=True keeps every call a token
+    recurrence at fp32's precision, whatever the lengths of its batch, and slower for prompts."""
     if dtype not in _DTYPES or state_dtype not in _DTYPES:
         raise ValueError("dtype and state_dtype must be fp32 or bf16")
     if scale is None:
@@ -50,6 +53,7 @@ def make_gdr_state_plan(max_seqs: int, max_tokens: int, H: int, Dk: int, Dv: int
     c.q_stride = c.k_stride = (qk_heads * Dk, Dk)
     c.v_stride = (H * Dv, Dv)
     c.g_stride = c.beta_stride = H
+    c.recurrent = int(recurrent)
     need = C.rm_gdr_state_workspace_size(c)
     if need == 0:
         raise C.RmCpError(C.load().rm_gdr_state_forward(c, *[None] * 12), C.load().rm_cp_last_error().decode())

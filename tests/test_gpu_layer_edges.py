@@ -244,6 +244,24 @@ def test_gdr_strides_of_one_token_or_one_head_do_not_matter(dtype, n):
     assert torch.equal(o2[0], o) and torch.equal(again, state)
 
 
+@pytest.mark.parametrize("Dk,Dv,sdt", [(64, 72, F32), (128, 128, F32), (128, 136, BF16)])
+def test_gdr_prefill_as_a_recurrence_by_choice(Dk, Dv, sdt):
+    """bf16 prompts that would run in chunks, at fp32's precision; a prompt's bits do not depend on its batch."""
+    lens, H = [200, 7, 0, 64], 2
+    q, k, v, g, beta, state, slots = gds_inputs(lens, H, 1, Dk, Dv, BF16, sdt, 5)
+    how = dict(num_slots=5, qk_heads=1, state_dtype=sdt)
+    plan = api.make_gdr_state_plan(4, sum(lens), H, Dk, Dv, recurrent=True, **how)
+    assert C.rm_gdr_state_path(plan.c) == 0 and C.rm_gdr_state_path(api.make_gdr_state_plan(4, sum(lens), H, Dk, Dv, **how).c) == 1
+    before, tol = state.clone(), (max(lens) + Dk) * U
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda())
+    gds_check(lens, q, k, v, g, beta, before, state, o, slots, None, Dk ** -0.5, tol, tol)
+    one = before.clone()
+    o2 = api.gdr_prefill(plan, *(x[200:207] for x in (q, k, v, g, beta)), one, torch.tensor([0, 7], dtype=torch.int32, device="cuda"),
+                         slots=slots[1:2].cuda())
+    assert torch.equal(o2, o[200:207]) and torch.equal(one[int(slots[1])], state[int(slots[1])])
+
+
 # ------------------------------------------------------------------ what a call writes in place
 
 def test_calls_raise_the_versions_of_what_they_write():
