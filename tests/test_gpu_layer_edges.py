@@ -110,6 +110,57 @@ def test_qkr_refuses_no_heads(Hq, Hk, D):
         api.qk_norm_rope_backward(q, k, q, k)
 
 
+LONG = [  # B, T, Hq, Hk, D, R, norm, weights, interleaved, dtype, fused, positions
+    # enough tokens and heads for rows streamed through shared memory
+    (1, 7297, 16, 16, 128, 128, "rms", True, False, BF16, False, None),
+    (1, 8009, 8, 4, 128, 64, "l2", True, True, BF16, True, torch.int64),
+    (3, 2501, 8, 9, 64, 64, "rms", True, False, F32, True, torch.int32),
+    (2, 4001, 9, 5, 80, 48, "rms", True, False, F32, False, torch.int32),
+    (1, 9001, 8, 8, 96, 96, "l2", False, True, BF16, False, None),
+    (1, 7411, 16, 17, 32, 0, "rms", True, False, F32, False, None),
+    (1, 16001, 4, 7, 256, 128, "none", True, False, BF16, True, torch.int32),
+    (1, 7500, 4, 3, 256, 256, "rms", True, True, F32, False, torch.int64),
+    # few heads, or pairs that straddle lanes: a loop over groups of heads, past a warp's first tokens
+    (1, 20011, 2, 1, 64, 64, "rms", True, False, BF16, True, None),
+    (1, 10001, 3, 2, 128, 128, "l2", True, True, F32, False, torch.int32),
+    (1, 5003, 16, 2, 80, 20, "rms", True, False, BF16, False, torch.int32),
+    (1, 2003, 5, 3, 128, 128, "rms", True, False, F32, True, torch.int32),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_qkr_long_inputs_against_64_bits(case):
+    B, T, Hq, Hk, D, R, norm, weights, inter, dtype, fused, pos = case
+    q, k, how, full = qkr_case(B, T, Hq, Hk, D, R, dtype, fused, pos, weights)
+    qkr_check(q, k, {**how, "norm": norm, "eps": 1e-5, "interleaved": inter}, full)
+
+
+def test_qkr_long_inputs_with_rows_of_zeros_and_bad_positions():
+    T, H, D, R = 8009, 16, 64, 32
+    q, k = rnd(1, T, H, D), rnd(1, T, H, D, seed=1)
+    q[0, 1] = 0
+    k[0, T - 2, 3] = 0
+    q[0, 2, 0, 5] = float("nan")
+    table = api.make_rope_table(10, R)
+    pos = torch.randint(0, 10, (T,), generator=torch.Generator("cuda").manual_seed(2), device="cuda", dtype=torch.int32)
+    bad = torch.tensor([4, 700, 3648, T - 1], device="cuda")
+    pos[bad] = torch.tensor([10, -1, 1 << 30, -(1 << 31)], device="cuda", dtype=torch.int32)
+    how = dict(table=table, positions=pos, norm="l2", eps=1e-6)
+    y, z = api.qk_norm_rope(q, k, **how)
+    assert torch.equal(y[0, 1], torch.zeros_like(y[0, 1]))
+    assert torch.isnan(y[0, 2, 0]).all() and not torch.isnan(y[0, 2, 1:]).any()
+    for x in (y, z):
+        assert torch.isnan(x[0, bad, :, :R]).all() and not torch.isnan(x[0, bad, :, R:]).any()
+    fine = torch.ones(T, dtype=torch.bool, device="cuda")
+    fine[bad] = False
+    want = qkr_ref(k.double(), None, table.double(), pos.clamp(0, 9).long()[None], "l2", 1e-6, False)
+    close(z[0, fine], want[0, fine], 32 * U, F32, "k'")
+    dq, dk, _, _ = api.qk_norm_rope_backward(q, k, torch.ones_like(q), torch.ones_like(k), **how)
+    assert torch.isnan(dk[0, bad]).all() and torch.isfinite(dk[0, fine]).all()
+    fine[2] = False
+    assert torch.isfinite(dq[0, fine]).all()
+
+
 # ------------------------------------------------------------------ the delta rule with a state
 
 @pytest.mark.parametrize("lens,H,Hqk,Dk,Dv", [([1] * 5, 4, 2, 128, 128), ([1] * 3, 3, 3, 16, 40), ([4] * 3, 2, 1, 64, 72),
@@ -260,6 +311,68 @@ def test_gdr_prefill_as_a_recurrence_by_choice(Dk, Dv, sdt):
     o2 = api.gdr_prefill(plan, *(x[200:207] for x in (q, k, v, g, beta)), one, torch.tensor([0, 7], dtype=torch.int32, device="cuda"),
                          slots=slots[1:2].cuda())
     assert torch.equal(o2, o[200:207]) and torch.equal(one[int(slots[1])], state[int(slots[1])])
+
+
+def chunked_check(lens, q, k, v, g, beta, before, after, o, slots, which=None):
+    """In chunks, with the tolerances of test_gdr_prefill_in_chunks_against_64_bits."""
+    at, sdt = 0, after.dtype
+    for i, n in enumerate(lens):
+        s, j = slice(at, at + n), int(slots[i])
+        at += n
+        if not 0 <= j < before.shape[0]:
+            assert not o[s].any()
+        elif n == 0:
+            assert torch.equal(after[j], before[j])
+        elif which is None or i in which:
+            want_o, want_S = gds_ref(q[s], k[s], v[s], g[s], beta[s], before[j], q.shape[-1] ** -0.5)
+            assert rel2(o[s], want_o) <= 2.0 ** -8, (i, rel2(o[s], want_o))
+            assert rel2(after[j], want_S) <= 2e-3 + (2.0 ** -8 if sdt == BF16 else 0), (i, rel2(after[j], want_S))
+
+
+@pytest.mark.parametrize("S,n,Dk,Dv", [(3, 48, 64, 64), (5, 65, 128, 72), (2, 130, 64, 256)])
+def test_gdr_decode_of_many_tokens_in_chunks(S, n, Dk, Dv):
+    q, k, v, g, beta, state, slots = gds_inputs([n] * S, 4, 2, Dk, Dv, BF16, F32, S + 2)
+    slots[1] = -1
+    plan = api.make_gdr_state_plan(S, S * n, 4, Dk, Dv, num_slots=S + 2, qk_heads=2, max_len=n)
+    assert C.rm_gdr_state_path(plan.c) == 1
+    before = state.clone()
+    o = api.gdr_decode(plan, *(x.unflatten(0, (S, n)) for x in (q, k, v, g, beta)), state, slots=slots.cuda())
+    chunked_check([n] * S, q, k, v, g, beta, before, state, o.flatten(0, 1), slots)
+
+
+@pytest.mark.parametrize("S,Dk,Dv", [(33, 64, 64), (70, 128, 128), (1100, 64, 40)])
+def test_gdr_prefill_of_many_prompts_in_chunks(S, Dk, Dv):
+    lens = torch.randint(0, 140 if S < 1000 else 70, (S,), generator=torch.Generator().manual_seed(S)).tolist()
+    lens[S // 2], lens[S - 1] = 0, 128
+    q, k, v, g, beta, state, slots = gds_inputs(lens, 2, 1, Dk, Dv, BF16, F32, S + 2)
+    slots[5] = S + 9
+    plan = api.make_gdr_state_plan(S, sum(lens), 2, Dk, Dv, num_slots=S + 2, qk_heads=1, max_len=max(lens))
+    before = state.clone()
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda())
+    chunked_check(lens, q, k, v, g, beta, before, state, o, slots, range(0, S, 1 + S // 40))
+
+
+@pytest.mark.parametrize("sdt", [F32, BF16])
+@pytest.mark.parametrize("bound,launches", [(4100, 4), (6600, 4), (4100, 2)])
+def test_gdr_prefill_at_128_through_strong_decay(sdt, bound, launches):
+    """Strong chunks among weak ones, next to one another, at both ends of a segment and in the last chunk; in
+    segments, and whole where the heads are many."""
+    lens, H = [4100, 2500], 2 if launches == 4 else 40
+    q, k, v, g, beta, state, slots = gds_inputs(lens, H, 1, 128, 128, BF16, sdt, 2, seed=4)
+    g[300:420, 0] = -3.0
+    g[900] = -float("inf")
+    g[2000:2300, 1] *= 40
+    g[4090:4100, 1] = -9.0   # the last tokens of the first prompt
+    g[4500:4570, 0] = -4.0
+    g[5000:5700:128, 1] = -70.0
+    g[6000:6200, 1] = -0.95  # near the limit of a weak chunk
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    plan = api.make_gdr_state_plan(2, sum(lens), H, 128, 128, num_slots=2, qk_heads=1, state_dtype=sdt)
+    before, n0 = state.clone(), C.rm_cp_launch_count()
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda(), max_len=bound)
+    assert C.rm_cp_launch_count() - n0 == launches
+    chunked_check(lens, q, k, v, g, beta, before, state, o, slots)
 
 
 # ------------------------------------------------------------------ what a call writes in place
