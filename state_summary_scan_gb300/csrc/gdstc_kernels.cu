@@ -37,7 +37,6 @@
 #include <cstdio>
 
 #include "gds.cuh"
-#include "gdr_tri.cuh"
 
 namespace rmcp {
 namespace gds {
