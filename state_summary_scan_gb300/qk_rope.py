@@ -12,6 +12,7 @@ import threading
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _capi as C
 
@@ -181,6 +182,7 @@ class QkNormRope(torch.autograd.Function):
         return qk_norm_rope(q, k, table, positions, q_weight, k_weight, **ctx.how)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, table, positions = ctx.saved_tensors
         dq, dk, dwq, dwk = qk_norm_rope_backward(q, k, dq_out.contiguous(), dk_out.contiguous(), table, positions,

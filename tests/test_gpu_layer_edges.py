@@ -161,6 +161,15 @@ def test_qkr_long_inputs_with_rows_of_zeros_and_bad_positions():
     assert torch.isfinite(dq[0, fine]).all()
 
 
+def test_qkr_adapter_refuses_second_derivatives():
+    """The backward's result has no graph: a second derivative through it would be taken for 0."""
+    q = rnd(1, 3, 2, 64).requires_grad_(True)
+    y, z = api.qk_norm_rope_train(q, rnd(1, 3, 1, 64, seed=1), norm="l2")
+    dq, = torch.autograd.grad((y * y * y).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        (dq.square().sum() + q.square().sum()).backward()
+
+
 # ------------------------------------------------------------------ the delta rule with a state
 
 @pytest.mark.parametrize("lens,H,Hqk,Dk,Dv", [([1] * 5, 4, 2, 128, 128), ([1] * 3, 3, 3, 16, 40), ([4] * 3, 2, 1, 64, 72),
