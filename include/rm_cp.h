@@ -599,7 +599,9 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  * rejects.  recurrent != 0 keeps every call a token recurrence.  In chunks, the state
  * and two factors that meet it are rounded to bf16 where they enter a product
  * (the state itself is kept in fp32): outputs are off by up to one and a half
- * times their own rounding in norm, the final state by some 1e-4.
+ * times their own rounding in norm, the final state by some 1e-4.  A NaN or an
+ * infinity in a token then reaches the outputs of all 64 tokens of its chunk
+ * (in the recurrence: its own and those after it), never another sequence.
  */
 typedef struct {
     int32_t num_seqs, num_tokens, max_len;
@@ -625,7 +627,9 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * n tensors, numels[i] elements each (0 allowed), dtypes[i] RM_F32 or RM_BF16
  * for grads[i] and out_dtypes[i] for outs[i]; grads, outs, numels, dtypes and
  * out_dtypes are HOST arrays, the pointers in them device pointers aligned to
- * their elements.  outs[i] may be grads[i] (in place).  outs NULL: the norm
+ * their elements.  outs[i] may be grads[i] (in place); otherwise no output
+ * overlaps a gradient or another output (so a gradient that is clipped in
+ * place is listed once).  outs NULL: the norm
  * alone.  norm: one fp32 on the device.  The squares are summed in fp32 within
  * a thread's few elements of a piece, in fp64 beyond, in an order that depends
  * on the sizes alone; pieces whose squares would leave fp32's range are summed

@@ -79,12 +79,12 @@ __device__ __forceinline__ void zero_others(const Args& a, int i, const Seq& s, 
 
 // The chunked form on the tensor cores, for calls whose longest sequence has this many tokens.  Its two
 // launches take a chunk of 64 rows however few of them are tokens, and the recurrence grows with the
-// tokens (us, recurrence / chunks; bf16, fp32 state):
+// tokens (us in a CUDA graph, recurrence / chunks; bf16, fp32 state):
 //     tokens                               32          40          48          64
-//     64 sequences, 16 heads, 128 x 128    91 / 117    107 / 118   126 / 120   160 / 115
-//     64 sequences, 32 heads, 64 x 256     195 / 285   236 / 286   277 / 290   359 / 265
-//     8 sequences, 32 heads, 128 x 128     36 / 44     40 / 43     46 / 44     56 / 42
-//     one sequence, 16 heads, 128 x 128    17 / 26     19 / 26     21 / 26     25 / 24
+//     64 sequences, 16 heads, 128 x 128    87 / 107    105 / 109   122 / 111   157 / 105
+//     64 sequences, 32 heads, 64 x 256     193 / 279   234 / 283   275 / 285   358 / 259
+//     8 sequences, 32 heads, 128 x 128     28 / 33     33 / 33     39 / 34     50 / 32
+//     one sequence, 16 heads, 128 x 128    10 / 17     12 / 17     14 / 17     17 / 16
 constexpr int kChunkedLen = 48;
 bool tc_supports(const Args& a, rm_dtype dt);
 size_t tc_workspace_bytes(const Args& a);

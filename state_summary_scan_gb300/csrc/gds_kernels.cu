@@ -14,7 +14,8 @@
 //                     heads 32 or more CTAs.  Several tokens are taken four at a time, so that four share
 //                     one pass over the state, one reduction across the threads and one update.
 //                     256 sequences, one token, 16 heads of 128 x 128, fp32 state: 82 us, 6.6 TB/s.
-//                     Ragged fp32 prompts of up to 301 tokens: 88 us, the latency of 75 tiles.
+//                     Ragged fp32 prompts of up to 301 tokens: 86 us, the latency of 75 tiles; one fp32
+//                     prompt of 8192 tokens, 16 heads of 128 x 128: 4.4 ms.
 //   gds_tile_kernel   bf16 inputs, four tokens as products of the warp's matrix instructions
 #include <cstdio>
 #include <type_traits>
@@ -314,12 +315,14 @@ __global__ void __launch_bounds__(kTpb, NT == 1 ? 8 : 5) gds_token_kernel(const 
 // Dk, so that no two warps meet; the lanes' rows and columns are permuted such that the state's
 // elements are loaded and stored straight from the registers that enter the products.
 //
-// 61 sequences, four tokens, 32 heads of 128 x 256, bf16 state: 55.7 us, 4.8 TB/s, against 120 us of
+// 61 sequences, four tokens, 32 heads of 128 x 256, bf16 state: 53.9 us, 4.9 TB/s, against 120 us of
 // the fp32 recurrence, whose 1294 instructions for 4096 elements of state bound it.  What bounds it
 // now is the latency of the state's reads at 12 warps an SM: 32 columns a warp (8 bytes a lane and
 // row; 16 columns and 20 warps an SM: 78 us), everything else loaded before the state (after it:
-// 64 us).  Longer calls keep the state in fp32 and 16 columns a warp, for twice the warps (32
-// columns: 21 instead of 17 us for one prompt of 32 tokens and 16 heads).
+// 64 us).  Longer calls keep the state in fp32 and 16 columns a warp, for twice the warps.  In a CUDA graph the
+// same sequences take 50 us for four tokens, 102 for five to eight and 134 for twelve (32 columns a warp: 122 to 126,
+// 158); with a fp32 state 79 for one token, 99 to 102 for two to four (152), 128 to 134 for five to eight (180).  One
+// prompt of 32 tokens and 16 heads: 10 us (23).
 //
 // Keys and queries are bf16 and enter as they are.  A bf16 state enters its first tile as it is; a
 // state in fp32, and d of a token, as the sum of three bf16, which hold its 24 bits.  Products
@@ -663,8 +666,8 @@ bool token_launch(const Args& a, cudaStream_t s) {
 template <typename TS>
 bool recurrence(const Args& a, bool f32, cudaStream_t s) {
     // Single tokens with a fp32 state: the token kernel, whose loads of 16 bytes a lane fill whole lines
-    // (256 sequences, 16 heads of 128 x 128: 82 us; tiles: 97).  With a bf16 state: tiles (54 us; the
-    // token kernel 66).
+    // (256 sequences, 16 heads of 128 x 128: 82 us; tiles: 98).  With a bf16 state: tiles (50 us; the
+    // token kernel 64).
     const bool one = a.max_len <= 1;
     if (f32) return one ? token_launch<float, TS, 1>(a, s) : token_launch<float, TS, 4>(a, s);
     if constexpr (sizeof(TS) == 2) {

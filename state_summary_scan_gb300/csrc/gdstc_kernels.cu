@@ -70,8 +70,9 @@ __device__ __forceinline__ int first_chunk(const Args& a, int i) {
     const int b = a.cu ? min(max(__ldg(a.cu + i), 0), a.N) : i * a.each;
     return b / kChunk + i;
 }
-// The y-th longest of up to 32 sequences, so that the longest walks begin first (13 ragged prompts of up to
-// 4096 tokens: 208 to 181 us; with more sequences they even out by themselves).  Whole-warp call.
+// The y-th longest of up to 32 sequences, one a lane, so that the longest walks begin first (13 ragged prompts
+// of up to 4096 tokens: 208 to 181 us).  With 33 to 128 ragged prompts of 32 heads a call with the longest
+// given first takes 2 to 3.5% less (33 of up to 2048 tokens: 804 for 833 us), which is left.  Whole-warp call.
 __device__ __forceinline__ int by_length(const Args& a, int y) {
     if (a.cu == nullptr || a.S > 32) return y;
     const int lane = threadIdx.x & 31, i = min(lane, a.S - 1);
@@ -1116,11 +1117,16 @@ size_t factors_bytes(const Args& a) { return size_t(chunk_slots(a)) * a.H * fact
 // CTAs (one per block of columns for the first segment, one more for M in each inner one) on the
 // GPU's 152 multiprocessors at once, of eight chunks or more.  With n segments the chain is two walks
 // of 1 / n of the chunks, some 1.2 us a chunk; two more launches and the composition cost some 30 us.  So
-// a cut has to save 28 chunks.  us, whole / cut, 128 x 128:
-//     chunks                          16          32          128
-//     16 heads (6 segments)           48 / 60     76 / 85     240 / 177
-//     32 heads (3)                    56 / 74     91 / 103    292 / 283
-//     48 heads (3)                    64 / 89     107 / 130   347 / 365
+// a cut has to save 28 chunks.  us in a CUDA graph, whole / cut:
+//     chunks                          16          32          64          128
+//     16 heads of 128 x 128           38 / 54     68 / 76     122 / 111   230 / 176 (strong decay 232 / 176)
+//     two prompts of 8 such heads                 68 / 79                 230 / 176
+//     32 heads of 128 x 128                       82 / 102                278 / 277
+//     48 heads of 128 x 128                                               331 / 360
+//     16 heads of 64 x 64                         55 / 55                 185 / 128
+//     4 heads of 64 x 64                                      81 / 51
+//     8 heads of 128 x 256                        61 / 65                 211 / 150
+//     16 heads of 128 x 256 (4 segments)                                  242 / 226
 // and with three segments the second walk shares the memory with too many others to gain.
 int segments(const Args& a, int* chunks) {
     const int all = (a.max_len + kChunk - 1) / kChunk, blocks = (a.Dv + 127) / 128;

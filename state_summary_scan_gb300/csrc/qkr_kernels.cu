@@ -12,8 +12,9 @@
 // sums of a row are a few shuffles and nothing is staged in shared memory; in the half layout
 // the partner of a lane's eight elements is the eight elements of the lane R/16 away.  A warp
 // keeps one token's cos and sin in registers over that token's heads.  Long inputs go through
-// qkr_stream_kernel.  32768 tokens, 16 + 16 heads of 128 in bf16: forward 87 us (6.1 TB/s), backward with
-// both weight gradients 139 us (5.8 TB/s); one token of 32 + 8 heads: 5 us, a launch.
+// qkr_stream_kernel.  32768 tokens, 16 + 16 heads of 128 in bf16: forward 95 us (5.7 TB/s), backward with
+// both weight gradients 136 us (5.9 TB/s); one token of 32 + 8 heads: 2.9 us, a launch.  (All times here: calls
+// one after another in a CUDA graph, on inputs that together exceed the L2.)
 #include <cstdio>
 
 #include "pairs.cuh"
@@ -532,10 +533,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) qkr_backward_kernel(const __gr
 // token's row of the table) while it works on the other.  The loop above waits for memory between
 // its groups; this one needs a token's heads side by side in memory, and enough of them to be worth
 // a copy.  us, the loop / this kernel, forward and backward:
-//     16 + 16 heads of 128, bf16, 8192 tokens     40 / 33      52 / 48
-//     the same, 32768 tokens                      107 / 101    150 / 130
-//     8 + 4 heads of 128, bf16, 32768 tokens      54 / 52      70 / 72
-//     16 + 16 heads of 64, fp32, 32768 tokens     101 / 99     129 / 102
+//     16 + 16 heads of 128, bf16, 8192 tokens     34 / 28      56 / 45
+//     the same, 32768 tokens                      101 / 95     172 / 136
+//     8 + 4 heads of 128, bf16, 32768 tokens      48 / 48      77 / 68
+//     16 + 16 heads of 64, fp32, 32768 tokens     96 / 98      148 / 133
 // Three blocks of eight warps forward, one of twelve backward: the stages fill the shared memory.
 // ---------------------------------------------------------------------------
 template <bool kBack>

@@ -29,7 +29,8 @@ def make_rope_table(max_positions: int, rotary_dim: int, base: float = 10000.0, 
     the trained one: "linear" divides every frequency by factor; "ntk" raises the base so that the
     slowest pair's frequency is divided by factor and the fastest is kept; "yarn" keeps pairs
     that turn at least beta_fast times over trained_positions, divides those that turn at most
-    beta_slow times, blends between them, and scales cos and sin by 0.1 ln(factor) + 1."""
+    beta_slow times, blends between them, and scales cos and sin by 0.1 ln(factor) + 1.  The blend
+    is linear in the turns of a pair; tables that blend over the pair's index differ between the two."""
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be positive and even")
     if max_positions <= 0:
