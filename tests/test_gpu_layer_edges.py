@@ -412,3 +412,113 @@ def test_calls_raise_the_versions_of_what_they_write():
     api.clip_grad_norm(clip, grads, 1.0)
     with pytest.raises(RuntimeError):
         y.sum().backward()
+
+
+# ------------------------------------------------------------------ offsets beyond 32 bits
+
+@pytest.mark.parametrize("lens,dtype,sdt", [([1, 1], F32, F32), ([3, 2], F32, BF16), ([4, 1], BF16, BF16), ([9, 2], BF16, BF16), ([1, 1], BF16, F32),
+                                            ([70, 5], BF16, F32), ([3100, 40], BF16, BF16)], ids=str)
+def test_gdr_states_beyond_32_bits(lens, dtype, sdt):
+    """The last slots of a pool of more than 2^31 elements; the first ones, where a 32-bit offset would lead, stay."""
+    H, D = 2, 128
+    slots_n = 2 ** 31 // (H * D * D) + 10
+    q, k, v, g, beta, few, _ = gds_inputs(lens, H, 1, D, D, dtype, sdt, 20)
+    state = torch.empty(slots_n, H, D, D, device="cuda", dtype=sdt)
+    state[:10], state[-10:] = few[:10], few[10:]
+    slots = torch.tensor([slots_n - 1, slots_n - 7], dtype=torch.int32)
+    plan = api.make_gdr_state_plan(2, sum(lens), H, D, D, num_slots=slots_n, qk_heads=1, max_len=max(lens), dtype=dtype, state_dtype=sdt)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    o = api.gdr_prefill(plan, q, k, v, g, beta, state, cu, slots=slots.cuda())
+    after, at = torch.cat([state[:10], state[-10:]]), torch.tensor([19, 13])
+    if max(lens) >= 48:
+        chunked_check(lens, q, k, v, g, beta, few, after, o, at)
+        after[at] = few[at]
+        assert torch.equal(after, few)
+    else:
+        tol = (max(lens) + D) * U
+        gds_check(lens, q, k, v, g, beta, few, after, o, at, None, D ** -0.5, tol, tol)
+
+
+@pytest.mark.parametrize("n,dtype,sdt", [(3, F32, F32), (3, BF16, BF16), (9, BF16, F32), (60, BF16, F32)], ids=str)
+def test_gdr_tokens_beyond_32_bits(n, dtype, sdt):
+    """Tokens that lie more than 2^31 elements apart."""
+    H, D, step = 2, 64, (2 ** 31 // (n - 1) + 4096) // 8 * 8
+    big = torch.empty((n - 1) * step + 8 * D, device="cuda", dtype=dtype)
+    dense = gds_inputs([n], H, H, D, D, dtype, sdt, 1)
+    q, k, v = (big.as_strided((n, H, D), (step, D, 1), 2 * i * D) for i in range(3))
+    for to, x in zip((q, k, v), dense[:3]):
+        to.copy_(x)
+    g, beta, state = dense[3:6]
+    plan = api.make_gdr_state_plan(1, n, H, D, D, dtype=dtype, state_dtype=sdt)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    one, two = state.clone(), state.clone()
+    want = api.gdr_prefill(plan, *dense[:5], one, cu)
+    assert torch.equal(api.gdr_prefill(plan, q, k, v, g, beta, two, cu), want) and torch.equal(one, two)
+
+
+def test_gdr_outputs_beyond_32_bits():
+    """65535 sequences of 132 heads of 256 values: only the last two have a state."""
+    S, H, Dk, Dv = 65535, 132, 16, 256
+    v = torch.empty(S, 1, H, Dv, device="cuda", dtype=BF16)
+    assert v.numel() > 2 ** 31
+    q, k, last, g, beta, state, _ = gds_inputs([1] * 2, H, 1, Dk, Dv, BF16, F32, 2)
+    v[-2:, 0] = last
+    slots = torch.full((S,), -1, dtype=torch.int32, device="cuda")
+    slots[-2:] = torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+
+    def spread(x):
+        y = torch.zeros(S, 1, *x.shape[1:], device="cuda", dtype=x.dtype)
+        y[-2:, 0] = x
+        return y
+
+    plan = api.make_gdr_state_plan(S, S, H, Dk, Dv, num_slots=2, qk_heads=1, max_len=1)
+    before = state.clone()
+    o = api.gdr_decode(plan, spread(q), spread(k), v, spread(g), spread(beta), state, slots=slots)
+    tol = (1 + Dk) * U
+    gds_check([1, 1], q, k, last, g, beta, before, state, o[-2:, 0], [1, 0], None, Dk ** -0.5, tol, tol)
+    assert not o[:-2].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_qkr_strides_beyond_32_bits(dtype):
+    step = 2 ** 30 + 64
+    big = torch.empty(2 * step + 512, device="cuda", dtype=dtype)
+    q, k, how, pos = qkr_case(1, 3, 4, 2, 64, 32, dtype)
+    far_q, far_k = big.as_strided(q.shape, (0, step, 64, 1)), big.as_strided(k.shape, (0, step, 64, 1), 256)
+    far_q.copy_(q)
+    far_k.copy_(k)
+    dy = rnd(*q.shape, seed=7, dtype=dtype), rnd(*k.shape, seed=8, dtype=dtype)
+    for a, b in zip(api.qk_norm_rope(far_q, far_k, **how), api.qk_norm_rope(q, k, **how)):
+        assert torch.equal(a, b)
+    for a, b in zip(api.qk_norm_rope_backward(far_q, far_k, *dy, **how), api.qk_norm_rope_backward(q, k, *dy, **how)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("R", [64, 20])
+def test_qkr_rows_beyond_32_bits(R):
+    """More than 2^31 elements of queries, through both forms for long inputs: the last tokens are as they are alone."""
+    T, Hq, Hk, D = 2 ** 31 // (32 * 64) + 13, 32, 8, 64
+    q = torch.randn(1, T, Hq, D, device="cuda", dtype=BF16, generator=torch.Generator("cuda").manual_seed(1))
+    k = rnd(1, T, Hk, D, dtype=BF16)
+    pos = torch.randint(0, 99, (1, T), device="cuda", dtype=torch.int32)
+    table = api.make_rope_table(99, R)
+    y, z = api.qk_norm_rope(q, k, table, pos)
+    dq, dk, _, _ = api.qk_norm_rope_backward(q, k, y, z, table, pos)
+    for at in (slice(0, 9), slice(T - 9, T)):
+        cut = [x[:, at].contiguous() for x in (q, k, y, z, pos)]
+        a, b = api.qk_norm_rope(cut[0], cut[1], table, cut[4])
+        assert torch.equal(a, cut[2]) and torch.equal(b, cut[3])
+        a, b, _, _ = api.qk_norm_rope_backward(*cut[:4], table, cut[4])
+        close(dq[:, at], a, 64 * U, BF16, "dq")
+        close(dk[:, at], b, 64 * U, BF16, "dk")
+
+
+def test_clip_of_a_tensor_beyond_32_bits():
+    n = 2 ** 31 + 1001
+    g = torch.full((n,), 2.0 ** -10, device="cuda", dtype=BF16)
+    g[-1000:] = 2.0 ** -3
+    want = ((n - 1000) * 2.0 ** -20 + 1000 * 2.0 ** -6) ** 0.5
+    norm = float(api.clip_grad_norm(api.make_clip_plan(1), [g], want / 2))
+    assert abs(norm - want) <= 40 * U * want
+    # the factor is a half but for eps: half of a power of two, rounded to bf16
+    assert bool((g[-1000:] == 2.0 ** -4).all()) and bool((g[:-1000] == 2.0 ** -11).all())
