@@ -599,7 +599,9 @@ rm_status rm_cp_qkr_backward(const rm_cp_qkr_problem* p, const void* q, const vo
  * rejects.  recurrent != 0 keeps every call a token recurrence.  In chunks, the state
  * and two factors that meet it are rounded to bf16 where they enter a product
  * (the state itself is kept in fp32): outputs are off by up to one and a half
- * times their own rounding in norm, the final state by some 1e-4.  A NaN or an
+ * times their own rounding in norm, the final state by some 1e-4; by up to
+ * 2e-3 a chunk of what is left of a state far larger than what the chunk's
+ * values write (one short prompt on such a state).  A NaN or an
  * infinity in a token then reaches the outputs of all 64 tokens of its chunk
  * (in the recurrence: its own and those after it), never another sequence.
  */

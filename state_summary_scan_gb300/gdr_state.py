@@ -39,7 +39,8 @@ def make_gdr_state_plan(max_seqs: int, max_tokens: int, H: int, Dk: int, Dv: int
     sequence (default max_tokens).  qk_heads > 0: q and k have that many heads, each shared by
     H / qk_heads consecutive heads.  bf16 calls of 48 tokens a sequence or more (Dk 64 or 128) run in
     chunks on the tensor cores, which rounds some factors to bf16: outputs are off by up to one and a
-    half times their own rounding, the state by some 1e-4.  recurrent=True keeps every call a token
+    half times their own rounding, the state by some 1e-4 (2e-3 where a short prompt meets a state
+    far larger than its values).  recurrent=True keeps every call a token
     recurrence at fp32's precision, whatever the lengths of its batch, and slower for prompts."""
     if dtype not in _DTYPES or state_dtype not in _DTYPES:
         raise ValueError("dtype and state_dtype must be fp32 or bf16")
