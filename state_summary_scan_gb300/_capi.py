@@ -438,7 +438,8 @@ def on_stream(make, stream, device: int):
         return make()
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+        # (handles 0 and 1 are the legacy default stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return make()
 

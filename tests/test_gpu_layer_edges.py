@@ -63,6 +63,18 @@ def test_calls_on_another_stream_keep_their_buffers_to_themselves(given):
             assert torch.equal(x, y), i
 
 
+@pytest.mark.parametrize("handle", [0, 1])
+def test_calls_take_the_default_streams_handles(handle):
+    q, k, how, _ = qkr_case(1, 30, 4, 2, 128, 64, F32)
+    want = api.qk_norm_rope(q, k, **how)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = api.qk_norm_rope(q, k, **how, stream=handle)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def qkr_check(q, k, how, pos, tol=32 * U, seed=9):
     """Forward and backward against 64 bits, with the tolerances of test_qkr_against_64_bits."""
     dtype, t64 = q.dtype, None if how["table"] is None else how["table"].double()
