@@ -629,10 +629,9 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * n tensors, numels[i] elements each (0 allowed), dtypes[i] RM_F32 or RM_BF16
  * for grads[i] and out_dtypes[i] for outs[i]; grads, outs, numels, dtypes and
  * out_dtypes are HOST arrays, the pointers in them device pointers aligned to
- * their elements.  outs[i] may be grads[i] (in place); otherwise no output
- * overlaps a gradient or another output (so a gradient that is clipped in
- * place is listed once).  outs NULL: the norm
- * alone.  norm: one fp32 on the device.  The squares are summed in fp32 within
+ * their elements.  outs[i] may be grads[i] (in place); an output that overlaps
+ * another output or any other gradient is refused (so a gradient that is
+ * clipped in place is listed once).  outs NULL: the norm alone.  norm: one fp32 on the device.  The squares are summed in fp32 within
  * a thread's few elements of a piece, in fp64 beyond, in an order that depends
  * on the sizes alone; pieces whose squares would leave fp32's range are summed
  * in fp64.  An infinite norm gives the factor 0 and a NaN norm a NaN factor,

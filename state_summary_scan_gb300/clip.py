@@ -51,7 +51,7 @@ def clip_grad_norm(plan: ClipPlan, grads: Sequence[torch.Tensor], max_norm: Opti
     """The 2-norm over every element of grads (a fp32 scalar on the device, no host read).  With
     max_norm each gradient is multiplied by min(1, max_norm / (norm + eps)), in place or, with
     out, into the tensors of out (same sizes, fp32 or bf16 each; gradients can be cast on the
-    way); tensors that are written overlap no others.  grads: contiguous fp32 and bf16 tensors of any sizes and alignments, mixed."""
+    way); a tensor that is written may not overlap any other.  grads: contiguous fp32 and bf16 tensors of any sizes and alignments, mixed."""
     grads = grads if isinstance(grads, (list, tuple)) else list(grads)
     if not grads:
         raise ValueError("no gradients")

@@ -14,7 +14,10 @@
 // the second read makes the floor 938 us.  Pieces of 16384 elements on four blocks a multiprocessor took
 // 1.23 ms.  75 small tensors of 2 million elements: 25 us on the device, 11 of them the norm (with pieces of this
 // size they are on some 120 of the 912 blocks), and the host's path of 75 us, most of it collecting addresses.
+#include <algorithm>
 #include <cstdio>
+#include <new>
+#include <vector>
 
 #include "tc_tiles.cuh"
 
@@ -241,6 +244,32 @@ struct Call {
     const int32_t* out_dtypes;
 };
 
+// Whether an output lies over another output or over a gradient that is not its own: blocks read and write them in
+// no order.  (Memory in ascending order, as the parts of one buffer are, is not sorted.)
+bool overlapping(const Call& c) {
+    struct Range {
+        uintptr_t begin, end;
+        bool out;
+    };
+    std::vector<Range> r;
+    r.reserve(2 * size_t(c.n));
+    for (int i = 0; i < c.n; ++i) {
+        if (c.numels[i] == 0) continue;
+        const uintptr_t g = reinterpret_cast<uintptr_t>(c.grads[i]), o = reinterpret_cast<uintptr_t>(c.outs[i]);
+        if (g != o) r.push_back({g, g + uintptr_t(c.numels[i]) * (c.dtypes[i] == RM_F32 ? 4 : 2), false});
+        r.push_back({o, o + uintptr_t(c.numels[i]) * (c.out_dtypes[i] == RM_F32 ? 4 : 2), true});
+    }
+    auto before = [](const Range& x, const Range& y) { return x.begin < y.begin; };
+    if (!std::is_sorted(r.begin(), r.end(), before)) std::sort(r.begin(), r.end(), before);
+    uintptr_t any = 0, out = 0;  // ends of what was passed
+    for (const Range& x : r) {
+        if (x.begin < (x.out ? any : out)) return true;
+        any = std::max(any, x.end);
+        if (x.out) out = std::max(out, x.end);
+    }
+    return false;
+}
+
 // Tensors [t0, t0 + N) of the call.
 template <int N>
 void fill(const Call& c, int t0, Batch<N>* b) {
@@ -319,8 +348,13 @@ rm_status rm_cp_clip_grad_norm(int32_t n, const void* const* grads, const int64_
             if (reinterpret_cast<uintptr_t>(p) % (dt == RM_F32 ? 4 : 2)) return api_fail(RM_ERR_ALIGNMENT, "a tensor is not aligned to its elements");
         }
     }
-    rmcp::begin_launches();
     const rmcp::clip::Call c{n, grads, numels, dtypes, outs, out_dtypes};
+    try {
+        if (outs != nullptr && rmcp::clip::overlapping(c)) return api_fail(RM_ERR_INVALID_ARG, "an output overlaps another output or another gradient");
+    } catch (const std::bad_alloc&) {
+        return api_fail(RM_ERR_INVALID_ARG, "out of host memory");
+    }
+    rmcp::begin_launches();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool ok = n <= rmcp::clip::kFew ? rmcp::clip::run<rmcp::clip::kFew>(c, max_norm, eps, norm, static_cast<double*>(ws), s)
                                           : rmcp::clip::run<rmcp::clip::kMany>(c, max_norm, eps, norm, static_cast<double*>(ws), s);
