@@ -624,6 +624,78 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
                                void* state, void* o, void* ws, rm_stream_t stream);
 
 /*
+ * Linear attention with a decay for each head and a carried state, for
+ * serving (the recurrence of rm_cp_forward_* without segments): per sequence
+ * and head, from S = the sequence's slot (zero where fresh[seq] != 0), for
+ * each of its tokens:
+ *     S <- exp(g_t) S + k_t v_t^T,   o_t = scale S^T q_t.
+ * The problem is an rm_gdr_state_problem (beta_stride is not used), and
+ * tokens, sequences, slots, fresh, state, strides, sizes and outputs are as
+ * in rm_gdr_state_forward; g_stride 0: g is [H], one log-decay for each head
+ * whatever the token.
+ *   ws: rm_gla_state_workspace_size bytes, for problems of these sizes or
+ *   smaller num_seqs, num_tokens and max_len; not shared by calls that overlap.
+ * rm_gla_state_path: 0 when the call runs as a token recurrence in fp32,
+ * -1 for a problem it rejects.
+ */
+int32_t rm_gla_state_path(const rm_gdr_state_problem* p);
+size_t rm_gla_state_workspace_size(const rm_gdr_state_problem* p);
+rm_status rm_gla_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k,
+                               const void* v, const float* g, const int32_t* cu_seqlens,
+                               const int32_t* slots, const uint8_t* fresh, void* state, void* o,
+                               void* ws, rm_stream_t stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it, a
+ * gate, and an output in 8 bits.  Rows x [N,H,n] in dtype (H = 1: plain rows),
+ * residual [N,H,n] in res_dtype, gate [N,H,n] in dtype, weight [n] fp32; any
+ * of the three may be NULL (gate: where the problem's gate is 0):
+ *     h = x + residual, rounded to res_dtype and written (else h is x)
+ *     u = h, or h silu(gate) with gate 2
+ *     y = u r w, times silu(gate) with gate 1,   r = (sum u^2 / n + eps)^(-1/2)
+ * silu(z) = z / (1 + e^-z).  Arithmetic and sums are fp32, y is rounded once.
+ * rm_cp_rms_quant gives y in 8 bits: for each `group` adjacent elements (32,
+ * 64 or 128, dividing n; 0: the row) scale = max |y| / 448, at least 2^-126,
+ * and y8 = e4m3(y / scale), to nearest even; scales [N,H,n/group].  A NaN
+ * in a row makes all of its scales NaN.
+ *   x, residual and gate have strides in elements for (token, head), elements
+ *   of a row adjacent, every stride and base a multiple of 16 bytes; h, y,
+ *   y8, scales and all gradients are contiguous.  n is a multiple of 8 up to
+ *   32768 (RM_ERR_UNSUPPORTED otherwise).  res_dtype is dtype or RM_F32; a
+ *   residual and a gate exclude one another.  h may be the (contiguous)
+ *   residual itself and y the (contiguous) x; any other overlap of an output
+ *   is refused.
+ * rm_cp_rms_backward: with h as the forward gave it (res_dtype, r_stride; x
+ *   where there was no residual, then res_dtype = dtype), dy in dtype and dh
+ *   in res_dtype (NULL: 0), the gradients of sum(dy y) + sum(dh h): dx in
+ *   dtype, dresidual (the same values in res_dtype; only where it is not
+ *   dtype), dgate in dtype (with a gate), dweight [n] fp32 (or NULL; a sum
+ *   over rows in an order that depends on the sizes alone).  x_stride and
+ *   group are not used.  ws: rm_cp_rms_workspace_size bytes (for dweight only).
+ */
+typedef struct {
+    int32_t N, H, n;
+    float eps;
+    rm_dtype dtype, res_dtype;
+    int32_t gate;
+    int32_t group;
+    int64_t x_stride[2];
+    int64_t r_stride[2];
+    int64_t z_stride[2];
+} rm_cp_rms_problem;
+size_t rm_cp_rms_workspace_size(const rm_cp_rms_problem* p);
+rm_status rm_cp_rms_forward(const rm_cp_rms_problem* p, const void* x, const void* residual,
+                            const void* gate, const float* weight, void* h, void* y,
+                            rm_stream_t stream);
+rm_status rm_cp_rms_quant(const rm_cp_rms_problem* p, const void* x, const void* residual,
+                          const void* gate, const float* weight, void* h, void* y8, float* scales,
+                          rm_stream_t stream);
+rm_status rm_cp_rms_backward(const rm_cp_rms_problem* p, const void* h, const void* gate,
+                             const float* weight, const void* dy, const void* dh, void* dx,
+                             void* dresidual, void* dgate, float* dweight, void* ws,
+                             rm_stream_t stream);
+
+/*
  * Global norm of many gradient tensors, and clipping:
  *     norm = sqrt(sum_i sum g_i^2),   out_i = g_i * min(1, max_norm / (norm + eps)).
  * n tensors, numels[i] elements each (0 allowed), dtypes[i] RM_F32 or RM_BF16

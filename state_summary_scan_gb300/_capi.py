@@ -36,6 +36,8 @@ EXPORTS = (
     "rm_cp_qkr_workspace_size", "rm_cp_qkr_forward", "rm_cp_qkr_backward",
     "rm_gdr_state_path", "rm_gdr_state_workspace_size", "rm_gdr_state_forward",
     "rm_cp_clip_workspace_size", "rm_cp_clip_grad_norm",
+    "rm_gla_state_path", "rm_gla_state_workspace_size", "rm_gla_state_forward",
+    "rm_cp_rms_workspace_size", "rm_cp_rms_forward", "rm_cp_rms_quant", "rm_cp_rms_backward",
 )
 
 
@@ -91,6 +93,13 @@ class GdrStateProblem(ctypes.Structure):
         ("g_stride", ctypes.c_int64), ("beta_stride", ctypes.c_int64), ("recurrent", ctypes.c_int32)]
 
 
+class RmsProblem(ctypes.Structure):
+    """Mirror of rm_cp_rms_problem."""
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("n", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("res_dtype", ctypes.c_int), ("gate", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 2), ("r_stride", ctypes.c_int64 * 2), ("z_stride", ctypes.c_int64 * 2)]
+
+
 _P = ctypes.c_void_p
 _PP = ctypes.POINTER(Problem)
 _S = ctypes.c_int
@@ -136,6 +145,13 @@ _SIGS = {
     "rm_gdr_state_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GdrStateProblem)]),
     "rm_gdr_state_forward": (_S, [ctypes.POINTER(GdrStateProblem)] + [_P] * 12),
     "rm_cp_clip_workspace_size": (ctypes.c_size_t, [ctypes.c_int32]),
+    "rm_gla_state_path": (ctypes.c_int32, [ctypes.POINTER(GdrStateProblem)]),
+    "rm_gla_state_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GdrStateProblem)]),
+    "rm_gla_state_forward": (_S, [ctypes.POINTER(GdrStateProblem)] + [_P] * 11),
+    "rm_cp_rms_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(RmsProblem)]),
+    "rm_cp_rms_forward": (_S, [ctypes.POINTER(RmsProblem)] + [_P] * 7),
+    "rm_cp_rms_quant": (_S, [ctypes.POINTER(RmsProblem)] + [_P] * 8),
+    "rm_cp_rms_backward": (_S, [ctypes.POINTER(RmsProblem)] + [_P] * 11),
     "rm_cp_clip_grad_norm": (_S, [ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P]),
 }
 
@@ -161,7 +177,8 @@ def load(build_if_needed: bool = True):
                 fn = getattr(so, name)
                 fn.restype = res
                 fn.argtypes = args
-            for name in ("rm_cp_qkr_forward", "rm_cp_qkr_backward", "rm_gdr_state_forward"):
+            for name in ("rm_cp_qkr_forward", "rm_cp_qkr_backward", "rm_gdr_state_forward", "rm_gla_state_forward",
+                         "rm_cp_rms_forward", "rm_cp_rms_quant", "rm_cp_rms_backward"):
                 fn = so[name]  # a function object of its own, taking the problem's address
                 fn.restype, fn.argtypes = _S, [_P] * len(_SIGS[name][1])
                 _by_address[name] = fn
@@ -400,9 +417,9 @@ def rm_gdr_backward_apply(p, q, k, v, g, beta, dO, dS_out, dk, dv, dg, dbeta, ws
                                         _ptr(dbeta), _ptr(ws), _stream(stream)))
 
 
-# ----------------------------------------------------------------- norm and rotation, carried state, clipping
+# ----------------------------------------------------------------- norms and rotation, carried states, clipping
 # These calls take strides in their problem, so tensors need only have adjacent head elements;
-# the callers in qk_rope.py, gdr_state.py and clip.py check shapes, types and strides.  Pointers are
+# the callers in qk_rope.py, gdr_state.py, gla_state.py, rms_norm.py and clip.py check shapes, types and strides.  Pointers are
 # passed as addresses and problems as the address of their struct: a decoding step is a few
 # microseconds long, and so must its call be.
 
@@ -494,6 +511,58 @@ def rm_gdr_state_forward(p: int, q, k, v, g, beta, cu_seqlens, slots, fresh, sta
     fn = _on_device(_by_address["rm_gdr_state_forward"], q.get_device())
     status = fn(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(cu_seqlens), _addr(slots),
                 _addr(fresh), state.data_ptr(), o.data_ptr(), ws.data_ptr(), stream)
+    if status:
+        _check(status)
+
+
+def rm_gla_state_path(p: GdrStateProblem) -> int:
+    return int(load().rm_gla_state_path(ctypes.byref(p)))
+
+
+def rm_gla_state_workspace_size(p: GdrStateProblem) -> int:
+    return int(load().rm_gla_state_workspace_size(ctypes.byref(p)))
+
+
+def rm_gla_state_forward(p: int, q, k, v, g, cu_seqlens, slots, fresh, state, o, ws, stream):
+    """p: the address of a GdrStateProblem."""
+    if _lib is None:
+        load()
+    fn = _on_device(_by_address["rm_gla_state_forward"], q.get_device())
+    status = fn(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(cu_seqlens), _addr(slots), _addr(fresh),
+                state.data_ptr(), o.data_ptr(), ws.data_ptr(), stream)
+    if status:
+        _check(status)
+
+
+def rm_cp_rms_workspace_size(p: RmsProblem) -> int:
+    return int(load().rm_cp_rms_workspace_size(ctypes.byref(p)))
+
+
+def rm_cp_rms_forward(p: int, x, residual, gate, weight, h, y, stream):
+    """p: the address of an RmsProblem."""
+    if _lib is None:
+        load()
+    fn = _on_device(_by_address["rm_cp_rms_forward"], x.get_device())
+    status = fn(p, x.data_ptr(), _addr(residual), _addr(gate), _addr(weight), _addr(h), y.data_ptr(), stream)
+    if status:
+        _check(status)
+
+
+def rm_cp_rms_quant(p: int, x, residual, gate, weight, h, y8, scales, stream):
+    if _lib is None:
+        load()
+    fn = _on_device(_by_address["rm_cp_rms_quant"], x.get_device())
+    status = fn(p, x.data_ptr(), _addr(residual), _addr(gate), _addr(weight), _addr(h), y8.data_ptr(), scales.data_ptr(), stream)
+    if status:
+        _check(status)
+
+
+def rm_cp_rms_backward(p: int, h, gate, weight, dy, dh, dx, dresidual, dgate, dweight, ws, stream):
+    if _lib is None:
+        load()
+    fn = _on_device(_by_address["rm_cp_rms_backward"], h.get_device())
+    status = fn(p, h.data_ptr(), _addr(gate), _addr(weight), dy.data_ptr(), _addr(dh), dx.data_ptr(), _addr(dresidual), _addr(dgate),
+                _addr(dweight), _addr(ws), stream)
     if status:
         _check(status)
 

@@ -445,10 +445,13 @@ class GdrStepGraph:
 
 
 # ------------------------------------------------------------------ around the recurrences
-# per-head norm with rotation, the delta rule with a carried state, gradient clipping
+# per-head norm with rotation, the recurrences with a carried state, norms of rows, gradient clipping
 
 from .clip import ClipPlan, clip_grad_norm, make_clip_plan  # noqa: E402,F401
 from .gdr_state import (GdrStatePlan, gdr_decode, gdr_prefill, make_gdr_state,  # noqa: E402,F401
                         make_gdr_state_plan)
+from .gla_state import (GlaStatePlan, gla_decode, gla_prefill, make_gla_state,  # noqa: E402,F401
+                        make_gla_state_plan)
 from .qk_rope import (QkNormRope, make_rope_table, qk_norm_rope, qk_norm_rope_backward,  # noqa: E402,F401
                       qk_norm_rope_train)
+from .rms_norm import RmsNorm, rms_norm, rms_norm_backward, rms_norm_quant, rms_norm_train  # noqa: E402,F401

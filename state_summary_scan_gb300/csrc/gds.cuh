@@ -86,6 +86,9 @@ __device__ __forceinline__ void zero_others(const Args& a, int i, const Seq& s, 
 //     8 sequences, 32 heads, 128 x 128     28 / 33     33 / 33     39 / 34     50 / 32
 //     one sequence, 16 heads, 128 x 128    10 / 17     12 / 17     14 / 17     17 / 16
 constexpr int kChunkedLen = 48;
+// Host checks of a problem, and of a pointer's alignment to its elements (gds_kernels.cu).
+rm_status check(const rm_gdr_state_problem* p, Args* a);
+rm_status element_aligned(const void* p, const char* name, int size);
 bool tc_supports(const Args& a, rm_dtype dt);
 size_t tc_workspace_bytes(const Args& a);
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s);

@@ -678,6 +678,8 @@ bool recurrence(const Args& a, bool f32, cudaStream_t s) {
     return tile_launch<TS, 1, false>(a, s);
 }
 
+}  // namespace
+
 rm_status check(const rm_gdr_state_problem* p, Args* a) {
     if (p == nullptr) return api_fail(RM_ERR_INVALID_ARG, "problem is null");
     if (p->num_seqs <= 0 || p->num_tokens < 0 || p->max_len < 0 || p->H <= 0 || p->qk_heads <= 0 || p->num_slots <= 0)
@@ -720,7 +722,6 @@ rm_status element_aligned(const void* p, const char* name, int size) {
     return RM_OK;
 }
 
-}  // namespace
 }  // namespace gds
 }  // namespace rmcp
 

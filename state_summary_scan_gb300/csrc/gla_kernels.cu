@@ -1,0 +1,304 @@
+// gla_kernels.cu -- linear attention with a decay for each head and a carried state as a token
+// recurrence (rm_gla_state_forward): decoding a few tokens for each of many sequences, and every
+// shape that the chunked form on the tensor cores does not take.
+//
+// Per token, S in R^{Dk x Dv}:
+//     S <- e^g S + k v^T,   o = scale S^T q
+// The columns of S are independent.  Bound by HBM when decoding: the state's read and write are
+// nearly all of the traffic, and each is done once.
+//
+// A CTA owns 32 columns of one sequence's head and keeps them in registers over its tokens: a thread has
+// 4 columns of Dk / 16 rows (two of 16), which it loads in pieces of 16 bytes (fp32).  It reads its own rows of q and k and its
+// own columns of v straight from memory, the next tokens' before it takes these.  Arithmetic is fp32, on
+// pairs of rows.  Tokens go NT at a time, whose outputs are summed across the threads at once.
+#include <cstdio>
+
+#include "gla.cuh"
+
+namespace rmcp {
+namespace gla {
+
+namespace {
+
+constexpr int kCols = 32;  // columns of a CTA
+constexpr unsigned kAllLanes = 0xffffffffu;
+
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+
+// N adjacent elements as they lie in memory; N * sizeof(T) is a multiple of 4.
+template <typename T, int N>
+struct Raw {
+    static constexpr int W = N * int(sizeof(T)) / 4;
+    uint32_t x[W];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (W == 1) {
+            x[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        } else if constexpr (W == 2) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            x[0] = u.x, x[1] = u.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+                x[i] = u.x, x[i + 1] = u.y, x[i + 2] = u.z, x[i + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ uint64_t two(int i) const {  // elements 2i and 2i + 1
+        if constexpr (sizeof(T) == 2) return widen2(x[i]);
+        else return pair(x[2 * i], x[2 * i + 1]);
+    }
+};
+
+__device__ __forceinline__ void load4(const float* p, float* x) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* x) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    x[0] = __uint_as_float(u.x << 16), x[1] = __uint_as_float(u.x & 0xffff0000u);
+    x[2] = __uint_as_float(u.y << 16), x[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* x) { *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]); }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+}
+
+// N values of each lane, summed over the lanes that differ in bit `bit`, and shared between them: a lane keeps
+// the first or the second half of them, by that bit.
+template <int N>
+__device__ __forceinline__ void halve(float* x, int bit) {
+    const bool upper = threadIdx.x & bit;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float give = upper ? x[i] : x[N / 2 + i], keep = upper ? x[N / 2 + i] : x[i];
+        x[i] = keep + __shfl_xor_sync(kAllLanes, give, bit);
+    }
+}
+
+constexpr int rows_of(int DK) { return DK >= 32 ? DK / 16 : 2; }
+constexpr int threads_of(int DK) { return DK / rows_of(DK) * 8; }
+
+// A thread's part of NT tokens
+template <typename T, int KR, int NT>
+struct Tokens {
+    Raw<T, KR> q[NT], k[NT];
+    Raw<T, 4> v[NT];
+    float g[NT];
+};
+
+// A CTA: blockIdx.x = column block + blocks * head, blockIdx.y = sequence.
+template <typename T, typename TS, int DK, int NT>
+__global__ void __launch_bounds__(threads_of(DK), NT == 1 ? 8 : 4) gla_token_kernel(const __grid_constant__ Args a) {
+    constexpr int KR = rows_of(DK), TPB = threads_of(DK), WARPS = TPB / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = lane & 7;
+    const int blocks = (a.Dv + kCols - 1) / kCols;
+    const int h = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * kCols;
+    const int col = c0 + quad * 4, row = (tid >> 3) * KR;
+    const bool live = col < a.Dv;  // Dv is a multiple of 8, a thread's columns of 4
+    const int cols = min(a.Dv - c0, kCols);
+    const Seq sq = sequence(a, blockIdx.y);
+    zero_others(a, blockIdx.y, sq, static_cast<T*>(a.o) + int64_t(h) * a.Dv + c0, cols, tid, TPB);
+    if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
+    T* o = static_cast<T*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + c0;
+    const int64_t os = int64_t(a.H) * a.Dv;
+    if (sq.slot < 0) {  // padding
+        zero_outputs(o, os, sq.len, cols, tid, TPB);
+        return;
+    }
+    const int hk = h / a.hdiv;
+    const T* q = static_cast<const T*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1] + row;
+    const T* k = static_cast<const T*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1] + row;
+    const T* v = static_cast<const T*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + (live ? col : 0);
+    const float* g = a.g + sq.begin * a.gs + h;
+    Tokens<T, KR, NT> next;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t0 + t < sq.len) {
+                next.k[t].load(k + (t0 + t) * a.ks[0]);
+                next.v[t].load(v + (t0 + t) * a.vs[0]);
+                next.q[t].load(q + (t0 + t) * a.qs[0]);
+                next.g[t] = __ldg(g + (t0 + t) * a.gs);
+            }
+        }
+    };
+    if (sq.len > 0) fetch(0);
+    TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * DK + row) * a.Dv + col;
+    uint64_t S[KR / 2][4];  // pairs of rows
+#pragma unroll
+    for (int i = 0; i < KR / 2; ++i) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+        if (live && !sq.fresh) {
+            load4(st + 2 * i * a.Dv, x);
+            load4(st + (2 * i + 1) * a.Dv, y);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[i][c] = pair(x[c], y[c]);
+    }
+
+    // [warp][column quad][token of the quad's lanes][4]; two, so that a tile's sums are read while the next ones come
+    __shared__ __align__(16) float part[2][WARPS][32][NT];
+    for (int t0 = 0; t0 < sq.len; t0 += NT) {
+        const int n = min(sq.len - t0, NT), b = (t0 / NT) & 1;
+        const Tokens<T, KR, NT> now = next;
+        if (t0 + NT < sq.len) fetch(t0 + NT);
+        float x[4 * NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (t < n) {
+                const uint64_t al = both(expf(now.g[t]));
+                uint64_t acc[4] = {0, 0, 0, 0}, vv[4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t lo, hi;
+                    unpair(now.v[t].two(c), lo, hi);
+                    vv[2 * c] = pair(lo, lo), vv[2 * c + 1] = pair(hi, hi);
+                }
+#pragma unroll
+                for (int i = 0; i < KR / 2; ++i) {
+                    const uint64_t kk = now.k[t].two(i), qq = now.q[t].two(i);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        S[i][c] = fma2(kk, vv[c], mul2(al, S[i][c]));
+                        acc[c] = fma2(qq, S[i][c], acc[c]);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t lo, hi;
+                    unpair(acc[c], lo, hi);
+                    x[4 * t + c] = __uint_as_float(lo) + __uint_as_float(hi);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[4 * t + c] = 0.f;
+            }
+        }
+        // value i of a lane's 4 NT is that of token i / 4 and column i % 4; lane bits 4 and 3 choose a quarter
+        halve<4 * NT>(x, 16);
+        halve<2 * NT>(x, 8);
+        float* to = part[b][warp][lane];
+        if constexpr (NT % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < NT; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) to[i] = x[i];
+        }
+        __syncthreads();
+        for (int i = tid; i < n * kCols; i += TPB) {
+            const int t = i / kCols, c = i % kCols, at = 4 * t + c % 4;  // value `at` of the quad c / 4
+            const int from = at / NT * 8 + c / 4;                        // the lane that has it
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) y += part[b][w][from][at % NT];
+            if (c < cols) o[(t0 + t) * os + c] = from_f32<T>(a.scale * y);
+        }
+    }
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < KR / 2; ++i) {
+            float x[4], y[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t lo, hi;
+                unpair(S[i][c], lo, hi);
+                x[c] = __uint_as_float(lo), y[c] = __uint_as_float(hi);
+            }
+            store4(st + 2 * i * a.Dv, x);
+            store4(st + (2 * i + 1) * a.Dv, y);
+        }
+    }
+}
+
+template <typename T, typename TS, int NT>
+bool token_launch(const Args& a, cudaStream_t s) {
+    const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
+    auto run = [&](auto f, int DK) { f<<<grid, threads_of(DK), 0, s>>>(a); };
+    if (a.Dk == 16) run(gla_token_kernel<T, TS, 16, NT>, 16);
+    else if (a.Dk == 32) run(gla_token_kernel<T, TS, 32, NT>, 32);
+    else if (a.Dk == 64) run(gla_token_kernel<T, TS, 64, NT>, 64);
+    else run(gla_token_kernel<T, TS, 128, NT>, 128);
+    note_launch(1);
+    return launch_ok();
+}
+
+template <typename T, typename TS>
+bool recurrence(const Args& a, cudaStream_t s) {
+    return a.max_len <= 1 ? token_launch<T, TS, 1>(a, s) : token_launch<T, TS, 4>(a, s);
+}
+
+}  // namespace
+}  // namespace gla
+}  // namespace rmcp
+
+#define RM_GLA_NEED(ptr)                            \
+    do {                                            \
+        rm_status s_ = rmcp::api_need((ptr), #ptr); \
+        if (s_ != RM_OK) return s_;                 \
+    } while (0)
+#define RM_GLA_ELEM(ptr, size)                                           \
+    do {                                                                 \
+        rm_status s_ = rmcp::gds::element_aligned((ptr), #ptr, (size)); \
+        if (s_ != RM_OK) return s_;                                      \
+    } while (0)
+
+extern "C" {
+
+int32_t rm_gla_state_path(const rm_gdr_state_problem* p) {
+    rmcp::gla::Args a{};
+    if (rmcp::gds::check(p, &a) != RM_OK) return -1;
+    return rmcp::gla::tc_supports(a, p->dtype) ? 1 : 0;
+}
+
+size_t rm_gla_state_workspace_size(const rm_gdr_state_problem* p) {
+    rmcp::gla::Args a{};
+    if (rmcp::gds::check(p, &a) != RM_OK) return 0;
+    return rmcp::gla::tc_supports(a, p->dtype) ? rmcp::gla::tc_workspace_bytes(a) : 16;
+}
+
+rm_status rm_gla_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k, const void* v, const float* g,
+                               const int32_t* cu_seqlens, const int32_t* slots, const uint8_t* fresh, void* state, void* o,
+                               void* ws, rm_stream_t stream) {
+    using namespace rmcp;
+    gla::Args a{};
+    rm_status st = gds::check(p, &a);
+    if (st != RM_OK) return st;
+    if (cu_seqlens == nullptr) {
+        if (a.N % a.S) return api_fail(RM_ERR_SHAPE, "without cu_seqlens num_seqs must divide num_tokens");
+        a.each = a.N / a.S;
+        if (a.each > a.max_len) return api_fail(RM_ERR_SHAPE, "max_len is below the sequences' length");
+    } else {
+        RM_GLA_ELEM(cu_seqlens, 4);
+    }
+    if (slots == nullptr && a.S > a.slots_n) return api_fail(RM_ERR_SHAPE, "without slots num_seqs must not exceed num_slots");
+    RM_GLA_NEED(state);
+    if (a.N > 0) {
+        RM_GLA_NEED(q);
+        RM_GLA_NEED(k);
+        RM_GLA_NEED(v);
+        RM_GLA_ELEM(g, 4);
+        RM_GLA_NEED(o);
+    }
+    if (slots != nullptr) RM_GLA_ELEM(slots, 4);
+    a.q = q, a.k = k, a.v = v, a.g = g, a.beta = nullptr, a.cu = cu_seqlens, a.slots = slots, a.fresh = fresh;
+    a.state = state, a.o = o, a.ws = ws;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool sf = p->state_dtype == RM_F32;
+    if (gla::tc_supports(a, p->dtype)) {
+        RM_GLA_NEED(ws);
+        begin_launches();
+        return gla::tc_launch(a, p->state_dtype, s);
+    }
+    begin_launches();
+    bool ok;
+    if (p->dtype == RM_F32) ok = sf ? gla::recurrence<float, float>(a, s) : gla::recurrence<float, __nv_bfloat16>(a, s);
+    else ok = sf ? gla::recurrence<__nv_bfloat16, float>(a, s) : gla::recurrence<__nv_bfloat16, __nv_bfloat16>(a, s);
+    if (ok) return RM_OK;
+    char msg[256];
+    std::snprintf(msg, sizeof(msg), "linear attention with a carried state: launch failed: %s", cuda_error_text());
+    return api_fail(RM_ERR_CUDA, msg);
+}
+
+}  // extern "C"

@@ -1,0 +1,576 @@
+// rms_kernels.cu -- root-mean-square norm of rows, with the residual's addition before it, a gate, and an
+// output in 8 bits with scales (rm_cp_rms_*), forward and backward.
+//
+// Per row x in R^n, with residual q, gate z and weight w (each optional), a(z) = z / (1 + e^-z):
+//     h = x + q (rounded to the residual's type and kept),   u = h  or  h a(z)  (gate first)
+//     y = u r w  or  u r w a(z),   r = (sum u^2 / n + eps)^(-1/2)
+// In 8 bits: s = max |y| of a group of elements / 448 (at least 2^-126), y8 = e4m3(y / s).
+// Backward, with e = dy a(z) (gate after) or dy, d = e w:
+//     du = r (d - u r (r sum d u / n)),   dw = sum over rows of e u r
+//     dz = dy u r w a'(z),  or du h a'(z) (gate first);   dh = du [a(z)] + what comes down the residual stream
+//
+// Bound by HBM: a row stays in registers between its sums and its outputs, so that every input is read and
+// every output written once.  Sums and the arithmetic are fp32; an output is rounded once.
+#include <cuda_fp8.h>
+
+#include <cstdio>
+#include <type_traits>
+
+#include "internal.h"
+#include "pairs.cuh"
+#include "tc_tiles.cuh"
+
+namespace rmcp {
+namespace rms {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126: the smallest scale
+constexpr float kF8Max = 448.f;
+
+struct Args {
+    int N, H, n;
+    float eps, inv_n;
+    int group;                    // elements of a scale; 0: the row
+    int64_t xs[2], rs[2], zs[2];  // token and head strides (elements) of x, of the residual (backward: h), of the gate
+    const void* x;                // backward: dy
+    const void* res;              // backward: h
+    const void* z;
+    const float* w;
+    const void* dh;               // backward: the gradient of h from the residual stream
+    void* h;                      // backward: dresidual, where its type is not that of dx
+    void* y;                      // or y8; backward: dx
+    void* dz;
+    float* scale;
+    float* part;                  // backward: [blocks][n] partial weight gradients
+};
+
+// Eight elements
+__device__ __forceinline__ void load8(const float* p, float* x) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) { tc::unpack8(*reinterpret_cast<const uint4*>(p), x); }
+__device__ __forceinline__ void store8(float* p, const float* x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) { *reinterpret_cast<uint4*>(p) = tc::pack8(x); }
+__device__ __forceinline__ void round8(float*, const float*) {}
+__device__ __forceinline__ void round8(__nv_bfloat16*, float* x) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(__float2bfloat16_rn(x[i]));
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// Sum of x and the largest of the bits m over the TPR threads of a row.  (The bits of |y| order as the values do, with NaN above all.)
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float& x, uint32_t& m, int& turn) {
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(kAll, x, o);
+        m = max(m, __shfl_xor_sync(kAll, m, o));
+    }
+    if constexpr (TPR > 32) {
+        __shared__ float xs[2][TPR / 32];
+        __shared__ uint32_t ms[2][TPR / 32];
+        if ((threadIdx.x & 31) == 0) xs[turn][threadIdx.x >> 5] = x, ms[turn][threadIdx.x >> 5] = m;
+        __syncthreads();
+        x = 0.f, m = 0;
+#pragma unroll
+        for (int i = 0; i < TPR / 32; ++i) x += xs[turn][i], m = max(m, ms[turn][i]);
+        turn ^= 1;
+    }
+}
+template <int TPR>
+__device__ __forceinline__ void row_reduce2(float& x, float& y, int& turn) {
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(kAll, x, o);
+        y += __shfl_xor_sync(kAll, y, o);
+    }
+    if constexpr (TPR > 32) {
+        __shared__ float2 s[2][TPR / 32];
+        if ((threadIdx.x & 31) == 0) s[turn][threadIdx.x >> 5] = make_float2(x, y);
+        __syncthreads();
+        x = y = 0.f;
+#pragma unroll
+        for (int i = 0; i < TPR / 32; ++i) x += s[turn][i].x, y += s[turn][i].y;
+        turn ^= 1;
+    }
+}
+
+constexpr int threads_of(int TPR) { return TPR < 256 && TPR <= 32 ? 256 : TPR; }
+
+// A row is taken by TPR threads, VPT times eight elements each: those of unit i are 8 (lane + i TPR) ..
+// kGate: 0 none, 1 after the norm, 2 before it.  kOut: 0 y, 1 y8 and scales.
+template <typename T, typename R, bool kRes, int kGate, bool kQuant, int TPR, int VPT>
+__global__ void __launch_bounds__(threads_of(TPR)) rms_forward_kernel(const __grid_constant__ Args a) {
+    constexpr int RPB = threads_of(TPR) / TPR;
+    const int lane = threadIdx.x % TPR, rows = a.N * a.H;
+    int turn = 0;
+    for (int64_t first = int64_t(blockIdx.x) * RPB; first < rows; first += int64_t(gridDim.x) * RPB) {
+        const int64_t row = first + threadIdx.x / TPR;
+        const bool there = row < rows;
+        const int t = there ? int(row / a.H) : 0, hd = there ? int(row % a.H) : 0;
+        const T* x = static_cast<const T*>(a.x) + t * a.xs[0] + hd * a.xs[1];
+        const R* q = kRes ? static_cast<const R*>(a.res) + t * a.rs[0] + hd * a.rs[1] : nullptr;
+        const T* z = kGate ? static_cast<const T*>(a.z) + t * a.zs[0] + hd * a.zs[1] : nullptr;
+        float m[VPT][8];
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 8 * (lane + i * TPR);
+            const bool live = there && e < a.n;
+            float b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m[i][j] = b[j] = 0.f;
+            if (live) load8(x + e, m[i]);
+            if (kRes) {
+                if (live) load8(q + e, b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m[i][j] += b[j];
+                if (live) store8(static_cast<R*>(a.h) + row * a.n + e, m[i]);
+                round8(static_cast<R*>(nullptr), m[i]);
+            }
+            float act[8];
+            if (kGate) {
+                if (live) load8(z + e, b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) act[j] = b[j] * sigmoid(b[j]);
+            }
+            if (kGate == 2) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m[i][j] *= act[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq = fmaf(m[i][j], m[i][j], sq);
+            if (a.w != nullptr && live) {
+                load8(a.w + e, b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m[i][j] *= b[j];
+            }
+            if (kGate == 1) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m[i][j] *= act[j];
+            }
+        }
+        uint32_t big[VPT], most = 0;
+        if (kQuant) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                big[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) big[i] = max(big[i], __float_as_uint(m[i][j]) & 0x7fffffffu);
+                most = max(most, big[i]);
+            }
+        }
+        row_reduce<TPR>(sq, most, turn);
+        const float r = rsqrtf(fmaf(sq, a.inv_n, a.eps));
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 8 * (lane + i * TPR);
+            const bool live = there && e < a.n;
+            if (kQuant) {
+                uint32_t top = most;
+                if (a.group) {
+                    top = big[i];
+                    for (int o = a.group / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+                }
+                float s = __uint_as_float(top) * r / kF8Max;
+                s = s < kTiny ? kTiny : s;  // (a NaN stays)
+                const float f = 1.f / s;
+                uint32_t out[2];
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(m[i][j] * r * f, m[i][j + 1] * r * f), __NV_SATFINITE, __NV_E4M3);
+                    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(m[i][j + 2] * r * f, m[i][j + 3] * r * f), __NV_SATFINITE, __NV_E4M3);
+                    out[j / 4] = uint32_t(lo) | uint32_t(hi) << 16;
+                }
+                if (live) {
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + row * a.n + e) = make_uint2(out[0], out[1]);
+                    const int of = a.group ? a.group : a.n;
+                    if (e % of == 0) a.scale[row * (a.n / of) + e / of] = s;
+                }
+            } else if (live) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m[i][j] *= r;
+                store8(static_cast<T*>(a.y) + row * a.n + e, m[i]);
+            }
+        }
+    }
+}
+
+// Rows are taken in a fixed order by a fixed number of blocks, so that the weight's gradient does not depend on
+// the launch.
+template <typename T, typename R, int kGate, bool kDh, bool kTwo, int TPR, int VPT>
+__global__ void __launch_bounds__(threads_of(TPR)) rms_backward_kernel(const __grid_constant__ Args a) {
+    constexpr int TPB = threads_of(TPR), RPB = TPB / TPR;
+    const int lane = threadIdx.x % TPR, rows = a.N * a.H;
+    int turn = 0;
+    float dw[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    for (int64_t first = int64_t(blockIdx.x) * RPB; first < rows; first += int64_t(gridDim.x) * RPB) {
+        const int64_t row = first + threadIdx.x / TPR;
+        const bool there = row < rows;
+        const int t = there ? int(row / a.H) : 0, hd = there ? int(row % a.H) : 0;
+        const R* h = static_cast<const R*>(a.res) + t * a.rs[0] + hd * a.rs[1];
+        const T* z = kGate ? static_cast<const T*>(a.z) + t * a.zs[0] + hd * a.zs[1] : nullptr;
+        float u[VPT][8], d[VPT][8], zz[VPT][8];
+        float sq = 0.f, du = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 8 * (lane + i * TPR);
+            const bool live = there && e < a.n;
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[i][j] = d[i][j] = zz[i][j] = 0.f, w[j] = 1.f;
+            if (live) {
+                load8(h + e, u[i]);
+                load8(static_cast<const T*>(a.x) + row * a.n + e, d[i]);
+                if (kGate) load8(z + e, zz[i]);
+                if (a.w != nullptr) load8(a.w + e, w);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float act = kGate ? zz[i][j] * sigmoid(zz[i][j]) : 1.f;
+                const float uu = kGate == 2 ? u[i][j] * act : u[i][j];
+                const float dd = (kGate == 1 ? d[i][j] * act : d[i][j]) * w[j];
+                sq = fmaf(uu, uu, sq);
+                du = fmaf(dd, uu, du);
+            }
+        }
+        row_reduce2<TPR>(sq, du, turn);
+        const float r = rsqrtf(fmaf(sq, a.inv_n, a.eps)), c = r * du * a.inv_n;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 8 * (lane + i * TPR);
+            const bool live = there && e < a.n;
+            if (!live) continue;
+            float w[8], dh[8], dz[8], out[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = 1.f, dh[j] = 0.f;
+            if (a.w != nullptr) load8(a.w + e, w);
+            if (kDh) load8(static_cast<const R*>(a.dh) + row * a.n + e, dh);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float sg = kGate ? sigmoid(zz[i][j]) : 0.f, act = kGate ? zz[i][j] * sg : 1.f;
+                const float slope = sg * fmaf(zz[i][j], 1.f - sg, 1.f);
+                const float uh = (kGate == 2 ? u[i][j] * act : u[i][j]) * r;
+                const float ee = kGate == 1 ? d[i][j] * act : d[i][j];
+                dw[i][j] = fmaf(ee, uh, dw[i][j]);
+                float g = r * fmaf(ee, w[j], -uh * c);
+                if (kGate == 1) dz[j] = d[i][j] * uh * w[j] * slope;
+                if (kGate == 2) dz[j] = g * u[i][j] * slope, g *= act;
+                out[j] = g + dh[j];
+            }
+            if (kGate) store8(static_cast<T*>(a.dz) + row * a.n + e, dz);
+            if (kTwo) store8(static_cast<R*>(a.h) + row * a.n + e, out);
+            store8(static_cast<T*>(a.y) + row * a.n + e, out);
+        }
+    }
+    if (a.part == nullptr) return;
+    float* to = a.part + int64_t(blockIdx.x) * a.n;
+    if constexpr (RPB > 1) {  // the block's rows, group after group
+        __shared__ float sum[TPR * VPT * 8];
+        for (int g = 0; g < RPB; ++g) {
+            if (int(threadIdx.x) / TPR == g) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float& s = sum[8 * (lane + i * TPR) + j];
+                        s = g ? s + dw[i][j] : dw[i][j];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int e = threadIdx.x; e < a.n; e += TPB) to[e] = sum[e];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 8 * (lane + i * TPR);
+            if (e < a.n) store8(to + e, dw[i]);
+        }
+    }
+}
+
+// dw[e] = sum of the blocks' parts: 32 columns a block, eight threads a column
+__global__ void __launch_bounds__(256) rms_weight_kernel(const float* part, float* dw, int blocks, int n) {
+    __shared__ float s[8][32];
+    const int e = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    float x = 0.f;
+    if (e < n)
+        for (int b = g; b < blocks; b += 8) x += part[int64_t(b) * n + e];
+    s[g][threadIdx.x & 31] = x;
+    __syncthreads();
+    if (g == 0 && e < n) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) x += s[i][threadIdx.x & 31];
+        dw[e] = x;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int kMostBlocks = 152 * 4;
+
+// f(TPR, VPT) of the row length
+template <typename F>
+auto by_length(int n, F f) {
+    using std::integral_constant;
+#define RM_RMS_SHAPE(t, v) f(integral_constant<int, t>{}, integral_constant<int, v>{})
+    if (n <= 64) return RM_RMS_SHAPE(8, 1);
+    if (n <= 128) return RM_RMS_SHAPE(16, 1);
+    if (n <= 256) return RM_RMS_SHAPE(32, 1);
+    if (n <= 512) return RM_RMS_SHAPE(32, 2);
+    if (n <= 1024) return RM_RMS_SHAPE(128, 1);
+    if (n <= 2048) return RM_RMS_SHAPE(256, 1);
+    if (n <= 4096) return RM_RMS_SHAPE(256, 2);
+    if (n <= 8192) return RM_RMS_SHAPE(512, 2);
+    if (n <= 16384) return RM_RMS_SHAPE(512, 4);
+    return RM_RMS_SHAPE(1024, 4);
+#undef RM_RMS_SHAPE
+}
+
+int blocks_of(int64_t rows, int TPR, int most) {
+    const int64_t per = threads_of(TPR) / TPR, b = (rows + per - 1) / per;
+    return int(b < most ? b : most);
+}
+
+rm_status launched() {
+    note_launch(1);
+    if (launch_ok()) return RM_OK;
+    char msg[256];
+    std::snprintf(msg, sizeof(msg), "norm: launch failed: %s", cuda_error_text());
+    return api_fail(RM_ERR_CUDA, msg);
+}
+
+template <typename T, typename R, bool kRes, int kGate>
+rm_status forward(const Args& a, cudaStream_t s) {
+    const int64_t rows = int64_t(a.N) * a.H;
+    return by_length(a.n, [&](auto tpr, auto vpt) {
+        const int blocks = blocks_of(rows, tpr, 0x7fffffff);
+        if (a.scale != nullptr) rms_forward_kernel<T, R, kRes, kGate, true, tpr(), vpt()><<<blocks, threads_of(tpr), 0, s>>>(a);
+        else rms_forward_kernel<T, R, kRes, kGate, false, tpr(), vpt()><<<blocks, threads_of(tpr), 0, s>>>(a);
+        return launched();
+    });
+}
+
+template <typename T, typename R, int kGate, bool kDh, bool kTwo>
+rm_status backward(const Args& a, float* dw, cudaStream_t s) {
+    const int64_t rows = int64_t(a.N) * a.H;
+    return by_length(a.n, [&](auto tpr, auto vpt) {
+        const int blocks = blocks_of(rows, tpr, kMostBlocks);
+        rms_backward_kernel<T, R, kGate, kDh, kTwo, tpr(), vpt()><<<blocks, threads_of(tpr), 0, s>>>(a);
+        const rm_status st = launched();
+        if (st != RM_OK || dw == nullptr) return st;
+        rms_weight_kernel<<<(a.n + 31) / 32, 256, 0, s>>>(a.part, dw, blocks, a.n);
+        return launched();
+    });
+}
+
+struct Shape {
+    bool bf16, res_bf16;
+    int gate;
+};
+
+rm_status check(const rm_cp_rms_problem* p, Args* a, Shape* k) {
+    if (p == nullptr) return api_fail(RM_ERR_INVALID_ARG, "problem is null");
+    if (p->N < 0 || p->H <= 0 || p->n <= 0) return api_fail(RM_ERR_INVALID_ARG, "H and n must be positive, N not negative");
+    if ((p->dtype != RM_F32 && p->dtype != RM_BF16) || (p->res_dtype != RM_F32 && p->res_dtype != RM_BF16))
+        return api_fail(RM_ERR_INVALID_ARG, "dtype and res_dtype must be RM_F32 or RM_BF16");
+    if (p->dtype == RM_F32 && p->res_dtype != RM_F32) return api_fail(RM_ERR_UNSUPPORTED, "fp32 rows need an fp32 residual");
+    if (!(p->eps >= 0.f && p->eps < 3.0e38f)) return api_fail(RM_ERR_INVALID_ARG, "eps must be finite and not negative");
+    if (p->gate < 0 || p->gate > 2) return api_fail(RM_ERR_INVALID_ARG, "gate must be 0, 1 or 2");
+    if (p->n % 8 || p->n > 32768) return api_fail(RM_ERR_UNSUPPORTED, "n must be a multiple of 8 up to 32768");
+    if (p->group != 0 && (p->group != 32 && p->group != 64 && p->group != 128)) return api_fail(RM_ERR_UNSUPPORTED, "group must be 0, 32, 64 or 128");
+    if (p->group && p->n % p->group) return api_fail(RM_ERR_SHAPE, "group must divide n");
+    if (int64_t(p->N) * p->H > (int64_t(1) << 31) - 1) return api_fail(RM_ERR_SHAPE, "too many rows");
+    const int es = p->dtype == RM_F32 ? 4 : 2, rs = p->res_dtype == RM_F32 ? 4 : 2;
+    for (int i = 0; i < 2; ++i) {
+        if (p->x_stride[i] < 0 || p->r_stride[i] < 0 || p->z_stride[i] < 0) return api_fail(RM_ERR_INVALID_ARG, "strides must not be negative");
+        if (p->x_stride[i] * es % 16 || p->r_stride[i] * rs % 16 || p->z_stride[i] * es % 16)
+            return api_fail(RM_ERR_ALIGNMENT, "strides must be multiples of 16 bytes");
+        a->xs[i] = p->x_stride[i], a->rs[i] = p->r_stride[i], a->zs[i] = p->z_stride[i];
+    }
+    a->N = p->N, a->H = p->H, a->n = p->n, a->eps = p->eps, a->inv_n = 1.f / float(p->n);
+    a->group = p->group == p->n ? 0 : p->group;
+    *k = Shape{p->dtype == RM_BF16, p->res_dtype == RM_BF16, p->gate};
+    return RM_OK;
+}
+
+template <typename T, typename R, bool kRes>
+rm_status forward_gates(const Args& a, const Shape& k, cudaStream_t s) {
+    return k.gate == 0 ? forward<T, R, kRes, 0>(a, s) : k.gate == 1 ? forward<T, R, kRes, 1>(a, s) : forward<T, R, kRes, 2>(a, s);
+}
+rm_status forward_any(const Args& a, const Shape& k, cudaStream_t s) {
+    using B = __nv_bfloat16;
+    if (a.res == nullptr) return k.bf16 ? forward_gates<B, B, false>(a, k, s) : forward_gates<float, float, false>(a, k, s);
+    if (!k.bf16) return forward<float, float, true, 0>(a, s);
+    return k.res_bf16 ? forward<B, B, true, 0>(a, s) : forward<B, float, true, 0>(a, s);
+}
+
+template <typename T, typename R, int kGate>
+rm_status backward_dh(const Args& a, float* dw, cudaStream_t s) {
+    constexpr bool kTwo = !std::is_same<T, R>::value;
+    if (kGate) return backward<T, R, kGate, false, kTwo>(a, dw, s);
+    return a.dh ? backward<T, R, 0, true, kTwo>(a, dw, s) : backward<T, R, 0, false, kTwo>(a, dw, s);
+}
+rm_status backward_any(const Args& a, const Shape& k, float* dw, cudaStream_t s) {
+    using B = __nv_bfloat16;
+    if (k.bf16 && !k.res_bf16) return backward_dh<B, float, 0>(a, dw, s);
+    if (k.bf16) return k.gate == 0 ? backward_dh<B, B, 0>(a, dw, s) : k.gate == 1 ? backward_dh<B, B, 1>(a, dw, s) : backward_dh<B, B, 2>(a, dw, s);
+    return k.gate == 0   ? backward_dh<float, float, 0>(a, dw, s)
+           : k.gate == 1 ? backward_dh<float, float, 1>(a, dw, s)
+                         : backward_dh<float, float, 2>(a, dw, s);
+}
+
+rm_status aligned(const void* p, const char* name, int size) {
+    if (p != nullptr && reinterpret_cast<uintptr_t>(p) % size == 0) return RM_OK;
+    char msg[96];
+    std::snprintf(msg, sizeof(msg), "%s is %s", name, p ? "not aligned" : "NULL");
+    return api_fail(p ? RM_ERR_ALIGNMENT : RM_ERR_INVALID_ARG, msg);
+}
+
+// Bytes that a tensor [N,H,n] with the given strides reaches over
+int64_t reach(const rm_cp_rms_problem* p, const int64_t* st, int es) { return ((p->N - 1) * st[0] + (p->H - 1) * st[1] + p->n) * es; }
+
+struct Range {
+    const void* at;
+    int64_t bytes;
+    bool dense;  // contiguous: an output of the same size may lie exactly on it
+};
+// Whether an output meets another tensor otherwise than by being one it may replace
+bool meets(const Range& out, const Range& other, bool may_replace) {
+    if (out.at == nullptr || other.at == nullptr || out.bytes <= 0 || other.bytes <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(out.at), y = reinterpret_cast<uintptr_t>(other.at);
+    if (x + uint64_t(out.bytes) <= y || y + uint64_t(other.bytes) <= x) return false;
+    return !(may_replace && x == y && out.bytes == other.bytes && other.dense);
+}
+bool dense(const rm_cp_rms_problem* p, const int64_t* st) {
+    return (p->H == 1 || st[1] == p->n) && (p->N <= 1 || st[0] == int64_t(p->H) * p->n);
+}
+
+}  // namespace
+}  // namespace rms
+}  // namespace rmcp
+
+#define RM_RMS_NEED(ptr, size)                                        \
+    do {                                                              \
+        rm_status s_ = rmcp::rms::aligned((ptr), #ptr, (size));       \
+        if (s_ != RM_OK) return s_;                                   \
+    } while (0)
+
+extern "C" {
+
+static rm_status rms_forward(const rm_cp_rms_problem* p, const void* x, const void* residual, const void* gate, const float* weight,
+                             void* h, void* y, float* scales, bool quant, rm_stream_t stream) {
+    using namespace rmcp;
+    rms::Args a{};
+    rms::Shape k;
+    rm_status st = rms::check(p, &a, &k);
+    if (st != RM_OK) return st;
+    if (residual != nullptr && k.gate) return api_fail(RM_ERR_UNSUPPORTED, "a residual and a gate exclude one another");
+    if (p->N == 0) return RM_OK;
+    RM_RMS_NEED(x, 16);
+    if (residual != nullptr) {
+        RM_RMS_NEED(residual, 16);
+        RM_RMS_NEED(h, 16);
+    }
+    if (k.gate) RM_RMS_NEED(gate, 16);
+    if (weight != nullptr) RM_RMS_NEED(weight, 16);
+    RM_RMS_NEED(y, 16);
+    if (quant) RM_RMS_NEED(scales, 4);
+    const int es = k.bf16 ? 2 : 4, rs = k.res_bf16 ? 2 : 4;
+    const int64_t all = int64_t(p->N) * p->H * p->n;
+    const rms::Range rx{x, rms::reach(p, p->x_stride, es), rms::dense(p, p->x_stride)}, rw{weight, int64_t(p->n) * 4, false},
+        rr{residual, rms::reach(p, p->r_stride, rs), rms::dense(p, p->r_stride)}, rz{k.gate ? gate : nullptr, rms::reach(p, p->z_stride, es), rms::dense(p, p->z_stride)},
+        ry{y, all * (quant ? 1 : es), true}, rh{residual ? h : nullptr, all * rs, true},
+        rsc{quant ? scales : nullptr, int64_t(p->N) * p->H * (a.group ? p->n / a.group : 1) * 4, true};
+    const bool bad = rms::meets(ry, rx, !quant) || rms::meets(ry, rr, false) || rms::meets(ry, rz, false) || rms::meets(ry, rw, false) ||
+                     rms::meets(rh, rx, false) || rms::meets(rh, rr, true) || rms::meets(rh, rw, false) || rms::meets(rh, ry, false) ||
+                     rms::meets(rsc, rx, false) || rms::meets(rsc, rr, false) || rms::meets(rsc, rz, false) || rms::meets(rsc, rw, false) ||
+                     rms::meets(rsc, ry, false) || rms::meets(rsc, rh, false);
+    if (bad) return api_fail(RM_ERR_INVALID_ARG, "an output overlaps another tensor (only h may replace the residual, and y replace x)");
+    a.x = x, a.res = residual, a.z = gate, a.w = weight, a.h = h, a.y = y, a.scale = quant ? scales : nullptr;
+    begin_launches();
+    return rms::forward_any(a, k, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rm_status rm_cp_rms_forward(const rm_cp_rms_problem* p, const void* x, const void* residual, const void* gate, const float* weight,
+                            void* h, void* y, rm_stream_t stream) {
+    return rms_forward(p, x, residual, gate, weight, h, y, nullptr, false, stream);
+}
+
+rm_status rm_cp_rms_quant(const rm_cp_rms_problem* p, const void* x, const void* residual, const void* gate, const float* weight,
+                          void* h, void* y8, float* scales, rm_stream_t stream) {
+    return rms_forward(p, x, residual, gate, weight, h, y8, scales, true, stream);
+}
+
+size_t rm_cp_rms_workspace_size(const rm_cp_rms_problem* p) {
+    rmcp::rms::Args a{};
+    rmcp::rms::Shape k;
+    if (rmcp::rms::check(p, &a, &k) != RM_OK) return 0;
+    return size_t(rmcp::rms::kMostBlocks) * size_t(a.n) * sizeof(float);
+}
+
+rm_status rm_cp_rms_backward(const rm_cp_rms_problem* p, const void* h, const void* gate, const float* weight, const void* dy,
+                             const void* dh, void* dx, void* dresidual, void* dgate, float* dweight, void* ws, rm_stream_t stream) {
+    using namespace rmcp;
+    rms::Args a{};
+    rms::Shape k;
+    rm_status st = rms::check(p, &a, &k);
+    if (st != RM_OK) return st;
+    const bool two = k.bf16 && !k.res_bf16;
+    if ((dh != nullptr || two) && k.gate) return api_fail(RM_ERR_UNSUPPORTED, "a residual and a gate exclude one another");
+    if (dweight != nullptr && weight == nullptr) return api_fail(RM_ERR_INVALID_ARG, "the weight's gradient without the weight");
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (p->N == 0) {  // no rows: their sum is 0
+        if (dweight == nullptr) return RM_OK;
+        RM_RMS_NEED(dweight, 4);
+        begin_launches();
+        rms::rms_weight_kernel<<<(a.n + 31) / 32, 256, 0, s>>>(nullptr, dweight, 0, a.n);
+        return rms::launched();
+    }
+    RM_RMS_NEED(h, 16);
+    RM_RMS_NEED(dy, 16);
+    RM_RMS_NEED(dx, 16);
+    if (k.gate) {
+        RM_RMS_NEED(gate, 16);
+        RM_RMS_NEED(dgate, 16);
+    }
+    if (weight != nullptr) RM_RMS_NEED(weight, 16);
+    if (dh != nullptr) RM_RMS_NEED(dh, 16);
+    if (two) RM_RMS_NEED(dresidual, 16);
+    if (dweight != nullptr) {
+        RM_RMS_NEED(dweight, 4);
+        RM_RMS_NEED(ws, 16);
+    }
+    const int es = k.bf16 ? 2 : 4, rs = k.res_bf16 ? 2 : 4;
+    const int64_t all = int64_t(p->N) * p->H * p->n;
+    const rms::Range in[] = {{h, rms::reach(p, p->r_stride, rs), rms::dense(p, p->r_stride)}, {dy, all * es, true}, {dh, all * rs, true},
+                             {k.gate ? gate : nullptr, rms::reach(p, p->z_stride, es), rms::dense(p, p->z_stride)}},
+                     out[] = {{dx, all * es, true}, {two ? dresidual : nullptr, all * rs, true}, {k.gate ? dgate : nullptr, all * es, true},
+                              {dweight, int64_t(p->n) * 4, false}, {dweight ? ws : nullptr, int64_t(rms::kMostBlocks) * p->n * 4, false}},
+                     w{weight, int64_t(p->n) * 4, false};
+    bool bad = false;
+    for (int i = 0; i < 5; ++i) {
+        for (const rms::Range& x : in) bad |= rms::meets(out[i], x, i < 3);
+        for (int j = 0; j < i; ++j) bad |= rms::meets(out[i], out[j], false);
+        bad |= rms::meets(out[i], w, false);
+    }
+    if (bad) return api_fail(RM_ERR_INVALID_ARG, "an output overlaps another tensor");
+    a.x = dy, a.res = h, a.z = gate, a.w = weight, a.dh = dh, a.h = dresidual, a.y = dx, a.dz = dgate;
+    a.part = dweight ? static_cast<float*>(ws) : nullptr;
+    begin_launches();
+    return rms::backward_any(a, k, dweight, s);
+}
+
+}  // extern "C"
