@@ -14,7 +14,8 @@ using gds::sequence;
 using gds::zero_others;
 using gds::zero_outputs;
 
-// The chunked form on the tensor cores
+// The chunked form on the tensor cores, for calls whose longest sequence has this many tokens.
+constexpr int kChunkedLen = 48;
 bool tc_supports(const Args& a, rm_dtype dt);
 size_t tc_workspace_bytes(const Args& a);
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s);

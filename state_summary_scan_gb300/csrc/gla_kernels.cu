@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(threads_of(DK), NT == 1 ? 8 : 4) gla_token_ker
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             if (t < n) {
-                const uint64_t al = both(expf(now.g[t]));
+                // S + (e^g - 1) S near 1, where e^g itself has lost the bits that many tokens of a slow decay add up
+                const bool near = now.g[t] > -0.7f && now.g[t] < 0.7f;
+                const uint64_t al = both(near ? expm1f(now.g[t]) : expf(now.g[t]));
                 uint64_t acc[4] = {0, 0, 0, 0}, vv[4];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(threads_of(DK), NT == 1 ? 8 : 4) gla_token_ker
                     const uint64_t kk = now.k[t].two(i), qq = now.q[t].two(i);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        S[i][c] = fma2(kk, vv[c], mul2(al, S[i][c]));
+                        S[i][c] = fma2(kk, vv[c], near ? fma2(al, S[i][c], S[i][c]) : mul2(al, S[i][c]));
                         acc[c] = fma2(qq, S[i][c], acc[c]);
                     }
                 }
