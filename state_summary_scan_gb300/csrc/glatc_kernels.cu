@@ -9,7 +9,7 @@
 // write them, and O^T, K^T V~ leave as rows of it.  The state itself stays in registers in fp32: K^T V~ is formed
 // for each chunk by itself, so that no product waits for the state but Q S, and the state's sum is rounded to
 // nearest, with no run of accumulations.  The decays within a chunk are at most 1 wherever the gates are at most 0: they are formed
-// from differences of running sums in fixed point, within 32 tokens directly, and across them through the border.
+// from differences of running sums held in two floats, and across the 32nd token through the sums there.
 //
 // Where the sequences and heads are too few to fill the GPU, long sequences are cut into segments.  A segment's
 // map of the state is S -> e^{sum g} S + dS: a first launch walks the first segment, and the inner ones from zero
@@ -34,48 +34,63 @@ using gds::map_of;
 using gds::mma_ts;
 using gds::tmem_ld;
 using gds::tmem_st;
-using gds::wait;
 using gds::warp_arrive;
 using gds::zero_rows;
 
 namespace {
 
 constexpr float kForget = 110.f;             // e^-110 is 0 in fp32: lower gates are raised to -110
-constexpr float kFixed = 1099511627776.f;    // gates in units of 2^-40
-constexpr int kSub = 32;                     // tokens whose decays are formed pair by pair
 constexpr int kMostSegments = 16;
 constexpr int kMostStates = 320;             // of segments: see tc_workspace_bytes()
 
-// A chunk's gates in shared memory, in floats
+// A chunk's gates in shared memory, in floats.  Decays between tokens of one block of 16 are formed from their
+// distances in it, those between blocks through the blocks' ends.
+constexpr int kSub = 16;
 constexpr int kOut = 0;      // scale e^{b_t}
 constexpr int kDec = 64;     // e^{b_63 - b_t}
-constexpr int kLocal = 128;  // b_t from the start of its 32 tokens
-constexpr int kCross = 192;  // e^{b_31 - b_s} of the first 32
-constexpr int kEnd = 224;    // the state's decay: S + kEnd S (kNear), or kEnd S
-constexpr int kNear = 225;
-constexpr uint32_t kGateBytes = 1024;
-constexpr int kGateRing = 8;
-constexpr int kStages = 3;
-constexpr int kGroups = 4;                                  // groups of four warps of the state
-constexpr int kWalkThreads = (4 * kGroups + 4 + 2 + 2) * 32;  // and four output warps, two of scores, the products', the copies' and gates'
-constexpr int kOutWarp = 4 * kGroups, kScoreWarp = kOutWarp + 4, kMmaWarp = kScoreWarp + 2;
+constexpr int kLocal = 128;  // b_t from the start of its block
+constexpr int kBack = 192;   // e^{-that}
+constexpr int kCross = 256;  // e^{(b at the block's end) - b_t}
+constexpr int kEnd = 320;    // the state's decay: S + kEnd S (kNear), or kEnd S
+constexpr int kNear = 321;
+constexpr int kWeak = 322;   // every |b_t| from the start of its block is below kWeakLimit: e^{b_t - b_s} as a product
+constexpr float kWeakLimit = 60.f;
+constexpr int kBlocks = 324; // [3] e^{sum of the gates of block 1}, of blocks 1 and 2, of block 2: the decays over blocks between
+constexpr uint32_t kGateBytes = 1408;
+constexpr int kGateRing = 4;
+constexpr int kStages = 4;
+constexpr int kAhead = 2;  // chunks whose copies are under way: into stages that were left a chunk ago, so that no copy waits
+constexpr int kGroups = 2;  // groups of four warps of the state, and of V~
+// then four warps of outputs, four of scores, two of products (the first makes the copies too), two of gates
+constexpr int kValueWarp = 4 * kGroups, kOutWarp = 2 * kValueWarp, kScoreWarp = kOutWarp + 4, kMmaWarp = kScoreWarp + 4, kGateWarp = kMmaWarp + 2, kGateWarps = 2;
+constexpr int kWalkThreads = (kGateWarp + kGateWarps) * 32;
+// Registers a thread: 72 at the launch, of which some warps take others': 896 x 72 = 256 x 104 (the state) + 256 x 56 (V~) +
+// 128 x (80 (the outputs) + 48 (the scores) + 56)
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <int DK>
 struct WalkSmem {
     static constexpr int NP = DK / 64;
-    // a stage: for each 64 dimensions 64 rows of Q, then 64 of K (one operand of 128 rows); then V
+    // a stage: for each 64 dimensions 64 rows of Q, then 64 of K; then V
     static constexpr uint32_t panel = 2 * T8, V = NP * panel, stage = V + 2 * T8;
     static constexpr uint32_t P = kStages * stage, OUT = P + T8, GATES = OUT + 2 * T8;
     static constexpr size_t bytes = GATES + kGateRing * kGateBytes + 1024;
 };
 static_assert(WalkSmem<128>::bytes <= 227 * 1024, "shared memory of a CTA");
 
-// Tensor-memory columns: K^T V~ transposed, scores, Q S and P V transposed (fp32), then S^T and V~^T (bf16 pairs)
+// Tensor-memory columns: K^T V~ transposed, scores, Q S and P V transposed (fp32), then S^T and V~^T (bf16 pairs; of a
+// half of the tokens its parts)
 constexpr uint32_t TM_D = 0, TM_SC = 128, TM_O1 = 192, TM_O2 = 256, TM_S = 320, TM_V = 384;
 
 struct WalkBars {
-    uint64_t full[kStages], empty[kStages], gates[kGateRing];
-    uint64_t scores, scores_free, p_ready, ready, d_done, o_done, o_free, fixed;
+    uint64_t full[kStages], empty[kStages], gates[kGateRing], gates_free[kGateRing];
+    uint64_t v_free[kGroups];  // a group's half of V~ has been used
+    uint64_t d_ready;          // V~ is there, and K^T V~ of the chunk before has been read
+    uint64_t o1_ready;         // S is there, and the outputs of the chunk before have been read
+    uint64_t scores, p_ready, d_done, o1_done, o_done, fixed;
 };
 
 enum class Part { whole, first, rest };  // as the delta rule's walk divides the sequences (gdstc_kernels.cu)
@@ -97,6 +112,60 @@ __device__ __forceinline__ void arrived(uint32_t* r) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// A converged warp's bounded wait, in few instructions (the warps' loops together fill the instruction cache): a
+// poll suspends the warp for a microsecond at most, 2^18 of them end it; after one that ran out its others give up soon.
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, uint32_t& polls) {
+    const uint32_t b = smem_u32(bar);
+    for (uint32_t i = 0; i < polls; ++i) {
+        uint32_t ok;
+        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\nselp.u32 %0, 1, 0, p;\n}\n"
+                     : "=r"(ok) : "r"(b), "r"(parity) : "memory");
+        if (ok) {
+            __syncwarp();
+            return;
+        }
+    }
+    atomicExch(&g_timeout_flag, 1);
+    polls = 16;
+}
+
+// A sum held as two floats, to some 2^-48 of its terms
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 sum2(Sum2 x, Sum2 y) {
+    const float s = x.hi + y.hi, z = s - x.hi, e = (x.hi - (s - z)) + (y.hi - z);
+    return Sum2{s, e + (x.lo + y.lo)};
+}
+__device__ __forceinline__ float operator-(Sum2 x, Sum2 y) { return (x.hi - y.hi) + (x.lo - y.lo); }
+
+// The upper halves of a pair as bf16, and the pair less them (exactly)
+__device__ __forceinline__ uint32_t cut2(uint64_t& y) {
+    uint32_t y0, y1;
+    unpair(y, y0, y1);
+    y = sub2(y, pair(y0 & 0xffff0000u, y1 & 0xffff0000u));
+    return __byte_perm(y0, y1, 0x7632);
+}
+
+// Four 8 x 8 tiles of 16-bit elements, transposed: lane i gives the address of row i % 8 of tile i / 8, and has
+// column i / 4 of each tile, rows 2 (i % 4) and the next.
+__device__ __forceinline__ void ldmatrix_t(uint32_t at, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void stmatrix_t(uint32_t at, const uint32_t* r) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+// The same fragments in tensor memory, 16 lanes: eight words of them (two tiles above one another, twice)
+__device__ __forceinline__ void tmem_st_16x128(uint32_t at, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+// and 16 columns of fp32: pairs of columns 2 (i % 4) .. of lanes i / 4 and i / 4 + 8, for each eight columns
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t at, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+}
+
 template <int DK, typename TS, Part kPart>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     gla_walk_kernel(const __grid_constant__ Args a, const Segments seg, const __grid_constant__ CUtensorMap mq,
@@ -110,6 +179,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     uint8_t* smem = align1024(smem_raw);
     __shared__ __align__(8) WalkBars bar;
     __shared__ uint32_t tmem_slot;
+    __shared__ float sum_s[kGateWarps];
+    __shared__ int lost_s[kGateWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blocks = (a.Dv + 127) / 128;
@@ -146,33 +217,41 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&bar.full[i]), 1);
-            mbar_init(smem_u32(&bar.empty[i]), 1 + quads * kGroups);
+            mbar_init(smem_u32(&bar.empty[i]), (outs ? 2 : 1) + quads * kGroups);
         }
-        for (int i = 0; i < kGateRing; ++i) mbar_init(smem_u32(&bar.gates[i]), 1);
+        for (int i = 0; i < kGateRing; ++i) {
+            mbar_init(smem_u32(&bar.gates[i]), 1);
+            mbar_init(smem_u32(&bar.gates_free[i]), quads * (kGroups + (outs ? 1 : 0)));  // the state's and the outputs' warps are the last readers
+        }
+        for (int i = 0; i < kGroups; ++i) mbar_init(smem_u32(&bar.v_free[i]), 1);
+        mbar_init(smem_u32(&bar.d_ready), 2 * quads * kGroups);
+        mbar_init(smem_u32(&bar.o1_ready), quads * (kGroups + 1));
         mbar_init(smem_u32(&bar.scores), 1);
-        mbar_init(smem_u32(&bar.scores_free), 2);
-        mbar_init(smem_u32(&bar.p_ready), 2);
-        mbar_init(smem_u32(&bar.ready), quads * kGroups);
+        mbar_init(smem_u32(&bar.p_ready), 4);
         mbar_init(smem_u32(&bar.d_done), 1);
+        mbar_init(smem_u32(&bar.o1_done), 1);
         mbar_init(smem_u32(&bar.o_done), 1);
-        mbar_init(smem_u32(&bar.o_free), quads);
         mbar_init(smem_u32(&bar.fixed), quads * kGroups);
         mbar_fence_init();
     }
     if (warp == 0) tmem_alloc(smem_u32(&tmem_slot), 512);
+    // P: what lies above the diagonal's blocks stays zero
+    for (int i = tid; i < int(T8) / 16; i += kWalkThreads) *reinterpret_cast<uint4*>(smem + L::P + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    bool dead = false;
+    uint32_t polls = 1u << 18;
     auto gates_of = [&](int c) {  // the chunk's gates, once they are there
-        wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, dead);
+        wait(&bar.gates[c % kGateRing], (c / kGateRing) & 1, polls);
         return reinterpret_cast<const float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
     };
-    auto wait_full = [&](int c) { wait(&bar.full[c % kStages], (c / kStages) & 1, dead); };
+    auto wait_full = [&](int c) { wait(&bar.full[c % kStages], (c / kStages) & 1, polls); };
 
-    if (warp < kOutWarp) {
-        // ---- the state: a lane is a value column, a group has a quarter of its rows, and of a chunk's tokens
+    if (warp < kValueWarp) {
+        // ---- the state: a lane is a value column, a group has half of its rows
+        more_registers<112>();
         if ((warp & 3) < quads) {
             const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
             const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
@@ -203,72 +282,48 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     }
                 }
             }
-            // S <- e^{b_63} S + K^T V~ of chunk c
-            auto update = [&](int c) {
-                const float* gates = gates_of(c);
-                const uint64_t end = pair(gates[kEnd], gates[kEnd]);
-                const bool near = gates[kNear] != 0.f;
-                uint32_t d[GC];
-                tmem_ld<GC>(tl + TM_D + r0, d);
-                arrived<GC>(d);
-                if (near) {  // near 1 the decay's distance from 1 is what is known to all its bits
-#pragma unroll
-                    for (int i = 0; i < GC / 2; ++i) S[i] = add2(fma2(end, S[i], pair(d[2 * i], d[2 * i + 1])), S[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < GC / 2; ++i) S[i] = fma2(end, S[i], pair(d[2 * i], d[2 * i + 1]));
-                }
-            };
-            for (int c = 0; c < chunks; ++c) {
-                const uint8_t* stage = smem + (c % kStages) * L::stage;
-                const float* gates = gates_of(c);
-                wait_full(c);
-                const bool tail = ragged && c == chunks - 1;
-                const int n = tail ? last : kChunk;
-                if (tail) {  // keys and values past the sequence's end are other tokens': they must not meet a zero as NaN
-                    const int at = (grp * quads + (warp & 3)) * 32 + lane, threads = 32 * quads * kGroups;
-                    for (int p = 0; p < NP; ++p) zero_rows(smem + (c % kStages) * L::stage + p * L::panel + T8, 1, n, at, threads);
-                    zero_rows(smem + (c % kStages) * L::stage + L::V, 2, n, at, threads);
-                    fence_async_smem();
-                    warp_arrive(&bar.fixed, lane);
-                }
-                uint32_t v[kParts][GT / 2];
-#pragma unroll
-                for (int i = 0; i < GT / 2; ++i) {
-                    const int t = GT * grp + 2 * i;
-                    const uint32_t x = *reinterpret_cast<const uint16_t*>(stage + L::V + sw_off(64, t, row)),
-                                   y = *reinterpret_cast<const uint16_t*>(stage + L::V + sw_off(64, t + 1, row));
-                    uint64_t w = mul2(pair(x << 16, y << 16), *reinterpret_cast<const uint64_t*>(gates + kDec + t));
-                    if (tail) {
-                        uint32_t w0, w1;
-                        unpair(w, w0, w1);
-                        w = pair(t < n ? w0 : 0u, t + 1 < n ? w1 : 0u);
-                    }
-                    if (kParts == 3) split2(w, v[0][i], v[1][i], v[kParts - 1][i]);
-                    else split2(w, v[0][i], v[1][i]);
-                }
-                warp_arrive(&bar.empty[c % kStages], lane);
-                if (c > 0) {
-                    wait(&bar.d_done, (c - 1) & 1, dead);
+            warp_arrive(&bar.d_ready, lane);
+            for (int c = 0;; ++c) {
+                if (c > 0) {  // S <- e^{b_63} S + K^T V~ of the chunk before
+                    const float* gates = gates_of(c - 1);
+                    const uint64_t end = pair(gates[kEnd], gates[kEnd]);
+                    const bool near = gates[kNear] != 0.f;
+                    warp_arrive(&bar.gates_free[(c - 1) % kGateRing], lane);
+                    wait(&bar.d_done, (c - 1) & 1, polls);
                     tc_fence_after();
-                }
 #pragma unroll
-                for (int p = 0; p < kParts; ++p) tmem_st<GT / 2>(tl + TM_V + 32 * p + GT / 2 * grp, v[p]);
-                if (c > 0) update(c - 1);
-                if (outs) {
-                    uint32_t s[GC / 2];
+                    for (int i0 = 0; i0 < GC / 2; i0 += 8) {
+                        uint32_t d[16];
+                        tmem_ld<16>(tl + TM_D + r0 + 2 * i0, d);
+                        arrived<16>(d);
+                        if (i0 + 8 == GC / 2) {
+                            tc_fence_before();
+                            warp_arrive(&bar.d_ready, lane);
+                        }
+                        if (near) {  // near 1 the decay's distance from 1 is what is known to all its bits
 #pragma unroll
-                    for (int i = 0; i < GC / 2; ++i) s[i] = pack2(S[i]);
-                    tmem_st<GC / 2>(tl + TM_S + r0 / 2, s);
+                            for (int i = 0; i < 8; ++i) S[i0 + i] = add2(fma2(end, S[i0 + i], pair(d[2 * i], d[2 * i + 1])), S[i0 + i]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) S[i0 + i] = fma2(end, S[i0 + i], pair(d[2 * i], d[2 * i + 1]));
+                        }
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                warp_arrive(&bar.ready, lane);
+                if (c == chunks) break;
+                if (outs) {  // S rounded, as an operand
+                    if (c > 0) {
+                        wait(&bar.o1_done, (c - 1) & 1, polls);
+                        tc_fence_after();
+                    }
+                    uint32_t x[GC / 2];
+#pragma unroll
+                    for (int i = 0; i < GC / 2; ++i) x[i] = pack2(S[i]);
+                    tmem_st<GC / 2>(tl + TM_S + r0 / 2, x);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(&bar.o1_ready, lane);
+                }
             }
-            wait(&bar.d_done, (chunks - 1) & 1, dead);
-            tc_fence_after();
-            update(chunks - 1);
-            tc_fence_before();
             if (live && (ends || kPart == Part::first)) {
                 float* to = ends ? nullptr : seg.ends + segment_at(a, seg, si, h, j) * DK * a.Dv + v0 + row;
 #pragma unroll
@@ -284,36 +339,112 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 }
             }
         }
+    } else if (warp < kOutWarp) {
+        // ---- V~: a group has half of a chunk's tokens
+        fewer_registers<56>();
+        if ((warp & 3) < quads) {
+            const int grp = (warp - kValueWarp) >> 2;
+            const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16) + TM_V + kParts * (GT / 2) * grp;
+            // values come as fragments of 8 x 8: this lane has pairs of tokens 2 (lane % 4) .. of columns lane / 4 .. + 8 m
+            const int tok = GT * grp + 2 * (lane & 3);
+            uint32_t from[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                from[i] = smem_u32(smem) + L::V + sw_chunk(64, GT * grp + (lane >> 4) * 8 + (lane & 7), 4 * (warp & 3) + 2 * i + ((lane >> 3) & 1));
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t stage = (c % kStages) * L::stage;
+                const float* gates = gates_of(c);
+                wait_full(c);
+                if (ragged && c == chunks - 1) {  // keys and values past the sequence's end are other tokens': they must not meet a zero as NaN
+                    const int at = (grp * quads + (warp & 3)) * 32 + lane, threads = 32 * quads * kGroups;
+#pragma unroll 1
+                    for (int p = 0; p < NP; ++p) zero_rows(smem + stage + p * L::panel + T8, 1, last, at, threads);
+                    zero_rows(smem + stage + L::V, 2, last, at, threads);
+                    fence_async_smem();
+                    warp_arrive(&bar.fixed, lane);
+                    wait(&bar.fixed, 0, polls);
+                }
+                if (c > 0) wait(&bar.v_free[grp], (c - 1) & 1, polls);
+                tc_fence_after();
+#pragma unroll 1
+                for (int u = 0; u < GT / 16; ++u) {
+                    uint32_t v[2][4];
+                    uint64_t w[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        ldmatrix_t(from[i] + stage + u * 2048, v[i]);
+                        w[i] = *reinterpret_cast<const uint64_t*>(gates + kDec + tok + 16 * u + 8 * i);
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t x[kParts][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint64_t y = mul2(widen2(v[half][i]), w[i >> 1]);
+                            x[0][i] = cut2(y);
+                            if (kParts == 3) x[1][i] = cut2(y);
+                            x[kParts - 1][i] = pack2(y);
+                        }
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p) tmem_st_16x128(tl + (uint32_t(16 * half) << 16) + GT / 2 * p + 8 * u, x[p]);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bar.d_ready));
+                    mbar_arrive(smem_u32(&bar.empty[c % kStages]));
+                }
+            }
+        }
     } else if (warp < kScoreWarp) {
         // ---- the outputs: a lane is a value column; whole chunks leave as tiles, the last one by rows
-        const int w = warp & 3, row = 32 * w + lane;
+        fewer_registers<56>();
+        const int w = warp & 3;
         if (outs && w < quads) {
             const uint32_t tl = tmem + (uint32_t(32 * w) << 16);
             uint8_t* tile = smem + L::OUT;
+            const uint32_t to = smem_u32(tile);
+            uint32_t half_off[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) half_off[i] = sw_chunk(64, (lane >> 4) * 8 + (lane & 7), 4 * w + 2 * i + ((lane >> 3) & 1));
+            warp_arrive(&bar.o1_ready, lane);
             for (int c = 0; c < chunks; ++c) {
                 const float* gates = gates_of(c);
-                wait(&bar.o_done, c & 1, dead);
-                tc_fence_after();
-                uint32_t y[kChunk / 2];
-#pragma unroll
-                for (int t0 = 0; t0 < kChunk; t0 += 16) {
-                    uint32_t p[32];
-                    tmem_ld<16>(tl + TM_O1 + t0, p);
-                    tmem_ld<16>(tl + TM_O2 + t0, p + 16);
-                    arrived<32>(p);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        y[(t0 + i) / 2] = pack2(fma2(*reinterpret_cast<const uint64_t*>(gates + kOut + t0 + i), pair(p[i], p[i + 1]), pair(p[16 + i], p[17 + i])));
-                }
-                tc_fence_before();
-                warp_arrive(&bar.o_free, lane);  // the accumulators and the gates have been read
                 // the store of the chunk before has read the staging
                 if (warp == kOutWarp && lane == 0) bulk_wait_read();
                 asm volatile("bar.sync 1, %0;" ::"r"(32 * quads) : "memory");
+                wait(&bar.o_done, c & 1, polls);
+                tc_fence_after();
+#pragma unroll 1
+                for (int t0 = 0; t0 < kChunk; t0 += 16) {  // 16 tokens of 32 columns, as fragments of 8 x 8
+                    uint32_t p[2][16];
 #pragma unroll
-                for (int i = 0; i < kChunk; ++i)
-                    *reinterpret_cast<uint16_t*>(tile + (row >> 6) * T8 + sw_off(64, i, row & 63)) =
-                        uint16_t(i & 1 ? y[i / 2] >> 16 : y[i / 2] & 0xffffu);
+                    for (int half = 0; half < 2; ++half) {
+                        tmem_ld_16x256(tl + (uint32_t(16 * half) << 16) + TM_O1 + t0, p[half]);
+                        tmem_ld_16x256(tl + (uint32_t(16 * half) << 16) + TM_O2 + t0, p[half] + 8);
+                    }
+                    uint64_t f[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) f[u] = *reinterpret_cast<const uint64_t*>(gates + kOut + t0 + 8 * u + 2 * (lane & 3));
+                    arrived<16>(p[0]);
+                    arrived<16>(p[1]);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            y[u] = pack2(fma2(f[u >> 1], pair(p[half][2 * u], p[half][2 * u + 1]), pair(p[half][8 + 2 * u], p[half][9 + 2 * u])));
+                        stmatrix_t(to + half_off[half] + t0 * 128, y);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {  // the accumulators and the gates have been read
+                    mbar_arrive(smem_u32(&bar.o1_ready));
+                    mbar_arrive(smem_u32(&bar.gates_free[c % kGateRing]));
+                }
                 const bool whole = c < chunks - 1 || !ragged;
                 if (whole) fence_async_smem();
                 asm volatile("bar.sync 1, %0;" ::"r"(32 * quads) : "memory");
@@ -335,190 +466,226 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
             if (warp == kOutWarp && lane == 0) bulk_wait_read();  // shared memory is read before the CTA ends
         }
     } else if (warp < kMmaWarp) {
-        // ---- the scores: a lane is a token's row
+        // ---- the scores: a warp has a block of 16 rows, in fragments of 8 x 8: rows lane / 4 and + 8, pairs of columns
+        // 2 (lane % 4) ..
+        fewer_registers<56>();
         if (outs) {
-            const int half = warp & 3, t = 32 * half + lane;  // (kScoreWarp is a multiple of four)
-            const uint32_t tl = tmem + (uint32_t(32 * half) << 16) + TM_SC;
+            const int block = warp & 3, row = lane >> 2, col = 2 * (lane & 3);
+            const uint32_t tl = tmem + (uint32_t(32 * block) << 16) + TM_SC;
+            const uint32_t to = smem_u32(smem) + L::P + (16 * block + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
             for (int c = 0; c < chunks; ++c) {
                 const float* gates = gates_of(c);
-                wait(&bar.scores, c & 1, dead);
+                wait(&bar.scores, c & 1, polls);
                 tc_fence_after();
-                const float bt = gates[kLocal + t];
+                const float b0 = gates[kLocal + 16 * block + row], b1 = gates[kLocal + 16 * block + row + 8];
+                const float f0 = a.scale * __expf(b0), f1 = a.scale * __expf(b1);
+                const bool weak = gates[kWeak] != 0.f;
+#pragma unroll 1
+                for (int j = 0; j <= block; ++j) {
+                    uint32_t x[8], y[4];
+                    tmem_ld_16x256(tl + 16 * j, x);
+                    arrived<8>(x);
+                    if (j < block || weak) {
+                        const float m = block - j < 2 ? 1.f : gates[kBlocks + (j == 1 ? 2 : block - 2)];
+                        const float* w = gates + (j < block ? kCross : kBack) + 16 * j + col;
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint32_t y[16];
-                    if (part > half) {  // the first tokens do not see the second ones
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = 0;
+                        for (int u = 0; u < 2; ++u) {
+                            const uint64_t v = mul2(*reinterpret_cast<const uint64_t*>(w + 8 * u), pair(m, m));
+                            y[2 * u] = pack2(mul2(mul2(pair(f0, f0), pair(x[4 * u], x[4 * u + 1])), v));
+                            y[2 * u + 1] = pack2(mul2(mul2(pair(f1, f1), pair(x[4 * u + 2], x[4 * u + 3])), v));
+                        }
                     } else {
-                        uint32_t x[32];
-                        tmem_ld<32>(tl + 32 * part, x);
-                        arrived<32>(x);
-                        if (part < half) {
-                            const float f = a.scale * __expf(bt);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                y[i] = pack2(mul2(mul2(pair(f, f), pair(x[2 * i], x[2 * i + 1])), *reinterpret_cast<const uint64_t*>(gates + kCross + 2 * i)));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                float m[2];
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int s = 2 * i + u;
-                                    m[u] = s <= lane ? a.scale * __uint_as_float(x[s]) * __expf(bt - gates[kLocal + 32 * part + s]) : 0.f;
-                                }
-                                y[i] = pack2(m[0], m[1]);
-                            }
+                        for (int u = 0; u < 2; ++u) {
+                            const float2 b = *reinterpret_cast<const float2*>(gates + kLocal + 16 * j + 8 * u + col);
+                            y[2 * u] = pack2(a.scale * __uint_as_float(x[4 * u]) * __expf(b0 - b.x), a.scale * __uint_as_float(x[4 * u + 1]) * __expf(b0 - b.y));
+                            y[2 * u + 1] = pack2(a.scale * __uint_as_float(x[4 * u + 2]) * __expf(b1 - b.x), a.scale * __uint_as_float(x[4 * u + 3]) * __expf(b1 - b.y));
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(smem + L::P + sw_chunk(64, t, 4 * part + i)) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    if (j == block) {  // tokens after the row's own are not seen, whatever they hold
+                        const uint32_t own = col < row ? 0xffffffffu : col == row ? 0xffffu : 0u;
+                        y[0] &= own, y[2] = 0, y[3] &= own;
+                    }
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(to + (((2 * j + (lane >> 4)) ^ (lane & 7)) << 4)),
+                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                 : "memory");
                 }
                 tc_fence_before();
                 fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&bar.scores_free));
-                    mbar_arrive(smem_u32(&bar.p_ready));
-                }
+                warp_arrive(&bar.p_ready, lane);  // P is there, and the scores have been read
             }
         }
     } else if (warp == kMmaWarp) {
-        // ---- the products, in order: Q K^T a chunk ahead, Q S, P V, K^T V~.  The whole warp walks the loop and one
-        // elected lane issues.
+        // ---- the copies, and the products of the state, K^T V~.  The whole warp walks the loop and one elected lane issues.
+        fewer_registers<56>();
         const uint32_t base = smem_u32(smem);
-        constexpr uint32_t kSc = idesc_bf16(128, 64, 0, 0), kTS = idesc_bf16(128, 64, 0, 0), kPV = idesc_bf16(128, 64, 1, 0),
-                           kTD = idesc_bf16(128, DK, 0, 1);
-        auto scores = [&](int c) {  // rows 0 .. 63: Q K^T (64 .. 127: K K^T, not read)
-            const uint32_t at = base + (c % kStages) * L::stage;
-            const uint64_t d = sdesc(at, 16, 1024), dk = sdesc(at + T8, 16, 1024);
-            wait_full(c);
-            if (c > 0) wait(&bar.scores_free, (c - 1) & 1, dead);
-            tc_fence_after();
+        constexpr uint32_t kTD = idesc_bf16(128, DK, 0, 1);
+        auto copies = [&](int c) {
+            const int i = c % kStages, row = sq.begin + (c_first + c) * kChunk;
+            if (c >= kStages) wait(&bar.empty[i], ((c / kStages) - 1) & 1, polls);
             if (elect()) {
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const uint32_t off = (k >> 2) * L::panel + (k & 3) * 32;
-                    mma_bf16(tmem + TM_SC, desc_plus(d, off), desc_plus(dk, off), kSc, k > 0);
+                const uint32_t at = base + i * L::stage, full = smem_u32(&bar.full[i]);
+                const int vt = (nv + 63) / 64;
+                mbar_expect_tx(full, (NP * (outs ? 2 : 1) + vt) * T8);
+#pragma unroll 1
+                for (int p = 0; p < NP; ++p) {
+                    tma_load_3d(at + p * L::panel + T8, &mk, 64 * p, h / a.hdiv, row, full);
+                    if (outs) tma_load_3d(at + p * L::panel, &mq, 64 * p, h / a.hdiv, row, full);
                 }
-                mma_commit(smem_u32(&bar.scores));
+#pragma unroll 1
+                for (int p = 0; p < vt; ++p) tma_load_3d(at + L::V + p * T8, &mv, v0 + 64 * p, h, row, full);
             }
             __syncwarp();
         };
-        if (outs) scores(0);
+#pragma unroll 1
+        for (int c = 0; c < min(chunks, kAhead); ++c) copies(c);
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t at = base + (c % kStages) * L::stage;
-            const uint64_t dq = sdesc(at, 16, 1024), dk = sdesc(at + T8, L::panel, 1024), dv = sdesc(at + L::V, T8, 1024),
-                           dp = sdesc(base + L::P, 16, 1024);
-            const bool tail = ragged && c == chunks - 1;
-            wait(&bar.ready, c & 1, dead);
-            if (outs) {
-                if (c > 0) wait(&bar.o_free, (c - 1) & 1, dead);
-                tc_fence_after();
-                if (elect()) {
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)  // (Q S)^T
-                        mma_ts(tmem + TM_O1, tmem + TM_S + 8 * k, desc_plus(dq, (k >> 2) * L::panel + (k & 3) * 32), kTS, k > 0);
-                }
-                __syncwarp();
-                wait(&bar.p_ready, c & 1, dead);
-            }
-            if (tail) wait(&bar.fixed, 0, dead);
+            if (c + kAhead < chunks) copies(c + kAhead);
+            const uint64_t dk = sdesc(base + (c % kStages) * L::stage + T8, L::panel, 1024);
+            wait_full(c);
+            if (ragged && c == chunks - 1) wait(&bar.fixed, 0, polls);
+            wait(&bar.d_ready, c & 1, polls);
             tc_fence_after();
-            if (outs) {
-                if (elect()) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)  // (P V)^T
-                        mma_bf16(tmem + TM_O2, desc_plus(dv, k * 2048), desc_plus(dp, k * 32), kPV, k > 0);
-                    mma_commit(smem_u32(&bar.o_done));
-                }
-                __syncwarp();
-                if (c + 1 < chunks) scores(c + 1);
-            }
             if (elect()) {
+#pragma unroll 1
+                for (int half = 0; half < kGroups; ++half) {
 #pragma unroll
-                for (int k = 0; k < 4 * kParts; ++k)  // (K^T V~)^T
-                    mma_ts(tmem + TM_D, tmem + TM_V + 32 * (k >> 2) + 8 * (k & 3), desc_plus(dk, (k & 3) * 2048), kTD, k > 0);
+                    for (int k = 0; k < 2 * kParts; ++k)  // the parts of V~ on 32 tokens
+                        mma_ts(tmem + TM_D, tmem + TM_V + kParts * 16 * half + 8 * k, desc_plus(dk, half * 4096 + (k & 1) * 2048), kTD, half + k > 0);
+                    mma_commit(smem_u32(&bar.v_free[half]));
+                }
                 mma_commit(smem_u32(&bar.d_done));
                 mma_commit(smem_u32(&bar.empty[c % kStages]));
             }
             __syncwarp();
         }
-        wait(&bar.d_done, (chunks - 1) & 1, dead);
-    } else {
-        // ---- the copies, and the gates: two tokens a lane, sums in fixed point
-        auto copies = [&](int c) {
-            const int i = c % kStages, row = sq.begin + (c_first + c) * kChunk;
-            if (elect()) {
-                const uint32_t at = smem_u32(smem + i * L::stage), full = smem_u32(&bar.full[i]);
-                const int vt = (nv + 63) / 64;
-                mbar_expect_tx(full, (NP * (outs ? 2 : 1) + vt) * T8);
-                for (int p = 0; p < NP; ++p) {
-                    tma_load_3d(at + p * L::panel + T8, &mk, 64 * p, h / a.hdiv, row, full);
-                    if (outs) tma_load_3d(at + p * L::panel, &mq, 64 * p, h / a.hdiv, row, full);
+        wait(&bar.d_done, (chunks - 1) & 1, polls);  // (every copy has come)
+    } else if (warp == kMmaWarp + 1) {
+        // ---- the products of the outputs: Q S, P V, and Q K^T of the next chunk
+        fewer_registers<56>();
+        if (outs) {
+            const uint32_t base = smem_u32(smem);
+            constexpr uint32_t kSc = idesc_bf16(64, 64, 0, 0), kTS = idesc_bf16(128, 64, 0, 0), kPV = idesc_bf16(128, 64, 1, 0);
+            for (int c = -1; c < chunks; ++c) {
+                const uint32_t at = base + (c % kStages) * L::stage;
+                if (c >= 0) {
+                    const uint64_t dq = sdesc(at, 16, 1024), dv = sdesc(at + L::V, T8, 1024), dp = sdesc(base + L::P, 16, 1024);
+                    if (c + 1 < chunks) wait_full(c + 1);
+                    wait(&bar.o1_ready, c & 1, polls);
+                    tc_fence_after();
+                    if (elect()) {
+#pragma unroll 1
+                        for (int p = 0; p < NP; ++p)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // (Q S)^T
+                                mma_ts(tmem + TM_O1, tmem + TM_S + 32 * p + 8 * k, desc_plus(dq, p * L::panel + k * 32), kTS, p + k > 0);
+                        mma_commit(smem_u32(&bar.o1_done));
+                    }
+                    __syncwarp();
+                    if (ragged && c == chunks - 1) wait(&bar.fixed, 0, polls);
+                    wait(&bar.p_ready, c & 1, polls);
+                    tc_fence_after();
+                    if (elect()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // (P V)^T
+                            mma_bf16(tmem + TM_O2, desc_plus(dv, k * 2048), desc_plus(dp, k * 32), kPV, k > 0);
+                        mma_commit(smem_u32(&bar.o_done));
+                        mma_commit(smem_u32(&bar.empty[c % kStages]));
+                    }
+                    __syncwarp();
                 }
-                for (int p = 0; p < vt; ++p) tma_load_3d(at + L::V + p * T8, &mv, v0 + 64 * p, h, row, full);
+                if (c + 1 < chunks) {  // Q K^T of the next chunk, which may replace this one's: its P has been used
+                    const uint32_t next = base + ((c + 1) % kStages) * L::stage;
+                    const uint64_t d = sdesc(next, 16, 1024), dk = sdesc(next + T8, 16, 1024);
+                    if (c < 0) wait_full(0);
+                    tc_fence_after();
+                    if (elect()) {
+#pragma unroll 1
+                        for (int p = 0; p < NP; ++p)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16(tmem + TM_SC, desc_plus(d, p * L::panel + k * 32), desc_plus(dk, p * L::panel + k * 32), kSc, p + k > 0);
+                        mma_commit(smem_u32(&bar.scores));
+                    }
+                    __syncwarp();
+                }
             }
-            __syncwarp();
-        };
-        int64_t total = 0;
+            wait(&bar.o_done, (chunks - 1) & 1, polls);
+        }
+    } else {
+        // ---- the gates, two tokens a lane, every other chunk a warp, as far ahead as there is room
+        fewer_registers<56>();
+        Sum2 total{0.f, 0.f};
         auto load = [&](int c, float* g) {
             const int64_t t = int64_t(c_first + c) * kChunk + 2 * lane;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) g[u] = t + u < sq.len ? __ldg(a.g + (sq.begin + t + u) * a.gs + h) : 0.f;
+            for (int u = 0; u < 2; ++u) g[u] = t + u < sq.len && c < chunks ? __ldg(a.g + (sq.begin + t + u) * a.gs + h) : 0.f;
         };
         float next[2];
-        load(0, next);
+        load(warp - kGateWarp, next);
         bool lost = false;  // a NaN among the gates
-        for (int c = 0; c < chunks; ++c) {
-            if (c >= kStages) wait(&bar.empty[c % kStages], ((c / kStages) - 1) & 1, dead);
-            copies(c);
+        for (int c = warp - kGateWarp; c < chunks; c += kGateWarps) {
             float g[2] = {next[0], next[1]};
-            if (c + 1 < chunks) load(c + 1, next);
+            load(c + kGateWarps, next);
             const unsigned n0 = __ballot_sync(kFull, g[0] != g[0]), n1 = __ballot_sync(kFull, g[1] != g[1]);
             // a NaN's token and all after it
             const int nan = min(n0 ? 2 * (__ffs(n0) - 1) : 64, n1 ? 2 * __ffs(n1) - 1 : 64);
-            int64_t b[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) b[u] = __float2ll_rn(fminf(fmaxf(g[u], -kForget), kForget) * kFixed);
-            b[1] += b[0];
-            int64_t ps = b[1];
+            for (int u = 0; u < 2; ++u) g[u] = fminf(fmaxf(g[u], -kForget), kForget);
+            const Sum2 own = sum2(Sum2{g[0], 0.f}, Sum2{g[1], 0.f});
+            Sum2 ps = own;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
-                const int64_t x = __shfl_up_sync(kFull, ps, s);
-                if (lane >= s) ps += x;
+                const Sum2 x{__shfl_up_sync(kFull, ps.hi, s), __shfl_up_sync(kFull, ps.lo, s)};
+                if (lane >= s) ps = sum2(ps, x);
             }
-            b[0] += ps - b[1], b[1] = ps;
-            const int64_t end = __shfl_sync(kFull, ps, 31), mid = __shfl_sync(kFull, ps, 15);
-            const float unit = 1.f / kFixed, bad = __int_as_float(0x7fffffff);
+            const Sum2 before = sum2(ps, Sum2{-g[1], 0.f});
+            const Sum2 end{__shfl_sync(kFull, ps.hi, 31), __shfl_sync(kFull, ps.lo, 31)};
+            // the sums at the end of this lane's block of 16, and before it
+            const Sum2 own_end{__shfl_sync(kFull, ps.hi, lane | 7), __shfl_sync(kFull, ps.lo, lane | 7)};
+            Sum2 begin{__shfl_sync(kFull, ps.hi, (lane | 7) - 8 & 31), __shfl_sync(kFull, ps.lo, (lane | 7) - 8 & 31)};
+            if (lane < 8) begin = Sum2{0.f, 0.f};
+            const float bad = __int_as_float(0x7fffffff);
+            if (c >= kGateRing) wait(&bar.gates_free[c % kGateRing], ((c / kGateRing) - 1) & 1, polls);
             float* to = reinterpret_cast<float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
-#pragma unroll
+            bool weak = true;
+#pragma unroll 1
             for (int u = 0; u < 2; ++u) {
                 const int t = 2 * lane + u;
                 const bool x = t >= nan;
-                to[kOut + t] = x ? bad : a.scale * expf(__ll2float_rn(b[u]) * unit);
-                to[kDec + t] = nan < 64 ? bad : expf(__ll2float_rn(end - b[u]) * unit);
-                to[kLocal + t] = x ? bad : __ll2float_rn(b[u] - (t < kSub ? 0 : mid)) * unit;
-                if (t < kSub) to[kCross + t] = nan < kSub ? bad : expf(__ll2float_rn(mid - b[u]) * unit);
+                const Sum2 bt = u ? ps : before;
+                const float local = bt - begin;
+                weak = weak && fabsf(local) < kWeakLimit;
+                to[kOut + t] = x ? bad : a.scale * __expf(bt.hi + bt.lo);
+                to[kDec + t] = nan < 64 ? bad : __expf(end - bt);
+                to[kLocal + t] = x ? bad : local;
+                to[kBack + t] = __expf(-local);
+                to[kCross + t] = nan <= (t | (kSub - 1)) ? bad : __expf(own_end - bt);
             }
+            weak = __all_sync(kFull, weak);
+            // (lanes 15 and 23 end blocks 1 and 2; a NaN there reaches the rows by their own sums)
+            const Sum2 e0{__shfl_sync(kFull, ps.hi, 7), __shfl_sync(kFull, ps.lo, 7)}, e1{__shfl_sync(kFull, ps.hi, 15), __shfl_sync(kFull, ps.lo, 15)},
+                e2{__shfl_sync(kFull, ps.hi, 23), __shfl_sync(kFull, ps.lo, 23)};
+            if (lane < 3) to[kBlocks + lane] = __expf(lane == 0 ? e1 - e0 : lane == 1 ? e2 - e0 : e2 - e1);
             if (lane == 0) {
-                const float e = __ll2float_rn(end) * unit;
+                const float e = end.hi + end.lo;
                 const bool near = e > -0.7f && e < 0.7f && nan == 64;
                 to[kEnd] = nan < 64 ? bad : near ? expm1f(e) : expf(e);
                 to[kNear] = near ? 1.f : 0.f;
+                to[kWeak] = weak ? 1.f : 0.f;
             }
             warp_arrive(&bar.gates[c % kGateRing], lane);
-            total += end;
-            total = total < -(int64_t(1) << 60) ? -(int64_t(1) << 60) : total > (int64_t(1) << 60) ? (int64_t(1) << 60) : total;
+            total = sum2(total, end);
             lost |= nan < 64;
         }
-        for (int c = max(0, chunks - kStages); c < chunks; ++c) wait_full(c);  // every copy has come before the CTA ends
-        if (kPart == Part::first && lane == 0 && v0 == 0)
-            seg.fades[segment_at(a, seg, si, h, j)] = lost ? __int_as_float(0x7fffffff) : expf(__ll2float_rn(total) * (1.f / kFixed));
+        if (kPart == Part::first && lane == 0) {
+            sum_s[warp - kGateWarp] = total.hi + total.lo;
+            lost_s[warp - kGateWarp] = lost;
+        }
     }
     __syncthreads();
+    if (kPart == Part::first && tid == 0 && v0 == 0)
+        seg.fades[segment_at(a, seg, si, h, j)] = lost_s[0] || lost_s[1] ? __int_as_float(0x7fffffff) : expf(sum_s[0] + sum_s[1]);
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
