@@ -89,6 +89,9 @@ constexpr int kChunkedLen = 48;
 // Host checks of a problem, and of a pointer's alignment to its elements (gds_kernels.cu).
 rm_status check(const rm_gdr_state_problem* p, Args* a);
 rm_status element_aligned(const void* p, const char* name, int size);
+// Linear attention in bf16, four tokens as products of the warp (gds_kernels.cu: the tiles of the delta rule without its
+// correction).  False: the launch failed.
+bool plain_tiles(const Args& a, rm_dtype state_dt, cudaStream_t s);
 bool tc_supports(const Args& a, rm_dtype dt);
 size_t tc_workspace_bytes(const Args& a);
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s);

@@ -470,7 +470,9 @@ __device__ __forceinline__ void store_rows(float* p, int b, int Dv, const float 
     }
 }
 
-template <typename TS, int DK, int W, bool kPacked>
+//
+// Without kDelta the same for linear attention, S <- e^g S + k v^T (rm_gla_state_forward): d is v itself.
+template <typename TS, int DK, int W, bool kPacked, bool kDelta = true>
 __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant__ Args a) {
     constexpr int NP = DK / 8, kRun = Rows<DK>::kRun;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
     const __nv_bfloat16* up_row = k + i0 * a.ks[0] + kRun * (g >> 1);
     const uint32_t half = g & 1 ? 0x7632 : 0x5410;
     const float* gate = a.g + sq.begin * a.gs + h;
-    const float* beta = a.beta + sq.begin * a.bs + h;
+    const float* beta = kDelta ? a.beta + sq.begin * a.bs + h : nullptr;
 
     uint32_t kq[NP], vx[4][W];
     float al1, be1;  // the gate and beta of token t
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
             if (live && i < n) load_words<W>(v + (t0 + i) * a.vs[0], vx[i]);
         }
         al1 = t < n ? __ldg(gate + (t0 + t) * a.gs) : 0.f;
-        be1 = t < n ? __ldg(beta + (t0 + t) * a.bs) : 0.f;
+        be1 = kDelta && t < n ? __ldg(beta + (t0 + t) * a.bs) : 0.f;
     };
     if (sq.len > 0) fetch(0);
     TileState<DK, W, kPacked> S;
@@ -543,31 +545,34 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
         float total = 1.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float al = __shfl_sync(kAllLanes, al_t, i, 4), be = __shfl_sync(kAllLanes, be_t, i, 4);
+            const float al = __shfl_sync(kAllLanes, al_t, i, 4), be = kDelta ? __shfl_sync(kAllLanes, be_t, i, 4) : 1.f;
             total *= al;
             const uint64_t al2 = pair(al, al), be2 = pair(be, be), to2 = pair(total, total), neg2 = pair(-total, -total);
             uint64_t x[W], z[W];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const float s0 = __shfl_sync(kAllLanes, y[w][i & 1], i >> 1, 4), s1 = __shfl_sync(kAllLanes, y[w][2 + (i & 1)], i >> 1, 4);
-                x[w] = fma2(neg2, pair(s0, s1), vf[i][w]);
+                if constexpr (kDelta) {
+                    const float s0 = __shfl_sync(kAllLanes, y[w][i & 1], i >> 1, 4), s1 = __shfl_sync(kAllLanes, y[w][2 + (i & 1)], i >> 1, 4);
+                    x[w] = fma2(neg2, pair(s0, s1), vf[i][w]);
+                }
                 z[w] = mul2(to2, pair(y[w][i & 1], y[w][2 + (i & 1)]));  // lanes t >= 2: S^T q of i0 and i0 + 1
             }
 #pragma unroll
             for (int r = 0; r < i; ++r) {
-                const float kr = -__shfl_sync(kAllLanes, kk[r & 1], 4 * i + (r >> 1));
+                const float kr = kDelta ? -__shfl_sync(kAllLanes, kk[r & 1], 4 * i + (r >> 1)) : 0.f;
                 const float qr = __shfl_sync(kAllLanes, kk[r & 1], 16 + 4 * i + (r >> 1));
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     d[r][w] = mul2(al2, d[r][w]);
-                    x[w] = fma2(pair(kr, kr), d[r][w], x[w]);
+                    if constexpr (kDelta) x[w] = fma2(pair(kr, kr), d[r][w], x[w]);
                     z[w] = fma2(pair(qr, qr), d[r][w], z[w]);
                 }
             }
             const float qi = __shfl_sync(kAllLanes, kk[i & 1], 16 + 4 * i + (i >> 1));
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                d[i][w] = mul2(be2, x[w]);
+                if constexpr (kDelta) d[i][w] = mul2(be2, x[w]);
+                else d[i][w] = vf[i][w];
                 z[w] = fma2(pair(qi, qi), d[i][w], z[w]);
                 if (i < 2 || t & 1) out[i & 1][w] = z[w];
             }
@@ -638,14 +643,14 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
     }
 }
 
-template <typename TS, int W, bool kPacked>
+template <typename TS, int W, bool kPacked, bool kDelta = true>
 bool tile_launch(const Args& a, cudaStream_t s) {
     const int64_t units = int64_t((a.Dv + 16 * W - 1) / (16 * W)) * a.H;
     const dim3 grid(unsigned((units + kTpb / 32 - 1) / (kTpb / 32)), unsigned(a.S));
-    auto f = a.Dk == 16   ? gds_tile_kernel<TS, 16, W, kPacked>
-             : a.Dk == 32 ? gds_tile_kernel<TS, 32, W, kPacked>
-             : a.Dk == 64 ? gds_tile_kernel<TS, 64, W, kPacked>
-                          : gds_tile_kernel<TS, 128, W, kPacked>;
+    auto f = a.Dk == 16   ? gds_tile_kernel<TS, 16, W, kPacked, kDelta>
+             : a.Dk == 32 ? gds_tile_kernel<TS, 32, W, kPacked, kDelta>
+             : a.Dk == 64 ? gds_tile_kernel<TS, 64, W, kPacked, kDelta>
+                          : gds_tile_kernel<TS, 128, W, kPacked, kDelta>;
     f<<<grid, kTpb, 0, s>>>(a);
     note_launch(1);
     return launch_ok();
@@ -679,6 +684,11 @@ bool recurrence(const Args& a, bool f32, cudaStream_t s) {
 }
 
 }  // namespace
+
+bool plain_tiles(const Args& a, rm_dtype state_dt, cudaStream_t s) {
+    if (state_dt == RM_F32) return tile_launch<float, 1, false, false>(a, s);
+    return a.max_len <= 4 ? tile_launch<__nv_bfloat16, 2, true, false>(a, s) : tile_launch<__nv_bfloat16, 1, false, false>(a, s);
+}
 
 rm_status check(const rm_gdr_state_problem* p, Args* a) {
     if (p == nullptr) return api_fail(RM_ERR_INVALID_ARG, "problem is null");

@@ -1,6 +1,7 @@
 // gla_kernels.cu -- linear attention with a decay for each head and a carried state as a token
 // recurrence (rm_gla_state_forward): decoding a few tokens for each of many sequences, and every
-// shape that the chunked form on the tensor cores does not take.
+// shape that the chunked form on the tensor cores does not take.  (Several bf16 tokens go four at a
+// time through the warp's matrix instructions: gds_kernels.cu.)
 //
 // Per token, S in R^{Dk x Dv}:
 //     S <- e^g S + k v^T,   o = scale S^T q
@@ -228,7 +229,12 @@ bool token_launch(const Args& a, cudaStream_t s) {
 
 template <typename T, typename TS>
 bool recurrence(const Args& a, cudaStream_t s) {
-    return a.max_len <= 1 ? token_launch<T, TS, 1>(a, s) : token_launch<T, TS, 4>(a, s);
+    if constexpr (sizeof(T) == 4) return a.max_len <= 1 ? token_launch<T, TS, 1>(a, s) : token_launch<T, TS, 4>(a, s);
+    // Single tokens: the token kernel, but tiles for a bf16 state of 128 rows (256 sequences of 16 heads of 128 x 128: fp32 81
+    // us and tiles 93, bf16 53 and tiles 48; 64 of 64 x 64, bf16: 6.5 and tiles 7.1).  Several: tiles (61 sequences, four
+    // tokens, 32 heads of 128 x 256, bf16: 48 us, the token kernel 96).
+    const bool tiles = a.max_len > 1 || (sizeof(TS) == 2 && a.Dk == 128);
+    return tiles ? gds::plain_tiles(a, sizeof(TS) == 4 ? RM_F32 : RM_BF16, s) : token_launch<T, TS, 1>(a, s);
 }
 
 }  // namespace

@@ -65,79 +65,124 @@ __device__ __forceinline__ void round8(__nv_bfloat16*, float* x) {
 
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-// Sum of x and the largest of the bits m over the TPR threads of a row.  (The bits of |y| order as the values do, with NaN above all.)
-template <int TPR>
-__device__ __forceinline__ void row_reduce(float& x, uint32_t& m, int& turn) {
+// Eight elements as they lie in memory
+template <typename T>
+struct Raw {
+    uint4 x[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+        for (int i = 0; i < int(sizeof(T)) / 2; ++i) x[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T)) / 2; ++i) x[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float* y) const {
+        if constexpr (sizeof(T) == 2) tc::unpack8(x[0], y);
+        else load8(reinterpret_cast<const float*>(x), y);
+    }
+};
+
+// Threads of a row: LANES of a warp (several rows a warp), or with LANES 0 the whole block.
+// Sums x and y over them; the largest of the bits m.  (The bits of |y| order as the values do, with NaN above all.)
+template <int LANES, typename M>
+__device__ __forceinline__ void row_reduce(float& x, M& m, int& turn) {
+    auto join = [](M p, M q) { return std::is_same<M, float>::value ? M(p + q) : (p > q ? p : q); };
+#pragma unroll
+    for (int o = (LANES ? LANES : 32) / 2; o > 0; o >>= 1) {
         x += __shfl_xor_sync(kAll, x, o);
-        m = max(m, __shfl_xor_sync(kAll, m, o));
+        m = join(m, __shfl_xor_sync(kAll, m, o));
     }
-    if constexpr (TPR > 32) {
-        __shared__ float xs[2][TPR / 32];
-        __shared__ uint32_t ms[2][TPR / 32];
-        if ((threadIdx.x & 31) == 0) xs[turn][threadIdx.x >> 5] = x, ms[turn][threadIdx.x >> 5] = m;
+    if constexpr (LANES == 0) {
+        __shared__ float xs[2][32];
+        __shared__ M ms[2][32];
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) xs[turn][threadIdx.x >> 5] = x, ms[turn][threadIdx.x >> 5] = m;
         __syncthreads();
-        x = 0.f, m = 0;
+        x = lane < warps ? xs[turn][lane] : 0.f, m = lane < warps ? ms[turn][lane] : M(0);
 #pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) x += xs[turn][i], m = max(m, ms[turn][i]);
-        turn ^= 1;
-    }
-}
-template <int TPR>
-__device__ __forceinline__ void row_reduce2(float& x, float& y, int& turn) {
-#pragma unroll
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
-        x += __shfl_xor_sync(kAll, x, o);
-        y += __shfl_xor_sync(kAll, y, o);
-    }
-    if constexpr (TPR > 32) {
-        __shared__ float2 s[2][TPR / 32];
-        if ((threadIdx.x & 31) == 0) s[turn][threadIdx.x >> 5] = make_float2(x, y);
-        __syncthreads();
-        x = y = 0.f;
-#pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) x += s[turn][i].x, y += s[turn][i].y;
-        turn ^= 1;
+        for (int o = 16; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(kAll, x, o);
+            m = join(m, __shfl_xor_sync(kAll, m, o));
+        }
+        turn ^= 1;  // (the next row's sums go elsewhere: a slow warp may still read these)
     }
 }
 
-constexpr int threads_of(int TPR) { return TPR < 256 && TPR <= 32 ? 256 : TPR; }
+// This thread's row of those that a block takes at once, its place in the row, and the threads of a row
+template <int LANES>
+__device__ __forceinline__ int row_of_block() { return LANES ? int(threadIdx.x) / (LANES ? LANES : 1) : 0; }
+template <int LANES>
+__device__ __forceinline__ int place_in_row() { return LANES ? int(threadIdx.x) % (LANES ? LANES : 1) : int(threadIdx.x); }
+template <int LANES>
+__device__ __forceinline__ int row_threads() { return LANES ? LANES : int(blockDim.x); }
+__device__ __forceinline__ void place(const Args& a, int64_t row, int& t, int& h) {
+    t = a.H == 1 ? int(row) : int(uint32_t(row) / uint32_t(a.H));
+    h = int(row - int64_t(t) * a.H);
+}
 
-// A row is taken by TPR threads, VPT times eight elements each: those of unit i are 8 (lane + i TPR) ..
-// kGate: 0 none, 1 after the norm, 2 before it.  kOut: 0 y, 1 y8 and scales.
-template <typename T, typename R, bool kRes, int kGate, bool kQuant, int TPR, int VPT>
-__global__ void __launch_bounds__(threads_of(TPR)) rms_forward_kernel(const __grid_constant__ Args a) {
-    constexpr int RPB = threads_of(TPR) / TPR;
-    const int lane = threadIdx.x % TPR, rows = a.N * a.H;
+// What a thread reads of a row
+template <typename T, typename R, bool kRes, bool kGate, int VPT>
+struct Row {
+    Raw<T> x[VPT], z[kGate ? VPT : 1];
+    Raw<R> q[kRes ? VPT : 1];
+};
+
+// A thread has VPT times eight elements of a row: those of unit i are 8 (place + i threads) ..  A block goes on to the
+// rows gridDim.x further on, whose loads are under way while it takes a row.
+// kGate: 0 none, 1 after the norm, 2 before it.
+template <typename T, typename R, bool kRes, int kGate, bool kQuant, int LANES, int VPT, int TPB>
+__global__ void __launch_bounds__(TPB) rms_forward_kernel(const __grid_constant__ Args a) {
+    constexpr bool kAhead = VPT == 1;
+    const int RPB = LANES ? TPB / (LANES ? LANES : 1) : 1, at = place_in_row<LANES>(), step = row_threads<LANES>();
+    const int64_t rows = int64_t(a.N) * a.H, hop = int64_t(gridDim.x) * RPB;
+    int64_t row = int64_t(blockIdx.x) * RPB + row_of_block<LANES>();
     int turn = 0;
-    for (int64_t first = int64_t(blockIdx.x) * RPB; first < rows; first += int64_t(gridDim.x) * RPB) {
-        const int64_t row = first + threadIdx.x / TPR;
-        const bool there = row < rows;
-        const int t = there ? int(row / a.H) : 0, hd = there ? int(row % a.H) : 0;
+    Row<T, R, kRes, kGate != 0, VPT> next;
+    auto load = [&](int64_t r) {
+        int t, hd;
+        place(a, r < rows ? r : 0, t, hd);
         const T* x = static_cast<const T*>(a.x) + t * a.xs[0] + hd * a.xs[1];
         const R* q = kRes ? static_cast<const R*>(a.res) + t * a.rs[0] + hd * a.rs[1] : nullptr;
         const T* z = kGate ? static_cast<const T*>(a.z) + t * a.zs[0] + hd * a.zs[1] : nullptr;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int e = 8 * (at + i * step);
+            const bool live = r < rows && e < a.n;
+            if (live) next.x[i].load(x + e);
+            else next.x[i].zero();
+            if (kRes) {
+                if (live) next.q[i].load(q + e);
+                else next.q[i].zero();
+            }
+            if (kGate) {
+                if (live) next.z[i].load(z + e);
+                else next.z[i].zero();
+            }
+        }
+    };
+    load(row);
+    for (int64_t first = int64_t(blockIdx.x) * RPB; first < rows; first += hop, row += hop) {
+        const Row<T, R, kRes, kGate != 0, VPT> now = next;
+        if (kAhead && first + hop < rows) load(row + hop);
+        const bool there = row < rows;
         float m[VPT][8];
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int e = 8 * (lane + i * TPR);
+            const int e = 8 * (at + i * step);
             const bool live = there && e < a.n;
-            float b[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m[i][j] = b[j] = 0.f;
-            if (live) load8(x + e, m[i]);
+            float b[8], act[8];
+            now.x[i].get(m[i]);
             if (kRes) {
-                if (live) load8(q + e, b);
+                now.q[i].get(b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) m[i][j] += b[j];
                 if (live) store8(static_cast<R*>(a.h) + row * a.n + e, m[i]);
                 round8(static_cast<R*>(nullptr), m[i]);
             }
-            float act[8];
             if (kGate) {
-                if (live) load8(z + e, b);
+                now.z[i].get(b);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) act[j] = b[j] * sigmoid(b[j]);
             }
@@ -167,11 +212,11 @@ __global__ void __launch_bounds__(threads_of(TPR)) rms_forward_kernel(const __gr
                 most = max(most, big[i]);
             }
         }
-        row_reduce<TPR>(sq, most, turn);
+        row_reduce<LANES>(sq, most, turn);
         const float r = rsqrtf(fmaf(sq, a.inv_n, a.eps));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int e = 8 * (lane + i * TPR);
+            const int e = 8 * (at + i * step);
             const bool live = there && e < a.n;
             if (kQuant) {
                 uint32_t top = most;
@@ -179,9 +224,9 @@ __global__ void __launch_bounds__(threads_of(TPR)) rms_forward_kernel(const __gr
                     top = big[i];
                     for (int o = a.group / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
                 }
-                float s = __uint_as_float(top) * r / kF8Max;
+                float s = __uint_as_float(top) * r * (1.f / kF8Max);
                 s = s < kTiny ? kTiny : s;  // (a NaN stays)
-                const float f = 1.f / s;
+                const float f = __fdividef(1.f, s);  // (r f may leave fp32 where y is all but 0)
                 uint32_t out[2];
 #pragma unroll
                 for (int j = 0; j < 8; j += 4) {
@@ -200,91 +245,119 @@ __global__ void __launch_bounds__(threads_of(TPR)) rms_forward_kernel(const __gr
                 store8(static_cast<T*>(a.y) + row * a.n + e, m[i]);
             }
         }
+        if (!kAhead && first + hop < rows) load(row + hop);
     }
 }
 
-// Rows are taken in a fixed order by a fixed number of blocks, so that the weight's gradient does not depend on
-// the launch.
-template <typename T, typename R, int kGate, bool kDh, bool kTwo, int TPR, int VPT>
-__global__ void __launch_bounds__(threads_of(TPR)) rms_backward_kernel(const __grid_constant__ Args a) {
-    constexpr int TPB = threads_of(TPR), RPB = TPB / TPR;
-    const int lane = threadIdx.x % TPR, rows = a.N * a.H;
+// Threads of a multiprocessor that a backward is compiled for: as many as its registers allow
+template <typename T, typename R, int kGate>
+constexpr int backward_threads() { return kGate || sizeof(T) == 4 || sizeof(R) == 4 ? 768 : 1024; }
+
+// Rows are taken in a fixed order by a fixed number of blocks, so that the weight's gradient does not depend on the
+// launch.  With one unit a thread a row's inputs, dh among them, are on their way while the row before is taken, and the weights
+// stay in registers.  What was read stays as it was read (bf16: half the registers) between the sums and the outputs.
+template <typename T, typename R, int kGate, bool kDh, bool kTwo, int LANES, int VPT, int TPB>
+__global__ void __launch_bounds__(TPB, VPT > 1 || TPB > backward_threads<T, R, kGate>() ? 1 : backward_threads<T, R, kGate>() / TPB) rms_backward_kernel(const __grid_constant__ Args a) {
+    constexpr bool kAhead = VPT == 1;
+    const int RPB = LANES ? TPB / (LANES ? LANES : 1) : 1, at = place_in_row<LANES>(), step = row_threads<LANES>();
+    const int64_t rows = int64_t(a.N) * a.H, hop = int64_t(gridDim.x) * RPB;
+    int64_t row = int64_t(blockIdx.x) * RPB + row_of_block<LANES>();
     int turn = 0;
-    float dw[VPT][8];
+    float ws[8], dw[VPT][8];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int j = 0; j < 8; ++j) {
+        ws[j] = 1.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-    for (int64_t first = int64_t(blockIdx.x) * RPB; first < rows; first += int64_t(gridDim.x) * RPB) {
-        const int64_t row = first + threadIdx.x / TPR;
-        const bool there = row < rows;
-        const int t = there ? int(row / a.H) : 0, hd = there ? int(row % a.H) : 0;
+        for (int i = 0; i < VPT; ++i) dw[i][j] = 0.f;
+    }
+    if (kAhead && a.w != nullptr && 8 * at < a.n) load8(a.w + 8 * at, ws);
+    struct In {
+        Raw<R> h[VPT], dh[kDh ? VPT : 1];
+        Raw<T> d[VPT], z[kGate ? VPT : 1];
+    } next;
+    auto load = [&](int64_t r) {
+        int t, hd;
+        place(a, r < rows ? r : 0, t, hd);
         const R* h = static_cast<const R*>(a.res) + t * a.rs[0] + hd * a.rs[1];
         const T* z = kGate ? static_cast<const T*>(a.z) + t * a.zs[0] + hd * a.zs[1] : nullptr;
-        float u[VPT][8], d[VPT][8], zz[VPT][8];
-        float sq = 0.f, du = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int e = 8 * (lane + i * TPR);
-            const bool live = there && e < a.n;
-            float w[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[i][j] = d[i][j] = zz[i][j] = 0.f, w[j] = 1.f;
-            if (live) {
-                load8(h + e, u[i]);
-                load8(static_cast<const T*>(a.x) + row * a.n + e, d[i]);
-                if (kGate) load8(z + e, zz[i]);
-                if (a.w != nullptr) load8(a.w + e, w);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float act = kGate ? zz[i][j] * sigmoid(zz[i][j]) : 1.f;
-                const float uu = kGate == 2 ? u[i][j] * act : u[i][j];
-                const float dd = (kGate == 1 ? d[i][j] * act : d[i][j]) * w[j];
-                sq = fmaf(uu, uu, sq);
-                du = fmaf(dd, uu, du);
+            const int e = 8 * (at + i * step);
+            if (r < rows && e < a.n) {
+                next.h[i].load(h + e);
+                next.d[i].load(static_cast<const T*>(a.x) + r * a.n + e);
+                if (kGate) next.z[i].load(z + e);
+                if (kDh) next.dh[i].load(static_cast<const R*>(a.dh) + r * a.n + e);
+            } else {
+                next.h[i].zero(), next.d[i].zero();
+                if (kGate) next.z[i].zero();
             }
         }
-        row_reduce2<TPR>(sq, du, turn);
+    };
+    load(row);
+    for (int64_t first = int64_t(blockIdx.x) * RPB; first < rows; first += hop, row += hop) {
+        const In now = next;
+        if (kAhead && first + hop < rows) load(row + hop);
+        float sg[kGate ? VPT : 1][8], sq = 0.f, du = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float u[8], d[8], zz[8], wl[8];
+            now.h[i].get(u);
+            now.d[i].get(d);
+            if (kGate) now.z[i].get(zz);
+            if (!kAhead && a.w != nullptr && 8 * (at + i * step) < a.n) load8(a.w + 8 * (at + i * step), wl);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (kGate) sg[i][j] = sigmoid(zz[j]);
+                const float act = kGate ? zz[j] * sg[i][j] : 1.f, w = kAhead ? ws[j] : a.w != nullptr ? wl[j] : 1.f;
+                const float uu = kGate == 2 ? u[j] * act : u[j];
+                const float dd = (kGate == 1 ? d[j] * act : d[j]) * w;
+                sq = fmaf(uu, uu, sq);
+                if (8 * (at + i * step) < a.n) du = fmaf(dd, uu, du);
+            }
+        }
+        row_reduce<LANES>(sq, du, turn);
         const float r = rsqrtf(fmaf(sq, a.inv_n, a.eps)), c = r * du * a.inv_n;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int e = 8 * (lane + i * TPR);
-            const bool live = there && e < a.n;
-            if (!live) continue;
-            float w[8], dh[8], dz[8], out[8];
+            const int e = 8 * (at + i * step);
+            if (row < rows && e < a.n) {
+                float u[8], d[8], zz[8], wl[8], add[8], dz[8], out[8];
+                now.h[i].get(u);
+                now.d[i].get(d);
+                if (kGate) now.z[i].get(zz);
+                if (kDh) now.dh[i].get(add);
+                if (!kAhead && a.w != nullptr) load8(a.w + e, wl);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 1.f, dh[j] = 0.f;
-            if (a.w != nullptr) load8(a.w + e, w);
-            if (kDh) load8(static_cast<const R*>(a.dh) + row * a.n + e, dh);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float sg = kGate ? sigmoid(zz[i][j]) : 0.f, act = kGate ? zz[i][j] * sg : 1.f;
-                const float slope = sg * fmaf(zz[i][j], 1.f - sg, 1.f);
-                const float uh = (kGate == 2 ? u[i][j] * act : u[i][j]) * r;
-                const float ee = kGate == 1 ? d[i][j] * act : d[i][j];
-                dw[i][j] = fmaf(ee, uh, dw[i][j]);
-                float g = r * fmaf(ee, w[j], -uh * c);
-                if (kGate == 1) dz[j] = d[i][j] * uh * w[j] * slope;
-                if (kGate == 2) dz[j] = g * u[i][j] * slope, g *= act;
-                out[j] = g + dh[j];
+                for (int j = 0; j < 8; ++j) {
+                    const float s = kGate ? sg[i][j] : 0.f, w = kAhead ? ws[j] : a.w != nullptr ? wl[j] : 1.f;
+                    const float act = kGate ? zz[j] * s : 1.f, slope = kGate ? s * fmaf(zz[j], 1.f - s, 1.f) : 0.f;
+                    const float uh = (kGate == 2 ? u[j] * act : u[j]) * r;
+                    const float ee = kGate == 1 ? d[j] * act : d[j];
+                    dw[i][j] = fmaf(ee, uh, dw[i][j]);
+                    float g = r * fmaf(ee, w, -uh * c);
+                    if (kGate == 1) dz[j] = d[j] * uh * w * slope;
+                    if (kGate == 2) dz[j] = g * u[j] * slope, g *= act;
+                    out[j] = kDh ? g + add[j] : g;
+                }
+                if (kGate) store8(static_cast<T*>(a.dz) + row * a.n + e, dz);
+                if (kTwo) store8(static_cast<R*>(a.h) + row * a.n + e, out);
+                store8(static_cast<T*>(a.y) + row * a.n + e, out);
             }
-            if (kGate) store8(static_cast<T*>(a.dz) + row * a.n + e, dz);
-            if (kTwo) store8(static_cast<R*>(a.h) + row * a.n + e, out);
-            store8(static_cast<T*>(a.y) + row * a.n + e, out);
         }
+        if (!kAhead && first + hop < rows) load(row + hop);
     }
     if (a.part == nullptr) return;
     float* to = a.part + int64_t(blockIdx.x) * a.n;
-    if constexpr (RPB > 1) {  // the block's rows, group after group
-        __shared__ float sum[TPR * VPT * 8];
+    if constexpr (LANES > 0) {  // the block's rows, group after group
+        __shared__ float sum[LANES * VPT * 8];
         for (int g = 0; g < RPB; ++g) {
-            if (int(threadIdx.x) / TPR == g) {
+            if (row_of_block<LANES>() == g) {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float& s = sum[8 * (lane + i * TPR) + j];
+                        float& s = sum[8 * (at + i * step) + j];
                         s = g ? s + dw[i][j] : dw[i][j];
                     }
             }
@@ -294,7 +367,7 @@ __global__ void __launch_bounds__(threads_of(TPR)) rms_backward_kernel(const __g
     } else {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int e = 8 * (lane + i * TPR);
+            const int e = 8 * (at + i * step);
             if (e < a.n) store8(to + e, dw[i]);
         }
     }
@@ -319,29 +392,41 @@ __global__ void __launch_bounds__(256) rms_weight_kernel(const float* part, floa
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-constexpr int kMostBlocks = 152 * 4;
-
-// f(TPR, VPT) of the row length
-template <typename F>
+// f(LANES, VPT, TPB) of the row length and the direction.  Rows of up to 256 elements take the lanes of a warp, longer ones a block of as
+// many warps as they need, with eight elements a thread: more of them in a thread leave fewer loads under way (2048
+// elements, 32768 rows: 81 us with one unit of eight a thread, and 4096 with two: 92; see the table of times).
+template <bool kBackward, typename F>
 auto by_length(int n, F f) {
     using std::integral_constant;
-#define RM_RMS_SHAPE(t, v) f(integral_constant<int, t>{}, integral_constant<int, v>{})
-    if (n <= 64) return RM_RMS_SHAPE(8, 1);
-    if (n <= 128) return RM_RMS_SHAPE(16, 1);
-    if (n <= 256) return RM_RMS_SHAPE(32, 1);
-    if (n <= 512) return RM_RMS_SHAPE(32, 2);
-    if (n <= 1024) return RM_RMS_SHAPE(128, 1);
-    if (n <= 2048) return RM_RMS_SHAPE(256, 1);
-    if (n <= 4096) return RM_RMS_SHAPE(256, 2);
-    if (n <= 8192) return RM_RMS_SHAPE(512, 2);
-    if (n <= 16384) return RM_RMS_SHAPE(512, 4);
-    return RM_RMS_SHAPE(1024, 4);
+#define RM_RMS_SHAPE(l, v, t) f(integral_constant<int, l>{}, integral_constant<int, v>{}, integral_constant<int, t>{})
+    if (n <= 64) return RM_RMS_SHAPE(8, 1, 256);
+    if (n <= 128) return RM_RMS_SHAPE(16, 1, 256);
+    if (n <= 256) return RM_RMS_SHAPE(32, 1, 256);
+    if (n <= 1024) return RM_RMS_SHAPE(0, 1, 128);
+    if (n <= 2048) return RM_RMS_SHAPE(0, 1, 256);
+    if (n <= 4096) return RM_RMS_SHAPE(0, 1, 512);
+    if constexpr (!kBackward)
+        if (n <= 8192) return RM_RMS_SHAPE(0, 1, 1024);
+    if (n <= 8192) return RM_RMS_SHAPE(0, 2, 512);
+    if (n <= 16384) return RM_RMS_SHAPE(0, 2, 1024);
+    return RM_RMS_SHAPE(0, 4, 1024);
 #undef RM_RMS_SHAPE
 }
-
-int blocks_of(int64_t rows, int TPR, int most) {
-    const int64_t per = threads_of(TPR) / TPR, b = (rows + per - 1) / per;
+int threads_of(int n, int LANES, int VPT, int TPB) {
+    const int need = ((n + 8 * VPT - 1) / (8 * VPT) + 31) / 32 * 32;
+    return LANES ? TPB : need < TPB ? need : TPB;
+}
+int blocks_of(int64_t rows, int LANES, int TPB, int64_t most) {
+    const int64_t per = LANES ? TPB / LANES : 1, b = (rows + per - 1) / per;
     return int(b < most ? b : most);
+}
+
+// Blocks of a backward, whose partial gradients the workspace holds: as many as run at once
+int blocks_of_backward(int n, int threads = 1024) {
+    return by_length<true>(n, [&](auto l, auto v, auto t) {
+        const int each = (v() > 1 ? t() : threads) / threads_of(n, l, v, t);
+        return 152 * (each > 0 ? each : 1);
+    });
 }
 
 rm_status launched() {
@@ -355,10 +440,13 @@ rm_status launched() {
 template <typename T, typename R, bool kRes, int kGate>
 rm_status forward(const Args& a, cudaStream_t s) {
     const int64_t rows = int64_t(a.N) * a.H;
-    return by_length(a.n, [&](auto tpr, auto vpt) {
-        const int blocks = blocks_of(rows, tpr, 0x7fffffff);
-        if (a.scale != nullptr) rms_forward_kernel<T, R, kRes, kGate, true, tpr(), vpt()><<<blocks, threads_of(tpr), 0, s>>>(a);
-        else rms_forward_kernel<T, R, kRes, kGate, false, tpr(), vpt()><<<blocks, threads_of(tpr), 0, s>>>(a);
+    return by_length<false>(a.n, [&](auto l, auto v, auto t) {
+        // With a gate, whose arithmetic would leave the memory idle, and for long rows, blocks go on to further rows whose
+        // loads are ahead (gated, 32768 x 16 rows of 128: 69 us, a block for its rows alone 80; rows of 4096: 85 and 109);
+        // else a block has its rows alone (32768 rows of 2048: 85 us, and 89 with 2048 threads a multiprocessor going on)
+        const int threads = threads_of(a.n, l, v, t), blocks = blocks_of(rows, l, t, kGate || a.n > 2048 ? 152 * (1024 / threads) : 0x7fffffff);
+        if (a.scale != nullptr) rms_forward_kernel<T, R, kRes, kGate, true, l(), v(), t()><<<blocks, threads, 0, s>>>(a);
+        else rms_forward_kernel<T, R, kRes, kGate, false, l(), v(), t()><<<blocks, threads, 0, s>>>(a);
         return launched();
     });
 }
@@ -366,9 +454,9 @@ rm_status forward(const Args& a, cudaStream_t s) {
 template <typename T, typename R, int kGate, bool kDh, bool kTwo>
 rm_status backward(const Args& a, float* dw, cudaStream_t s) {
     const int64_t rows = int64_t(a.N) * a.H;
-    return by_length(a.n, [&](auto tpr, auto vpt) {
-        const int blocks = blocks_of(rows, tpr, kMostBlocks);
-        rms_backward_kernel<T, R, kGate, kDh, kTwo, tpr(), vpt()><<<blocks, threads_of(tpr), 0, s>>>(a);
+    return by_length<true>(a.n, [&](auto l, auto v, auto t) {
+        const int threads = threads_of(a.n, l, v, t), blocks = blocks_of(rows, l, t, blocks_of_backward(a.n, backward_threads<T, R, kGate>()));
+        rms_backward_kernel<T, R, kGate, kDh, kTwo, l(), v(), t()><<<blocks, threads, 0, s>>>(a);
         const rm_status st = launched();
         if (st != RM_OK || dw == nullptr) return st;
         rms_weight_kernel<<<(a.n + 31) / 32, 256, 0, s>>>(a.part, dw, blocks, a.n);
@@ -518,7 +606,7 @@ size_t rm_cp_rms_workspace_size(const rm_cp_rms_problem* p) {
     rmcp::rms::Args a{};
     rmcp::rms::Shape k;
     if (rmcp::rms::check(p, &a, &k) != RM_OK) return 0;
-    return size_t(rmcp::rms::kMostBlocks) * size_t(a.n) * sizeof(float);
+    return size_t(rmcp::rms::blocks_of_backward(a.n)) * size_t(a.n) * sizeof(float);
 }
 
 rm_status rm_cp_rms_backward(const rm_cp_rms_problem* p, const void* h, const void* gate, const float* weight, const void* dy,
@@ -558,7 +646,7 @@ rm_status rm_cp_rms_backward(const rm_cp_rms_problem* p, const void* h, const vo
     const rms::Range in[] = {{h, rms::reach(p, p->r_stride, rs), rms::dense(p, p->r_stride)}, {dy, all * es, true}, {dh, all * rs, true},
                              {k.gate ? gate : nullptr, rms::reach(p, p->z_stride, es), rms::dense(p, p->z_stride)}},
                      out[] = {{dx, all * es, true}, {two ? dresidual : nullptr, all * rs, true}, {k.gate ? dgate : nullptr, all * es, true},
-                              {dweight, int64_t(p->n) * 4, false}, {dweight ? ws : nullptr, int64_t(rms::kMostBlocks) * p->n * 4, false}},
+                              {dweight, int64_t(p->n) * 4, false}, {dweight ? ws : nullptr, int64_t(rms::blocks_of_backward(p->n)) * p->n * 4, false}},
                      w{weight, int64_t(p->n) * 4, false};
     bool bad = false;
     for (int i = 0; i < 5; ++i) {
