@@ -215,6 +215,244 @@ __global__ void __launch_bounds__(threads_of(DK), NT == 1 ? 8 : 4) gla_token_ker
     }
 }
 
+// ---------------------------------------------------------------------------
+// fp32 prompts in chunks of 32 tokens.  With b_t the running sum of a chunk's gates and S the state before it:
+//     o_t = scale (e^{b_t} S^T q_t + sum_{s <= t} e^{b_t - b_s} (q_t.k_s) v_s),   S <- e^{b_31} S + sum_s e^{b_31 - b_s} k_s v_s^T
+// A CTA has 32 columns of a sequence's head.  The products are plain fp32 multiply-adds on tiles in shared memory, two tokens x
+// four columns (of scores, of outputs) or Dk / 16 rows x four columns (of the state) a thread, the next chunk's tokens on
+// their way meanwhile.  What bounds it is the multiply-adds and, in short sequences, the three barriers of a chunk; the
+// recurrence, which it replaces, pays the latency of a barrier every four tokens (7 prompts of up to 301 tokens, 6 heads of 32 x
+// 40: 53 us).
+// ---------------------------------------------------------------------------
+constexpr int kTokens = 32;
+// Tokens of the longest sequence from which it is taken.  us in a CUDA graph, recurrence / chunks:
+//     tokens                               12           16           24           64
+//     one sequence, 16 heads of 128 x 128  11.0 / 7.8   14.3 / 7.8   20.8 / 7.8   53 / 13
+//     64 sequences, 16 heads of 64 x 64    31 / 46      39 / 47      55 / 48      138 / 86
+//     7 sequences, 6 heads of 32 x 40      3.8 / 4.9    4.5 / 5.0    5.9 / 4.9    12.3 / 8.1
+//     61 sequences, 16 heads of 128 x 128  147 / 149    191 / 149    280 / 151    723 / 272
+constexpr int kTokenLen = 20;
+template <int DK>
+struct ChunkSmem {
+    static constexpr int row = DK + 4;  // (rows of 16 keys side by side lie in different banks)
+    struct In {
+        float q[kTokens][row], k[kTokens][row], v[kTokens][kCols];
+    } in[2];
+    float S[DK][kCols];
+    float P[kTokens][kTokens + 4];
+    float out[kTokens], dec[kTokens], hi[kTokens], lo[kTokens];  // scale e^{b_t}, e^{b_31 - b_t}, b_t in two parts
+    float end;
+    int near;
+};
+__device__ __forceinline__ void copy16(float* to, const float* from, bool live) {  // zeros where it is not live
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+
+template <typename TS, int DK>
+__global__ void __launch_bounds__(128) gla_chunk_kernel(const __grid_constant__ Args a) {
+    // tokens of a thread (one, and 256 threads: 2048 tokens of 16 heads of 128 x 128 456 us for 382, 8 prompts of 300 of 64 x
+    // 64 82 for 60), and rows
+    constexpr int TOK = 2, TPB = 256 / TOK, KR = DK / 16;
+    using L = ChunkSmem<DK>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    L& sm = *reinterpret_cast<L*>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = tid & 7, t0 = TOK * (tid >> 3), row = (tid >> 3) * KR;
+    const int blocks = (a.Dv + kCols - 1) / kCols;
+    const int h = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * kCols, col = c0 + quad * 4;
+    const bool live = col < a.Dv;  // Dv is a multiple of 8, a thread's columns of 4
+    const int cols = min(a.Dv - c0, kCols);
+    const Seq sq = sequence(a, blockIdx.y);
+    zero_others(a, blockIdx.y, sq, static_cast<float*>(a.o) + int64_t(h) * a.Dv + c0, cols, tid, TPB);
+    if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
+    float* o = static_cast<float*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + c0;
+    const int64_t os = int64_t(a.H) * a.Dv;
+    if (sq.slot < 0) {  // padding
+        zero_outputs(o, os, sq.len, cols, tid, TPB);
+        return;
+    }
+    const int hk = h / a.hdiv;
+    const float* q = static_cast<const float*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
+    const float* k = static_cast<const float*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1];
+    const float* v = static_cast<const float*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + c0;
+    const float* g = a.g + sq.begin * a.gs + h;
+    auto fetch = [&](int from) {  // a chunk's tokens; those past the end are zeros
+        typename L::In& to = sm.in[(from / kTokens) & 1];
+        for (int u = tid; u < kTokens * (DK / 4); u += TPB) {
+            const int t = u / (DK / 4), e = u % (DK / 4) * 4;
+            const bool there = from + t < sq.len;
+            copy16(&to.q[t][e], q + (there ? from + t : 0) * a.qs[0] + e, there);
+            copy16(&to.k[t][e], k + (there ? from + t : 0) * a.ks[0] + e, there);
+        }
+        for (int u = tid; u < kTokens * (kCols / 4); u += TPB) {
+            const int t = u / (kCols / 4), e = u % (kCols / 4) * 4;
+            const bool there = from + t < sq.len && e < cols;
+            copy16(&to.v[t][e], v + (there ? (from + t) * a.vs[0] + e : 0), there);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto gate = [&](int from) { return warp == 0 && from + lane < sq.len ? __ldg(g + (from + lane) * a.gs) : 0.f; };
+    if (sq.len > 0) fetch(0);
+    float next = gate(0);
+    TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * DK + row) * a.Dv + col;
+    float S[KR][4];
+#pragma unroll
+    for (int i = 0; i < KR; ++i) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[i][c] = 0.f;
+        if (live && !sq.fresh) load4(st + i * a.Dv, S[i]);
+        store4(&sm.S[row + i][4 * quad], S[i]);
+    }
+    for (int from = 0; from < sq.len; from += kTokens) {
+        const typename L::In& in = sm.in[(from / kTokens) & 1];
+        const int n = min(sq.len - from, kTokens);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // the tokens and the state are there, the other tokens and P have been used
+        if (from + kTokens < sq.len) fetch(from + kTokens);
+        if (warp == 0) {  // the gates: a token a lane, sums held as two floats
+            float x = next, y = 0.f;
+            next = gate(from + kTokens);
+            x = x < -110.f ? -110.f : x;  // (e^-110 is 0)
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const float u = __shfl_up_sync(kAllLanes, x, s), w = __shfl_up_sync(kAllLanes, y, s);
+                if (lane >= s) {
+                    const float sum = x + u, z = sum - x;
+                    y += w + ((x - (sum - z)) + (u - z));
+                    x = sum;
+                }
+            }
+            const float ex = __shfl_sync(kAllLanes, x, 31), ey = __shfl_sync(kAllLanes, y, 31), e = ex + ey;
+            sm.out[lane] = a.scale * expf(x + y);
+            sm.dec[lane] = expf((ex - x) + (ey - y));
+            sm.hi[lane] = x, sm.lo[lane] = y;
+            if (lane == 0) {
+                sm.near = e > -0.7f && e < 0.7f;  // near 1 the decay as its distance from 1 (see gla_token_kernel)
+                sm.end = sm.near ? expm1f(e) : expf(e);
+            }
+        }
+        float x[TOK][4];  // scores of the thread's tokens with quad + 8 j
+#pragma unroll
+        for (int i = 0; i < TOK; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+#pragma unroll 4
+        for (int e = 0; e < DK; e += 4) {
+            float4 u[TOK];
+#pragma unroll
+            for (int i = 0; i < TOK; ++i) u[i] = *reinterpret_cast<const float4*>(&in.q[t0 + i][e]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 y = *reinterpret_cast<const float4*>(&in.k[quad + 8 * j][e]);
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) x[i][j] = fmaf(u[i].w, y.w, fmaf(u[i].z, y.z, fmaf(u[i].y, y.y, fmaf(u[i].x, y.x, x[i][j]))));
+            }
+        }
+        __syncthreads();  // the gates are there
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
+            const float bh = sm.hi[t0 + i], bl = sm.lo[t0 + i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int s = quad + 8 * j;
+                sm.P[t0 + i][s] = s <= t0 + i ? a.scale * x[i][j] * expf((bh - sm.hi[s]) + (bl - sm.lo[s])) : 0.f;
+            }
+        }
+        float y[TOK][4];
+#pragma unroll
+        for (int i = 0; i < TOK; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[i][c] = 0.f;
+        auto product = [&](const float* l, int stride, const float* m, int count) {  // y += l m, four terms at a time
+#pragma unroll 4
+            for (int e = 0; e < count; e += 4) {
+                float u[TOK][4];
+#pragma unroll
+                for (int i = 0; i < TOK; ++i) load4(l + i * stride + e, u[i]);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float r[4];
+                    load4(m + (e + b) * kCols + 4 * quad, r);
+#pragma unroll
+                    for (int i = 0; i < TOK; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) y[i][c] = fmaf(u[i][b], r[c], y[i][c]);
+                }
+            }
+        };
+        product(in.q[t0], L::row, sm.S[0], DK);
+#pragma unroll
+        for (int i = 0; i < TOK; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[i][c] *= sm.out[t0 + i];
+        __syncthreads();  // P is there, and the state has been read
+        product(sm.P[t0], kTokens + 4, in.v[0], (t0 + TOK + 3) / 4 * 4);
+#pragma unroll
+        for (int i = 0; i < TOK; ++i)
+            if (live && t0 + i < n) store4(o + (from + t0 + i) * os + 4 * quad, y[i]);
+        const float end = sm.end;
+        if (sm.near) {
+#pragma unroll
+            for (int i = 0; i < KR; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) S[i][c] = fmaf(end, S[i][c], S[i][c]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KR; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) S[i][c] *= end;
+        }
+        float w[KR][4];  // summed by itself: the state's bits are rounded once a chunk
+#pragma unroll
+        for (int i = 0; i < KR; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[i][c] = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < kTokens; ++s) {  // (past the end keys and values are zeros)
+            float r[4], ks[KR];
+            load4(&in.v[s][4 * quad], r);
+            const float d = sm.dec[s];
+            if constexpr (KR >= 4) {
+#pragma unroll
+                for (int i = 0; i < KR; i += 4) load4(&in.k[s][row + i], ks + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < KR; ++i) ks[i] = in.k[s][row + i];
+            }
+#pragma unroll
+            for (int i = 0; i < KR; ++i) {
+                const float x = ks[i] * d;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[i][c] = fmaf(x, r[c], w[i][c]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < KR; ++i) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) S[i][c] += w[i][c];
+            store4(&sm.S[row + i][4 * quad], S[i]);
+        }
+    }
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < KR; ++i) store4(st + i * a.Dv, S[i]);
+    }
+}
+
+template <typename TS>
+bool chunk_launch(const Args& a, cudaStream_t s) {
+    const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
+    auto run = [&](auto f, size_t bytes) {
+        if (!tc::set_smem(f, bytes)) return false;
+        f<<<grid, 128, bytes, s>>>(a);
+        note_launch(1);
+        return launch_ok();
+    };
+    return a.Dk == 16   ? run(gla_chunk_kernel<TS, 16>, sizeof(ChunkSmem<16>))
+           : a.Dk == 32 ? run(gla_chunk_kernel<TS, 32>, sizeof(ChunkSmem<32>))
+           : a.Dk == 64 ? run(gla_chunk_kernel<TS, 64>, sizeof(ChunkSmem<64>))
+                        : run(gla_chunk_kernel<TS, 128>, sizeof(ChunkSmem<128>));
+}
+
 template <typename T, typename TS, int NT>
 bool token_launch(const Args& a, cudaStream_t s) {
     const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
@@ -229,7 +467,10 @@ bool token_launch(const Args& a, cudaStream_t s) {
 
 template <typename T, typename TS>
 bool recurrence(const Args& a, cudaStream_t s) {
-    if constexpr (sizeof(T) == 4) return a.max_len <= 1 ? token_launch<T, TS, 1>(a, s) : token_launch<T, TS, 4>(a, s);
+    if constexpr (sizeof(T) == 4) {
+        if (!a.recurrent && a.max_len >= kTokenLen) return chunk_launch<TS>(a, s);
+        return a.max_len <= 1 ? token_launch<T, TS, 1>(a, s) : token_launch<T, TS, 4>(a, s);
+    }
     // Single tokens: the token kernel, but tiles for a bf16 state of 128 rows (256 sequences of 16 heads of 128 x 128: fp32 81
     // us and tiles 93, bf16 53 and tiles 48; 64 of 64 x 64, bf16: 6.5 and tiles 7.1).  Several: tiles (61 sequences, four
     // tokens, 32 heads of 128 x 256, bf16: 48 us, the token kernel 96).

@@ -13,8 +13,8 @@
 //
 // Where the sequences and heads are too few to fill the GPU, long sequences are cut into segments.  A segment's
 // map of the state is S -> e^{sum g} S + dS: a first launch walks the first segment, and the inner ones from zero
-// without outputs; a second one walks the segments after the first, each from the state that it folds together
-// from the first one's end and the maps between.
+// without outputs; gla_compose_kernel carries the states from segment to segment, and a second walk takes the segments
+// after the first from them.
 //
 // Rounding: K, Q and V enter as they are; V~ as the sum of two bf16, or of three (all 24 bits) where the pool is
 // fp32, because its errors reach the state undamped.  S and P are rounded once to bf16: they only enter O,
@@ -268,18 +268,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     else rows([&](int r) { return to_f32(st[int64_t(r) * a.Dv + row]); });
                 } else if (kPart == Part::first) {
                     rows([](int) { return 0.f; });
-                } else {  // the first segment's end, through the maps of those up to this one
-                    const float* e = seg.ends + segment_at(a, seg, si, h, 0) * DK * a.Dv + v0 + row;
+                } else {  // the end of the segment before
+                    const float* e = seg.ends + segment_at(a, seg, si, h, j - 1) * DK * a.Dv + v0 + row;
                     rows([&](int r) { return e[int64_t(r) * a.Dv]; });
-                    for (int i = 1; i < j; ++i) {
-                        const float f = seg.fades[segment_at(a, seg, si, h, i)];
-                        e += int64_t(DK) * a.Dv;
-                        if (live) {
-#pragma unroll
-                            for (int u = 0; u < GC / 2; ++u)
-                                S[u] = fma2(pair(f, f), S[u], pair(e[int64_t(r0 + 2 * u) * a.Dv], e[int64_t(r0 + 2 * u + 1) * a.Dv]));
-                        }
-                    }
                 }
             }
             warp_arrive(&bar.d_ready, lane);
@@ -689,6 +680,27 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
+// The states at the segments' ends, in their place: S_j = e^{sum g} S_{j-1} + dS_j.  Four elements a thread, all segments; the loads of
+// several are under way at once.  (Folded by each walk for itself the last ones would read all the others': 6 us of 67.)
+__global__ void __launch_bounds__(256) gla_compose_kernel(const __grid_constant__ Args a, const Segments seg) {
+    const int64_t at = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4, size = int64_t(a.Dk) * a.Dv;
+    const int h = blockIdx.y, i = blockIdx.z;
+    const Seq sq = sequence(a, i);
+    // the segments that end before the sequence's last one
+    const int all = (sq.len + kChunk - 1) / kChunk, inner = min((all - 1) / seg.chunks, seg.most - 1);
+    if (at >= size || sq.slot < 0 || inner < 2) return;
+    float* e = seg.ends + segment_at(a, seg, i, h, 0) * size + at;
+    const float* f = seg.fades + segment_at(a, seg, i, h, 0);
+    float4 s = *reinterpret_cast<const float4*>(e);
+#pragma unroll 4
+    for (int j = 1; j < inner; ++j) {
+        const float4 d = *reinterpret_cast<const float4*>(e + j * size);
+        const float x = f[j];
+        s.x = fmaf(x, s.x, d.x), s.y = fmaf(x, s.y, d.y), s.z = fmaf(x, s.z, d.z), s.w = fmaf(x, s.w, d.w);
+        *reinterpret_cast<float4*>(e + j * size) = s;
+    }
+}
+
 __global__ void read_flag_kernel(int* out, int clear) {
     *out = g_timeout_flag;
     if (clear) g_timeout_flag = 0;
@@ -740,6 +752,9 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     const dim3 grid(blocks * a.H, a.S, segs - 1);
     const rm_status st = f ? walk(gla_walk_kernel<DK, float, Part::first>, grid) : walk(gla_walk_kernel<DK, __nv_bfloat16, Part::first>, grid);
     if (st != RM_OK) return st;
+    gla_compose_kernel<<<dim3(unsigned((a.Dk * a.Dv + 1023) / 1024), unsigned(a.H), unsigned(a.S)), 256, 0, s>>>(a, seg);
+    note_launch(1);
+    if (!launch_ok()) return fail("launch of the composition", false);
     return f ? walk(gla_walk_kernel<DK, float, Part::rest>, grid) : walk(gla_walk_kernel<DK, __nv_bfloat16, Part::rest>, grid);
 }
 

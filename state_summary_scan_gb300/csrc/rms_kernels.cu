@@ -373,20 +373,19 @@ __global__ void __launch_bounds__(TPB, VPT > 1 || TPB > backward_threads<T, R, k
     }
 }
 
-// dw[e] = sum of the blocks' parts: 32 columns a block, eight threads a column
-__global__ void __launch_bounds__(256) rms_weight_kernel(const float* part, float* dw, int blocks, int n) {
-    __shared__ float s[8][32];
-    const int e = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+// dw[e] = sum of the blocks' parts: 32 columns a block, 32 threads a column
+__global__ void __launch_bounds__(1024) rms_weight_kernel(const float* part, float* dw, int blocks, int n) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
     float x = 0.f;
-    if (e < n)
-        for (int b = g; b < blocks; b += 8) x += part[int64_t(b) * n + e];
-    s[g][threadIdx.x & 31] = x;
-    __syncthreads();
-    if (g == 0 && e < n) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i) x += s[i][threadIdx.x & 31];
-        dw[e] = x;
+    if (e < n) {
+#pragma unroll 4
+        for (int b = g; b < blocks; b += 32) x += part[int64_t(b) * n + e];
     }
+    s[g][lane] = x;
+    __syncthreads();
+    x = warp_sum(s[lane][g]);
+    if (lane == 0 && blockIdx.x * 32 + g < n) dw[blockIdx.x * 32 + g] = x;
 }
 
 // ---------------------------------------------------------------------------
@@ -459,7 +458,7 @@ rm_status backward(const Args& a, float* dw, cudaStream_t s) {
         rms_backward_kernel<T, R, kGate, kDh, kTwo, l(), v(), t()><<<blocks, threads, 0, s>>>(a);
         const rm_status st = launched();
         if (st != RM_OK || dw == nullptr) return st;
-        rms_weight_kernel<<<(a.n + 31) / 32, 256, 0, s>>>(a.part, dw, blocks, a.n);
+        rms_weight_kernel<<<(a.n + 31) / 32, 1024, 0, s>>>(a.part, dw, blocks, a.n);
         return launched();
     });
 }
@@ -624,7 +623,7 @@ rm_status rm_cp_rms_backward(const rm_cp_rms_problem* p, const void* h, const vo
         if (dweight == nullptr) return RM_OK;
         RM_RMS_NEED(dweight, 4);
         begin_launches();
-        rms::rms_weight_kernel<<<(a.n + 31) / 32, 256, 0, s>>>(nullptr, dweight, 0, a.n);
+        rms::rms_weight_kernel<<<(a.n + 31) / 32, 1024, 0, s>>>(nullptr, dweight, 0, a.n);
         return rms::launched();
     }
     RM_RMS_NEED(h, 16);

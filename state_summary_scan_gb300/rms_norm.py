@@ -45,13 +45,13 @@ def _rows(tensors):
 
 
 def _problem(x, residual, weight, gate, gate_first, group, eps, dy=None, dh=None):
-    """(problem, its address) of a call, checked once for each combination of shapes, strides, types and options."""
+    """(problem, its address, shape of its scales), checked once for each combination of shapes, strides, types and options."""
     sig = C.signature
     key = (sig(x), sig(residual), sig(weight), sig(gate), gate_first, group, eps, sig(dy), sig(dh))
     hit = _CACHE.get(key)
     if hit is None:
         p = _checked_problem(x, residual, weight, gate, gate_first, group, eps, dy, dh)
-        hit = (p, ctypes.addressof(p))
+        hit = (p, ctypes.addressof(p), torch.Size((*x.shape[:-1], p.n // group if group else 1)))
         with _CACHE_LOCK:
             _CACHE[key] = hit
             while len(_CACHE) > _CACHE_MAX:
@@ -106,8 +106,8 @@ def _checked_problem(x, residual, weight, gate, gate_first, group, eps, dy, dh) 
                         zero if dy is not None else xs, rs, zs)
 
 
-def _new(x, dtype=None):
-    return torch.empty_like(x, memory_format=torch.contiguous_format, dtype=dtype)
+def _new(x):
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _given(t, like, dtype, name):
@@ -115,16 +115,13 @@ def _given(t, like, dtype, name):
         raise ValueError(f"{name} must be contiguous, {dtype}, and have the shape and device of x")
 
 
-def _sum_out(x, residual, h):
-    """Where the sum goes: h as given (or the residual itself), a new tensor, or x where there is no sum."""
-    if residual is None:
-        if h is not None:
+def _check_given(x, residual, h, out, dtype):
+    if h is not None:
+        if residual is None:
             raise ValueError("h needs a residual")
-        return x
-    if h is None:
-        return _new(residual)
-    _given(h, residual, residual.dtype, "h")
-    return h
+        _given(h, residual, residual.dtype, "h")
+    if out is not None:
+        _given(out, x, dtype, "out")
 
 
 def rms_norm(x, weight=None, residual=None, gate=None, gate_first: bool = False, eps: float = 1e-6, out=None, h=None,
@@ -138,17 +135,18 @@ def rms_norm(x, weight=None, residual=None, gate=None, gate_first: bool = False,
     [n] fp32.  x, residual and gate may be slices of a fused projection (adjacent elements, 16-byte strides, rows
     evenly spaced in at most two dimensions); y and h are contiguous, and y may go into a contiguous x (out=x).
     n is a multiple of 8 up to 32768."""
-    p, at = _problem(x, residual, weight, gate, gate_first, 0, eps)
+    _, at, _ = _problem(x, residual, weight, gate, gate_first, 0, eps)
+    device = x.get_device()
+    if out is not None or h is not None:
+        _check_given(x, residual, h, out, x.dtype)
+        C.written([t for t in (out, h) if t is not None])
 
     def buffers():
-        return (_new(x) if out is None else out), _sum_out(x, residual, h)
+        return _new(x) if out is None else out, x if residual is None else _new(residual) if h is None else h
 
-    if out is not None:
-        _given(out, x, x.dtype, "out")
-    y, total = C.on_stream(buffers, stream, x.get_device())
-    C.written([t for t in (out, h) if t is not None])
+    y, total = buffers() if stream is None else C.on_stream(buffers, stream, device)
     if x.numel():
-        C.rm_cp_rms_forward(at, x, residual, gate, weight, total if residual is not None else None, y, C._raw_stream(stream, x.get_device()))
+        C.rm_cp_rms_forward(at, x, residual, gate, weight, total if residual is not None else None, y, C._raw_stream(stream, device))
     return y, total
 
 
@@ -158,24 +156,24 @@ def rms_norm_quant(x, weight=None, residual=None, gate=None, gate_first: bool = 
 
     A scale is max |y| / 448 of `group` adjacent elements (32, 64 or 128; 0: of the row), at least 2^-126; y is not
     rounded before it is divided by it.  out: (y8, scales) to write into.  A row with a NaN has NaN scales."""
-    p, at = _problem(x, residual, weight, gate, gate_first, group, eps)
-    groups = p.n // group if group else 1
+    _, at, scale_shape = _problem(x, residual, weight, gate, gate_first, group, eps)
+    device = x.get_device()
+    if out is not None or h is not None:
+        _check_given(x, residual, h, None if out is None else out[0], torch.float8_e4m3fn)
+        if out is not None and (out[1].shape != scale_shape or out[1].dtype != torch.float32 or out[1].device != x.device or not out[1].is_contiguous()):
+            raise ValueError(f"out[1] must be {list(scale_shape)} fp32, contiguous, on the device of x")
+        C.written([t for t in (*(out or ()), h) if t is not None])
 
     def buffers():
-        if out is None:
-            y8 = _new(x, torch.float8_e4m3fn)
-            return y8, torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=x.device), _sum_out(x, residual, h)
-        return out[0], out[1], _sum_out(x, residual, h)
+        total = x if residual is None else _new(residual) if h is None else h
+        if out is not None:
+            return out[0], out[1], total
+        return (torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format),
+                torch.empty(scale_shape, dtype=torch.float32, device=x.device), total)
 
-    if out is not None:
-        _given(out[0], x, torch.float8_e4m3fn, "out[0]")
-        if tuple(out[1].shape) != (*x.shape[:-1], groups) or out[1].dtype != torch.float32 or out[1].device != x.device or not out[1].is_contiguous():
-            raise ValueError(f"out[1] must be [..., {groups}] fp32, contiguous, on the device of x")
-    y8, scales, total = C.on_stream(buffers, stream, x.get_device())
-    C.written([t for t in (*(out or ()), h) if t is not None])
+    y8, scales, total = buffers() if stream is None else C.on_stream(buffers, stream, device)
     if x.numel():
-        C.rm_cp_rms_quant(at, x, residual, gate, weight, total if residual is not None else None, y8, scales,
-                          C._raw_stream(stream, x.get_device()))
+        C.rm_cp_rms_quant(at, x, residual, gate, weight, total if residual is not None else None, y8, scales, C._raw_stream(stream, device))
     return y8, scales, total
 
 
@@ -184,7 +182,8 @@ def rms_norm_backward(h, dy, weight=None, dh=None, gate=None, gate_first: bool =
     no residual).  dh: the gradient that comes down the residual stream, or None.  dx has the type of dy; dresidual
     is the same values in the type of h (dx itself where the types are equal); dgate (None without a gate) has the
     type of dy; dweight is [n] fp32, None without the weight.  dy and dh are contiguous."""
-    p, at = _problem(h, None, weight, gate, gate_first, 0, eps, dy, dh)
+    p, at, _ = _problem(h, None, weight, gate, gate_first, 0, eps, dy, dh)
+    device = h.get_device()
     size = C.rm_cp_rms_workspace_size(p) if weight is not None else 0
 
     def buffers():
@@ -193,9 +192,9 @@ def rms_norm_backward(h, dy, weight=None, dh=None, gate=None, gate_first: bool =
                 None if weight is None else torch.empty_like(weight),
                 torch.empty(size, dtype=torch.uint8, device=h.device) if size else None)
 
-    dx, dresidual, dgate, dweight, ws = C.on_stream(buffers, stream, h.get_device())
+    dx, dresidual, dgate, dweight, ws = buffers() if stream is None else C.on_stream(buffers, stream, device)
     if h.numel() or weight is not None:
-        C.rm_cp_rms_backward(at, h, gate, weight, dy, dh, dx, dresidual, dgate, dweight, ws, C._raw_stream(stream, h.get_device()))
+        C.rm_cp_rms_backward(at, h, gate, weight, dy, dh, dx, dresidual, dgate, dweight, ws, C._raw_stream(stream, device))
     return dx, dresidual, dgate, dweight
 
 
