@@ -635,8 +635,21 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * whatever the token.
  *   ws: rm_gla_state_workspace_size bytes, for problems of these sizes or
  *   smaller num_seqs, num_tokens and max_len; not shared by calls that overlap.
- * rm_gla_state_path: 0 when the call runs as a token recurrence in fp32,
- * -1 for a problem it rejects.
+ * rm_gla_state_path: 1 when the call runs in chunks of 64 tokens on the
+ * tensor cores (dtype bf16, Dk 64 or 128, max_len and num_tokens >= 32, or 64
+ * where Dk is 64 and Dv below 128, recurrent 0), 0 when it runs in fp32
+ * arithmetic (bf16 tokens and single ones one after another; fp32 tokens in
+ * chunks of 32 with max_len >= 20), -1 for a problem it rejects.
+ * recurrent != 0 keeps every call a token recurrence.  In
+ * chunks on the tensor cores the scores and the state are rounded to bf16
+ * where they enter an output: outputs are off by up to one and a half times
+ * their own rounding in norm.  The state itself is kept to fp32's precision
+ * in an fp32 pool, and in a bf16 pool to 2^-16 of what is added to it beside
+ * the pool's own rounding, once a call (with max_len <= 4 once every four
+ * tokens).  A log-gate below -110 is taken as -110 there, and one above 110 as
+ * 110.  A NaN or an infinity in a token reaches the outputs of all tokens of
+ * its chunk (in the recurrence: its own and those after it), never another
+ * sequence.
  */
 int32_t rm_gla_state_path(const rm_gdr_state_problem* p);
 size_t rm_gla_state_workspace_size(const rm_gdr_state_problem* p);

@@ -40,7 +40,7 @@ using gds::zero_rows;
 namespace {
 
 constexpr float kForget = 110.f;             // e^-110 is 0 in fp32: lower gates are raised to -110
-constexpr int kMostSegments = 16;
+constexpr int kMostSegments = 32;
 constexpr int kMostStates = 320;             // of segments: see tc_workspace_bytes()
 
 // A chunk's gates in shared memory, in floats.  Decays between tokens of one block of 16 are formed from their
@@ -713,14 +713,21 @@ rm_status fail(const char* what, bool map) {
     return api_fail(RM_ERR_CUDA, msg);
 }
 
-// Segments of the longest sequence (1: not cut), and their chunks: as many as keep each launch's CTAs on the GPU's
-// 152 multiprocessors at once, of four chunks or more.
+// Segments of the longest sequence (1: not cut), and their chunks: as many as keep each walk's CTAs on the GPU's 152
+// multiprocessors at once, of two chunks or more.  A chunk takes some 1.45 us (64 x 64: 1.1), two more launches and the
+// states between them some 13; with n segments the chain is two walks of 1 / n of the chunks.  us in a CUDA graph, whole / cut:
+//     tokens                          512          1024         2048         8192
+//     16 heads of 128 x 128           18.9 / 23.0  30.8 / 25.9  53.8 / 32.5  192 / 60
+//     32 heads, or two prompts of 16  19.6 / 24.8  31.4 / 32.1  54.6 / 41.0  193 / 97
+//     48 heads (4 segments)           20.1 / 27.2  31.9 / 35.1  54.9 / 46.6  193 / 117
+//     8 heads of 128 x 256            18.5 / 22.9  30.5 / 25.5  53.8 / 31.7  194 / 58
+//     4 heads of 64 x 64              13.9 / 16.2  22.8 / 17.3  40.5 / 20.0  147 / 35
 int segments(const Args& a, int* chunks) {
     const int all = (a.max_len + kChunk - 1) / kChunk, blocks = (a.Dv + 127) / 128;
     int n = 1 + int(152 / (int64_t(a.H) * blocks * a.S));
     n = n < kMostSegments ? n : kMostSegments;
-    n = n < all / 4 ? n : all / 4;
-    if (n < 4) return 1;
+    n = n < all / 2 ? n : all / 2;
+    if (int64_t(all) * (n - 2) <= 9 * n) return 1;
     *chunks = (all + n - 1) / n;
     return (all + *chunks - 1) / *chunks;
 }
@@ -761,11 +768,11 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
 }  // namespace
 
 bool tc_supports(const Args& a, rm_dtype dt) {
-    return !a.recurrent && dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= kChunkedLen && a.H <= 65535;
+    return !a.recurrent && dt == RM_BF16 && (a.Dk == 64 || a.Dk == 128) && a.max_len >= chunked_len(a) && a.H <= 65535;
 }
 
-// A smaller problem may be cut into more segments than this one, so the bound is that of all of them: with n >= 4
-// segments heads x sequences x (n - 1) <= 152, so heads x sequences x n <= 152 + 152 / 3 = 202.
+// A smaller problem may be cut into more segments than this one, so the bound is that of all of them: with n >= 3
+// segments heads x sequences x (n - 1) <= 152, so heads x sequences x n <= 152 + 152 / 2 = 228.
 size_t tc_workspace_bytes(const Args& a) { return size_t(kMostStates) * (size_t(a.Dk) * a.Dv + 1) * sizeof(float) + 16; }
 
 rm_status tc_launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {

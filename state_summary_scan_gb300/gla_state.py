@@ -36,7 +36,10 @@ def make_gla_state_plan(max_seqs: int, max_tokens: int, H: int, Dk: int, Dv: int
                         state_dtype=torch.float32, device="cuda", recurrent: bool = False) -> GlaStatePlan:
     """Plan of calls with up to max_seqs sequences, max_tokens tokens in all and max_len tokens a
     sequence (default max_tokens).  qk_heads > 0: q and k have that many heads, each shared by
-    H / qk_heads consecutive heads."""
+    H / qk_heads consecutive heads.  bf16 calls of 32 tokens a sequence or more (Dk 128, or Dv 128 and more; 64 with Dk 64 and
+    smaller Dv) run in chunks on the tensor cores, which rounds scores and states to bf16 where they enter an output: outputs
+    are off by up to one and a half times their own rounding; the state keeps the pool's precision.  recurrent=True keeps
+    every call a token recurrence, whatever the lengths of its batch, and slower for prompts."""
     if dtype not in _DTYPES or state_dtype not in _DTYPES:
         raise ValueError("dtype and state_dtype must be fp32 or bf16")
     if scale is None:

@@ -109,7 +109,7 @@ def test_ragged_prompts(H, Hqk, Dk, Dv, gate, dtype, state_dtype):
     x, slots, fresh, cu = make(LENS, H, Hqk, Dk, Dv, dtype, state_dtype, gate)
     o, state, plan = prefill(x, slots, fresh, cu, LENS, H, Hqk, Dk, Dv)
     chunks = C.rm_gla_state_path(plan.c) == 1
-    assert chunks == (dtype == BF and Dk >= 64)
+    assert chunks == (dtype == BF and Dk >= 64)  # (the longest has 200 tokens)
     check(o, state, reference(x, slots, fresh, cu, Dk), LENS, Dk, dtype, state_dtype, chunks)
 
 
