@@ -7,7 +7,7 @@ Layers:
   _capi                    ctypes binding, one Python function per C call
   api                      buffer allocation, call sequence, autograd adapter
   qk_rope, gdr_state,      the operators around the mixer: per-head norm with rotation, the gated
-  gla_state, rms_norm,     delta rule and linear attention on a pool of states (prefill, decoding),
+  gla_state, row_norm,     delta rule and linear attention on a pool of states (prefill, decoding),
   clip                     norms of rows with residual, gate and 8-bit outputs, gradient clipping
   workloads                seeded synthetic inputs (no method arithmetic)
 """

@@ -419,7 +419,7 @@ def rm_gdr_backward_apply(p, q, k, v, g, beta, dO, dS_out, dk, dv, dg, dbeta, ws
 
 # ----------------------------------------------------------------- norms and rotation, carried states, clipping
 # These calls take strides in their problem, so tensors need only have adjacent head elements;
-# the callers in qk_rope.py, gdr_state.py, gla_state.py, rms_norm.py and clip.py check shapes, types and strides.  Pointers are
+# the callers in qk_rope.py, gdr_state.py, gla_state.py, row_norm.py and clip.py check shapes, types and strides.  Pointers are
 # passed as addresses and problems as the address of their struct: a decoding step is a few
 # microseconds long, and so must its call be.
 

@@ -454,4 +454,4 @@ from .gla_state import (GlaStatePlan, gla_decode, gla_prefill, make_gla_state,  
                         make_gla_state_plan)
 from .qk_rope import (QkNormRope, make_rope_table, qk_norm_rope, qk_norm_rope_backward,  # noqa: E402,F401
                       qk_norm_rope_train)
-from .rms_norm import RmsNorm, rms_norm, rms_norm_backward, rms_norm_quant, rms_norm_train  # noqa: E402,F401
+from .row_norm import RmsNorm, rms_norm, rms_norm_backward, rms_norm_quant, rms_norm_train  # noqa: E402,F401
