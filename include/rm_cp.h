@@ -633,9 +633,9 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * tokens, sequences, slots, fresh, state, strides, sizes and outputs are as
  * in rm_gdr_state_forward; g_stride 0: g is [H], one log-decay for each head
  * whatever the token.
- *   ws: rm_gla_state_workspace_size bytes, for problems of these sizes or
+ *   ws: rm_cp_gla_state_workspace_size bytes, for problems of these sizes or
  *   smaller num_seqs, num_tokens and max_len; not shared by calls that overlap.
- * rm_gla_state_path: 1 when the call runs in chunks of 64 tokens on the
+ * rm_cp_gla_state_path: 1 when the call runs in chunks of 64 tokens on the
  * tensor cores (dtype bf16, Dk 64 or 128, max_len and num_tokens >= 32, or 64
  * where Dk is 64 and Dv below 128, recurrent 0), 0 when it runs in fp32
  * arithmetic (bf16 tokens and single ones one after another; fp32 tokens in
@@ -651,9 +651,9 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * its chunk (in the recurrence: its own and those after it), never another
  * sequence.
  */
-int32_t rm_gla_state_path(const rm_gdr_state_problem* p);
-size_t rm_gla_state_workspace_size(const rm_gdr_state_problem* p);
-rm_status rm_gla_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k,
+int32_t rm_cp_gla_state_path(const rm_gdr_state_problem* p);
+size_t rm_cp_gla_state_workspace_size(const rm_gdr_state_problem* p);
+rm_status rm_cp_gla_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k,
                                const void* v, const float* g, const int32_t* cu_seqlens,
                                const int32_t* slots, const uint8_t* fresh, void* state, void* o,
                                void* ws, rm_stream_t stream);

@@ -36,7 +36,7 @@ EXPORTS = (
     "rm_cp_qkr_workspace_size", "rm_cp_qkr_forward", "rm_cp_qkr_backward",
     "rm_gdr_state_path", "rm_gdr_state_workspace_size", "rm_gdr_state_forward",
     "rm_cp_clip_workspace_size", "rm_cp_clip_grad_norm",
-    "rm_gla_state_path", "rm_gla_state_workspace_size", "rm_gla_state_forward",
+    "rm_cp_gla_state_path", "rm_cp_gla_state_workspace_size", "rm_cp_gla_state_forward",
     "rm_cp_rms_workspace_size", "rm_cp_rms_forward", "rm_cp_rms_quant", "rm_cp_rms_backward",
 )
 
@@ -145,9 +145,9 @@ _SIGS = {
     "rm_gdr_state_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GdrStateProblem)]),
     "rm_gdr_state_forward": (_S, [ctypes.POINTER(GdrStateProblem)] + [_P] * 12),
     "rm_cp_clip_workspace_size": (ctypes.c_size_t, [ctypes.c_int32]),
-    "rm_gla_state_path": (ctypes.c_int32, [ctypes.POINTER(GdrStateProblem)]),
-    "rm_gla_state_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GdrStateProblem)]),
-    "rm_gla_state_forward": (_S, [ctypes.POINTER(GdrStateProblem)] + [_P] * 11),
+    "rm_cp_gla_state_path": (ctypes.c_int32, [ctypes.POINTER(GdrStateProblem)]),
+    "rm_cp_gla_state_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(GdrStateProblem)]),
+    "rm_cp_gla_state_forward": (_S, [ctypes.POINTER(GdrStateProblem)] + [_P] * 11),
     "rm_cp_rms_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(RmsProblem)]),
     "rm_cp_rms_forward": (_S, [ctypes.POINTER(RmsProblem)] + [_P] * 7),
     "rm_cp_rms_quant": (_S, [ctypes.POINTER(RmsProblem)] + [_P] * 8),
@@ -177,7 +177,7 @@ def load(build_if_needed: bool = True):
                 fn = getattr(so, name)
                 fn.restype = res
                 fn.argtypes = args
-            for name in ("rm_cp_qkr_forward", "rm_cp_qkr_backward", "rm_gdr_state_forward", "rm_gla_state_forward",
+            for name in ("rm_cp_qkr_forward", "rm_cp_qkr_backward", "rm_gdr_state_forward", "rm_cp_gla_state_forward",
                          "rm_cp_rms_forward", "rm_cp_rms_quant", "rm_cp_rms_backward"):
                 fn = so[name]  # a function object of its own, taking the problem's address
                 fn.restype, fn.argtypes = _S, [_P] * len(_SIGS[name][1])
@@ -515,19 +515,19 @@ def rm_gdr_state_forward(p: int, q, k, v, g, beta, cu_seqlens, slots, fresh, sta
         _check(status)
 
 
-def rm_gla_state_path(p: GdrStateProblem) -> int:
-    return int(load().rm_gla_state_path(ctypes.byref(p)))
+def rm_cp_gla_state_path(p: GdrStateProblem) -> int:
+    return int(load().rm_cp_gla_state_path(ctypes.byref(p)))
 
 
-def rm_gla_state_workspace_size(p: GdrStateProblem) -> int:
-    return int(load().rm_gla_state_workspace_size(ctypes.byref(p)))
+def rm_cp_gla_state_workspace_size(p: GdrStateProblem) -> int:
+    return int(load().rm_cp_gla_state_workspace_size(ctypes.byref(p)))
 
 
-def rm_gla_state_forward(p: int, q, k, v, g, cu_seqlens, slots, fresh, state, o, ws, stream):
+def rm_cp_gla_state_forward(p: int, q, k, v, g, cu_seqlens, slots, fresh, state, o, ws, stream):
     """p: the address of a GdrStateProblem."""
     if _lib is None:
         load()
-    fn = _on_device(_by_address["rm_gla_state_forward"], q.get_device())
+    fn = _on_device(_by_address["rm_cp_gla_state_forward"], q.get_device())
     status = fn(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(cu_seqlens), _addr(slots), _addr(fresh),
                 state.data_ptr(), o.data_ptr(), ws.data_ptr(), stream)
     if status:

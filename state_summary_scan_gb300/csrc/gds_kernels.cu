@@ -471,7 +471,7 @@ __device__ __forceinline__ void store_rows(float* p, int b, int Dv, const float 
 }
 
 //
-// Without kDelta the same for linear attention, S <- e^g S + k v^T (rm_gla_state_forward): d is v itself.
+// Without kDelta the same for linear attention, S <- e^g S + k v^T (rm_cp_gla_state_forward): d is v itself.
 template <typename TS, int DK, int W, bool kPacked, bool kDelta = true>
 __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant__ Args a) {
     constexpr int NP = DK / 8, kRun = Rows<DK>::kRun;
@@ -534,6 +534,17 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
             mma(kk, rows, kq[2 * s], kq[2 * s + 1]);
         }
         const float al_t = expf(al1), be_t = be1;
+        // linear attention in an fp32 state: its decay over the four, near 1 as its distance from 1 (e^g itself has lost the
+        // bits that many tokens of a slow decay add up; in a bf16 state it would be lost anyway)
+        constexpr bool kFade = !kDelta && sizeof(TS) == 4;
+        float fade = 0.f;
+        bool near = false;
+        if constexpr (kFade) {
+            float sum = al1 + __shfl_xor_sync(kAllLanes, al1, 1);
+            sum += __shfl_xor_sync(kAllLanes, sum, 2);
+            near = sum > -0.7f && sum < 0.7f;
+            fade = near ? expm1f(sum) : expf(sum);
+        }
         uint64_t vf[4][W];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -604,7 +615,7 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
         uint32_t ku[2][NP];
 #pragma unroll
         for (int e = 0; e < 2; ++e) load_pairs<DK>(up_row + (t0 + e) * a.ks[0], i0 + e < n, ku[e]);
-        const uint64_t al = pair(total, total);
+        const uint64_t al = kFade ? pair(fade, fade) : pair(total, total);
 #pragma unroll
         for (int b = 0; b < NP; ++b) {
             const uint32_t kb = __byte_perm(ku[0][b], ku[1][b], half);
@@ -612,11 +623,25 @@ __global__ void __launch_bounds__(kTpb, 3) gds_tile_kernel(const __grid_constant
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 uint32_t x[4];
-                unpair(mul2(al, S.at(w, b, 0)), x[0], x[1]);
-                unpair(mul2(al, S.at(w, b, 1)), x[2], x[3]);
+                if constexpr (!kFade) {
+                    unpair(mul2(al, S.at(w, b, 0)), x[0], x[1]);
+                    unpair(mul2(al, S.at(w, b, 1)), x[2], x[3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) c[w][i] = __uint_as_float(x[i]);
-                mma(c[w], da[w], kb, kb);
+                    for (int i = 0; i < 4; ++i) c[w][i] = __uint_as_float(x[i]);
+                    mma(c[w], da[w], kb, kb);
+                } else {  // the product by itself: its unit cuts off what it adds to, and the state's sum is rounded here
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[w][i] = 0.f;
+                    mma(c[w], da[w], kb, kb);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint64_t y = fma2(al, S.at(w, b, e), pair(c[w][2 * e], c[w][2 * e + 1]));
+                        if (near) y = add2(y, S.at(w, b, e));
+                        unpair(y, x[2 * e], x[2 * e + 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) c[w][i] = __uint_as_float(x[i]);
+                }
                 if constexpr (!kPacked) S.x[w][b][0] = pair(c[w][0], c[w][1]), S.x[w][b][1] = pair(c[w][2], c[w][3]);
             }
             if (kPacked && live) store_rows<DK, W>(st, b, a.Dv, c);

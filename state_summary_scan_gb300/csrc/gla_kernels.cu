@@ -1,5 +1,5 @@
 // gla_kernels.cu -- linear attention with a decay for each head and a carried state as a token
-// recurrence (rm_gla_state_forward): decoding a few tokens for each of many sequences, and every
+// recurrence (rm_cp_gla_state_forward): decoding a few tokens for each of many sequences, and every
 // shape that the chunked form on the tensor cores does not take.  (Several bf16 tokens go four at a
 // time through the warp's matrix instructions: gds_kernels.cu.)
 //
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(threads_of(DK), NT == 1 ? 8 : 4) gla_token_ker
 }
 
 // ---------------------------------------------------------------------------
-// fp32 prompts in chunks of 32 tokens.  With b_t the running sum of a chunk's gates and S the state before it:
+// Prompts in chunks of 32 tokens in fp32 arithmetic: fp32 tokens, and bf16 ones of shapes that the tensor cores do not take.  With b_t the running sum of a chunk's gates and S the state before it:
 //     o_t = scale (e^{b_t} S^T q_t + sum_{s <= t} e^{b_t - b_s} (q_t.k_s) v_s),   S <- e^{b_31} S + sum_s e^{b_31 - b_s} k_s v_s^T
 // A CTA has 32 columns of a sequence's head.  The products are plain fp32 multiply-adds on tiles in shared memory, two tokens x
 // four columns (of scores, of outputs) or Dk / 16 rows x four columns (of the state) a thread, the next chunk's tokens on
@@ -248,7 +248,7 @@ __device__ __forceinline__ void copy16(float* to, const float* from, bool live) 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)), "l"(from), "r"(live ? 16 : 0) : "memory");
 }
 
-template <typename TS, int DK>
+template <typename T, typename TS, int DK>
 __global__ void __launch_bounds__(128) gla_chunk_kernel(const __grid_constant__ Args a) {
     // tokens of a thread (one, and 256 threads: 2048 tokens of 16 heads of 128 x 128 456 us for 382, 8 prompts of 300 of 64 x
     // 64 82 for 60), and rows
@@ -262,36 +262,80 @@ __global__ void __launch_bounds__(128) gla_chunk_kernel(const __grid_constant__ 
     const bool live = col < a.Dv;  // Dv is a multiple of 8, a thread's columns of 4
     const int cols = min(a.Dv - c0, kCols);
     const Seq sq = sequence(a, blockIdx.y);
-    zero_others(a, blockIdx.y, sq, static_cast<float*>(a.o) + int64_t(h) * a.Dv + c0, cols, tid, TPB);
+    zero_others(a, blockIdx.y, sq, static_cast<T*>(a.o) + int64_t(h) * a.Dv + c0, cols, tid, TPB);
     if (sq.len <= 0 && !(sq.fresh && sq.slot >= 0)) return;  // a fresh empty sequence leaves a zero state
-    float* o = static_cast<float*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + c0;
+    T* o = static_cast<T*>(a.o) + (int64_t(sq.begin) * a.H + h) * a.Dv + c0;
     const int64_t os = int64_t(a.H) * a.Dv;
     if (sq.slot < 0) {  // padding
         zero_outputs(o, os, sq.len, cols, tid, TPB);
         return;
     }
     const int hk = h / a.hdiv;
-    const float* q = static_cast<const float*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
-    const float* k = static_cast<const float*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1];
-    const float* v = static_cast<const float*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + c0;
+    const T* q = static_cast<const T*>(a.q) + sq.begin * a.qs[0] + hk * a.qs[1];
+    const T* k = static_cast<const T*>(a.k) + sq.begin * a.ks[0] + hk * a.ks[1];
+    const T* v = static_cast<const T*>(a.v) + sq.begin * a.vs[0] + h * a.vs[1] + c0;
     const float* g = a.g + sq.begin * a.gs + h;
-    auto fetch = [&](int from) {  // a chunk's tokens; those past the end are zeros
-        typename L::In& to = sm.in[(from / kTokens) & 1];
-        for (int u = tid; u < kTokens * (DK / 4); u += TPB) {
-            const int t = u / (DK / 4), e = u % (DK / 4) * 4;
-            const bool there = from + t < sq.len;
-            copy16(&to.q[t][e], q + (there ? from + t : 0) * a.qs[0] + e, there);
-            copy16(&to.k[t][e], k + (there ? from + t : 0) * a.ks[0] + e, there);
+    // A chunk's tokens; those past the end are zeros.  fp32 is copied into shared memory as it is; bf16 is read into
+    // registers, and put there as fp32 when the chunk before has been taken.
+    constexpr bool kCopy = sizeof(T) == 4;
+    constexpr int NQ = kTokens * DK / 8 / TPB > 0 ? kTokens * DK / 8 / TPB : 1;  // units of eight of q, and of k, a thread
+    Raw<T, 8> raw[kCopy ? 1 : 2 * NQ + 1];
+    auto fetch = [&](int from) {
+        if constexpr (kCopy) {
+            typename L::In& to = sm.in[(from / kTokens) & 1];
+            for (int u = tid; u < kTokens * (DK / 4); u += TPB) {
+                const int t = u / (DK / 4), e = u % (DK / 4) * 4;
+                const bool there = from + t < sq.len;
+                copy16(&to.q[t][e], q + (there ? from + t : 0) * a.qs[0] + e, there);
+                copy16(&to.k[t][e], k + (there ? from + t : 0) * a.ks[0] + e, there);
+            }
+            for (int u = tid; u < kTokens * (kCols / 4); u += TPB) {
+                const int t = u / (kCols / 4), e = u % (kCols / 4) * 4;
+                const bool there = from + t < sq.len && e < cols;
+                copy16(&to.v[t][e], v + (there ? (from + t) * a.vs[0] + e : 0), there);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i <= 2 * NQ; ++i)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) raw[i].x[w] = 0;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int u = tid + i * TPB, t = u / (DK / 8), e = u % (DK / 8) * 8;
+                if (t < kTokens && from + t < sq.len) {
+                    raw[i].load(q + (from + t) * a.qs[0] + e);
+                    raw[NQ + i].load(k + (from + t) * a.ks[0] + e);
+                }
+            }
+            const int t = tid / (kCols / 8), e = tid % (kCols / 8) * 8;  // (32 x 32 values: one unit a thread)
+            if (from + t < sq.len && e < cols) raw[2 * NQ].load(v + (from + t) * a.vs[0] + e);
         }
-        for (int u = tid; u < kTokens * (kCols / 4); u += TPB) {
-            const int t = u / (kCols / 4), e = u % (kCols / 4) * 4;
-            const bool there = from + t < sq.len && e < cols;
-            copy16(&to.v[t][e], v + (there ? (from + t) * a.vs[0] + e : 0), there);
+    };
+    auto place = [&](int from) {  // what fetch() read
+        if constexpr (!kCopy) {
+            typename L::In& to = sm.in[(from / kTokens) & 1];
+            auto put = [](float* p, const Raw<T, 8>& r) {
+#pragma unroll
+                for (int w = 0; w < 4; w += 2)
+                    *reinterpret_cast<ulonglong2*>(p + 2 * w) = make_ulonglong2(r.two(w), r.two(w + 1));
+            };
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int u = tid + i * TPB, t = u / (DK / 8), e = u % (DK / 8) * 8;
+                if (t < kTokens) {
+                    put(&to.q[t][e], raw[i]);
+                    put(&to.k[t][e], raw[NQ + i]);
+                }
+            }
+            put(&to.v[tid / (kCols / 8)][tid % (kCols / 8) * 8], raw[2 * NQ]);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto gate = [&](int from) { return warp == 0 && from + lane < sq.len ? __ldg(g + (from + lane) * a.gs) : 0.f; };
-    if (sq.len > 0) fetch(0);
+    if (sq.len > 0) {
+        fetch(0);
+        place(0);
+    }
     float next = gate(0);
     TS* st = static_cast<TS*>(a.state) + ((int64_t(sq.slot) * a.H + h) * DK + row) * a.Dv + col;
     float S[KR][4];
@@ -305,7 +349,7 @@ __global__ void __launch_bounds__(128) gla_chunk_kernel(const __grid_constant__ 
     for (int from = 0; from < sq.len; from += kTokens) {
         const typename L::In& in = sm.in[(from / kTokens) & 1];
         const int n = min(sq.len - from, kTokens);
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (kCopy) asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();  // the tokens and the state are there, the other tokens and P have been used
         if (from + kTokens < sq.len) fetch(from + kTokens);
         if (warp == 0) {  // the gates: a token a lane, sums held as two floats
@@ -389,6 +433,7 @@ __global__ void __launch_bounds__(128) gla_chunk_kernel(const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < TOK; ++i)
             if (live && t0 + i < n) store4(o + (from + t0 + i) * os + 4 * quad, y[i]);
+        if (from + kTokens < sq.len) place(from + kTokens);
         const float end = sm.end;
         if (sm.near) {
 #pragma unroll
@@ -438,7 +483,7 @@ __global__ void __launch_bounds__(128) gla_chunk_kernel(const __grid_constant__ 
     }
 }
 
-template <typename TS>
+template <typename T, typename TS>
 bool chunk_launch(const Args& a, cudaStream_t s) {
     const dim3 grid(unsigned((a.Dv + kCols - 1) / kCols * a.H), unsigned(a.S));
     auto run = [&](auto f, size_t bytes) {
@@ -447,10 +492,10 @@ bool chunk_launch(const Args& a, cudaStream_t s) {
         note_launch(1);
         return launch_ok();
     };
-    return a.Dk == 16   ? run(gla_chunk_kernel<TS, 16>, sizeof(ChunkSmem<16>))
-           : a.Dk == 32 ? run(gla_chunk_kernel<TS, 32>, sizeof(ChunkSmem<32>))
-           : a.Dk == 64 ? run(gla_chunk_kernel<TS, 64>, sizeof(ChunkSmem<64>))
-                        : run(gla_chunk_kernel<TS, 128>, sizeof(ChunkSmem<128>));
+    return a.Dk == 16   ? run(gla_chunk_kernel<T, TS, 16>, sizeof(ChunkSmem<16>))
+           : a.Dk == 32 ? run(gla_chunk_kernel<T, TS, 32>, sizeof(ChunkSmem<32>))
+           : a.Dk == 64 ? run(gla_chunk_kernel<T, TS, 64>, sizeof(ChunkSmem<64>))
+                        : run(gla_chunk_kernel<T, TS, 128>, sizeof(ChunkSmem<128>));
 }
 
 template <typename T, typename TS, int NT>
@@ -467,15 +512,17 @@ bool token_launch(const Args& a, cudaStream_t s) {
 
 template <typename T, typename TS>
 bool recurrence(const Args& a, cudaStream_t s) {
+    // (bf16 with 64 rows and more is in chunks on the tensor cores from 32 or 64 tokens)
+    if (!a.recurrent && a.max_len >= kTokenLen && (sizeof(T) == 4 || a.Dk < 64)) return chunk_launch<T, TS>(a, s);
     if constexpr (sizeof(T) == 4) {
-        if (!a.recurrent && a.max_len >= kTokenLen) return chunk_launch<TS>(a, s);
         return a.max_len <= 1 ? token_launch<T, TS, 1>(a, s) : token_launch<T, TS, 4>(a, s);
+    } else {
+        // Single tokens: the token kernel, but tiles for a bf16 state of 128 rows (256 sequences of 16 heads of 128 x 128: fp32
+        // 81 us and tiles 93, bf16 53 and tiles 48; 64 of 64 x 64, bf16: 6.5 and tiles 7.1).  Several: tiles (61 sequences,
+        // four tokens, 32 heads of 128 x 256, bf16 state: 48 us, the token kernel 96; fp32 state: 108 us).
+        const bool tiles = a.max_len > 1 || (sizeof(TS) == 2 && a.Dk == 128);
+        return tiles ? gds::plain_tiles(a, sizeof(TS) == 4 ? RM_F32 : RM_BF16, s) : token_launch<T, TS, 1>(a, s);
     }
-    // Single tokens: the token kernel, but tiles for a bf16 state of 128 rows (256 sequences of 16 heads of 128 x 128: fp32 81
-    // us and tiles 93, bf16 53 and tiles 48; 64 of 64 x 64, bf16: 6.5 and tiles 7.1).  Several: tiles (61 sequences, four
-    // tokens, 32 heads of 128 x 256, bf16: 48 us, the token kernel 96).
-    const bool tiles = a.max_len > 1 || (sizeof(TS) == 2 && a.Dk == 128);
-    return tiles ? gds::plain_tiles(a, sizeof(TS) == 4 ? RM_F32 : RM_BF16, s) : token_launch<T, TS, 1>(a, s);
 }
 
 }  // namespace
@@ -495,19 +542,19 @@ bool recurrence(const Args& a, cudaStream_t s) {
 
 extern "C" {
 
-int32_t rm_gla_state_path(const rm_gdr_state_problem* p) {
+int32_t rm_cp_gla_state_path(const rm_gdr_state_problem* p) {
     rmcp::gla::Args a{};
     if (rmcp::gds::check(p, &a) != RM_OK) return -1;
     return rmcp::gla::tc_supports(a, p->dtype) ? 1 : 0;
 }
 
-size_t rm_gla_state_workspace_size(const rm_gdr_state_problem* p) {
+size_t rm_cp_gla_state_workspace_size(const rm_gdr_state_problem* p) {
     rmcp::gla::Args a{};
     if (rmcp::gds::check(p, &a) != RM_OK) return 0;
     return rmcp::gla::tc_supports(a, p->dtype) ? rmcp::gla::tc_workspace_bytes(a) : 16;
 }
 
-rm_status rm_gla_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k, const void* v, const float* g,
+rm_status rm_cp_gla_state_forward(const rm_gdr_state_problem* p, const void* q, const void* k, const void* v, const float* g,
                                const int32_t* cu_seqlens, const int32_t* slots, const uint8_t* fresh, void* state, void* o,
                                void* ws, rm_stream_t stream) {
     using namespace rmcp;

@@ -1,5 +1,5 @@
 """Linear attention with a decay for each head and a carried state: ragged prefill and recurrent decoding on a
-pool of states [num_slots, H, Dk, Dv] that the calls update in place (rm_gla_state_forward).
+pool of states [num_slots, H, Dk, Dv] that the calls update in place (rm_cp_gla_state_forward).
 
 `chunkwise_gla` trains the same recurrence over equal segments; these calls continue it one prompt, or one
 token, at a time.
@@ -53,9 +53,9 @@ def make_gla_state_plan(max_seqs: int, max_tokens: int, H: int, Dk: int, Dv: int
     c.v_stride = (H * Dv, Dv)
     c.g_stride, c.beta_stride = H, 0
     c.recurrent = int(recurrent)
-    need = C.rm_gla_state_workspace_size(c)
+    need = C.rm_cp_gla_state_workspace_size(c)
     if need == 0:
-        raise C.RmCpError(C.load().rm_gla_state_forward(c, *[None] * 11), C.load().rm_cp_last_error().decode())
+        raise C.RmCpError(C.load().rm_cp_gla_state_forward(c, *[None] * 11), C.load().rm_cp_last_error().decode())
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     return GlaStatePlan(c, max_seqs, max_tokens, max_len, dtype, state_dtype, ws)
 
@@ -114,7 +114,7 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, state, cu, slots, fresh, o, str
         given.append(o)
     C.written(given)
     if S:
-        C.rm_gla_state_forward(ctypes.addressof(p), q, k, v, g, cu, slots, fresh, state, o, plan.ws,
+        C.rm_cp_gla_state_forward(ctypes.addressof(p), q, k, v, g, cu, slots, fresh, state, o, plan.ws,
                                C._raw_stream(stream, q.get_device()))
     else:
         C.on_stream(o.zero_, stream, o.get_device())

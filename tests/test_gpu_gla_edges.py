@@ -29,7 +29,7 @@ def test_nothing_of_a_neighbour_is_used(H, Hqk, Dk, Dv, dtype):
     assert bool((o[:67] == 0).all()) and bool((o[cu[-1]:] == 0).all()) and bool((o[cu[2]: cu[3]] == 0).all())
     assert bool(state[other].isnan().all())
     keep = [s for i, s in enumerate(slots.tolist()) if i != 2]
-    check(o, state[keep], (want[0], want[1][keep], want[2], want[3][keep]), lens, Dk, dtype, F32, C.rm_gla_state_path(plan.c) == 1)
+    check(o, state[keep], (want[0], want[1][keep], want[2], want[3][keep]), lens, Dk, dtype, F32, C.rm_cp_gla_state_path(plan.c) == 1)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

@@ -108,7 +108,7 @@ LENS = [0, 1, 47, 48, 63, 64, 65, 130, 200]
 def test_ragged_prompts(H, Hqk, Dk, Dv, gate, dtype, state_dtype):
     x, slots, fresh, cu = make(LENS, H, Hqk, Dk, Dv, dtype, state_dtype, gate)
     o, state, plan = prefill(x, slots, fresh, cu, LENS, H, Hqk, Dk, Dv)
-    chunks = C.rm_gla_state_path(plan.c) == 1
+    chunks = C.rm_cp_gla_state_path(plan.c) == 1
     assert chunks == (dtype == BF and Dk >= 64)  # (the longest has 200 tokens)
     check(o, state, reference(x, slots, fresh, cu, Dk), LENS, Dk, dtype, state_dtype, chunks)
 
@@ -135,3 +135,16 @@ def test_decoding(H, Hqk, Dk, Dv, gate, n, dtype, state_dtype):
     split = lambda t: t.unflatten(0, (S, n)) if t.dim() > 1 else t  # noqa: E731
     o = api.gla_decode(plan, split(d["q"]), split(d["k"]), split(d["v"]), split(d["g"]), d["state"], slots=slots.cuda(), fresh=fresh.cuda())
     check(o.flatten(0, 1), d["state"], reference(x, slots, fresh, cu, Dk), [n], Dk, dtype, state_dtype, False)
+
+
+@pytest.mark.parametrize("dtype,Dk,Dv,T,recurrent", [(BF, 128, 128, 2048, False), (BF, 64, 64, 2048, False), (BF, 32, 48, 2048, False), (BF, 64, 64, 31, False),
+                                                     (BF, 64, 64, 2048, True), (F32, 64, 64, 2048, False), (F32, 64, 64, 1024, True), (F32, 128, 128, 8, False)])
+def test_slow_decays_lose_no_bits(dtype, Dk, Dv, T, recurrent):
+    """One decay near 1 for every token.  A decay rounded to fp32, or sums that are cut off, would be off the same way each
+    time: some T u of the state.  Roundings to nearest add up like sqrt(T), of a memory of 1000 tokens at most: three of them
+    a token stay within 3 sqrt(min(T, 1000)) u of its norm."""
+    x, slots, fresh, cu = make([T], 2, 2, Dk, Dv, dtype, F32, seed=11)
+    x["g"] = torch.tensor([-1.0e-3, -1.7e-3])
+    _, state, _ = prefill(x, slots, fresh, cu, [T], 2, 2, Dk, Dv, recurrent=recurrent)
+    want = reference(x, slots, fresh, cu, Dk)[1][slots[0]]
+    assert float((state[slots[0]].double().cpu() - want).norm() / want.norm()) <= 3 * math.sqrt(min(T, 1000)) * U

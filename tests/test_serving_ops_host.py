@@ -16,22 +16,22 @@ from state_summary_scan_gb300 import api, row_norm
 ])
 def test_gla_state_refuses_bad_problems(kw, want):
     p = gds(**kw)
-    assert status("rm_gla_state_forward", p, *[A] * 10, None) == want
-    assert C.rm_gla_state_workspace_size(p) == 0 and C.rm_gla_state_path(p) == -1
+    assert status("rm_cp_gla_state_forward", p, *[A] * 10, None) == want
+    assert C.rm_cp_gla_state_workspace_size(p) == 0 and C.rm_cp_gla_state_path(p) == -1
 
 
 @pytest.mark.parametrize("at,ptr,want", [(0, None, 1), (1, A + 8, 3), (2, None, 1), (3, A + 2, 3), (4, A + 2, 3), (5, A + 1, 3), (7, None, 1), (8, A + 8, 3)])
 def test_gla_state_refuses_bad_pointers(at, ptr, want):
     args = [A] * 10
     args[at] = ptr
-    assert status("rm_gla_state_forward", gds(), *args, None) == want
+    assert status("rm_cp_gla_state_forward", gds(), *args, None) == want
 
 
 def test_gla_state_refuses_uneven_and_too_many_sequences():
     none = [None] * 3
-    assert status("rm_gla_state_forward", gds(num_tokens=13), A, A, A, A, *none, A, A, A, None) == 2
-    assert status("rm_gla_state_forward", gds(max_len=3), A, A, A, A, *none, A, A, A, None) == 2
-    assert status("rm_gla_state_forward", gds(num_slots=2), A, A, A, A, *none, A, A, A, None) == 2
+    assert status("rm_cp_gla_state_forward", gds(num_tokens=13), A, A, A, A, *none, A, A, A, None) == 2
+    assert status("rm_cp_gla_state_forward", gds(max_len=3), A, A, A, A, *none, A, A, A, None) == 2
+    assert status("rm_cp_gla_state_forward", gds(num_slots=2), A, A, A, A, *none, A, A, A, None) == 2
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -41,11 +41,11 @@ def test_gla_state_refuses_uneven_and_too_many_sequences():
 ])
 def test_gla_state_paths(kw, want):
     p = gds(**kw)
-    assert C.rm_gla_state_path(p) == want
-    assert C.rm_gla_state_workspace_size(p) >= 16
+    assert C.rm_cp_gla_state_path(p) == want
+    assert C.rm_cp_gla_state_workspace_size(p) >= 16
     if want:  # one that keeps to the recurrence
         p.recurrent = 1
-        assert C.rm_gla_state_path(p) == 0
+        assert C.rm_cp_gla_state_path(p) == 0
 
 
 def rms(**kw):
@@ -155,10 +155,10 @@ def test_rows_of_two_tensors_are_found_together():
 @pytest.mark.parametrize("where", [0, 1])
 def test_calls_launch_on_the_device_of_their_tensors(gpus, where, monkeypatch):  # noqa: F811
     now, seen = gpus
-    for n in ("rm_gla_state_forward", "rm_cp_rms_forward", "rm_cp_rms_quant", "rm_cp_rms_backward"):
+    for n in ("rm_cp_gla_state_forward", "rm_cp_rms_forward", "rm_cp_rms_quant", "rm_cp_rms_backward"):
         monkeypatch.setitem(C._by_address, n, lambda *a: seen.append((now[0], a[-1])))
     t, s = Tensor(where), C._raw_stream(None, where)
-    C.rm_gla_state_forward(1, t, t, t, t, None, None, None, t, t, t, s)
+    C.rm_cp_gla_state_forward(1, t, t, t, t, None, None, None, t, t, t, s)
     C.rm_cp_rms_forward(1, t, None, None, None, None, t, s)
     C.rm_cp_rms_quant(1, t, t, None, t, t, t, t, s)
     C.rm_cp_rms_backward(1, t, None, None, t, None, t, t, None, None, None, s)
