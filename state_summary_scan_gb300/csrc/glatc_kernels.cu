@@ -680,8 +680,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// The states at the segments' ends, in their place: S_j = e^{sum g} S_{j-1} + dS_j.  Four elements a thread, all segments; the loads of
-// several are under way at once.  (Folded by each walk for itself the last ones would read all the others': 6 us of 67.)
+// The states at the segments' ends, in their place: S_j = e^{sum g} S_{j-1} + dS_j.  Four elements a thread, all segments, eight
+// of which are read at once.  (Folded by each walk for itself the last ones would read all the others': 6 us of 67.)
 __global__ void __launch_bounds__(256) gla_compose_kernel(const __grid_constant__ Args a, const Segments seg) {
     const int64_t at = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4, size = int64_t(a.Dk) * a.Dv;
     const int h = blockIdx.y, i = blockIdx.z;
@@ -692,12 +692,20 @@ __global__ void __launch_bounds__(256) gla_compose_kernel(const __grid_constant_
     float* e = seg.ends + segment_at(a, seg, i, h, 0) * size + at;
     const float* f = seg.fades + segment_at(a, seg, i, h, 0);
     float4 s = *reinterpret_cast<const float4*>(e);
-#pragma unroll 4
-    for (int j = 1; j < inner; ++j) {
-        const float4 d = *reinterpret_cast<const float4*>(e + j * size);
-        const float x = f[j];
-        s.x = fmaf(x, s.x, d.x), s.y = fmaf(x, s.y, d.y), s.z = fmaf(x, s.z, d.z), s.w = fmaf(x, s.w, d.w);
-        *reinterpret_cast<float4*>(e + j * size) = s;
+    constexpr int kBatch = 8;  // segments that are read together
+    for (int j0 = 1; j0 < inner; j0 += kBatch) {
+        float4 d[kBatch];
+        float x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (j0 + j < inner) d[j] = *reinterpret_cast<const float4*>(e + (j0 + j) * size), x[j] = f[j0 + j];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (j0 + j < inner) {
+                s.x = fmaf(x[j], s.x, d[j].x), s.y = fmaf(x[j], s.y, d[j].y), s.z = fmaf(x[j], s.z, d[j].z), s.w = fmaf(x[j], s.w, d[j].w);
+                *reinterpret_cast<float4*>(e + (j0 + j) * size) = s;
+            }
+        }
     }
 }
 

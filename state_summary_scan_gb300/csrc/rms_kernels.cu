@@ -57,11 +57,6 @@ __device__ __forceinline__ void store8(float* p, const float* x) {
     reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) { *reinterpret_cast<uint4*>(p) = tc::pack8(x); }
-__device__ __forceinline__ void round8(float*, const float*) {}
-__device__ __forceinline__ void round8(__nv_bfloat16*, float* x) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(__float2bfloat16_rn(x[i]));
-}
 
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
@@ -81,7 +76,29 @@ struct Raw {
         if constexpr (sizeof(T) == 2) tc::unpack8(x[0], y);
         else load8(reinterpret_cast<const float*>(x), y);
     }
+    __device__ __forceinline__ void pairs(uint64_t* y) const {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) y[i] = widen2(w[i]);
+            else y[i] = pair(w[2 * i], w[2 * i + 1]);
+        }
+    }
+    // pairs rounded to T
+    __device__ __forceinline__ void set(const uint64_t* y) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) w[i] = pack2(y[i]);
+            else unpair(y[i], w[2 * i], w[2 * i + 1]);
+        }
+    }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T)) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = x[i];
+    }
 };
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
 
 // Threads of a row: LANES of a warp (several rows a warp), or with LANES 0 the whole block.
 // Sums x and y over them; the largest of the bits m.  (The bits of |y| order as the values do, with NaN above all.)
@@ -166,49 +183,61 @@ __global__ void __launch_bounds__(TPB) rms_forward_kernel(const __grid_constant_
         const Row<T, R, kRes, kGate != 0, VPT> now = next;
         if (kAhead && first + hop < rows) load(row + hop);
         const bool there = row < rows;
-        float m[VPT][8];
-        float sq = 0.f;
+        uint64_t m[VPT][4], squares = 0;  // pairs of elements
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int e = 8 * (at + i * step);
             const bool live = there && e < a.n;
-            float b[8], act[8];
-            now.x[i].get(m[i]);
+            uint64_t b[4], act[4];
+            now.x[i].pairs(m[i]);
             if (kRes) {
-                now.q[i].get(b);
+                now.q[i].pairs(b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[i][j] += b[j];
-                if (live) store8(static_cast<R*>(a.h) + row * a.n + e, m[i]);
-                round8(static_cast<R*>(nullptr), m[i]);
+                for (int j = 0; j < 4; ++j) m[i][j] = add2(m[i][j], b[j]);
+                Raw<R> h;
+                h.set(m[i]);
+                if (live) h.store(static_cast<R*>(a.h) + row * a.n + e);
+                h.pairs(m[i]);
             }
             if (kGate) {
-                now.z[i].get(b);
+                float z[8];
+                now.z[i].get(z);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) act[j] = b[j] * sigmoid(b[j]);
+                for (int j = 0; j < 4; ++j) act[j] = pair(z[2 * j] * sigmoid(z[2 * j]), z[2 * j + 1] * sigmoid(z[2 * j + 1]));
             }
             if (kGate == 2) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[i][j] *= act[j];
+                for (int j = 0; j < 4; ++j) m[i][j] = mul2(m[i][j], act[j]);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sq = fmaf(m[i][j], m[i][j], sq);
+            for (int j = 0; j < 4; ++j) squares = fma2(m[i][j], m[i][j], squares);
             if (a.w != nullptr && live) {
-                load8(a.w + e, b);
+                Raw<float> w;
+                w.load(a.w + e);
+                w.pairs(b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[i][j] *= b[j];
+                for (int j = 0; j < 4; ++j) m[i][j] = mul2(m[i][j], b[j]);
             }
             if (kGate == 1) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[i][j] *= act[j];
+                for (int j = 0; j < 4; ++j) m[i][j] = mul2(m[i][j], act[j]);
             }
         }
+        uint32_t lo, hi;
+        unpair(squares, lo, hi);
+        float sq = __uint_as_float(lo) + __uint_as_float(hi);
         uint32_t big[VPT], most = 0;
         if (kQuant) {
+            // (a NaN in the row is in its sum, and so in r and every scale)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                big[i] = 0;
+                float top = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) big[i] = max(big[i], __float_as_uint(m[i][j]) & 0x7fffffffu);
+                for (int j = 0; j < 4; ++j) {
+                    unpair(m[i][j], lo, hi);
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(lo)), fabsf(__uint_as_float(hi))));
+                }
+                big[i] = __float_as_uint(top);
                 most = max(most, big[i]);
             }
         }
@@ -229,10 +258,13 @@ __global__ void __launch_bounds__(TPB) rms_forward_kernel(const __grid_constant_
                 const float f = __fdividef(1.f, s);  // (r f may leave fp32 where y is all but 0)
                 uint32_t out[2];
 #pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(m[i][j] * r * f, m[i][j + 1] * r * f), __NV_SATFINITE, __NV_E4M3);
-                    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(m[i][j + 2] * r * f, m[i][j + 3] * r * f), __NV_SATFINITE, __NV_E4M3);
-                    out[j / 4] = uint32_t(lo) | uint32_t(hi) << 16;
+                for (int j = 0; j < 4; j += 2) {
+                    uint32_t p[4];
+                    unpair(mul2(mul2(m[i][j], both(r)), both(f)), p[0], p[1]);
+                    unpair(mul2(mul2(m[i][j + 1], both(r)), both(f)), p[2], p[3]);
+                    const __nv_fp8x2_storage_t x = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(p[0]), __uint_as_float(p[1])), __NV_SATFINITE, __NV_E4M3);
+                    const __nv_fp8x2_storage_t y = __nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(p[2]), __uint_as_float(p[3])), __NV_SATFINITE, __NV_E4M3);
+                    out[j / 2] = uint32_t(x) | uint32_t(y) << 16;
                 }
                 if (live) {
                     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + row * a.n + e) = make_uint2(out[0], out[1]);
@@ -241,8 +273,10 @@ __global__ void __launch_bounds__(TPB) rms_forward_kernel(const __grid_constant_
                 }
             } else if (live) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[i][j] *= r;
-                store8(static_cast<T*>(a.y) + row * a.n + e, m[i]);
+                for (int j = 0; j < 4; ++j) m[i][j] = mul2(m[i][j], both(r));
+                Raw<T> y;
+                y.set(m[i]);
+                y.store(static_cast<T*>(a.y) + row * a.n + e);
             }
         }
         if (!kAhead && first + hop < rows) load(row + hop);
