@@ -11,7 +11,8 @@
 // A CTA owns 32 columns of one sequence's head and keeps them in registers over its tokens: a thread has
 // 4 columns of Dk / 16 rows (two of 16), which it loads in pieces of 16 bytes (fp32).  It reads its own rows of q and k and its
 // own columns of v straight from memory, the next tokens' before it takes these.  Arithmetic is fp32, on
-// pairs of rows.  Tokens go NT at a time, whose outputs are summed across the threads at once.
+// pairs of rows.  Tokens go NT at a time, whose outputs are summed across the threads at once.  256 sequences, one token, 16
+// heads of 128 x 128, fp32 state: 82 us, 6.6 TB/s.
 #include <cstdio>
 
 #include "gla.cuh"
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(threads_of(DK), NT == 1 ? 8 : 4) gla_token_ker
 // four columns (of scores, of outputs) or Dk / 16 rows x four columns (of the state) a thread, the next chunk's tokens on
 // their way meanwhile.  What bounds it is the multiply-adds and, in short sequences, the three barriers of a chunk; the
 // recurrence, which it replaces, pays the latency of a barrier every four tokens (7 prompts of up to 301 tokens, 6 heads of 32 x
-// 40: 53 us).
+// 40: 35 us, the recurrence 53; one of 2048, 16 heads of 128 x 128: 371 and 610).
 // ---------------------------------------------------------------------------
 constexpr int kTokens = 32;
 // Tokens of the longest sequence from which it is taken.  us in a CUDA graph, recurrence / chunks:
