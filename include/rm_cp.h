@@ -638,9 +638,9 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * rm_cp_gla_state_path: 1 when the call runs in chunks of 64 tokens on the
  * tensor cores (dtype bf16, Dk 64 or 128, max_len and num_tokens >= 32, or 64
  * where Dk is 64 and Dv below 128, recurrent 0), 0 when it runs in fp32
- * arithmetic (bf16 tokens and single ones one after another; fp32 tokens in
- * chunks of 32 with max_len >= 20), -1 for a problem it rejects.
- * recurrent != 0 keeps every call a token recurrence.  In
+ * arithmetic (single tokens and short prompts one after another; with max_len
+ * >= 20, fp32 tokens, and bf16 ones with Dk 16 or 32, in chunks of 32), -1 for a
+ * problem it rejects.  recurrent != 0 keeps every call a token recurrence.  In
  * chunks on the tensor cores the scores and the state are rounded to bf16
  * where they enter an output: outputs are off by up to one and a half times
  * their own rounding in norm.  The state itself is kept to fp32's precision

@@ -20,8 +20,8 @@
 // A chunk passes through groups of warps with barriers of their own: V~ (eight warps: fragments of V by ldmatrix, times the
 // decays, split, into tensor memory), the state (eight), the scores (four), the outputs (four), two that issue products,
 // one of which copies too, two of gates.  The code of all of them together has to stay small: with loops unrolled
-// the warps wait for instructions (a chunk took 6700 cycles at first, 94 KB of code; 2650 now).  A chunk and head is 1.45 us; what
-// bounds it is the loop scores -> P -> P V -> scores and the outputs' way out of tensor memory, which has no room for a second
+// the warps wait for instructions (a chunk took 6700 cycles at first, 94 KB of code).  A chunk and head takes 1.25 to 1.55 us now,
+// which with 152 equal heads is HBM's rate (one prompt of 8192: 191 us, 6.7 TB/s); with fewer, what bounds it is the loop scores -> P -> P V -> scores and the outputs' way out of tensor memory, which has no room for a second
 // set of accumulators, with issue at 55% and the tensor pipe at 36%.  13 ragged prompts of up to 4096 tokens, 32 heads of 128 x 128,
 // bf16 pool: 121 us, 4.6 TB/s of what the call cannot do without; one prompt of 8192, 16 heads: 31 + 5 + 31 us.
 //
@@ -738,7 +738,7 @@ rm_status fail(const char* what, bool map) {
 //     32 heads, or two prompts of 16  19.6 / 24.8  31.4 / 32.1  54.6 / 41.0  193 / 97
 //     48 heads (4 segments)           20.1 / 27.2  31.9 / 35.1  54.9 / 46.6  193 / 117
 //     8 heads of 128 x 256            18.5 / 22.9  30.5 / 25.5  53.8 / 31.7  194 / 58
-//     4 heads of 64 x 64              13.9 / 16.2  22.8 / 17.3  40.5 / 20.0  147 / 35
+//     4 heads of 64 x 64              13.9 / 16.2  22.8 / 17.3  40.5 / 20.0  147 / 27
 int segments(const Args& a, int* chunks) {
     const int all = (a.max_len + kChunk - 1) / kChunk, blocks = (a.Dv + 127) / 128;
     int n = 1 + int(152 / (int64_t(a.H) * blocks * a.S));
