@@ -24,19 +24,21 @@ _CACHE_LOCK = threading.Lock()
 
 def _steps(t, first, last):
     """The stride of dimensions [first, last) of t taken as one, or None where they have no single one."""
-    step = want = 0
+    step = want = None  # (a broadcast dimension's step is 0: none yet is not the same)
     for n, s in reversed(list(zip(t.shape[first:last], t.stride()[first:last]))):
         if n == 1:
             continue  # (takes no step)
-        if want and s != want:
+        if want is not None and s != want:
             return None
-        step, want = step or s, s * n
-    return step
+        step, want = s if step is None else step, s * n
+    return step or 0
 
 
 def _rows(tensors):
     """(N, H, strides of each tensor): the rows of tensors [..., n] of one shape as N tokens of H rows."""
     shape = tensors[0].shape[:-1]
+    if 0 in shape:
+        return 0, 1, [(0, 0)] * len(tensors)
     for at in range(len(shape), -1, -1):
         strides = [(_steps(t, 0, at), _steps(t, at, len(shape))) for t in tensors]
         if all(None not in s for s in strides):

@@ -317,3 +317,36 @@ def test_refused_sizes_and_overlaps():
         api.rms_norm(x, residual=x.clone(), h=x)
     with pytest.raises(ValueError):
         api.rms_norm(x, h=x)
+
+
+@pytest.mark.parametrize("base", [(5, 1, 128), (1, 3, 128), (128,), (5, 1, 1, 128)])
+def test_broadcast_inputs(base):
+    shape = (5, 3, 128) if len(base) < 4 else (5, 2, 3, 128)
+    g = torch.Generator().manual_seed(9)
+    one = torch.randn(*base, generator=g).to(BF)
+    other = torch.randn(*shape, generator=g).to(BF)
+    for x, res in ((one.expand(shape), other), (other, one.expand(shape))):
+        y, h = api.rms_norm(x.cuda().expand(shape) if x is other else one.cuda().expand(shape), residual=one.cuda().expand(shape) if res is not other else other.cuda())
+        total = (d(x) + d(res)).to(BF)
+        assert torch.equal(h.cpu(), total)
+        want = forward64(d(total), None, None, False)
+        close(y, want, y_limit(want, 128, None, BF), "y")
+    z = one.cuda().expand(shape)
+    y, _ = api.rms_norm(other.cuda(), gate=z)
+    want = forward64(d(other), None, d(z), False)
+    close(y, want, y_limit(want, 128, d(z), BF), "gated y")
+
+
+def test_gradient_of_a_broadcast_input():
+    x = torch.randn(5, 1, 128, generator=torch.Generator().manual_seed(3))
+    dy = torch.randn(5, 3, 128, generator=torch.Generator().manual_seed(4))
+    leaf = x.cuda().requires_grad_()
+    y, _ = api.rms_norm_train(leaf.expand(5, 3, 128))
+    y.backward(dy.cuda())
+    ref = x.double().requires_grad_()
+    forward64(ref.expand(5, 3, 128), None, None, False).backward(dy.double())
+    r = (ref.detach().pow(2).mean(-1, keepdim=True) + EPS).rsqrt()
+    # du = r (d - uh mean(d uh)), three rows added: the limits of a gradient of terms A and B, with two additions more
+    uh = ref.detach() * r
+    size = (dy.double().abs() * r + uh.abs() * r * (dy.double() * uh).abs().mean(-1, keepdim=True)).sum(1, keepdim=True)
+    close(leaf.grad, ref.grad, (128 / 8 + 34) * U * size + half(F32) * ref.grad.abs(), "dx")

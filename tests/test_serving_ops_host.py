@@ -164,3 +164,26 @@ def test_calls_launch_on_the_device_of_their_tensors(gpus, where, monkeypatch): 
     C.rm_cp_rms_backward(1, t, None, None, t, None, t, t, None, None, None, s)
     assert seen == [(where, 1000 + where)] * 4
     assert now == [0]
+
+
+def offsets(rows):
+    N, H, (step,) = rows
+    return [i * step[0] + j * step[1] for i in range(N) for j in range(H)]
+
+
+@pytest.mark.parametrize("base,shape", [((2, 1, 64), (2, 3, 64)), ((4, 1, 64), (4, 5, 64)), ((1, 3, 64), (2, 3, 64)), ((1, 64), (3, 64)), ((64,), (2, 3, 64)),
+                                        ((2, 1, 1, 64), (2, 3, 5, 64)), ((1, 3, 1, 64), (2, 3, 5, 64))])
+def test_rows_of_broadcast_tensors_stay_in_them(base, shape):
+    x = torch.zeros(base).expand(shape)
+    want = [int(i) for i in torch.arange(x.untyped_storage().size() // 4).reshape(base).expand(shape)[..., 0].flatten()]
+    try:
+        got = row_norm._rows([x])
+    except ValueError:
+        assert base == (1, 3, 1, 64)  # two broadcast dimensions around another: three steps
+    else:
+        assert offsets(got) == want
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (3, 0, 64), (0, 3, 64), (3, 0, 2, 64)])
+def test_tensors_without_rows_have_no_tokens(shape):
+    assert row_norm._rows([torch.zeros(shape)])[0] == 0
