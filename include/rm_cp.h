@@ -632,7 +632,8 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * The problem is an rm_gdr_state_problem (beta_stride is not used), and
  * tokens, sequences, slots, fresh, state, strides, sizes and outputs are as
  * in rm_gdr_state_forward; g_stride 0: g is [H], one log-decay for each head
- * whatever the token.
+ * whatever the token.  o and state overlap no other tensor (refused).  As
+ * there, a bf16 pool ends fp32's precision at the hand-over between calls.
  *   ws: rm_cp_gla_state_workspace_size bytes, for problems of these sizes or
  *   smaller num_seqs, num_tokens and max_len; not shared by calls that overlap.
  * rm_cp_gla_state_path: 1 when the call runs in chunks of 64 tokens on the
@@ -670,7 +671,8 @@ rm_status rm_cp_gla_state_forward(const rm_gdr_state_problem* p, const void* q, 
  * rm_cp_rms_quant gives y in 8 bits: for each `group` adjacent elements (32,
  * 64 or 128, dividing n; 0: the row) scale = max |y| / 448, at least 2^-126,
  * and y8 = e4m3(y / scale), to nearest even; scales [N,H,n/group].  A NaN
- * in a row makes all of its scales NaN.
+ * in a row of u makes all of its scales NaN; one in the weight, or in a gate
+ * behind the norm, its element of y8 (a scale is of the group's other elements).
  *   x, residual and gate have strides in elements for (token, head), elements
  *   of a row adjacent, every stride and base a multiple of 16 bytes; h, y,
  *   y8, scales and all gradients are contiguous.  n is a multiple of 8 up to

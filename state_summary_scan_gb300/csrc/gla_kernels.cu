@@ -579,6 +579,22 @@ rm_status rm_cp_gla_state_forward(const rm_gdr_state_problem* p, const void* q, 
         RM_GLA_NEED(o);
     }
     if (slots != nullptr) RM_GLA_ELEM(slots, 4);
+    // Heads and sequences are taken in no order: what one writes, another must not read
+    const int64_t es = p->dtype == RM_F32 ? 4 : 2, tokens = a.N;
+    const int64_t o_bytes = tokens * a.H * a.Dv * es, st_bytes = int64_t(a.slots_n) * a.H * a.Dk * a.Dv * (p->state_dtype == RM_F32 ? 4 : 2);
+    auto apart = [](const void* x, int64_t xb, const void* y, int64_t yb) {
+        const uintptr_t i = reinterpret_cast<uintptr_t>(x), j = reinterpret_cast<uintptr_t>(y);
+        return x == nullptr || y == nullptr || i + uint64_t(xb) <= j || j + uint64_t(yb) <= i;
+    };
+    auto reach = [&](const int64_t* steps, int heads, int n) { return ((tokens - 1) * steps[0] + (heads - 1) * steps[1] + n) * es; };
+    if (tokens > 0) {
+        const int qk = a.H / a.hdiv;
+        const struct { const void* at; int64_t bytes; } in[] = {{q, reach(a.qs, qk, a.Dk)}, {k, reach(a.ks, qk, a.Dk)}, {v, reach(a.vs, a.H, a.Dv)},
+                                                                {g, ((tokens - 1) * a.gs + a.H) * 4}};
+        bool ok = apart(o, o_bytes, state, st_bytes);
+        for (const auto& x : in) ok = ok && apart(o, o_bytes, x.at, x.bytes) && apart(state, st_bytes, x.at, x.bytes);
+        if (!ok) return api_fail(RM_ERR_INVALID_ARG, "o or the state overlaps another tensor");
+    }
     a.q = q, a.k = k, a.v = v, a.g = g, a.beta = nullptr, a.cu = cu_seqlens, a.slots = slots, a.fresh = fresh;
     a.state = state, a.o = o, a.ws = ws;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

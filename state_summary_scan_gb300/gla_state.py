@@ -125,7 +125,7 @@ def gla_decode(plan: GlaStatePlan, q, k, v, g, state, slots=None, fresh=None, o=
     """o [S,n,H,Dv] of n tokens for each of S sequences, q, k [S,n,qk_heads,Dk], v [S,n,H,Dv], the log-decays g
     [S,n,H] fp32, or [H]: one for each head.  The states of `state` at slots [S] int32 (None: 0 .. S-1) are
     updated in place.  A slot outside the pool marks a padding sequence (outputs 0).  fresh [S]: non-zero
-    starts from a zero state.  q, k, v may be slices of a fused projection."""
+    starts from a zero state.  q, k, v may be slices of a fused projection; o overlaps no input."""
     if q.dim() != 4:
         raise ValueError("q must be [sequences, tokens, heads, Dk]")
     S, n = q.shape[:2]

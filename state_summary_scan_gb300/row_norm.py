@@ -157,7 +157,8 @@ def rms_norm_quant(x, weight=None, residual=None, gate=None, gate_first: bool = 
     """(y8, scales, h): rms_norm with y in 8 bits, y8 [..., n] e4m3 and scales [..., n / group] fp32 with y ~ y8 scale.
 
     A scale is max |y| / 448 of `group` adjacent elements (32, 64 or 128; 0: of the row), at least 2^-126; y is not
-    rounded before it is divided by it.  out: (y8, scales) to write into.  A row with a NaN has NaN scales."""
+    rounded before it is divided by it.  out: (y8, scales) to write into.  A row with a NaN in u has NaN scales; a NaN in the weight,
+    or in a gate behind the norm, makes its element of y8 NaN."""
     _, at, scale_shape = _problem(x, residual, weight, gate, gate_first, group, eps)
     device = x.get_device()
     if out is not None or h is not None:

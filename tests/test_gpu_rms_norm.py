@@ -350,3 +350,23 @@ def test_gradient_of_a_broadcast_input():
     uh = ref.detach() * r
     size = (dy.double().abs() * r + uh.abs() * r * (dy.double() * uh).abs().mean(-1, keepdim=True)).sum(1, keepdim=True)
     close(leaf.grad, ref.grad, (128 / 8 + 34) * U * size + half(F32) * ref.grad.abs(), "dx")
+
+
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("first", [False, True])
+def test_nan_in_a_gate_of_8_bits(first, group):
+    x = make((5, 3, 128), BF, gate=True)
+    x["z"][2, 1, 70] = float("nan")
+    y8, s, _ = api.rms_norm_quant(x["x"], x["w"], gate=x["z"], gate_first=first, group=group)
+    back = y8.float() * s.repeat_interleave(group or 128, -1)
+    x["z"][2, 1, 70] = 0  # all but the row are as without it
+    clean8, cs, _ = api.rms_norm_quant(x["x"], x["w"], gate=x["z"], gate_first=first, group=group)
+    rest = torch.ones(5, 3, dtype=torch.bool, device="cuda")
+    rest[2, 1] = False
+    assert torch.equal(y8.view(torch.uint8)[rest], clean8.view(torch.uint8)[rest]) and torch.equal(s[rest], cs[rest])
+    bad = back[2, 1].isnan()
+    if first:
+        assert bool(bad.all()) and bool(s[2, 1].isnan().all())
+    else:
+        assert int(bad.sum()) == 1 and bool(bad[70]) and not bool(s.isnan().any())
+        assert torch.equal(s, cs)

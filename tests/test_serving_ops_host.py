@@ -187,3 +187,14 @@ def test_rows_of_broadcast_tensors_stay_in_them(base, shape):
 @pytest.mark.parametrize("shape", [(0, 64), (3, 0, 64), (0, 3, 64), (3, 0, 2, 64)])
 def test_tensors_without_rows_have_no_tokens(shape):
     assert row_norm._rows([torch.zeros(shape)])[0] == 0
+
+
+def test_gla_state_refuses_outputs_and_states_over_other_tensors():
+    p = gds()  # q, k, v, g, cu_seqlens, slots, fresh, state, o, ws
+    args = [at(i) for i in range(10)]
+    for out, over in [(8, 0), (8, 1), (8, 2), (8, 3), (8, 7), (7, 0), (7, 1), (7, 2), (7, 3)]:
+        for shift in (0, 16):
+            bad = list(args)
+            bad[out] = args[over] + shift
+            assert status("rm_cp_gla_state_forward", p, *bad, None) == 1, (out, over, shift)
+            assert b"overlap" in C.load().rm_cp_last_error()
