@@ -23,7 +23,7 @@
 // the warps wait for instructions (a chunk took 6700 cycles at first, 94 KB of code).  A chunk and head takes 1.25 to 1.55 us now,
 // which with 152 equal heads is HBM's rate (one prompt of 8192: 191 us, 6.7 TB/s); with fewer, what bounds it is the loop scores -> P -> P V -> scores and the outputs' way out of tensor memory, which has no room for a second
 // set of accumulators, with issue at 55% and the tensor pipe at 36%.  13 ragged prompts of up to 4096 tokens, 32 heads of 128 x 128,
-// bf16 pool: 121 us, 4.6 TB/s of what the call cannot do without; one prompt of 8192, 16 heads: 31 + 5 + 31 us.
+// bf16 pool: 121 us, 4.6 TB/s of what the call cannot do without; one prompt of 8192, 16 heads: 57 us.
 //
 // Rounding: K, Q and V enter as they are; V~ as the sum of two bf16, or of three (all 24 bits) where the pool is
 // fp32, because its errors reach the state undamped.  S and P are rounded once to bf16: they only enter O,
@@ -104,10 +104,12 @@ struct WalkBars {
 
 enum class Part { whole, first, rest };  // as the delta rule's walk divides the sequences (gdstc_kernels.cu)
 struct Segments {
-    int chunks;    // of a segment
+    int first;     // chunks of a sequence's first segment, at most those of the others
+    int chunks;    // of each other segment
     int most;      // segments of the longest sequence
     float* ends;   // [S][H][most][Dk][Dv]: dS of the inner segments, the first one's end
     float* fades;  // [S][H][most]: e^{sum g}
+    __device__ __forceinline__ int begin(int j) const { return j == 0 ? 0 : first + (j - 1) * chunks; }
 };
 __device__ __forceinline__ int64_t segment_at(const Args& a, const Segments& g, int seq, int h, int j) {
     return (int64_t(seq) * a.H + h) * g.most + j;
@@ -198,10 +200,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     const Seq sq = sequence(a, si);
     const int all = (sq.len + kChunk - 1) / kChunk;  // the sequence's chunks
     const int j = kPart == Part::whole ? 0 : int(blockIdx.z) + (kPart == Part::rest ? 1 : 0);
-    const int c_first = kPart == Part::whole ? 0 : j * seg.chunks;
+    const int c_first = kPart == Part::whole ? 0 : seg.begin(j);
     // the sequence's last segment (the last one that there is takes what a sequence has beyond max_len)
-    const bool ends = kPart == Part::whole || j == seg.most - 1 || c_first + seg.chunks >= all;
-    const int chunks = (ends ? all : c_first + seg.chunks) - c_first;
+    const bool ends = kPart == Part::whole || j == seg.most - 1 || seg.begin(j + 1) >= all;
+    const int chunks = (ends ? all : seg.begin(j + 1)) - c_first;
     if (kPart != Part::whole && j > 0 && (sq.slot < 0 || chunks <= 0)) return;
     if (kPart == Part::first && j > 0 && ends) return;
     const bool outs = kPart != Part::first || j == 0;  // it has outputs
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(256) gla_compose_kernel(const __grid_constant_
     const int h = blockIdx.y, i = blockIdx.z;
     const Seq sq = sequence(a, i);
     // the segments that end before the sequence's last one
-    const int all = (sq.len + kChunk - 1) / kChunk, inner = min((all - 1) / seg.chunks, seg.most - 1);
+    const int all = (sq.len + kChunk - 1) / kChunk, inner = min((all - 1 - seg.first + seg.chunks) / seg.chunks, seg.most - 1);
     if (at >= size || sq.slot < 0 || inner < 2) return;
     float* e = seg.ends + segment_at(a, seg, i, h, 0) * size + at;
     const float* f = seg.fades + segment_at(a, seg, i, h, 0);
@@ -732,21 +734,26 @@ rm_status fail(const char* what, bool map) {
 
 // Segments of the longest sequence (1: not cut), and their chunks: as many as keep each walk's CTAs on the GPU's 152
 // multiprocessors at once, of two chunks or more.  A chunk takes some 1.45 us (64 x 64: 1.1), two more launches and the
-// states between them some 13; with n segments the chain is two walks of 1 / n of the chunks.  us in a CUDA graph, whole / cut:
+// states between them some 13; with n segments the chain is two walks of 1 / n of the chunks.  The first segment gets what
+// the others leave, some 0.8 of one: the first walk takes its outputs, and those of no other, so that in equal segments the
+// others wait for it (one prompt of 8192, 16 and 32 heads: 58.7 and 97.6 us; with 0.8: 56.7 and 91.4; 0.5: 56.7 and 95.9).
+// us in a CUDA graph, whole / cut:
 //     tokens                          512          1024         2048         8192
-//     16 heads of 128 x 128           18.9 / 23.0  30.8 / 25.9  53.8 / 32.5  192 / 60
-//     32 heads, or two prompts of 16  19.6 / 24.8  31.4 / 32.1  54.6 / 41.0  193 / 97
-//     48 heads (4 segments)           20.1 / 27.2  31.9 / 35.1  54.9 / 46.6  193 / 117
-//     8 heads of 128 x 256            18.5 / 22.9  30.5 / 25.5  53.8 / 31.7  194 / 58
-//     4 heads of 64 x 64              13.9 / 16.2  22.8 / 17.3  40.5 / 20.0  147 / 27
-int segments(const Args& a, int* chunks) {
+//     16 heads of 128 x 128           18.9 / 23.0  30.8 / 25.4  53.8 / 32.3  192 / 57
+//     32 heads, or two prompts of 16  19.6 / 24.8  31.4 / 32.1  54.6 / 39.6  193 / 91
+//     48 heads (4 segments)           20.1 / 27.2  31.9 / 35.1  54.9 / 46.6  193 / 112
+//     8 heads of 128 x 256            18.5 / 22.9  30.5 / 25.5  53.8 / 31.7  194 / 55
+//     4 heads of 64 x 64              13.9 / 16.2  22.8 / 17.3  40.5 / 20.0  147 / 26
+int segments(const Args& a, Segments* seg) {
     const int all = (a.max_len + kChunk - 1) / kChunk, blocks = (a.Dv + 127) / 128;
     int n = 1 + int(152 / (int64_t(a.H) * blocks * a.S));
     n = n < kMostSegments ? n : kMostSegments;
     n = n < all / 2 ? n : all / 2;
     if (int64_t(all) * (n - 2) <= 9 * n) return 1;
-    *chunks = (all + n - 1) / n;
-    return (all + *chunks - 1) / *chunks;
+    const int c = (5 * all + 5 * n - 2) / (5 * n - 1);  // all / (n - 0.2) and more
+    seg->chunks = c;
+    seg->first = all % c ? all % c : c;
+    return (all + c - 1) / c;
 }
 
 template <int DK>
@@ -757,8 +764,8 @@ rm_status launch(const Args& a, rm_dtype state_dt, cudaStream_t s) {
     if (!map_of(&mk, a.k, DK, a.H / a.hdiv, a.N, a.ks)) return fail("k", true);
     if (!map_of(&mv, a.v, a.Dv, a.H, a.N, a.vs)) return fail("v", true);
     if (!map_of(&mo, a.o, a.Dv, a.H, a.N, ostr)) return fail("o", true);
-    Segments seg{0, 1, nullptr, nullptr};
-    const int segs = segments(a, &seg.chunks);
+    Segments seg{0, 0, 1, nullptr, nullptr};
+    const int segs = segments(a, &seg);
     const unsigned blocks = unsigned((a.Dv + 127) / 128);
     auto walk = [&](auto f, dim3 grid) {
         if (!set_smem(f, WalkSmem<DK>::bytes)) return fail("shared-memory attribute of the walk", false);
