@@ -739,17 +739,17 @@ rm_status fail(const char* what, bool map) {
 // others wait for it (one prompt of 8192, 16 and 32 heads: 58.7 and 97.6 us; with 0.8: 56.7 and 91.4; 0.5: 56.7 and 95.9).
 // us in a CUDA graph, whole / cut:
 //     tokens                          512          1024         2048         8192
-//     16 heads of 128 x 128           18.9 / 23.0  30.8 / 25.4  53.8 / 32.3  192 / 57
-//     32 heads, or two prompts of 16  19.6 / 24.8  31.4 / 32.1  54.6 / 39.6  193 / 91
-//     48 heads (4 segments)           20.1 / 27.2  31.9 / 35.1  54.9 / 46.6  193 / 112
-//     8 heads of 128 x 256            18.5 / 22.9  30.5 / 25.5  53.8 / 31.7  194 / 55
-//     4 heads of 64 x 64              13.9 / 16.2  22.8 / 17.3  40.5 / 20.0  147 / 26
+//     16 heads of 128 x 128           18.9 / 23.0  30.8 / 25.4  53.8 / 32.1  192 / 57
+//     32 heads, or two prompts of 16  19.6 / 24.8  31.4 / 33.1  54.6 / 39.6  193 / 91
+//     48 heads (4 segments)           20.1 / 27.2  31.9 / 35.1  54.9 / 46.4  193 / 112
+//     8 heads of 128 x 256            18.5 / 22.9  30.5 / 24.8  53.8 / 31.2  194 / 55
+//     4 heads of 64 x 64              13.9 / 16.2  22.8 / 17.7  40.5 / 19.0  147 / 26
 int segments(const Args& a, Segments* seg) {
     const int all = (a.max_len + kChunk - 1) / kChunk, blocks = (a.Dv + 127) / 128;
     int n = 1 + int(152 / (int64_t(a.H) * blocks * a.S));
     n = n < kMostSegments ? n : kMostSegments;
     n = n < all / 2 ? n : all / 2;
-    if (int64_t(all) * (n - 2) <= 9 * n) return 1;
+    if (int64_t(all) * (n - 2) <= 10 * n) return 1;
     const int c = (5 * all + 5 * n - 2) / (5 * n - 1);  // all / (n - 0.2) and more
     seg->chunks = c;
     seg->first = all % c ? all % c : c;

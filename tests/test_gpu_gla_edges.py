@@ -231,3 +231,14 @@ def test_refusals(bad):
         api.gla_prefill(plan, **a, **kw)
 
 
+
+
+@pytest.mark.parametrize("state_dtype", [F32, BF])
+@pytest.mark.parametrize("short", [(128, 129), (127, 320), (321, 64), (1, 512), (0, 1217)])
+def test_prompts_that_end_where_segments_do(short, state_dtype):
+    """1280 tokens are cut after 2 chunks, and then after every 3: tokens 128, 320, 512, ..., 1088."""
+    lens = [short[0], 1280, short[1]]
+    x, slots, fresh, cu = make(lens, 1, 1, 64, 128, BF, state_dtype, seed=sum(short))
+    o, state, plan = prefill(x, slots, fresh, cu, lens, 1, 1, 64, 128)
+    assert C.rm_cp_gla_state_path(plan.c) == 1
+    check(o, state, reference(x, slots, fresh, cu, 64), lens, 64, BF, state_dtype, True)
