@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
         for (int i = 0; i < kGateRing; ++i) {
             mbar_init(smem_u32(&bar.gates[i]), 1);
-            mbar_init(smem_u32(&bar.gates_free[i]), quads * (kGroups + (outs ? 1 : 0)));  // the state's and the outputs' warps are the last readers
+            // a chunk's gates are free when the state's warps have seen its K^T V~, for which V~'s warps have read them, and the
+            // outputs' warps its outputs, for which the scores' have
+            mbar_init(smem_u32(&bar.gates_free[i]), quads * (kGroups + (outs ? 1 : 0)));
         }
         for (int i = 0; i < kGroups; ++i) mbar_init(smem_u32(&bar.v_free[i]), 1);
         mbar_init(smem_u32(&bar.d_ready), 2 * quads * kGroups);
@@ -290,8 +292,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                     const float* gates = gates_of(c - 1);
                     const uint64_t end = pair(gates[kEnd], gates[kEnd]);
                     const bool near = gates[kNear] != 0.f;
-                    warp_arrive(&bar.gates_free[(c - 1) % kGateRing], lane);
                     wait(&bar.d_done, (c - 1) & 1, polls);
+                    warp_arrive(&bar.gates_free[(c - 1) % kGateRing], lane);  // (V~ of that chunk is in the product: its decays have been read)
                     tc_fence_after();
 #pragma unroll
                     for (int i0 = 0; i0 < GC / 2; i0 += 8) {
