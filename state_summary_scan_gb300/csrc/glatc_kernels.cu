@@ -73,8 +73,11 @@ constexpr int kGroups = 2;  // groups of four warps of the state, and of V~
 // then four warps of outputs, four of scores, two of products (the first makes the copies too), two of gates
 constexpr int kValueWarp = 4 * kGroups, kOutWarp = 2 * kValueWarp, kScoreWarp = kOutWarp + 4, kMmaWarp = kScoreWarp + 4, kGateWarp = kMmaWarp + 2, kGateWarps = 2;
 constexpr int kWalkThreads = (kGateWarp + kGateWarps) * 32;
-// Registers a thread: 72 at the launch, of which some warps take others': 896 x 72 = 256 x 104 (the state) + 256 x 56 (V~) +
-// 128 x (80 (the outputs) + 48 (the scores) + 56)
+// Registers a thread: at the launch, and then those of the state's warps and of all others, whose sum is the launch's
+constexpr int kLaunchRegisters = 65536 / kWalkThreads / 8 * 8, kStateRegisters = 112, kOtherRegisters = 56;
+static_assert(32 * kValueWarp * kStateRegisters + (kWalkThreads - 32 * kValueWarp) * kOtherRegisters <= kWalkThreads * kLaunchRegisters,
+              "more registers than the launch has: setmaxnreg.inc would wait for them without end");
+static_assert(kValueWarp % 4 == 0, "setmaxnreg is for warpgroups");
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -262,9 +265,11 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     };
     auto wait_full = [&](int c) { wait(&bar.full[c % kStages], (c / kStages) & 1, polls); };
 
+    // (one instruction for every warp of a warpgroup, whatever it goes on to: different ones are undefined)
+    if (warp < kValueWarp) more_registers<kStateRegisters>();
+    else fewer_registers<kOtherRegisters>();
     if (warp < kValueWarp) {
         // ---- the state: a lane is a value column, a group has half of its rows
-        more_registers<112>();
         if ((warp & 3) < quads) {
             const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
             const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
@@ -345,7 +350,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
     } else if (warp < kOutWarp) {
         // ---- V~: a group has half of a chunk's tokens
-        fewer_registers<56>();
         if ((warp & 3) < quads) {
             const int grp = (warp - kValueWarp) >> 2;
             const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16) + TM_V + kParts * (GT / 2) * grp;
@@ -404,7 +408,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
     } else if (warp < kScoreWarp) {
         // ---- the outputs: a lane is a value column; whole chunks leave as tiles, the last one by rows
-        fewer_registers<56>();
         const int w = warp & 3;
         if (outs && w < quads) {
             const uint32_t tl = tmem + (uint32_t(32 * w) << 16);
@@ -472,7 +475,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     } else if (warp < kMmaWarp) {
         // ---- the scores: a warp has a block of 16 rows, in fragments of 8 x 8: rows lane / 4 and + 8, pairs of columns
         // 2 (lane % 4) ..
-        fewer_registers<56>();
         if (outs) {
             const int block = warp & 3, row = lane >> 2, col = 2 * (lane & 3);
             const uint32_t tl = tmem + (uint32_t(32 * block) << 16) + TM_SC;
@@ -521,7 +523,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ---- the copies, and the products of the state, K^T V~.  The whole warp walks the loop and one elected lane issues.
-        fewer_registers<56>();
         const uint32_t base = smem_u32(smem);
         constexpr uint32_t kTD = idesc_bf16(128, DK, 0, 1);
         auto copies = [&](int c) {
@@ -566,7 +567,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         wait(&bar.d_done, (chunks - 1) & 1, polls);  // (every copy has come)
     } else if (warp == kMmaWarp + 1) {
         // ---- the products of the outputs: Q S, P V, and Q K^T of the next chunk
-        fewer_registers<56>();
         if (outs) {
             const uint32_t base = smem_u32(smem);
             constexpr uint32_t kSc = idesc_bf16(64, 64, 0, 0), kTS = idesc_bf16(128, 64, 0, 0), kPV = idesc_bf16(128, 64, 1, 0);
@@ -618,7 +618,6 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
     } else {
         // ---- the gates, two tokens a lane, every other chunk a warp, as far ahead as there is room
-        fewer_registers<56>();
         Sum2 total{0.f, 0.f};
         auto load = [&](int c, float* g) {
             const int64_t t = int64_t(c_first + c) * kChunk + 2 * lane;
