@@ -47,7 +47,8 @@ def _rows(tensors):
 
 
 def _problem(x, residual, weight, gate, gate_first, group, eps, dy=None, dh=None):
-    """(problem, its address, shape of its scales), checked once for each combination of shapes, strides, types and options."""
+    """(problem, its address, shape of its scales), checked once for each combination of shapes, strides, types and options.
+    The caller holds the problem until its C call has returned: another thread's calls may push it out of the cache."""
     sig = C.signature
     key = (sig(x), sig(residual), sig(weight), sig(gate), gate_first, group, eps, sig(dy), sig(dh))
     hit = _CACHE.get(key)
@@ -137,7 +138,7 @@ def rms_norm(x, weight=None, residual=None, gate=None, gate_first: bool = False,
     [n] fp32.  x, residual and gate may be slices of a fused projection (adjacent elements, 16-byte strides, rows
     evenly spaced in at most two dimensions); y and h are contiguous, and y may go into a contiguous x (out=x).
     n is a multiple of 8 up to 32768."""
-    _, at, _ = _problem(x, residual, weight, gate, gate_first, 0, eps)
+    p, at, _ = _problem(x, residual, weight, gate, gate_first, 0, eps)
     device = x.get_device()
     if out is not None or h is not None:
         _check_given(x, residual, h, out, x.dtype)
@@ -159,7 +160,7 @@ def rms_norm_quant(x, weight=None, residual=None, gate=None, gate_first: bool = 
     A scale is max |y| / 448 of `group` adjacent elements (32, 64 or 128; 0: of the row), at least 2^-126; y is not
     rounded before it is divided by it.  out: (y8, scales) to write into.  A row with a NaN in u has NaN scales; a NaN in the weight,
     or in a gate behind the norm, makes its element of y8 NaN."""
-    _, at, scale_shape = _problem(x, residual, weight, gate, gate_first, group, eps)
+    p, at, scale_shape = _problem(x, residual, weight, gate, gate_first, group, eps)
     device = x.get_device()
     if out is not None or h is not None:
         _check_given(x, residual, h, None if out is None else out[0], torch.float8_e4m3fn)
