@@ -202,6 +202,13 @@ def rms_norm_backward(h, dy, weight=None, dh=None, gate=None, gate_first: bool =
     return dx, dresidual, dgate, dweight
 
 
+def _dense(t):
+    """t contiguous and from a 16-byte boundary on: autograd hands over contiguous views at any offset (of a concatenation's
+    gradient)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class RmsNorm(torch.autograd.Function):
     """Autograd adapter: the backward recomputes the norm from the saved h."""
 
@@ -220,7 +227,7 @@ class RmsNorm(torch.autograd.Function):
         h, weight, gate = ctx.saved_tensors
         if dy is None:  # y is not used
             return (None if dh is None else dh.to(ctx.dtype)), None, dh, None, None, None
-        dx, dresidual, dgate, dweight = rms_norm_backward(h, dy.contiguous(), weight, None if dh is None else dh.contiguous(), gate, **ctx.how)
+        dx, dresidual, dgate, dweight = rms_norm_backward(h, _dense(dy), weight, None if dh is None else _dense(dh), gate, **ctx.how)
         return dx, dweight, dresidual if ctx.has_residual else None, dgate, None, None
 
 
