@@ -1,7 +1,7 @@
-"""Norms of rows: gradients as autograd hands them over."""
+"""Norms of rows: gradients as autograd hands them over, gates far from 0."""
 import pytest
 import torch
-from test_gpu_rms_norm import BF, F32, make
+from test_gpu_rms_norm import BF, F32, U, close, d, forward64, make
 
 from state_summary_scan_gb300 import api
 
@@ -25,3 +25,34 @@ def test_parts_of_a_concatenation(dtype, res, gate):
         return torch.autograd.grad(sum(loss(t, w) for t, w in zip(parts, weights)), list(leaves.values()), retain_graph=True)
 
     assert all(torch.equal(a, b) for a, b in zip(grads(True), grads(False)))
+
+
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("N,n", [(300, 64), (40, 1000), (9, 8192)])
+def test_wide_gates_of_fp32_rows(N, n, first):
+    """Gates far from 0: their error does not grow with them.  With u = 2^-24: e = e^-|z| is off by 2 u, e / (1 + e) by 7 u, one
+    less it by less, silu by 8 u; the slope s (1 + z (1 - s)) by 9 u of itself and 8 u of s |z| (1 - s).  The rest of
+    the limits is as in test_gpu_rms_norm.py; a gate before the norm enters the gradients' sums four times."""
+    x = make((N, n), F32, gate=True, seed=N)
+    g = torch.Generator().manual_seed(n)
+    x["z"] = ((torch.rand(N, n, generator=g) * 2 - 1) * 80).cuda()
+    dy = torch.randn(N, n, generator=g).cuda()
+    y, _ = api.rms_norm(x["x"], x["w"], gate=x["z"], gate_first=first)
+    want = forward64(d(x["x"]), d(x["w"]), d(x["z"]), first)
+    close(y, want, want.abs() * ((n / 16 + 14 + 1 + 8 + 16 * first) * U), "y")
+    dx, _, dz, dw = api.rms_norm_backward(x["x"], dy, x["w"], gate=x["z"], gate_first=first)
+    h64, w64, z64 = (d(x[k]).requires_grad_(True) for k in ("x", "w", "z"))
+    wx, ww, wz = torch.autograd.grad(forward64(h64, w64, z64, first), (h64, w64, z64), d(dy))
+    h, w, z = d(x["x"]), d(x["w"]), d(x["z"])
+    s = 1 / (1 + (-z).exp())
+    act, mixed = z * s, s * z.abs() * (1 / (1 + z.exp()))
+    slope = s * (1 + z * (1 / (1 + z.exp())))
+    u = h * act if first else h
+    r = 1 / (u.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt()
+    e = d(dy) if first else d(dy) * act
+    A = (e * w).abs() * r + u.abs() * r * r * (e * w * u * r).abs().mean(-1, keepdim=True)
+    rel = (n / 8 + 40 + 40) * U
+    close(dx, wx, rel * (A * act.abs() if first else A) + U * wx.abs() + 1e-44, "dx")
+    size = A * h.abs() if first else (u * r * w * d(dy)).abs()
+    close(dz, wz, size * (rel * slope.abs() + 8 * U * mixed) + U * wz.abs() + 1e-44, "dgate")
+    close(dw, ww, (N / 256 + n / 8 + 64 + 40) * U * (e * u * r).abs().sum(0), "dweight")
