@@ -1,5 +1,7 @@
-"""Norms of rows: gradients as autograd hands them over, gates far from 0."""
+"""Norms of rows: gradients as autograd hands them over, gates far from 0, and more rows than a
+launch takes at once."""
 import pytest
+import test_gpu_rms_norm as one_pass
 import torch
 from test_gpu_rms_norm import BF, F32, U, close, d, forward64, make
 
@@ -56,3 +58,34 @@ def test_wide_gates_of_fp32_rows(N, n, first):
     size = A * h.abs() if first else (u * r * w * d(dy)).abs()
     close(dz, wz, size * (rel * slope.abs() + 8 * U * mixed) + U * wz.abs() + 1e-44, "dgate")
     close(dw, ww, (N / 256 + n / 8 + 64 + 40) * U * (e * u * r).abs().sum(0), "dweight")
+
+
+# Rows a block takes one after another: a launch has 152 times the blocks that a multiprocessor holds (for rows of 128 a block takes
+# 16 at once), so each of these goes round several times, the last one not full.
+
+@pytest.mark.parametrize("N,n,dtype,res,gate,first,dh", [
+    (2500, 2048, BF, BF, False, False, True), (2500, 2048, BF, F32, False, False, True), (2500, 2048, F32, F32, False, False, True),
+    (2500, 1000, BF, None, False, False, False), (1301, 4096, BF, BF, False, False, True), (1301, 4096, BF, None, True, True, False),
+    (401, 8192, BF, BF, False, False, True), (401, 8192, BF, None, True, False, False), (331, 16384, BF, F32, False, False, True),
+    (311, 16384, F32, None, True, True, False), (20011, 128, BF, BF, False, False, True), (20011, 128, BF, None, True, False, False),
+    (20011, 128, BF, None, True, True, False), (20011, 128, F32, None, True, False, False), (20011, 128, F32, None, True, True, False),
+    (40009, 64, BF, None, True, False, False), (10007, 256, BF, F32, False, False, True)])
+def test_gradients_of_many_rows(N, n, dtype, res, gate, first, dh):
+    one_pass.test_gradients(N, n, dtype, res, gate, first, dh)
+
+
+@pytest.mark.parametrize("N,H,n,dtype,first", [(1300, 16, 128, BF, False), (1300, 16, 128, F32, True), (2501, 3, 256, BF, True), (700, 2, 2048, BF, False)])
+def test_gated_norm_of_many_rows(N, H, n, dtype, first):
+    one_pass.test_gated_norm_of_slices(N, H, n, dtype, first)
+
+
+@pytest.mark.parametrize("N,n,res,gate,first,group", [(20011, 128, None, True, False, 32), (20011, 128, None, True, True, 0), (1301, 4096, BF, False, False, 128),
+                                                      (811, 8192, BF, False, False, 0), (331, 16384, None, False, False, 64)])
+def test_eight_bits_of_many_rows(N, n, res, gate, first, group):
+    """Row by row the bits that calls of a few rows give (which are tested against the formula)."""
+    x = make((N, n), BF, res, gate, seed=N)
+    y8, scale, h = api.rms_norm_quant(x["x"], x["w"], residual=x["res"], gate=x["z"], gate_first=first, group=group)
+    part = lambda t, at: None if t is None else t[at: at + 100]  # noqa: E731
+    for at in range(0, N, 100):
+        few = api.rms_norm_quant(part(x["x"], at), x["w"], residual=part(x["res"], at), gate=part(x["z"], at), gate_first=first, group=group)
+        assert all(torch.equal(a.view(torch.uint8), part(b, at).contiguous().view(torch.uint8)) for a, b in zip(few, (y8, scale, h)))
