@@ -1,10 +1,10 @@
 """Prompts cut into segments of many chunks, with a gate for each token: every ring of the walks is used several times over, in
-segments with outputs and in those without.
+segments with outputs and in those without.  And the outputs of prompts that are longer than a bound of a few tokens.
 
 The limits are those of test_gpu_gla_state.py, against the recurrence in 64 bits in blocks (blocks())."""
 import pytest
 import torch
-from test_gpu_gla_state import BF, F32, check, make, plain, plan_of
+from test_gpu_gla_state import BF, F32, check, make, plain, plan_of, reference
 
 from state_summary_scan_gb300 import _capi as C
 from state_summary_scan_gb300 import api
@@ -77,3 +77,20 @@ def test_long_segments_with_a_gate_for_each_token(H, Hqk, Dk, Dv, lens, gate, st
     torch.cuda.synchronize()
     assert all(torch.equal(p, o) and torch.equal(s, state) for p, s in again)
     assert C.rm_cp_device_status(torch.zeros(1, dtype=torch.int32, device="cuda")) == 0  # no wait ran out
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 64), (64, 40), (16, 24)])
+@pytest.mark.parametrize("max_len", [1, 2, 4])
+def test_outputs_of_prompts_longer_than_a_bound_of_a_few_tokens(max_len, Dk, Dv):
+    """A bf16 pool is then rounded every four tokens, by w = 2^-8 of it, and the rounded states are what the next tokens see.  Every
+    head's decay is e^-0.6 or less: of a rounding e^-2.4 is left four tokens on, 1 / (1 - e^-2.4) = 1.1 of them in all."""
+    lens = [650, 5, 0, 66, 1]
+    x, slots, fresh, cu = make(lens, 2, 1, Dk, Dv, BF, BF, "head", seed=4)
+    x["g"] = torch.tensor([-0.6, -0.9])
+    plan = api.make_gla_state_plan(5, sum(lens), 2, Dk, Dv, num_slots=7, qk_heads=1, state_dtype=BF)
+    d = {n: t.cuda() for n, t in x.items()}
+    o = api.gla_prefill(plan, d["q"], d["k"], d["v"], d["g"], d["state"], cu.cuda(), slots=slots.cuda(), fresh=fresh.cuda(), max_len=max_len)
+    want, pool, A, B = reference(x, slots, fresh, cu, Dk)
+    u, w = 2.0 ** -24, 2.0 ** -8
+    assert bool(((o.double().cpu() - want).abs() <= (1.1 * w + (8 * 650 + Dk + 8) * u) * A + w * want.abs() + 1e-30).all())
+    assert bool(((d["state"].double().cpu() - pool).abs() <= (1.1 * w + (8 * 650 + 4) * u) * B + w * pool.abs() + 1e-30).all())
