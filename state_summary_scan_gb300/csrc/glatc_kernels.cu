@@ -265,11 +265,9 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     };
     auto wait_full = [&](int c) { wait(&bar.full[c % kStages], (c / kStages) & 1, polls); };
 
-    // (one instruction for every warp of a warpgroup, whatever it goes on to: different ones are undefined)
-    if (warp < kValueWarp) more_registers<kStateRegisters>();
-    else fewer_registers<kOtherRegisters>();
     if (warp < kValueWarp) {
         // ---- the state: a lane is a value column, a group has half of its rows
+        more_registers<kStateRegisters>();
         if ((warp & 3) < quads) {
             const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
             const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16);
@@ -350,6 +348,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
     } else if (warp < kOutWarp) {
         // ---- V~: a group has half of a chunk's tokens
+        fewer_registers<kOtherRegisters>();
         if ((warp & 3) < quads) {
             const int grp = (warp - kValueWarp) >> 2;
             const uint32_t tl = tmem + (uint32_t(32 * (warp & 3)) << 16) + TM_V + kParts * (GT / 2) * grp;
@@ -408,6 +407,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
         }
     } else if (warp < kScoreWarp) {
         // ---- the outputs: a lane is a value column; whole chunks leave as tiles, the last one by rows
+        fewer_registers<kOtherRegisters>();
         const int w = warp & 3;
         if (outs && w < quads) {
             const uint32_t tl = tmem + (uint32_t(32 * w) << 16);
@@ -475,6 +475,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
     } else if (warp < kMmaWarp) {
         // ---- the scores: a warp has a block of 16 rows, in fragments of 8 x 8: rows lane / 4 and + 8, pairs of columns
         // 2 (lane % 4) ..
+        fewer_registers<kOtherRegisters>();
         if (outs) {
             const int block = warp & 3, row = lane >> 2, col = 2 * (lane & 3);
             const uint32_t tl = tmem + (uint32_t(32 * block) << 16) + TM_SC;
@@ -521,169 +522,172 @@ __global__ void __launch_bounds__(kWalkThreads, 1)
                 warp_arrive(&bar.p_ready, lane);  // P is there, and the scores have been read
             }
         }
-    } else if (warp == kMmaWarp) {
-        // ---- the copies, and the products of the state, K^T V~.  The whole warp walks the loop and one elected lane issues.
-        const uint32_t base = smem_u32(smem);
-        constexpr uint32_t kTD = idesc_bf16(128, DK, 0, 1);
-        auto copies = [&](int c) {
-            const int i = c % kStages, row = sq.begin + (c_first + c) * kChunk;
-            if (c >= kStages) wait(&bar.empty[i], ((c / kStages) - 1) & 1, polls);
-            if (elect()) {
-                const uint32_t at = base + i * L::stage, full = smem_u32(&bar.full[i]);
-                const int vt = (nv + 63) / 64;
-                mbar_expect_tx(full, (NP * (outs ? 2 : 1) + vt) * T8);
-#pragma unroll 1
-                for (int p = 0; p < NP; ++p) {
-                    tma_load_3d(at + p * L::panel + T8, &mk, 64 * p, h / a.hdiv, row, full);
-                    if (outs) tma_load_3d(at + p * L::panel, &mq, 64 * p, h / a.hdiv, row, full);
-                }
-#pragma unroll 1
-                for (int p = 0; p < vt; ++p) tma_load_3d(at + L::V + p * T8, &mv, v0 + 64 * p, h, row, full);
-            }
-            __syncwarp();
-        };
-#pragma unroll 1
-        for (int c = 0; c < min(chunks, kAhead); ++c) copies(c);
-        for (int c = 0; c < chunks; ++c) {
-            if (c + kAhead < chunks) copies(c + kAhead);
-            const uint64_t dk = sdesc(base + (c % kStages) * L::stage + T8, L::panel, 1024);
-            wait_full(c);
-            if (ragged && c == chunks - 1) wait(&bar.fixed, 0, polls);
-            wait(&bar.d_ready, c & 1, polls);
-            tc_fence_after();
-            if (elect()) {
-#pragma unroll 1
-                for (int half = 0; half < kGroups; ++half) {
-#pragma unroll
-                    for (int k = 0; k < 2 * kParts; ++k)  // the parts of V~ on 32 tokens
-                        mma_ts(tmem + TM_D, tmem + TM_V + kParts * 16 * half + 8 * k, desc_plus(dk, half * 4096 + (k & 1) * 2048), kTD, half + k > 0);
-                    mma_commit(smem_u32(&bar.v_free[half]));
-                }
-                mma_commit(smem_u32(&bar.d_done));
-                mma_commit(smem_u32(&bar.empty[c % kStages]));
-            }
-            __syncwarp();
-        }
-        wait(&bar.d_done, (chunks - 1) & 1, polls);  // (every copy has come)
-    } else if (warp == kMmaWarp + 1) {
-        // ---- the products of the outputs: Q S, P V, and Q K^T of the next chunk
-        if (outs) {
-            const uint32_t base = smem_u32(smem);
-            constexpr uint32_t kSc = idesc_bf16(64, 64, 0, 0), kTS = idesc_bf16(128, 64, 0, 0), kPV = idesc_bf16(128, 64, 1, 0);
-            for (int c = -1; c < chunks; ++c) {
-                const uint32_t at = base + (c % kStages) * L::stage;
-                if (c >= 0) {
-                    const uint64_t dq = sdesc(at, 16, 1024), dv = sdesc(at + L::V, T8, 1024), dp = sdesc(base + L::P, 16, 1024);
-                    if (c + 1 < chunks) wait_full(c + 1);
-                    wait(&bar.o1_ready, c & 1, polls);
-                    tc_fence_after();
-                    if (elect()) {
-#pragma unroll 1
-                        for (int p = 0; p < NP; ++p)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)  // (Q S)^T
-                                mma_ts(tmem + TM_O1, tmem + TM_S + 32 * p + 8 * k, desc_plus(dq, p * L::panel + k * 32), kTS, p + k > 0);
-                        mma_commit(smem_u32(&bar.o1_done));
-                    }
-                    __syncwarp();
-                    if (ragged && c == chunks - 1) wait(&bar.fixed, 0, polls);
-                    wait(&bar.p_ready, c & 1, polls);
-                    tc_fence_after();
-                    if (elect()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)  // (P V)^T
-                            mma_bf16(tmem + TM_O2, desc_plus(dv, k * 2048), desc_plus(dp, k * 32), kPV, k > 0);
-                        mma_commit(smem_u32(&bar.o_done));
-                        mma_commit(smem_u32(&bar.empty[c % kStages]));
-                    }
-                    __syncwarp();
-                }
-                if (c + 1 < chunks) {  // Q K^T of the next chunk, which may replace this one's: its P has been used
-                    const uint32_t next = base + ((c + 1) % kStages) * L::stage;
-                    const uint64_t d = sdesc(next, 16, 1024), dk = sdesc(next + T8, 16, 1024);
-                    if (c < 0) wait_full(0);
-                    tc_fence_after();
-                    if (elect()) {
-#pragma unroll 1
-                        for (int p = 0; p < NP; ++p)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_bf16(tmem + TM_SC, desc_plus(d, p * L::panel + k * 32), desc_plus(dk, p * L::panel + k * 32), kSc, p + k > 0);
-                        mma_commit(smem_u32(&bar.scores));
-                    }
-                    __syncwarp();
-                }
-            }
-            wait(&bar.o_done, (chunks - 1) & 1, polls);
-        }
     } else {
-        // ---- the gates, two tokens a lane, every other chunk a warp, as far ahead as there is room
-        Sum2 total{0.f, 0.f};
-        auto load = [&](int c, float* g) {
-            const int64_t t = int64_t(c_first + c) * kChunk + 2 * lane;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) g[u] = t + u < sq.len && c < chunks ? __ldg(a.g + (sq.begin + t + u) * a.gs + h) : 0.f;
-        };
-        float next[2];
-        load(warp - kGateWarp, next);
-        bool lost = false;  // a NaN among the gates
-        for (int c = warp - kGateWarp; c < chunks; c += kGateWarps) {
-            float g[2] = {next[0], next[1]};
-            load(c + kGateWarps, next);
-            const unsigned n0 = __ballot_sync(kFull, g[0] != g[0]), n1 = __ballot_sync(kFull, g[1] != g[1]);
-            // a NaN's token and all after it
-            const int nan = min(n0 ? 2 * (__ffs(n0) - 1) : 64, n1 ? 2 * __ffs(n1) - 1 : 64);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) g[u] = fminf(fmaxf(g[u], -kForget), kForget);
-            const Sum2 own = sum2(Sum2{g[0], 0.f}, Sum2{g[1], 0.f});
-            Sum2 ps = own;
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const Sum2 x{__shfl_up_sync(kFull, ps.hi, s), __shfl_up_sync(kFull, ps.lo, s)};
-                if (lane >= s) ps = sum2(ps, x);
+        fewer_registers<kOtherRegisters>();  // (one instruction for every warp of a warpgroup: different ones are undefined)
+        if (warp == kMmaWarp) {
+            // ---- the copies, and the products of the state, K^T V~.  The whole warp walks the loop and one elected lane issues.
+            const uint32_t base = smem_u32(smem);
+            constexpr uint32_t kTD = idesc_bf16(128, DK, 0, 1);
+            auto copies = [&](int c) {
+                const int i = c % kStages, row = sq.begin + (c_first + c) * kChunk;
+                if (c >= kStages) wait(&bar.empty[i], ((c / kStages) - 1) & 1, polls);
+                if (elect()) {
+                    const uint32_t at = base + i * L::stage, full = smem_u32(&bar.full[i]);
+                    const int vt = (nv + 63) / 64;
+                    mbar_expect_tx(full, (NP * (outs ? 2 : 1) + vt) * T8);
+    #pragma unroll 1
+                    for (int p = 0; p < NP; ++p) {
+                        tma_load_3d(at + p * L::panel + T8, &mk, 64 * p, h / a.hdiv, row, full);
+                        if (outs) tma_load_3d(at + p * L::panel, &mq, 64 * p, h / a.hdiv, row, full);
+                    }
+    #pragma unroll 1
+                    for (int p = 0; p < vt; ++p) tma_load_3d(at + L::V + p * T8, &mv, v0 + 64 * p, h, row, full);
+                }
+                __syncwarp();
+            };
+    #pragma unroll 1
+            for (int c = 0; c < min(chunks, kAhead); ++c) copies(c);
+            for (int c = 0; c < chunks; ++c) {
+                if (c + kAhead < chunks) copies(c + kAhead);
+                const uint64_t dk = sdesc(base + (c % kStages) * L::stage + T8, L::panel, 1024);
+                wait_full(c);
+                if (ragged && c == chunks - 1) wait(&bar.fixed, 0, polls);
+                wait(&bar.d_ready, c & 1, polls);
+                tc_fence_after();
+                if (elect()) {
+    #pragma unroll 1
+                    for (int half = 0; half < kGroups; ++half) {
+    #pragma unroll
+                        for (int k = 0; k < 2 * kParts; ++k)  // the parts of V~ on 32 tokens
+                            mma_ts(tmem + TM_D, tmem + TM_V + kParts * 16 * half + 8 * k, desc_plus(dk, half * 4096 + (k & 1) * 2048), kTD, half + k > 0);
+                        mma_commit(smem_u32(&bar.v_free[half]));
+                    }
+                    mma_commit(smem_u32(&bar.d_done));
+                    mma_commit(smem_u32(&bar.empty[c % kStages]));
+                }
+                __syncwarp();
             }
-            const Sum2 before = sum2(ps, Sum2{-g[1], 0.f});
-            const Sum2 end{__shfl_sync(kFull, ps.hi, 31), __shfl_sync(kFull, ps.lo, 31)};
-            // the sums at the end of this lane's block of 16, and before it
-            const Sum2 own_end{__shfl_sync(kFull, ps.hi, lane | 7), __shfl_sync(kFull, ps.lo, lane | 7)};
-            Sum2 begin{__shfl_sync(kFull, ps.hi, (lane | 7) - 8 & 31), __shfl_sync(kFull, ps.lo, (lane | 7) - 8 & 31)};
-            if (lane < 8) begin = Sum2{0.f, 0.f};
-            const float bad = __int_as_float(0x7fffffff);
-            if (c >= kGateRing) wait(&bar.gates_free[c % kGateRing], ((c / kGateRing) - 1) & 1, polls);
-            float* to = reinterpret_cast<float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
-            bool weak = true;
-#pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-                const int t = 2 * lane + u;
-                const bool x = t >= nan;
-                const Sum2 bt = u ? ps : before;
-                const float local = bt - begin;
-                weak = weak && fabsf(local) < kWeakLimit;
-                to[kOut + t] = x ? bad : a.scale * __expf(bt.hi + bt.lo);
-                to[kDec + t] = nan < 64 ? bad : __expf(end - bt);
-                to[kLocal + t] = x ? bad : local;
-                to[kBack + t] = __expf(-local);
-                to[kCross + t] = nan <= (t | (kSub - 1)) ? bad : __expf(own_end - bt);
+            wait(&bar.d_done, (chunks - 1) & 1, polls);  // (every copy has come)
+        } else if (warp == kMmaWarp + 1) {
+            // ---- the products of the outputs: Q S, P V, and Q K^T of the next chunk
+            if (outs) {
+                const uint32_t base = smem_u32(smem);
+                constexpr uint32_t kSc = idesc_bf16(64, 64, 0, 0), kTS = idesc_bf16(128, 64, 0, 0), kPV = idesc_bf16(128, 64, 1, 0);
+                for (int c = -1; c < chunks; ++c) {
+                    const uint32_t at = base + (c % kStages) * L::stage;
+                    if (c >= 0) {
+                        const uint64_t dq = sdesc(at, 16, 1024), dv = sdesc(at + L::V, T8, 1024), dp = sdesc(base + L::P, 16, 1024);
+                        if (c + 1 < chunks) wait_full(c + 1);
+                        wait(&bar.o1_ready, c & 1, polls);
+                        tc_fence_after();
+                        if (elect()) {
+    #pragma unroll 1
+                            for (int p = 0; p < NP; ++p)
+    #pragma unroll
+                                for (int k = 0; k < 4; ++k)  // (Q S)^T
+                                    mma_ts(tmem + TM_O1, tmem + TM_S + 32 * p + 8 * k, desc_plus(dq, p * L::panel + k * 32), kTS, p + k > 0);
+                            mma_commit(smem_u32(&bar.o1_done));
+                        }
+                        __syncwarp();
+                        if (ragged && c == chunks - 1) wait(&bar.fixed, 0, polls);
+                        wait(&bar.p_ready, c & 1, polls);
+                        tc_fence_after();
+                        if (elect()) {
+    #pragma unroll
+                            for (int k = 0; k < 4; ++k)  // (P V)^T
+                                mma_bf16(tmem + TM_O2, desc_plus(dv, k * 2048), desc_plus(dp, k * 32), kPV, k > 0);
+                            mma_commit(smem_u32(&bar.o_done));
+                            mma_commit(smem_u32(&bar.empty[c % kStages]));
+                        }
+                        __syncwarp();
+                    }
+                    if (c + 1 < chunks) {  // Q K^T of the next chunk, which may replace this one's: its P has been used
+                        const uint32_t next = base + ((c + 1) % kStages) * L::stage;
+                        const uint64_t d = sdesc(next, 16, 1024), dk = sdesc(next + T8, 16, 1024);
+                        if (c < 0) wait_full(0);
+                        tc_fence_after();
+                        if (elect()) {
+    #pragma unroll 1
+                            for (int p = 0; p < NP; ++p)
+    #pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16(tmem + TM_SC, desc_plus(d, p * L::panel + k * 32), desc_plus(dk, p * L::panel + k * 32), kSc, p + k > 0);
+                            mma_commit(smem_u32(&bar.scores));
+                        }
+                        __syncwarp();
+                    }
+                }
+                wait(&bar.o_done, (chunks - 1) & 1, polls);
             }
-            weak = __all_sync(kFull, weak);
-            // (lanes 15 and 23 end blocks 1 and 2; a NaN there reaches the rows by their own sums)
-            const Sum2 e0{__shfl_sync(kFull, ps.hi, 7), __shfl_sync(kFull, ps.lo, 7)}, e1{__shfl_sync(kFull, ps.hi, 15), __shfl_sync(kFull, ps.lo, 15)},
-                e2{__shfl_sync(kFull, ps.hi, 23), __shfl_sync(kFull, ps.lo, 23)};
-            if (lane < 3) to[kBlocks + lane] = __expf(lane == 0 ? e1 - e0 : lane == 1 ? e2 - e0 : e2 - e1);
-            if (lane == 0) {
-                const float e = end.hi + end.lo;
-                const bool near = e > -0.7f && e < 0.7f && nan == 64;
-                to[kEnd] = nan < 64 ? bad : near ? expm1f(e) : expf(e);
-                to[kNear] = near ? 1.f : 0.f;
-                to[kWeak] = weak ? 1.f : 0.f;
+        } else {
+            // ---- the gates, two tokens a lane, every other chunk a warp, as far ahead as there is room
+            Sum2 total{0.f, 0.f};
+            auto load = [&](int c, float* g) {
+                const int64_t t = int64_t(c_first + c) * kChunk + 2 * lane;
+    #pragma unroll
+                for (int u = 0; u < 2; ++u) g[u] = t + u < sq.len && c < chunks ? __ldg(a.g + (sq.begin + t + u) * a.gs + h) : 0.f;
+            };
+            float next[2];
+            load(warp - kGateWarp, next);
+            bool lost = false;  // a NaN among the gates
+            for (int c = warp - kGateWarp; c < chunks; c += kGateWarps) {
+                float g[2] = {next[0], next[1]};
+                load(c + kGateWarps, next);
+                const unsigned n0 = __ballot_sync(kFull, g[0] != g[0]), n1 = __ballot_sync(kFull, g[1] != g[1]);
+                // a NaN's token and all after it
+                const int nan = min(n0 ? 2 * (__ffs(n0) - 1) : 64, n1 ? 2 * __ffs(n1) - 1 : 64);
+    #pragma unroll
+                for (int u = 0; u < 2; ++u) g[u] = fminf(fmaxf(g[u], -kForget), kForget);
+                const Sum2 own = sum2(Sum2{g[0], 0.f}, Sum2{g[1], 0.f});
+                Sum2 ps = own;
+    #pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const Sum2 x{__shfl_up_sync(kFull, ps.hi, s), __shfl_up_sync(kFull, ps.lo, s)};
+                    if (lane >= s) ps = sum2(ps, x);
+                }
+                const Sum2 before = sum2(ps, Sum2{-g[1], 0.f});
+                const Sum2 end{__shfl_sync(kFull, ps.hi, 31), __shfl_sync(kFull, ps.lo, 31)};
+                // the sums at the end of this lane's block of 16, and before it
+                const Sum2 own_end{__shfl_sync(kFull, ps.hi, lane | 7), __shfl_sync(kFull, ps.lo, lane | 7)};
+                Sum2 begin{__shfl_sync(kFull, ps.hi, (lane | 7) - 8 & 31), __shfl_sync(kFull, ps.lo, (lane | 7) - 8 & 31)};
+                if (lane < 8) begin = Sum2{0.f, 0.f};
+                const float bad = __int_as_float(0x7fffffff);
+                if (c >= kGateRing) wait(&bar.gates_free[c % kGateRing], ((c / kGateRing) - 1) & 1, polls);
+                float* to = reinterpret_cast<float*>(smem + L::GATES + (c % kGateRing) * kGateBytes);
+                bool weak = true;
+    #pragma unroll 1
+                for (int u = 0; u < 2; ++u) {
+                    const int t = 2 * lane + u;
+                    const bool x = t >= nan;
+                    const Sum2 bt = u ? ps : before;
+                    const float local = bt - begin;
+                    weak = weak && fabsf(local) < kWeakLimit;
+                    to[kOut + t] = x ? bad : a.scale * __expf(bt.hi + bt.lo);
+                    to[kDec + t] = nan < 64 ? bad : __expf(end - bt);
+                    to[kLocal + t] = x ? bad : local;
+                    to[kBack + t] = __expf(-local);
+                    to[kCross + t] = nan <= (t | (kSub - 1)) ? bad : __expf(own_end - bt);
+                }
+                weak = __all_sync(kFull, weak);
+                // (lanes 15 and 23 end blocks 1 and 2; a NaN there reaches the rows by their own sums)
+                const Sum2 e0{__shfl_sync(kFull, ps.hi, 7), __shfl_sync(kFull, ps.lo, 7)}, e1{__shfl_sync(kFull, ps.hi, 15), __shfl_sync(kFull, ps.lo, 15)},
+                    e2{__shfl_sync(kFull, ps.hi, 23), __shfl_sync(kFull, ps.lo, 23)};
+                if (lane < 3) to[kBlocks + lane] = __expf(lane == 0 ? e1 - e0 : lane == 1 ? e2 - e0 : e2 - e1);
+                if (lane == 0) {
+                    const float e = end.hi + end.lo;
+                    const bool near = e > -0.7f && e < 0.7f && nan == 64;
+                    to[kEnd] = nan < 64 ? bad : near ? expm1f(e) : expf(e);
+                    to[kNear] = near ? 1.f : 0.f;
+                    to[kWeak] = weak ? 1.f : 0.f;
+                }
+                warp_arrive(&bar.gates[c % kGateRing], lane);
+                total = sum2(total, end);
+                lost |= nan < 64;
             }
-            warp_arrive(&bar.gates[c % kGateRing], lane);
-            total = sum2(total, end);
-            lost |= nan < 64;
-        }
-        if (kPart == Part::first && lane == 0) {
-            sum_s[warp - kGateWarp] = total.hi + total.lo;
-            lost_s[warp - kGateWarp] = lost;
+            if (kPart == Part::first && lane == 0) {
+                sum_s[warp - kGateWarp] = total.hi + total.lo;
+                lost_s[warp - kGateWarp] = lost;
+            }
         }
     }
     __syncthreads();
