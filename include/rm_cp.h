@@ -647,10 +647,11 @@ rm_status rm_gdr_state_forward(const rm_gdr_state_problem* p, const void* q, con
  * their own rounding in norm.  The state itself is kept to fp32's precision
  * in an fp32 pool, and in a bf16 pool to 2^-16 of what is added to it beside
  * the pool's own rounding, once a call (with max_len <= 4 once every four
- * tokens).  A log-gate below -110 is taken as -110 there, and one above 110 as
- * 110.  A NaN or an infinity in a token reaches the outputs of all tokens of
- * its chunk (in the recurrence: its own and those after it), never another
- * sequence.
+ * tokens).  In chunks a log-gate below -110 is taken as -110 (what it leaves of
+ * the state is nothing beside the token's own write), and on the tensor cores
+ * one above 110 as 110.  A NaN or an infinity in a token reaches the outputs of
+ * all tokens of its chunk (in the recurrence: its own and those after it),
+ * never another sequence.
  */
 int32_t rm_cp_gla_state_path(const rm_gdr_state_problem* p);
 size_t rm_cp_gla_state_workspace_size(const rm_gdr_state_problem* p);

@@ -21,9 +21,9 @@
 // decays, split, into tensor memory), the state (eight), the scores (four), the outputs (four), two that issue products,
 // one of which copies too, two of gates.  The code of all of them together has to stay small: with loops unrolled
 // the warps wait for instructions (a chunk took 6700 cycles at first, 94 KB of code).  A chunk and head takes 1.25 to 1.55 us now,
-// which with 152 equal heads is HBM's rate (one prompt of 8192: 191 us, 6.7 TB/s); with fewer, what bounds it is the loop scores -> P -> P V -> scores and the outputs' way out of tensor memory, which has no room for a second
+// which with 152 equal heads is HBM's rate (one prompt of 8192: 192 us, 6.6 TB/s); with fewer, what bounds it is the loop scores -> P -> P V -> scores and the outputs' way out of tensor memory, which has no room for a second
 // set of accumulators, with issue at 55% and the tensor pipe at 36%.  13 ragged prompts of up to 4096 tokens, 32 heads of 128 x 128,
-// bf16 pool: 121 us, 4.6 TB/s of what the call cannot do without; one prompt of 8192, 16 heads: 57 us.
+// bf16 pool: 121 us, 4.6 TB/s of what the call cannot do without; one prompt of 8192, 16 heads: 58 us.
 //
 // Rounding: K, Q and V enter as they are; V~ as the sum of two bf16, or of three (all 24 bits) where the pool is
 // fp32, because its errors reach the state undamped.  S and P are rounded once to bf16: they only enter O,
@@ -739,9 +739,10 @@ rm_status fail(const char* what, bool map) {
 
 // Segments of the longest sequence (1: not cut), and their chunks: as many as keep each walk's CTAs on the GPU's 152
 // multiprocessors at once, of two chunks or more.  A chunk takes some 1.45 us (64 x 64: 1.1), two more launches and the
-// states between them some 13; with n segments the chain is two walks of 1 / n of the chunks.  The first segment gets what
-// the others leave, some 0.8 of one: the first walk takes its outputs, and those of no other, so that in equal segments the
-// others wait for it (one prompt of 8192, 16 and 32 heads: 58.7 and 97.6 us; with 0.8: 56.7 and 91.4; 0.5: 56.7 and 95.9).
+// states between them some 13; with n segments the chain is two walks of 1 / n of the chunks.  The others are as long as if the
+// first were 0.8 of one, and the first gets what they leave: the first walk takes its outputs, and those of no other, so that in
+// equal segments the others wait for it.  One prompt of 8192, 32 heads, chunks of the first and of each other segment, us: 24 and 26
+// 97.6, 20 and 27 91.4, 12 and 29 95.9; 16 heads: 11 and 13 58.7, 2 and 14 56.7.  (A gate for each token takes as long.)
 // us in a CUDA graph, whole / cut:
 //     tokens                          512          1024         2048         8192
 //     16 heads of 128 x 128           18.9 / 23.0  30.8 / 25.4  53.8 / 32.1  192 / 57

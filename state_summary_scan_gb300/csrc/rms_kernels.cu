@@ -63,7 +63,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) { *rein
 // What is kept of a gate's sigmoid s.  fp32: that of -|z|, the smaller of s and 1 - s, so that both are off by 7 u at most (u
 // = 2^-24: 2 of the exponential, 1 of the sum, 4 of the quotient) whatever z is.  bf16: s itself by the quick functions, off by
 // some (8 + |z|) u, far below bf16's 2^-8.  (16384 x 16 rows of 128 in fp32: 8 bits 54 us, with bf16's functions 47 and with a
-// quotient to nearest 62; 16 bits and the backward are bound by HBM all the same.)
+// quotient to nearest 62; fp32 outputs and the backward are bound by HBM all the same.)
 template <typename T>
 __device__ __forceinline__ float squash(float z) {
     if constexpr (sizeof(T) == 4) {
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(TPB) rms_forward_kernel(const __grid_constant_
                     top = big[i];
                     for (int o = a.group / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
                 }
+                // (the scale is off by three roundings, its inverse by two ulps more: in y8, far below e4m3's 2^-4)
                 float s = __uint_as_float(top) * r * (1.f / kF8Max);
                 s = s < kTiny ? kTiny : s;  // (a NaN stays)
                 const float f = __fdividef(1.f, s);  // (r f may leave fp32 where y is all but 0)

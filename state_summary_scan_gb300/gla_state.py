@@ -38,8 +38,10 @@ def make_gla_state_plan(max_seqs: int, max_tokens: int, H: int, Dk: int, Dv: int
     sequence (default max_tokens).  qk_heads > 0: q and k have that many heads, each shared by
     H / qk_heads consecutive heads.  bf16 calls of 32 tokens a sequence or more (Dk 128, or Dv 128 and more; 64 with Dk 64 and
     smaller Dv) run in chunks on the tensor cores, which rounds scores and states to bf16 where they enter an output: outputs
-    are off by up to one and a half times their own rounding; the state keeps the pool's precision.  recurrent=True keeps
-    every call a token recurrence, whatever the lengths of its batch, and slower for prompts."""
+    are off by up to one and a half times their own rounding; the state keeps the pool's precision.  What counts as a sequence's
+    tokens is the call's max_len: without one the plan's, or the prompts' tokens in all where they are fewer, so that the bits of a
+    short prompt can hang on its batch.  recurrent=True keeps every call a token recurrence, whatever the lengths of its batch, and
+    slower for prompts."""
     if dtype not in _DTYPES or state_dtype not in _DTYPES:
         raise ValueError("dtype and state_dtype must be fp32 or bf16")
     if scale is None:
@@ -124,7 +126,7 @@ def _call(plan, lead, S, N, max_len, q, k, v, g, state, cu, slots, fresh, o, str
 def gla_decode(plan: GlaStatePlan, q, k, v, g, state, slots=None, fresh=None, o=None, stream=None) -> torch.Tensor:
     """o [S,n,H,Dv] of n tokens for each of S sequences, q, k [S,n,qk_heads,Dk], v [S,n,H,Dv], the log-decays g
     [S,n,H] fp32, or [H]: one for each head.  The states of `state` at slots [S] int32 (None: 0 .. S-1) are
-    updated in place.  A slot outside the pool marks a padding sequence (outputs 0).  fresh [S]: non-zero
+    updated in place; those in the pool are distinct.  A slot outside the pool marks a padding sequence (outputs 0).  fresh [S]: non-zero
     starts from a zero state.  q, k, v may be slices of a fused projection; o overlaps no input."""
     if q.dim() != 4:
         raise ValueError("q must be [sequences, tokens, heads, Dk]")
@@ -135,7 +137,7 @@ def gla_decode(plan: GlaStatePlan, q, k, v, g, state, slots=None, fresh=None, o=
 def gla_prefill(plan: GlaStatePlan, q, k, v, g, state, cu_seqlens, slots=None, fresh=None, max_len=None, o=None,
                 stream=None) -> torch.Tensor:
     """o [N,H,Dv] of S ragged prompts packed along N tokens; cu_seqlens [S + 1] int32 on the
-    device.  max_len, a bound of the longest prompt (default the plan's), chooses the kernels: a
+    device.  max_len, a bound of the longest prompt (default the plan's, or N where that is less), chooses the kernels: a
     longer prompt is taken whole too, in a form made for shorter ones.  The rest as gla_decode, with
     q, k [N,qk_heads,Dk], v [N,H,Dv], g [N,H] or [H].  An empty prompt leaves its slot as it is, or
     zero when fresh.  Tokens before the first prompt and after the last one have outputs 0."""

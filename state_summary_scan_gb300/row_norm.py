@@ -135,7 +135,7 @@ def rms_norm(x, weight=None, residual=None, gate=None, gate_first: bool = False,
     which may be the residual itself (the residual stream updated in place).  Without one h is x.
     gate [..., n] (the norm of a mixer's outputs): y is times gate sigmoid(gate), or, with gate_first, u = x gate
     sigmoid(gate).  x and y are fp32 or bf16, the residual of x's type or fp32, the gate of x's type, the weight
-    [n] fp32.  x, residual and gate may be slices of a fused projection (adjacent elements, 16-byte strides, rows
+    [n] fp32.  x, residual and gate may be slices of a fused projection (adjacent elements, 16-byte bases and strides, rows
     evenly spaced in at most two dimensions); y and h are contiguous, and y may go into a contiguous x (out=x).
     n is a multiple of 8 up to 32768."""
     p, at, _ = _problem(x, residual, weight, gate, gate_first, 0, eps)
